@@ -33,8 +33,9 @@
  *   reads KV head h / (num_q_heads / num_kv_heads).
  * - The softmax scale is a required argument (there is no default 1/sqrt(d)):
  *   a query that already carries its scale is passed with scale = 1.0.
- * - There is no attention-bias, ALiBi or sliding-window argument: those are
- *   unsupported, not silently ignored.
+ * - There is no attention-bias or ALiBi argument: those are unsupported, not
+ *   silently ignored.  A sliding window is an argument of the _window calls
+ *   only.
  * - Device-side checks: a block_table entry outside [0, num_pages), a slot
  *   >= num_pages * page_size, or a seq_len outside [0, max_blocks_per_seq *
  *   page_size] is recorded in the device error word and the offending read
@@ -359,12 +360,162 @@ pa_status paged_attention_prefill(const pa_kv_pool* pool, const void* q, void* o
                                   int32_t max_seq_len, float scale, void* stream);
 
 /*
+ * paged_attention_decode_window / paged_attention_prefill_window --
+ * paged_attention_decode / paged_attention_prefill with a sliding window and
+ * sinks: a query at absolute position p (decode: p = seq_lens[b] - 1) attends
+ * to key j iff
+ *
+ *   j <= p  and  (j > p - window  or  j < num_sinks),
+ *
+ * i.e. to the last `window` keys up to its own and to the sequence's first
+ * num_sinks keys.  The pages have no counterpart of these calls.
+ *
+ * window        >= 1 (1: a query's own key and the sinks).
+ * num_sinks     >= 0.  Position indices are those of the whole sequence: keys
+ *               are not renumbered.
+ * block_table   as for the plain calls, with one difference: an entry whose
+ *               page holds no key that some query row of the sequence attends
+ *               to is never read, so the pages between the sinks and the
+ *               window may have been freed (any value, -1 included).
+ * Slots of read pages that no query row of the sequence attends to may hold
+ * anything, NaN included.  Keys and values that a row of the sequence attends
+ * to must be finite, as for the plain calls.
+ * Every other argument, limit, type, the workspace and the results are those
+ * of the plain calls; where the window reaches every key (window or num_sinks
+ * >= max_seq_len) the plain kernels run.
+ */
+pa_status paged_attention_decode_window(const pa_kv_pool* pool, const void* q, void* out,
+                                        int32_t batch, int32_t num_q_heads,
+                                        const int32_t* block_table, int32_t max_blocks_per_seq,
+                                        const int32_t* seq_lens, int32_t max_seq_len, float scale,
+                                        int32_t window, int32_t num_sinks, void* workspace,
+                                        size_t workspace_bytes, void* stream);
+
+pa_status paged_attention_prefill_window(const pa_kv_pool* pool, const void* q, void* out,
+                                         int32_t batch, int32_t num_q_heads,
+                                         const int32_t* query_start_loc, int64_t total_q,
+                                         int32_t max_q_len, const int32_t* block_table,
+                                         int32_t max_blocks_per_seq, const int32_t* seq_lens,
+                                         int32_t max_seq_len, float scale, int32_t window,
+                                         int32_t num_sinks, void* stream);
+
+/*
+ * paged_qk_norm_rope_append -- what a layer does between its qkv product and
+ * its attention, in one pass over the rows: the RMS norm of each query and key
+ * head, the rotation by position, and the append of the new K/V rows.  The
+ * pages have no counterpart of this call.  For token t with
+ * s = slot_mapping[t] >= 0 and p = positions[t]:
+ *
+ *   q_out[t, h]        = R_p(norm(q[t, h], q_weight))
+ *   key_pool.flat[s]   = R_p(norm(key[t, h], k_weight))    for every KV head h
+ *   value_pool.flat[s] = value[t]
+ *   norm(x, w)         = x / sqrt(mean(x^2) + eps) * w   (x itself when w is NULL)
+ *
+ * R_p turns the pairs of the first rotary_dim dims, with c_i =
+ * cos_sin[p, i] and s_i = cos_sin[p, rotary_dim / 2 + i]:
+ *   (x_a, x_b) -> (x_a c_i - x_b s_i, x_b c_i + x_a s_i),
+ *   (a, b) = (i, i + rotary_dim / 2), or (2i, 2i + 1) when interleaved = 1;
+ * the other dims pass through.  All arithmetic is fp32 with one rounding to
+ * the output's type; an e4m3 pool stores the code of the fp32 quotient by its
+ * scale (as paged_kv_append rounds).  The value rows are what paged_kv_append
+ * writes.
+ *
+ * q, key, value  device rows of num_q_heads / num_kv_heads heads of head_dim
+ *                contiguous elements (f32 for f32 pools, else bf16); token t
+ *                starts at t * q_stride (key_stride, value_stride) elements, so
+ *                slices of one qkv product can be passed.  Strides are at
+ *                least a row long.
+ * q_out          device [num_tokens, num_q_heads, head_dim], the rows' type; q
+ *                itself when its rows are contiguous, else memory that no row
+ *                of q overlaps (PA_ERR_SHAPE); no input overlaps q_out or the
+ *                pools otherwise.
+ * q_weight, k_weight  device [head_dim], the rows' type, or NULL: no norm.
+ * eps            >= 0, finite.
+ * positions      device int32 [num_tokens], each in [0, max_position).
+ * cos_sin        device f32 [max_position, rotary_dim].
+ * rotary_dim     a multiple of 8, at most head_dim; 0: no rotation (positions
+ *                and cos_sin may be NULL).
+ * slot_mapping   as for paged_kv_append; a negative entry marks a padding
+ *                token, of which nothing is read or written (its q_out row is
+ *                left as it was).
+ * A slot or position out of range is recorded in the device error word (codes
+ * 2 and 6) and that token is skipped like a padding token.
+ * head_dim a multiple of 8, at most 256 (PA_ERR_UNSUPPORTED); any alignment
+ * of the element type (16-byte aligned rows of bf16 heads whose head_dim and
+ * rotary_dim are multiples of 16 are the fast path).
+ */
+pa_status paged_qk_norm_rope_append(const pa_kv_pool* pool, const void* q, int64_t q_stride,
+                                    const void* key, int64_t key_stride, const void* value,
+                                    int64_t value_stride, void* q_out, int32_t num_q_heads,
+                                    const void* q_weight, const void* k_weight, float eps,
+                                    const int32_t* positions, const float* cos_sin,
+                                    int64_t max_position, int32_t rotary_dim, int32_t interleaved,
+                                    const int64_t* slot_mapping, int64_t num_tokens, void* stream);
+
+/*
+ * paged_kv_copy_pages -- copy whole pages inside the pools of all layers: in
+ * every pool of `pools`, K and V, page dst_pages[i] becomes page src_pages[i].
+ * A fork of a sequence shares its full pages and copies the page that both
+ * sequences will go on writing; defragmentation moves pages.  The pages name
+ * no such call.
+ *
+ * pools         host array of num_pools descriptors (at most 1024), e.g. one
+ *               per layer, read before the call returns: all of one geometry
+ *               and dtype, no two tensors of them overlapping (PA_ERR_SHAPE).
+ *               Any dtype: pages are copied bit for bit.
+ * src_pages, dst_pages  device int32 [num_copies].  A pair with a negative
+ *               entry is padding (skipped); a pair with src = dst copies
+ *               nothing; an entry >= num_pages is recorded in the device error
+ *               word (code 1) and the pair is skipped.  The pairs run in no
+ *               order: a destination page must appear once and must not be the
+ *               source of another pair (else which contents land there is
+ *               unspecified).
+ */
+pa_status paged_kv_copy_pages(const pa_kv_pool* pools, int32_t num_pools, const int32_t* src_pages,
+                              const int32_t* dst_pages, int64_t num_copies, void* stream);
+
+/*
+ * paged_kv_compact -- keep a part of each sequence's rows, moved together in
+ * place, in the pools of all layers: eviction of cached keys, or the accepted
+ * tokens of a verified draft.  With keep_b = keep[keep_indptr[b] ..
+ * keep_indptr[b+1]) and n_b its length, row base[b] + i of sequence b (through
+ * its block_table row) becomes its old row keep_b[i], i in [0, n_b), and
+ *
+ *   new_seq_lens[b] = base[b] + n_b.
+ *
+ * Rows below base[b] stay; rows at or past the new length are left as they
+ * were, and the pages past ceil(new_seq_lens[b] / page_size) are free for other
+ * use.  Keys move as stored: a rotation by position stays that of the old
+ * position.  The pages name no such call.
+ *
+ * pools         as for paged_kv_copy_pages, at least one.
+ * block_table   device int32 [batch, max_blocks_per_seq]; pages that hold rows
+ *               written here must not be shared by two sequences (copy them
+ *               first).  batch <= 65535.
+ * seq_lens      device int32 [batch]: the lengths before the call.
+ * base          device int32 [batch] in [0, seq_lens[b]], or NULL: all 0.
+ * keep_indptr   device int32 [batch + 1], non-decreasing, within [0, num_keep].
+ * keep          device int32 [num_keep]: old positions, strictly ascending per
+ *               sequence, in [base[b], seq_lens[b]).
+ * new_seq_lens  device int32 [batch], written; NULL: not wanted.  May not
+ *               overlap the inputs (PA_ERR_SHAPE).
+ * A position that is not ascending or out of range is recorded in the device
+ * error word (code 7) and its row is not moved; a sequence whose length or base
+ * (code 3) or slice of keep (code 7) is out of range is left as it was, with
+ * its length; a block_table entry out of range (code 1) skips the row.
+ */
+pa_status paged_kv_compact(const pa_kv_pool* pools, int32_t num_pools, const int32_t* block_table,
+                           int32_t max_blocks_per_seq, const int32_t* seq_lens, int32_t batch,
+                           const int32_t* base, const int32_t* keep_indptr, const int32_t* keep,
+                           int64_t num_keep, int32_t* new_seq_lens, void* stream);
+
+/*
  * paged_device_error -- read and clear the device error word of the current
  * device.  Synchronises the device.  *code = 0 when no violation was seen,
  * else 1 = block_table / kv_indices entry out of range, 2 = slot out of
  * range, 3 = seq_len (or CSR kv_indptr / kv_last_page_len) out of range,
  * 4 = query_start_loc inconsistent, 5 = a bounded wait inside a kernel gave
- * up; *detail holds the offending value.  Either pointer may be NULL.
+ * up, 6 = position out of range, 7 = compaction list inconsistent; *detail holds the offending value.  Either pointer may be NULL.
  */
 pa_status paged_device_error(int64_t* code, int64_t* detail);
 

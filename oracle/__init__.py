@@ -31,6 +31,10 @@ What it follows:
 * the compressed (CSR) page-table form ``kv_indptr`` / ``kv_indices`` /
   ``kv_last_page_len`` named by NVIDIA/recsys-examples PR #400
   (KVCacheMetadata);
+* attention over a sliding window and a sequence's first tokens
+  (:mod:`oracle.window`), the norm and rotation of queries and keys, page
+  copies and the compaction of a sequence's rows (:mod:`oracle.rows`): not on
+  the pages, defined plainly in those modules;
 * one decode step as one call: the append of the step's rows followed by
   the decode that attends to them (mobius page, "How it works (per
   attention layer)", steps 1 and 2).
@@ -56,5 +60,14 @@ from .paged_attention import (  # noqa: F401
     csr_pages,
     paged_attention_decode_csr,
     paged_attention_prefill_csr,
+)
+from .window import paged_attention_decode_window, paged_attention_prefill_window, visible_keys  # noqa: F401,E402
+from .rows import (  # noqa: F401,E402
+    paged_kv_compact,
+    paged_kv_copy_pages,
+    qk_norm_rope,
+    rms_norm,
+    rope_table,
+    rotate,
 )
 from . import kv_fp8  # noqa: F401,E402

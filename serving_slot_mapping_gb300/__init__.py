@@ -8,6 +8,12 @@ from .capi import (  # noqa: F401
     paged_kv_append,
     paged_attention_decode,
     paged_attention_prefill,
+    paged_attention_decode_window,
+    paged_attention_prefill_window,
+    paged_qk_norm_rope_append,
+    paged_kv_copy_pages,
+    paged_kv_compact,
+    make_pools,
     decode_workspace,
     decode_workspace_size,
     device_error,

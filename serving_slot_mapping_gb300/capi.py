@@ -65,6 +65,16 @@ SIGNATURES = {
                                            _c_void_p]),
     "paged_attention_prefill": (_i32, [_PPOOL, _c_void_p, _c_void_p, _i32, _i32, _c_void_p, _i64,
                                        _i32, _c_void_p, _i32, _c_void_p, _i32, _f32, _c_void_p]),
+    "paged_attention_decode_window": (_i32, [_PPOOL, _c_void_p, _c_void_p, _i32, _i32, _c_void_p, _i32,
+                                             _c_void_p, _i32, _f32, _i32, _i32, _c_void_p, _sz, _c_void_p]),
+    "paged_attention_prefill_window": (_i32, [_PPOOL, _c_void_p, _c_void_p, _i32, _i32, _c_void_p, _i64, _i32,
+                                              _c_void_p, _i32, _c_void_p, _i32, _f32, _i32, _i32, _c_void_p]),
+    "paged_qk_norm_rope_append": (_i32, [_PPOOL, _c_void_p, _i64, _c_void_p, _i64, _c_void_p, _i64, _c_void_p,
+                                         _i32, _c_void_p, _c_void_p, _f32, _c_void_p, _c_void_p, _i64, _i32, _i32,
+                                         _c_void_p, _i64, _c_void_p]),
+    "paged_kv_copy_pages": (_i32, [_PPOOL, _i32, _c_void_p, _c_void_p, _i64, _c_void_p]),
+    "paged_kv_compact": (_i32, [_PPOOL, _i32, _c_void_p, _i32, _c_void_p, _i32, _c_void_p, _c_void_p, _c_void_p,
+                                _i64, _c_void_p, _c_void_p]),
     "pa_testing_decode_part_wait": (_i32, [_PPOOL, _c_void_p, _c_void_p, _i32, _i32, _c_void_p, _i32,
                                            _c_void_p, _i32, _f32, _c_void_p, _sz, ctypes.c_uint64, _i32,
                                            _c_void_p]),
@@ -414,3 +424,238 @@ def paged_attention_prefill_csr(key_pool, value_pool, q, query_start_loc, kv_ind
                                            int(max_seq_len), float(scale), _stream(stream))
     _check(st, "paged_attention_prefill_csr")
     return out
+
+
+def _here(**tensors):
+    """Refuse tensors that are not on the current CUDA device (the kernels
+    get raw device pointers)."""
+    for name, t in tensors.items():
+        if t is not None and not t.is_cuda:
+            raise ValueError(f"{name} must be a CUDA tensor")
+    cur = torch.cuda.current_device()
+    for name, t in tensors.items():
+        if t is not None and t.get_device() != cur:
+            raise ValueError(f"{name} is on cuda:{t.get_device()}, the current device is cuda:{cur}")
+
+
+def _used_on(stream, *tensors):
+    """Tensors allocated here and used on a stream other than the current one:
+    their memory is not handed out again before that stream's work is done."""
+    if stream is None:
+        return
+    if not hasattr(stream, "cuda_stream"):
+        stream = torch.cuda.ExternalStream(int(stream))
+    for t in tensors:
+        if t is not None:
+            t.record_stream(stream)
+
+
+def _int32(**tensors):
+    for name, t in tensors.items():
+        if t is not None:
+            if t.dtype != torch.int32:
+                raise TypeError(f"{name} must be int32")
+            _contig(t, name)
+
+
+def paged_attention_decode_window(key_pool, value_pool, q, block_table, seq_lens, scale, window, num_sinks=0,
+                                  max_seq_len=None, out=None, workspace=None, stream=None, k_scale=1.0,
+                                  v_scale=1.0):
+    """Decode attention over a sliding window and the sequence's first tokens:
+    query ``q[b]`` (position ``seq_lens[b] - 1``) attends to the last ``window``
+    keys and to the first ``num_sinks``.
+
+    Arguments otherwise as for :func:`paged_attention_decode`; entries of
+    ``block_table`` whose pages hold no visible key are never read (those pages
+    may be freed)."""
+    pool = make_pool(key_pool, value_pool, k_scale, v_scale)
+    _int32(block_table=block_table, seq_lens=seq_lens)
+    made = out is None
+    out = _q_out(q, out, key_pool)
+    B, hq, _ = q.shape
+    if block_table.dim() != 2 or block_table.shape[0] != B or seq_lens.numel() != B:
+        raise ValueError("block_table must be [B, max_blocks] and seq_lens [B]")
+    mb = block_table.shape[1]
+    if max_seq_len is None:
+        max_seq_len = mb * pool.page_size
+    _here(key_pool=key_pool, value_pool=value_pool, q=q, block_table=block_table, seq_lens=seq_lens, out=out,
+          workspace=workspace)
+    if workspace is None:
+        workspace = decode_workspace(B, hq, key_pool)
+        _used_on(stream, workspace)
+    if made:
+        _used_on(stream, out)
+    wbytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
+    st = lib().paged_attention_decode_window(ctypes.byref(pool), _ptr(q), _ptr(out), B, hq, _ptr(block_table), mb,
+                                             _ptr(seq_lens), int(max_seq_len), float(scale), int(window),
+                                             int(num_sinks), _ptr(workspace), wbytes, _stream(stream))
+    _check(st, "paged_attention_decode_window")
+    return out
+
+
+def paged_attention_prefill_window(key_pool, value_pool, q, query_start_loc, block_table, seq_lens, scale,
+                                   max_q_len, window, num_sinks=0, max_seq_len=None, out=None, stream=None,
+                                   k_scale=1.0, v_scale=1.0):
+    """Varlen causal prefill over a sliding window and the sequence's first
+    tokens: the row at position p attends to keys j <= p with ``j > p - window``
+    or ``j < num_sinks``.  Arguments otherwise as for
+    :func:`paged_attention_prefill`; pages without a key that some row of the
+    sequence attends to are never read."""
+    pool = make_pool(key_pool, value_pool, k_scale, v_scale)
+    _int32(query_start_loc=query_start_loc, block_table=block_table, seq_lens=seq_lens)
+    made = out is None
+    out = _q_out(q, out, key_pool)
+    T, hq, _ = q.shape
+    B = query_start_loc.numel() - 1
+    if block_table.dim() != 2 or block_table.shape[0] != B or seq_lens.numel() != B:
+        raise ValueError("block_table must be [B, max_blocks] and seq_lens [B], with query_start_loc [B + 1]")
+    mb = block_table.shape[1]
+    if max_seq_len is None:
+        max_seq_len = mb * pool.page_size
+    _here(key_pool=key_pool, value_pool=value_pool, q=q, query_start_loc=query_start_loc, block_table=block_table,
+          seq_lens=seq_lens, out=out)
+    if made:
+        _used_on(stream, out)
+    st = lib().paged_attention_prefill_window(ctypes.byref(pool), _ptr(q), _ptr(out), B, hq, _ptr(query_start_loc),
+                                              T, int(max_q_len), _ptr(block_table), mb, _ptr(seq_lens),
+                                              int(max_seq_len), float(scale), int(window), int(num_sinks),
+                                              _stream(stream))
+    _check(st, "paged_attention_prefill_window")
+    return out
+
+
+def _token_rows(t, name, T, heads, d, dtype):
+    """Elements between the tokens of ``t [T, heads, d]`` (heads and dims
+    contiguous; the tokens may be slices of longer rows)."""
+    if t.dtype != dtype or t.shape != (T, heads, d):
+        raise ValueError(f"{name} must be [T, {heads}, {d}] of {dtype}")
+    s = t.stride()
+    if (d > 1 and s[2] != 1) or (heads > 1 and s[1] != d):
+        raise ValueError(f"the heads and dims of {name} must be contiguous")
+    return s[0] if T > 1 else heads * d
+
+
+def paged_qk_norm_rope_append(key_pool, value_pool, q, key, value, slot_mapping, positions=None, cos_sin=None,
+                              q_weight=None, k_weight=None, eps=1e-6, interleaved=False, out=None, stream=None,
+                              k_scale=1.0, v_scale=1.0):
+    """RMS norm and position rotation of each query and key head and the append
+    of the new K/V rows, in one pass.
+
+    ``q [T, Hq, D]``, ``key``/``value [T, Hkv, D]``: heads and dims contiguous,
+    any token stride (slices of one qkv product).  ``q_weight`` / ``k_weight``
+    ``[D]`` of the rows' dtype (None: no norm); ``cos_sin`` float32
+    ``[max_position, rotary_dim]``, cosines then sines (None: no rotation), read
+    at ``positions`` int32 ``[T]``; ``slot_mapping`` int64 ``[T]``, negative for
+    a padding token (nothing of it is read or written).  Returns the rotated
+    queries ``[T, Hq, D]`` (``out``, which may be ``q`` itself when contiguous);
+    the pools are updated in place."""
+    pool = make_pool(key_pool, value_pool, k_scale, v_scale)
+    if q.dim() != 3:
+        raise ValueError("q must be [T, num_q_heads, head_dim]")
+    T, hq, d = q.shape
+    row_dtype = torch.bfloat16 if key_pool.dtype == torch.float8_e4m3fn else key_pool.dtype
+    sq = _token_rows(q, "q", T, hq, pool.head_dim, row_dtype)
+    sk = _token_rows(key, "key", T, pool.num_kv_heads, pool.head_dim, row_dtype)
+    sv = _token_rows(value, "value", T, pool.num_kv_heads, pool.head_dim, row_dtype)
+    if slot_mapping.dtype != torch.int64:
+        raise TypeError("slot_mapping must be int64")
+    if slot_mapping.numel() != T:
+        raise ValueError("one slot per token: slot_mapping [T]")
+    _contig(slot_mapping, "slot_mapping")
+    rot = max_pos = 0
+    if cos_sin is not None:
+        if cos_sin.dtype != torch.float32 or cos_sin.dim() != 2:
+            raise ValueError("cos_sin must be float32 [max_position, rotary_dim]")
+        _contig(cos_sin, "cos_sin")
+        max_pos, rot = cos_sin.shape
+        if positions is None or positions.numel() != T:
+            raise ValueError("a rotation needs one position per token: positions [T]")
+        _int32(positions=positions)
+    for name, w in (("q_weight", q_weight), ("k_weight", k_weight)):
+        if w is not None:
+            if w.dtype != row_dtype or w.numel() != d:
+                raise ValueError(f"{name} must be [{d}] of {row_dtype}")
+            _contig(w, name)
+    made = out is None
+    if made:
+        out = torch.empty((T, hq, d), dtype=row_dtype, device=q.device)
+    else:
+        _contig(out, "out")
+        if out.shape != q.shape or out.dtype != q.dtype:
+            raise ValueError("out must match q in shape and dtype")
+    _here(key_pool=key_pool, value_pool=value_pool, q=q, key=key, value=value, slot_mapping=slot_mapping,
+          positions=positions if rot else None, cos_sin=cos_sin, q_weight=q_weight, k_weight=k_weight, out=out)
+    if made:
+        _used_on(stream, out)
+    st = lib().paged_qk_norm_rope_append(ctypes.byref(pool), _ptr(q), sq, _ptr(key), sk, _ptr(value), sv, _ptr(out),
+                                         hq, _ptr(q_weight), _ptr(k_weight), float(eps),
+                                         _ptr(positions if rot else None), _ptr(cos_sin), max_pos, rot,
+                                         1 if interleaved else 0, _ptr(slot_mapping), T, _stream(stream))
+    _check(st, "paged_qk_norm_rope_append")
+    return out
+
+
+class Pools:
+    """The K/V pools of several layers as one argument (see :func:`make_pools`)."""
+
+    def __init__(self, pairs):
+        pairs = list(pairs)
+        self.array = (PaKvPool * len(pairs))(*(make_pool(k, v) for k, v in pairs))
+        self.tensors = pairs  # the descriptors hold their addresses
+        self.count = len(pairs)
+        # where the kernels of a call on these pools run: the one device of all of them
+        for k, v in pairs:
+            if k.device != pairs[0][0].device or v.device != pairs[0][0].device:
+                raise ValueError("the pools must be on one device")
+
+
+def make_pools(pairs) -> Pools:
+    """Describe the ``(key_pool, value_pool)`` pairs of several layers (same
+    shape and dtype) once, for :func:`paged_kv_copy_pages` and
+    :func:`paged_kv_compact`."""
+    return Pools(pairs)
+
+
+def _pools(pools) -> Pools:
+    return pools if isinstance(pools, Pools) else Pools(pools)
+
+
+def paged_kv_copy_pages(pools, src_pages, dst_pages, stream=None):
+    """In every pool of ``pools`` (:func:`make_pools`, or a list of ``(key_pool,
+    value_pool)``), K and V: page ``dst_pages[i]`` becomes page ``src_pages[i]``
+    (int32 ``[n]``; a negative entry marks a padding pair).  Destinations must be
+    distinct and no pair's source."""
+    ps = _pools(pools)
+    _int32(src_pages=src_pages, dst_pages=dst_pages)
+    n = src_pages.numel()
+    if dst_pages.numel() != n:
+        raise ValueError("src_pages and dst_pages must have the same length")
+    _here(key_pool=ps.tensors[0][0] if ps.count else None, src_pages=src_pages, dst_pages=dst_pages)
+    st = lib().paged_kv_copy_pages(ps.array, ps.count, _ptr(src_pages), _ptr(dst_pages), n, _stream(stream))
+    _check(st, "paged_kv_copy_pages")
+
+
+def paged_kv_compact(pools, block_table, seq_lens, keep_indptr, keep, base=None, new_seq_lens=None, stream=None):
+    """Move the kept rows of each sequence to its front, in place, in every pool
+    of ``pools``: row ``base[b] + i`` becomes old row ``keep[keep_indptr[b] + i]``
+    (ascending positions per sequence; ``base`` None: 0).  Returns
+    ``new_seq_lens`` int32 ``[B]`` = ``base`` + the number of kept rows."""
+    ps = _pools(pools)
+    _int32(block_table=block_table, seq_lens=seq_lens, keep_indptr=keep_indptr, keep=keep, base=base,
+           new_seq_lens=new_seq_lens)
+    B = seq_lens.numel()
+    if block_table.dim() != 2 or block_table.shape[0] != B or keep_indptr.numel() != B + 1:
+        raise ValueError("block_table must be [B, max_blocks], seq_lens [B] and keep_indptr [B + 1]")
+    for name, t in (("base", base), ("new_seq_lens", new_seq_lens)):
+        if t is not None and t.numel() != B:
+            raise ValueError(f"{name} must be [B]")
+    _here(key_pool=ps.tensors[0][0] if ps.count else None, block_table=block_table, seq_lens=seq_lens,
+          keep_indptr=keep_indptr, keep=keep, base=base, new_seq_lens=new_seq_lens)
+    if new_seq_lens is None:
+        new_seq_lens = torch.empty_like(seq_lens)
+        _used_on(stream, new_seq_lens)
+    st = lib().paged_kv_compact(ps.array, ps.count, _ptr(block_table), block_table.shape[1], _ptr(seq_lens), B,
+                                _ptr(base), _ptr(keep_indptr), _ptr(keep), keep.numel(), _ptr(new_seq_lens),
+                                _stream(stream))
+    _check(st, "paged_kv_compact")
+    return new_seq_lens

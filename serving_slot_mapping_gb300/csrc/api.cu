@@ -2,6 +2,7 @@
 // argument checks, launch-shape choices and dispatch to the kernels.
 #include <algorithm>
 #include <atomic>
+#include <climits>
 #include <cmath>
 #include <cstdint>
 
@@ -233,11 +234,30 @@ Table dense_table(const int32_t* block_table, int32_t max_blocks, const int32_t*
   return t;
 }
 
+// Sliding window of the _window calls: position p sees keys j <= p with
+// j > p - size or j < sinks.
+struct Window {
+  int32_t size = INT32_MAX;
+  int32_t sinks = 0;
+};
+
+// The window to hand to the kernels for sequences of at most max_seq_len
+// keys: none when it hides no key of any of them.
+pa_status check_window(int32_t window, int32_t num_sinks, int32_t max_seq_len, Window* w) {
+  if (window < 1 || num_sinks < 0) return PA_ERR_SHAPE;
+  *w = Window{};
+  if (window >= max_seq_len || num_sinks >= max_seq_len) return PA_OK;
+  w->size = window;
+  w->sinks = std::min(num_sinks, INT32_MAX - 1024);  // the kernels round it up to whole tiles
+  return PA_OK;
+}
+
 // Launch parameters of the bf16 split-KV decode (shared by plain and cascade
 // decode); the partials take the first bytes of the workspace.
 pa_status bf16_decode_params(const pa_kv_pool* pool, const void* q, void* out, int32_t batch,
                              int32_t num_q_heads, const Table& t, int32_t max_seq_len, float scale, void* workspace,
-                             size_t workspace_bytes, pa::DecodeParams* p, int reserved_sms = 0) {
+                             size_t workspace_bytes, pa::DecodeParams* p, int reserved_sms = 0,
+                             const Window& win = Window{}) {
   const int32_t group = num_q_heads / pool->num_kv_heads;
   // the decode kernel's TMA boxes address a pool row (slot) with a 32-bit
   // coordinate: at most 2^31 - 1 slots per pool
@@ -248,7 +268,11 @@ pa_status bf16_decode_params(const pa_kv_pool* pool, const void* q, void* out, i
   if (!aligned(q, 16) || !aligned(out, 4)) return PA_ERR_ALIGN;
   const int hb = pa::decode_heads_per_box(pool->num_kv_heads, group, pool->page_size);
   const int sms = num_sms() - reserved_sms;
-  const int ctas = pa::decode_num_ctas(sms < 1 ? 1 : sms, batch, pool->num_kv_heads, max_seq_len, hb);
+  const bool windowed = win.size != INT32_MAX;
+  // keys in the blocks a sequence's units are: a window and sinks that end inside blocks
+  const int64_t used = windowed ? (int64_t)win.size + win.sinks + 48 : INT32_MAX;
+  const int ctas = pa::decode_num_ctas(sms < 1 ? 1 : sms, batch, pool->num_kv_heads,
+                                       (int32_t)std::min<int64_t>(max_seq_len, used), hb);
   const size_t need = decode_ws_bytes(batch, num_q_heads, pool->num_kv_heads, pool->head_dim, ctas, hb);
   if (need > 0 && (workspace == nullptr || workspace_bytes < need)) return PA_ERR_WORKSPACE;
   if (!aligned(workspace, 16)) return PA_ERR_ALIGN;
@@ -287,6 +311,8 @@ pa_status bf16_decode_params(const pa_kv_pool* pool, const void* q, void* out, i
   const int pen = pa::decode_segment_penalty(pool->head_dim, hb, group, kv8(pool), batch, pool->num_kv_heads, ctas);
   const int64_t max_keys = std::max<int64_t>(max_seq_len, (int64_t)t.max_blocks * pool->page_size);
   p->seg_penalty = (int64_t)batch * ((max_keys + 15) / 16 + pen) <= INT32_MAX ? pen : 0;
+  p->window = windowed ? win.size : 0;
+  p->num_sinks = windowed ? win.sinks : 0;
   p->err = error_word();
   return PA_OK;
 }
@@ -338,7 +364,7 @@ namespace {
 
 pa_status decode_impl(const pa_kv_pool* pool, const void* q, void* out, int32_t batch, int32_t num_q_heads,
                       const Table& t, int32_t max_seq_len, float scale, void* workspace, size_t workspace_bytes,
-                      void* stream) {
+                      void* stream, const Window& win = Window{}) {
   pa_status st = check_attention(pool, batch, num_q_heads, t.max_blocks, max_seq_len, scale);
   if (st != PA_OK) return st;
   if (batch == 0) return PA_OK;
@@ -366,18 +392,21 @@ pa_status decode_impl(const pa_kv_pool* pool, const void* q, void* out, int32_t 
     p.group = num_q_heads / pool->num_kv_heads;
     p.max_blocks = t.max_blocks;
     p.scale = scale;
+    p.window = win.size;
+    p.num_sinks = win.sinks;
     p.err = error_word();
     return pa::launch_attn_f32(p, num_sms(), s) == cudaSuccess ? PA_OK : PA_ERR_CUDA;
   }
   pa::DecodeParams p;
-  st = bf16_decode_params(pool, q, out, batch, num_q_heads, t, max_seq_len, scale, workspace, workspace_bytes, &p);
+  st = bf16_decode_params(pool, q, out, batch, num_q_heads, t, max_seq_len, scale, workspace, workspace_bytes, &p, 0,
+                          win);
   if (st != PA_OK) return st;
   return pa::launch_decode_bf16(p, s) == cudaSuccess ? PA_OK : PA_ERR_CUDA;
 }
 
 pa_status prefill_impl(const pa_kv_pool* pool, const void* q, void* out, int32_t batch, int32_t num_q_heads,
                        const int32_t* query_start_loc, int64_t total_q, int32_t max_q_len, const Table& t,
-                       int32_t max_seq_len, float scale, void* stream) {
+                       int32_t max_seq_len, float scale, void* stream, const Window& win = Window{}) {
   pa_status st = check_attention(pool, batch, num_q_heads, t.max_blocks, max_seq_len, scale);
   if (st != PA_OK) return st;
   if (total_q < 0 || max_q_len < 0 || total_q > INT32_MAX) return PA_ERR_SHAPE;
@@ -411,6 +440,8 @@ pa_status prefill_impl(const pa_kv_pool* pool, const void* q, void* out, int32_t
     p.group = group;
     p.max_blocks = t.max_blocks;
     p.scale = scale;
+    p.window = win.size;
+    p.num_sinks = win.sinks;
     p.err = error_word();
     return pa::launch_attn_f32(p, num_sms(), s) == cudaSuccess ? PA_OK : PA_ERR_CUDA;
   }
@@ -437,6 +468,8 @@ pa_status prefill_impl(const pa_kv_pool* pool, const void* q, void* out, int32_t
   p.kv8 = kv8(pool) ? 1 : 0;
   p.scale_log2 = (float)((double)scale * (kv8(pool) ? (double)pool->k_scale : 1.0) * kLog2e);
   p.v_scale = kv8(pool) ? pool->v_scale : 1.f;
+  p.window = win.size != INT32_MAX ? win.size : 0;
+  p.num_sinks = win.size != INT32_MAX ? win.sinks : 0;
   p.err = error_word();
   return pa::launch_prefill_bf16(p, s) == cudaSuccess ? PA_OK : PA_ERR_CUDA;
 }
@@ -643,6 +676,225 @@ pa_status paged_attention_prefill_csr(const pa_kv_pool* pool, const void* q, voi
   if (st != PA_OK) return st;
   return prefill_impl(pool, q, out, batch, num_q_heads, query_start_loc, total_q, max_q_len, t, max_seq_len, scale,
                       stream);
+}
+
+pa_status paged_attention_decode_window(const pa_kv_pool* pool, const void* q, void* out, int32_t batch,
+                                        int32_t num_q_heads, const int32_t* block_table,
+                                        int32_t max_blocks_per_seq, const int32_t* seq_lens, int32_t max_seq_len,
+                                        float scale, int32_t window, int32_t num_sinks, void* workspace,
+                                        size_t workspace_bytes, void* stream) {
+  Window w;
+  const pa_status st = check_window(window, num_sinks, max_seq_len, &w);
+  if (st != PA_OK) return st;
+  return decode_impl(pool, q, out, batch, num_q_heads, dense_table(block_table, max_blocks_per_seq, seq_lens),
+                     max_seq_len, scale, workspace, workspace_bytes, stream, w);
+}
+
+pa_status paged_attention_prefill_window(const pa_kv_pool* pool, const void* q, void* out, int32_t batch,
+                                         int32_t num_q_heads, const int32_t* query_start_loc, int64_t total_q,
+                                         int32_t max_q_len, const int32_t* block_table,
+                                         int32_t max_blocks_per_seq, const int32_t* seq_lens, int32_t max_seq_len,
+                                         float scale, int32_t window, int32_t num_sinks, void* stream) {
+  Window w;
+  const pa_status st = check_window(window, num_sinks, max_seq_len, &w);
+  if (st != PA_OK) return st;
+  return prefill_impl(pool, q, out, batch, num_q_heads, query_start_loc, total_q, max_q_len,
+                      dense_table(block_table, max_blocks_per_seq, seq_lens), max_seq_len, scale, stream, w);
+}
+
+pa_status paged_qk_norm_rope_append(const pa_kv_pool* pool, const void* q, int64_t q_stride, const void* key,
+                                    int64_t key_stride, const void* value, int64_t value_stride, void* q_out,
+                                    int32_t num_q_heads, const void* q_weight, const void* k_weight, float eps,
+                                    const int32_t* positions, const float* cos_sin, int64_t max_position,
+                                    int32_t rotary_dim, int32_t interleaved, const int64_t* slot_mapping,
+                                    int64_t num_tokens, void* stream) {
+  pa_status st = check_pool(pool);
+  if (st != PA_OK) return st;
+  const int32_t D = pool->head_dim;
+  if (num_tokens < 0 || num_q_heads <= 0 || rotary_dim < 0 || rotary_dim > D || (interleaved & ~1) != 0)
+    return PA_ERR_SHAPE;
+  if (D % 8 != 0 || D > 256 || rotary_dim % 8 != 0) return PA_ERR_UNSUPPORTED;
+  if (rotary_dim > 0 && max_position <= 0) return PA_ERR_SHAPE;
+  if (!(std::isfinite(eps) && eps >= 0.f)) return PA_ERR_RANGE;
+  const int64_t q_row = (int64_t)num_q_heads * D, kv_row = (int64_t)pool->num_kv_heads * D;
+  if (q_row > INT32_MAX || kv_row > INT32_MAX || num_tokens > INT32_MAX || max_position > INT32_MAX)
+    return PA_ERR_RANGE;
+  if (num_tokens > 1 && (q_stride < q_row || key_stride < kv_row || value_stride < kv_row)) return PA_ERR_SHAPE;
+  if (num_tokens == 0) return PA_OK;
+  if (q == nullptr || key == nullptr || value == nullptr || q_out == nullptr || slot_mapping == nullptr)
+    return PA_ERR_NULL;
+  if (rotary_dim > 0 && (positions == nullptr || cos_sin == nullptr)) return PA_ERR_NULL;
+  const size_t es = pool->dtype == PA_DTYPE_F32 ? 4 : 2;  // of the rows
+  if (!aligned(q, es) || !aligned(key, es) || !aligned(value, es) || !aligned(q_out, es) || !aligned(q_weight, es) ||
+      !aligned(k_weight, es) || !aligned(slot_mapping, 8) || !aligned(positions, 4) || !aligned(cos_sin, 4))
+    return PA_ERR_ALIGN;
+  // q_out is q itself, row for row, or memory that no row of q reaches
+  const uintptr_t q0 = reinterpret_cast<uintptr_t>(q), o0 = reinterpret_cast<uintptr_t>(q_out);
+  const uintptr_t q1 = q0 + (uintptr_t)(((num_tokens - 1) * q_stride + q_row) * (int64_t)es);
+  const uintptr_t o1 = o0 + (uintptr_t)(num_tokens * q_row * (int64_t)es);
+  if (q0 < o1 && o0 < q1 && !(q0 == o0 && (num_tokens == 1 || q_stride == q_row))) return PA_ERR_SHAPE;
+  pa::NormRopeParams p{};
+  p.key_pool = pool->key_pool;
+  p.value_pool = pool->value_pool;
+  p.q = q;
+  p.key = key;
+  p.value = value;
+  p.q_stride = q_stride;
+  p.key_stride = key_stride;
+  p.value_stride = value_stride;
+  p.q_out = q_out;
+  p.q_weight = q_weight;
+  p.k_weight = k_weight;
+  p.positions = positions;
+  p.cos_sin = cos_sin;
+  p.max_position = max_position;
+  p.slot_mapping = slot_mapping;
+  p.num_tokens = num_tokens;
+  p.num_slots = pool->num_pages * (int64_t)pool->page_size;
+  p.num_q_heads = num_q_heads;
+  p.num_kv_heads = pool->num_kv_heads;
+  p.head_dim = D;
+  p.rotary_dim = rotary_dim;
+  p.interleaved = interleaved;
+  p.eps = eps;
+  p.f32 = pool->dtype == PA_DTYPE_F32 ? 1 : 0;
+  p.kv8 = kv8(pool) ? 1 : 0;
+  p.k_scale = pool->k_scale;
+  p.v_scale = pool->v_scale;
+  p.err = error_word();
+  // Elements per access: 8 bf16 or 4 f32 (16 bytes) where both halves of the
+  // rotated and of the other dims are whole vectors and every row starts on
+  // one; else 4 bf16; else single elements.
+  auto rows_aligned = [&](int n) {
+    const size_t a = n * es, pa_ = kv8(pool) ? (size_t)n : a;
+    return aligned(q, a) && aligned(key, a) && aligned(value, a) && aligned(q_out, a) && aligned(q_weight, a) &&
+           aligned(k_weight, a) && aligned(pool->key_pool, pa_) && aligned(pool->value_pool, pa_) &&
+           (num_tokens == 1 || (q_stride % n == 0 && key_stride % n == 0 && value_stride % n == 0));
+  };
+  if (!p.f32 && D % 16 == 0 && rotary_dim % 16 == 0 && rows_aligned(8))
+    p.vec = 8;
+  else
+    p.vec = rows_aligned(4) ? 4 : 0;
+  return pa::launch_qk_norm_rope_append(p, num_sms(), static_cast<cudaStream_t>(stream)) == cudaSuccess ? PA_OK
+                                                                                                       : PA_ERR_CUDA;
+}
+
+namespace {
+
+constexpr int32_t kMaxPools = 1024;
+
+// The pools of one call over all layers: each valid, all of one geometry and
+// element type, and no two tensors of them overlapping (a row would be moved
+// twice).
+pa_status check_pools(const pa_kv_pool* pools, int32_t num_pools) {
+  if (num_pools < 0) return PA_ERR_SHAPE;
+  if (num_pools > kMaxPools) return PA_ERR_RANGE;
+  if (num_pools == 0) return PA_OK;
+  if (pools == nullptr) return PA_ERR_NULL;
+  uintptr_t starts[2 * kMaxPools];
+  for (int32_t i = 0; i < num_pools; ++i) {
+    const pa_status st = check_pool(pools + i);
+    if (st != PA_OK) return st;
+    if (pools[i].num_pages != pools[0].num_pages || pools[i].page_size != pools[0].page_size ||
+        pools[i].num_kv_heads != pools[0].num_kv_heads || pools[i].head_dim != pools[0].head_dim ||
+        pools[i].dtype != pools[0].dtype)
+      return PA_ERR_SHAPE;
+    starts[2 * i] = reinterpret_cast<uintptr_t>(pools[i].key_pool);
+    starts[2 * i + 1] = reinterpret_cast<uintptr_t>(pools[i].value_pool);
+  }
+  const uintptr_t bytes = (uintptr_t)pools[0].num_pages * pools[0].page_size * pools[0].num_kv_heads *
+                          pools[0].head_dim * elem_size(pools[0].dtype);
+  if (!std::is_sorted(starts, starts + 2 * num_pools)) std::sort(starts, starts + 2 * num_pools);
+  for (int32_t i = 1; i < 2 * num_pools; ++i)
+    if (starts[i] - starts[i - 1] < bytes) return PA_ERR_SHAPE;
+  return PA_OK;
+}
+
+// Largest vector (16 bytes at most) that divides unit_bytes and on which every pool starts.
+int pools_vec(const pa_kv_pool* pools, int32_t num_pools, int64_t unit_bytes) {
+  uintptr_t bits = (uintptr_t)unit_bytes | 16;
+  for (int32_t i = 0; i < num_pools; ++i)
+    bits |= reinterpret_cast<uintptr_t>(pools[i].key_pool) | reinterpret_cast<uintptr_t>(pools[i].value_pool);
+  return (int)(bits & (~bits + 1));
+}
+
+void fill_pools(pa::PoolList* list, const pa_kv_pool* pools, int32_t first, int32_t num_pools) {
+  list->count = std::min(num_pools - first, (int32_t)pa::kMaxPoolsPerLaunch);
+  for (int32_t i = 0; i < list->count; ++i) {
+    list->key_pool[i] = static_cast<char*>(pools[first + i].key_pool);
+    list->value_pool[i] = static_cast<char*>(pools[first + i].value_pool);
+  }
+}
+
+}  // namespace
+
+pa_status paged_kv_copy_pages(const pa_kv_pool* pools, int32_t num_pools, const int32_t* src_pages,
+                              const int32_t* dst_pages, int64_t num_copies, void* stream) {
+  const pa_status st = check_pools(pools, num_pools);
+  if (st != PA_OK) return st;
+  if (num_copies < 0) return PA_ERR_SHAPE;
+  if (num_copies > INT32_MAX) return PA_ERR_RANGE;
+  if (num_copies == 0 || num_pools == 0) return PA_OK;
+  if (src_pages == nullptr || dst_pages == nullptr) return PA_ERR_NULL;
+  if (!aligned(src_pages, 4) || !aligned(dst_pages, 4)) return PA_ERR_ALIGN;
+  pa::CopyPagesParams p{};
+  p.src = src_pages;
+  p.dst = dst_pages;
+  p.n = num_copies;
+  p.num_pages = pools->num_pages;
+  p.page_bytes = (int64_t)pools->page_size * pools->num_kv_heads * pools->head_dim * (int64_t)elem_size(pools->dtype);
+  p.err = error_word();
+  const int vec = pools_vec(pools, num_pools, p.page_bytes);
+  for (int32_t i = 0; i < num_pools; i += pa::kMaxPoolsPerLaunch) {
+    fill_pools(&p.pools, pools, i, num_pools);
+    if (pa::launch_copy_pages(p, vec, static_cast<cudaStream_t>(stream)) != cudaSuccess) return PA_ERR_CUDA;
+  }
+  return PA_OK;
+}
+
+pa_status paged_kv_compact(const pa_kv_pool* pools, int32_t num_pools, const int32_t* block_table,
+                           int32_t max_blocks_per_seq, const int32_t* seq_lens, int32_t batch, const int32_t* base,
+                           const int32_t* keep_indptr, const int32_t* keep, int64_t num_keep, int32_t* new_seq_lens,
+                           void* stream) {
+  const pa_status st = check_pools(pools, num_pools);
+  if (st != PA_OK) return st;
+  if (num_pools == 0 || batch < 0 || num_keep < 0 || max_blocks_per_seq <= 0) return PA_ERR_SHAPE;
+  if (batch > 65535 || num_keep > INT32_MAX || (int64_t)max_blocks_per_seq * pools->page_size > INT32_MAX)
+    return PA_ERR_RANGE;
+  if (batch == 0) return PA_OK;
+  if (block_table == nullptr || seq_lens == nullptr || keep_indptr == nullptr || (keep == nullptr && num_keep > 0))
+    return PA_ERR_NULL;
+  if (!aligned(block_table, 4) || !aligned(seq_lens, 4) || !aligned(base, 4) || !aligned(keep_indptr, 4) ||
+      !aligned(keep, 4) || !aligned(new_seq_lens, 4))
+    return PA_ERR_ALIGN;
+  // the inputs are read while the new lengths are written
+  auto meets_new_lens = [&](const int32_t* x, int64_t n) {
+    return new_seq_lens != nullptr && x != nullptr && x < new_seq_lens + batch && new_seq_lens < x + n;
+  };
+  if (meets_new_lens(seq_lens, batch) || meets_new_lens(base, batch) || meets_new_lens(keep_indptr, batch + 1) ||
+      meets_new_lens(keep, num_keep) || meets_new_lens(block_table, (int64_t)batch * max_blocks_per_seq))
+    return PA_ERR_SHAPE;
+  pa::CompactParams p{};
+  p.block_table = block_table;
+  p.seq_lens = seq_lens;
+  p.base = base;
+  p.keep_indptr = keep_indptr;
+  p.keep = keep;
+  p.new_seq_lens = new_seq_lens;
+  p.num_keep = num_keep;
+  p.num_pages = pools->num_pages;
+  p.row_bytes = (int64_t)pools->num_kv_heads * pools->head_dim * (int64_t)elem_size(pools->dtype);
+  p.batch = batch;
+  p.max_blocks = max_blocks_per_seq;
+  p.page_size = pools->page_size;
+  p.err = error_word();
+  const int vec = pools_vec(pools, num_pools, p.row_bytes);
+  for (int32_t i = 0; i < num_pools; i += pa::kMaxPoolsPerLaunch) {
+    fill_pools(&p.pools, pools, i, num_pools);
+    if (pa::launch_compact(p, vec, num_sms(), static_cast<cudaStream_t>(stream)) != cudaSuccess) return PA_ERR_CUDA;
+    p.new_seq_lens = nullptr;  // written by the first launch
+  }
+  return PA_OK;
 }
 
 pa_status paged_device_error(int64_t* code, int64_t* detail) {

@@ -68,7 +68,9 @@ __global__ void __launch_bounds__(256) attn_f32_kernel(AttnF32Params p) {
     }
     float m = -INFINITY, l = 0.f;
     const int32_t* bt = p.block_table + page_list_start(p.kv_indptr, p.max_blocks, b);
+    const int start = pos < p.window ? 0 : pos - p.window + 1;  // first key of the window
     for (int j = 0; j <= pos; ++j) {
+      if (j >= p.num_sinks && j < start) j = start;  // the keys between the sinks and the window are not read
       const int page = __ldg(bt + j / ps);
       if (page < 0 || page >= p.pool.num_pages) {
         if (lane == 0) record_error(p.err, ERR_BLOCK_TABLE, page);

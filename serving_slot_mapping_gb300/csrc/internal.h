@@ -35,6 +35,69 @@ struct AppendParams {
 };
 cudaError_t launch_append(const AppendParams& p, int vec_bytes, int num_sms, cudaStream_t s);
 
+// ---- norm, rotation and append (norm_rope.cu) --------------------------------
+struct NormRopeParams {
+  void* key_pool;
+  void* value_pool;
+  const void* q;            // token t's rows at q + t * q_stride (elements), [Hq, D] contiguous
+  const void* key;
+  const void* value;
+  int64_t q_stride, key_stride, value_stride;
+  void* q_out;              // [T, Hq, D]
+  const void* q_weight;     // [D] of the rows' type; nullptr: no norm
+  const void* k_weight;
+  const int32_t* positions; // [T] (unused when rotary_dim is 0)
+  const float* cos_sin;     // [max_position, rotary_dim]: cosines, then sines
+  int64_t max_position;
+  const int64_t* slot_mapping;
+  int64_t num_tokens;
+  int64_t num_slots;
+  int32_t num_q_heads, num_kv_heads, head_dim;
+  int32_t rotary_dim, interleaved;
+  float eps;
+  int32_t f32;              // rows and pools are f32
+  int32_t kv8;              // bf16 rows, e4m3 pools
+  float k_scale, v_scale;
+  int32_t vec;              // elements per vector access (8 or 4); 0: addresses not aligned to 4 elements
+  int32_t lanes_per_head;   // set by the launcher
+  unsigned long long* err;
+};
+cudaError_t launch_qk_norm_rope_append(const NormRopeParams& p, int num_sms, cudaStream_t s);
+
+// ---- page copies and in-place compaction over many pools (pages.cu) ----------
+constexpr int kMaxPoolsPerLaunch = 128;
+struct PoolList {
+  char* key_pool[kMaxPoolsPerLaunch];
+  char* value_pool[kMaxPoolsPerLaunch];
+  int32_t count;
+};
+struct CopyPagesParams {
+  PoolList pools;
+  const int32_t* src;       // [n] page ids
+  const int32_t* dst;
+  int64_t n;
+  int64_t num_pages;
+  int64_t page_bytes;
+  unsigned long long* err;
+};
+cudaError_t launch_copy_pages(const CopyPagesParams& p, int vec_bytes, cudaStream_t s);
+
+struct CompactParams {
+  PoolList pools;
+  const int32_t* block_table;
+  const int32_t* seq_lens;
+  const int32_t* base;         // [B] rows in front that stay (nullptr: none)
+  const int32_t* keep_indptr;  // [B + 1] into keep
+  const int32_t* keep;         // old positions, ascending per sequence
+  int32_t* new_seq_lens;       // [B], nullptr where another launch writes them
+  int64_t num_keep;
+  int64_t num_pages;
+  int64_t row_bytes;           // one slot: num_kv_heads * head_dim * elem_size
+  int32_t batch, max_blocks, page_size;
+  unsigned long long* err;
+};
+cudaError_t launch_compact(const CompactParams& p, int vec_bytes, int num_sms, cudaStream_t s);
+
 // ---- decode (bf16, split-KV over a balanced partition of 16-key blocks) ---
 struct DecodeParams {
   PoolGeom pool;
@@ -102,6 +165,10 @@ struct DecodeParams {
   // blocks of the box (decode_segment_penalty).  0 for cascade decode, whose
   // combine kernel recomputes the plain cut.
   int32_t seg_penalty;
+  // sliding window (the WIN instantiations): the last `window` keys and the
+  // first `num_sinks` are attended to
+  int32_t window;
+  int32_t num_sinks;
 };
 // Number of partial slots the split kernel may write for this launch.
 int decode_heads_per_box(int32_t num_kv_heads, int32_t group, int32_t page_size);
@@ -116,6 +183,11 @@ cudaError_t launch_decode_bf16(const DecodeParams& p, cudaStream_t s);
 // Cascade: split kernel on s, then the combine after `prefix_done` (an event
 // recorded once the prefix partials are written) has completed.
 cudaError_t launch_decode_cascade_bf16(const DecodeParams& p, cudaStream_t s, cudaEvent_t prefix_done);
+// Launch the sliding-window instantiations (decode_window.cu, decode_window_e4m3.cu).
+cudaError_t launch_split_window_bf16(const DecodeParams& p, const CUtensorMap& tk, const CUtensorMap& tv, int rt,
+                                     cudaStream_t s);
+cudaError_t launch_split_window_e4m3(const DecodeParams& p, const CUtensorMap& tk, const CUtensorMap& tv, int rt,
+                                     cudaStream_t s);
 // Dynamic shared memory the bf16 decode split kernel needs.
 // (size_t)-1 when no stage ring of >= 2 stages fits the budget.
 size_t decode_smem_bytes(int head_dim, int group, int batch, int heads_per_box, int budget, bool kv8);
@@ -173,8 +245,14 @@ struct PrefillParams {
   // output row multiplied by v_scale (1 for bf16 pools)
   int32_t kv8;
   float v_scale;
+  // sliding window (0: none): position p sees keys j <= p with j > p - window
+  // or j < num_sinks
+  int32_t window;
+  int32_t num_sinks;
 };
 cudaError_t launch_prefill_bf16(const PrefillParams& p, cudaStream_t s);
+// Launch the sliding-window instantiations (prefill_window.cu).
+cudaError_t launch_prefill_window(const PrefillParams& p, cudaStream_t s);
 
 // ---- fp32 path (decode = prefill with one row per sequence) --------------
 // The CUDA-core path (attn_f32.cu): f32 pools, and bf16 pools whose page
@@ -196,6 +274,10 @@ struct AttnF32Params {
   int32_t group;
   int32_t max_blocks;
   float scale;
+  // sliding window: position p sees keys j <= p with j > p - window or
+  // j < num_sinks (INT32_MAX: every key j <= p)
+  int32_t window;
+  int32_t num_sinks;
   unsigned long long* err;
 };
 cudaError_t launch_attn_f32(const AttnF32Params& p, int num_sms, cudaStream_t s);
