@@ -471,7 +471,8 @@ pa_status prefill_impl(const pa_kv_pool* pool, const void* q, void* out, int32_t
   p.window = win.size != INT32_MAX ? win.size : 0;
   p.num_sinks = win.size != INT32_MAX ? win.sinks : 0;
   p.err = error_word();
-  return pa::launch_prefill_bf16(p, s) == cudaSuccess ? PA_OK : PA_ERR_CUDA;
+  const cudaError_t e = p.window > 0 ? pa::launch_prefill_window(p, num_sms(), s) : pa::launch_prefill_bf16(p, s);
+  return e == cudaSuccess ? PA_OK : PA_ERR_CUDA;
 }
 
 // The CSR form as a Table; max_seq_len bounds every sequence's keys.

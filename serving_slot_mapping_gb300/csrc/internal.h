@@ -251,8 +251,8 @@ struct PrefillParams {
   int32_t num_sinks;
 };
 cudaError_t launch_prefill_bf16(const PrefillParams& p, cudaStream_t s);
-// Launch the sliding-window instantiations (prefill_window.cu).
-cudaError_t launch_prefill_window(const PrefillParams& p, cudaStream_t s);
+// The sliding-window kernel (prefill_window.cu), window > 0.
+cudaError_t launch_prefill_window(const PrefillParams& p, int num_sms, cudaStream_t s);
 
 // ---- fp32 path (decode = prefill with one row per sequence) --------------
 // The CUDA-core path (attn_f32.cu): f32 pools, and bf16 pools whose page

@@ -139,7 +139,8 @@ __device__ __forceinline__ void store_codes(unsigned char* dst, const float (&x)
 // row address is aligned to a vector of V elements.
 template <typename T, bool KV8, int V, bool VEC>
 __global__ void __launch_bounds__(kThreads) qk_norm_rope_append_kernel(NormRopeParams p) {
-  griddep_launch_dependents();
+  // No early trigger: the attention kernels read their queries and tables ahead
+  // of their own wait, and q_out is written here.
   const int lph = p.lanes_per_head;                  // power of two >= D / (2 V)
   const int D = p.head_dim, rot = p.rotary_dim;
   const int u = threadIdx.x & (lph - 1);             // this thread's chunk of a head

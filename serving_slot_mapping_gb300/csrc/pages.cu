@@ -24,7 +24,6 @@ constexpr int kCopyAhead = 4;  // vectors of a thread in flight
 template <typename V>
 __global__ void __launch_bounds__(kCopyThreads) copy_pages_kernel(const __grid_constant__ CopyPagesParams p,
                                                                   int chunks) {
-  griddep_launch_dependents();
   griddep_wait();
   const int64_t nvec = p.page_bytes / (int64_t)sizeof(V);
   const int tensors = 2 * p.pools.count;
@@ -82,7 +81,8 @@ constexpr int kMaxTile = kCompactThreads / kMinCols * kRowsAhead;
 // segment, so the move needs no second buffer.
 template <typename V>
 __global__ void __launch_bounds__(kCompactThreads) compact_kernel(const __grid_constant__ CompactParams p, int cols) {
-  griddep_launch_dependents();
+  // No early trigger: the attention kernels read seq_lens ahead of their own
+  // wait, and new_seq_lens is written here.
   __shared__ int64_t from[kMaxTile], to[kMaxTile];
   const int tensor = blockIdx.y, b = blockIdx.z;
   const int rows = kCompactThreads / cols;  // rows a pass of the block covers

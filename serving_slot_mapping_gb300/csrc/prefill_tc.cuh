@@ -1,7 +1,6 @@
 // The tensor-core prefill kernel of paged_attention_prefill (tcgen05 / TMEM
-// varlen causal attention), templated on head_dim, the pools' element type
-// (KV8) and WIN (paged_attention_prefill_window).  The plain instantiations are
-// compiled in prefill_bf16.cu, the windowed ones in prefill_window.cu.
+// varlen causal attention), instantiated in prefill_bf16.cu; its tiles and helpers
+// are also those of the sliding-window kernel in prefill_window.cu.
 //
 // What is computed: varlen causal attention for packed new tokens
 // (query_start_loc layout of ROCm/maxtext PR #93 "[Draft] kv paged kernels",
@@ -38,13 +37,6 @@
 //   updated reference max (O and l are rescaled in TMEM only when the row
 //   max grows by more than 2^8), and at the end write O / l as bf16.
 // Fully masked key tiles are never loaded or multiplied.
-//
-// Sliding window (WIN): a CTA's key tiles are those of the sinks and those
-// from the first key its first row sees through the window on; the tiles
-// between are skipped (tile j of the CTA is key tile key_tile(j)).  Pages
-// without a key that some row of the sequence sees are never looked up or
-// loaded, and the rows of V between the sinks and the sequence's first window
-// key are zeroed like those past L_b (their slots may hold anything).
 //
 // e4m3 pools (KV8): the TMA lands each page's codes ([keys][D B], unswizzled)
 // in the upper half of the K or V ring slot, and two more warps (one for K,
@@ -164,7 +156,7 @@ __device__ __forceinline__ void convert_tile_e4m3(unsigned char* slot, int valid
   }
 }
 
-template <int D, bool KV8, bool WIN = false>
+template <int D, bool KV8>
 __global__ void __launch_bounds__(PCfg<D, KV8>::kThreads, 1)
     prefill_tc_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_constant__ CUtensorMap tmap_v,
                       PrefillParams p) {
@@ -216,19 +208,6 @@ __global__ void __launch_bounds__(PCfg<D, KV8>::kThreads, 1)
 #pragma unroll
     for (int t = 0; t < kQT; ++t) nt_t[t] = min(nt_t[t], jb + p.chunk_tiles);
   }
-  // sliding window: the CTA's tiles are key tiles 0 .. head_tiles - 1 (sinks)
-  // and head_tiles + gap_tiles on; rows of keys hidden from the whole
-  // sequence are [num_sinks, seq_start)
-  int head_tiles = 0, gap_tiles = 0, seq_start = 0;
-  if constexpr (WIN) {
-    const int t0 = max(0, max(0, pmin_t[0]) - p.window + 1) / kBN;  // pmin_t[0]: the CTA's first row
-    head_tiles = min((p.num_sinks + kBN - 1) / kBN, t0);
-    gap_tiles = t0 - head_tiles;
-    seq_start = max(0, max(0, first) - p.window + 1);
-#pragma unroll
-    for (int t = 0; t < kQT; ++t) nt_t[t] = max(0, nt_t[t] - gap_tiles);
-  }
-  auto key_tile = [&](int j) { return WIN && j >= head_tiles ? j + gap_tiles : j; };
   const int nt = max(nt_t[0], nt_t[1]);  // end (exclusive) of the key tiles the CTA loads
 
   __nv_bfloat16* outp = static_cast<__nv_bfloat16*>(p.out);
@@ -297,13 +276,9 @@ __global__ void __launch_bounds__(PCfg<D, KV8>::kThreads, 1)
     const uint32_t box_bytes = (uint32_t)kpo * D * (KV8 ? 1 : 2);
     const int32_t* bt = p.block_table + (pre ? 0 : page_list_start(p.kv_indptr, p.max_blocks, b));
     int* page_ring = reinterpret_cast<int*>(smem + C::kPageOff);
-    auto box_used = [&](int key) {  // a box with a key of the sequence (that some row of it sees)
-      if constexpr (WIN) return key < L && (key < p.num_sinks || key + kpo > seq_start);
-      return key < L;
-    };
     auto fetch = [&](int j) {  // raw block_table entry of this lane's box in tile j, -1 if none
-      const int key = key_tile(j) * kBN + lane * kpo;
-      return (j < nt && lane < ops && box_used(key)) ? __ldg(bt + (key >> pshift)) : -1;
+      const int key = j * kBN + lane * kpo;
+      return (j < nt && lane < ops && key < L) ? __ldg(bt + (key >> pshift)) : -1;
     };
     auto issue = [&](const CUtensorMap* map, uint32_t dst, int j, int page, uint32_t full) {
       const bool ok = page >= 0;
@@ -311,7 +286,7 @@ __global__ void __launch_bounds__(PCfg<D, KV8>::kThreads, 1)
       if (lane == 0) mbar_arrive_expect_tx(full, (uint32_t)cnt * box_bytes);
       __syncwarp();
       if (ok) {
-        const int64_t slot = ((int64_t)page << pshift) + ((key_tile(j) * kBN + lane * kpo) & (ps - 1));
+        const int64_t slot = ((int64_t)page << pshift) + ((j * kBN + lane * kpo) & (ps - 1));
         if (KV8)  // codes in the slot's upper half, [keys][D B]
           tma_load_3d(dst + (uint32_t)(kBN * D + lane * kpo * D), map, 0, (int)slot, hk, full);
         else
@@ -324,7 +299,6 @@ __global__ void __launch_bounds__(PCfg<D, KV8>::kThreads, 1)
       return __shfl_sync(0xffffffffu, t, 0) != 0;
     };
     int jk = jb, jv = jb;  // next K / V tile to issue (absolute); ring slots count from jb
-    uint32_t vlast_phase = 0;
     int raw = fetch(jb);  // block_table is an input, not written by the append kernel
     griddep_wait();      // the pool rows of this step were written by the append kernel
     unsigned long long t_last = global_ns();
@@ -333,7 +307,7 @@ __global__ void __launch_bounds__(PCfg<D, KV8>::kThreads, 1)
       const int jkl = jk - jb, jvl = jv - jb;
       if (jk < nt && (jkl < kNSK || slot_free(((B_KEMPTY + jkl % kNSK) << 1) | (((jkl / kNSK) - 1) & 1)))) {
         int page = raw;
-        if (lane < ops && box_used(key_tile(jk) * kBN + lane * kpo)) {
+        if (lane < ops && jk * kBN + lane * kpo < L) {
           if (page < 0 || page >= p.pool.num_pages) {
             record_error(p.err, ERR_BLOCK_TABLE, page);
             page = -1;
@@ -351,33 +325,21 @@ __global__ void __launch_bounds__(PCfg<D, KV8>::kThreads, 1)
         const int s = jvl % kNSV;
         const int page = page_ring[(jv & 7) * 32 + lane];
         const uint32_t vdst = v_base + s * C::kKVTile;
-        const int key0 = key_tile(jv) * kBN;
-        const int valid = L - key0;  // keys of this tile below L (>= 1)
-        int hid0 = 0, hid1 = 0;       // rows of this tile hidden from the whole sequence
-        if constexpr (WIN) {
-          hid0 = max(0, p.num_sinks - key0);
-          hid1 = min(kBN, seq_start - key0);
-        }
-        if (KV8 || (valid >= kBN && hid0 >= hid1)) {  // (e4m3: the converter zeroes those rows)
+        const int valid = L - jv * kBN;  // keys of this tile below L (>= 1)
+        if (KV8 || valid >= kBN) {  // (e4m3: the converter zeroes the rows past L)
           issue(&tmap_v, vdst, jv, page, bar(B_VFULL + s));
         } else {
           // last tile: slots valid..127 must hold zeros (they meet P = 0, and
-          // the pool there may hold anything, NaN included); sliding window:
-          // the tiles with hidden rows likewise
+          // the pool there may hold anything, NaN included)
           issue(&tmap_v, vdst, jv, page, bar(B_VLAST));
-          alive = __all_sync(0xffffffffu, mbar_wait(bar(B_VLAST), vlast_phase, p.err));
-          if constexpr (WIN) vlast_phase ^= 1u;
+          alive = __all_sync(0xffffffffu, mbar_wait(bar(B_VLAST), 0, p.err));
           unsigned char* vt = smem + C::kVOff + s * C::kKVTile;
-          auto clear_rows = [&](int lo, int hi) {
-            const int chunks = (hi - lo) * (D / 8);  // 16-byte chunks to clear
-            for (int idx = lane; idx < chunks; idx += 32) {
-              const int k = lo + idx / (D / 8), c = idx % (D / 8);
-              *reinterpret_cast<uint4*>(vt + (k >> 3) * C::kRowBlock + (c >> 3) * 1024 + (k & 7) * 128 +
-                                        (c & 7) * 16) = make_uint4(0u, 0u, 0u, 0u);
-            }
-          };
-          clear_rows(valid, kBN);
-          if constexpr (WIN) clear_rows(hid0, hid1);
+          const int chunks = (kBN - valid) * (D / 8);  // 16-byte chunks to clear
+          for (int idx = lane; idx < chunks; idx += 32) {
+            const int k = valid + idx / (D / 8), c = idx % (D / 8);
+            *reinterpret_cast<uint4*>(vt + (k >> 3) * C::kRowBlock + (c >> 3) * 1024 + (k & 7) * 128 +
+                                      (c & 7) * 16) = make_uint4(0u, 0u, 0u, 0u);
+          }
           fence_proxy_async_smem();
           __syncwarp();
           if (lane == 0) mbar_arrive(bar(B_VFULL + s));
@@ -407,14 +369,10 @@ __global__ void __launch_bounds__(PCfg<D, KV8>::kThreads, 1)
     const bool isv = warp == kCvtWarp + 1;
     const int nslots = isv ? kNSV : kNSK;
     for (int j = jb; j < nt && alive; ++j) {
-      const int jl = j - jb, key0 = key_tile(j) * kBN, valid = min(L - key0, kBN), sl = jl % nslots;
+      const int jl = j - jb, valid = min(L - j * kBN, kBN), sl = jl % nslots;
       alive = __all_sync(0xffffffffu,
                          mbar_wait(bar((isv ? B_VFULL : B_KFULL) + sl), (uint32_t)((jl / nslots) & 1), p.err));
-      unsigned char* tile = smem + (isv ? C::kVOff : C::kKOff) + sl * C::kKVTile;
-      if constexpr (WIN)
-        convert_tile_e4m3<D>(tile, valid, lane, max(0, p.num_sinks - key0), seq_start - key0);
-      else
-        convert_tile_e4m3<D>(tile, valid, lane);
+      convert_tile_e4m3<D>(smem + (isv ? C::kVOff : C::kKOff) + sl * C::kKVTile, valid, lane);
       fence_proxy_async_smem();  // the f16 tile before the tensor core reads it
       __syncwarp();
       if (lane == 0) mbar_arrive(bar((isv ? B_VREADY : B_KREADY) + sl));
@@ -491,8 +449,6 @@ __global__ void __launch_bounds__(PCfg<D, KV8>::kThreads, 1)
     const bool valid_row = R < rows_total;
     const int ntt = t ? nt_t[1] : nt_t[0];
     const int pmin = t ? pmin_t[1] : pmin_t[0];
-    // position of the tile's last row (sliding window)
-    const int pmax = first + (min((t ? row0_t[1] : row0_t[0]) + kBM, rows_total) - 1) / G;
     {  // this thread's Q row into the UMMA A layout (K-major, 128-byte swizzle); zeros past the last row
       unsigned char* qt = q_s + t * C::kQBytes;
       const __nv_bfloat16* src = qp + (valid_row ? row_off(R) : 0);
@@ -525,24 +481,15 @@ __global__ void __launch_bounds__(PCfg<D, KV8>::kThreads, 1)
     for (int j = jb; j < ntt; ++j) {
       if (alive) alive = mbar_wait(bar(B_SFULL + t), (uint32_t)((j - jb) & 1), p.err);
       tc_fence_after();
-      const int key0 = key_tile(j) * kBN;
-      // some key of the tile lies past some row's position (or, sliding window,
-      // before some row's window and not among the sinks)
-      bool diag = key0 + kBN - 1 > pmin;
+      const int key0 = j * kBN;
+      const bool diag = key0 + kBN - 1 > pmin;  // some key of the tile lies past some row's position
       const int lim = pos - key0;                    // column c is visible iff c <= lim
-      int wlo = 0, shi = 0;                          // ... and c >= wlo (the window) or c < shi (the sinks)
-      if constexpr (WIN) {
-        diag = diag || (key0 <= pmax - p.window && key0 + kBN > p.num_sinks);
-        wlo = max(0, pos - p.window + 1) - key0;
-        shi = p.num_sinks - key0;
-      }
       // x = s * scale * log2(e), -inf where masked.  Off the diagonal with a
       // positive scale (the common case) the max is taken over raw S and
       // exp2 takes one fused multiply-add: no mask, no separate scaling.
       const bool plain = !diag && sl2 > 0.f;
       auto scaled = [&](uint32_t raw, int c) {
         const float x = __uint_as_float(raw) * sl2;
-        if constexpr (WIN) return (!diag || (c <= lim && (c >= wlo || c < shi))) ? x : -INFINITY;
         return (!diag || c <= lim) ? x : -INFINITY;
       };
       // pass 1: the row max, 64 columns at a time
@@ -699,24 +646,29 @@ __global__ void __launch_bounds__(PCfg<D, KV8>::kThreads, 1)
   if (warp == kMmaWarp) tmem_dealloc(tmem, C::kTmemCols);
 }
 
-template <int D, bool KV8, bool WIN = false>
+// TMA descriptors of the pools as the prefill kernels load them: one box per
+// page, or per 128 keys of a larger page.
+template <int D, bool KV8>
+bool encode_prefill_tmaps(const PrefillParams& p, CUtensorMap* tk, CUtensorMap* tv) {
+  const int ps = p.pool.page_size;
+  const int kpo = ps < kBN ? ps : kBN;  // keys per TMA box
+  const int64_t rows = p.pool.num_pages * (int64_t)ps;
+  if (KV8)
+    return encode_pool_tmap_u8(tk, p.pool.key_pool, rows, p.pool.num_kv_heads, D, kpo, 1, false) &&
+           encode_pool_tmap_u8(tv, p.pool.value_pool, rows, p.pool.num_kv_heads, D, kpo, 1, false);
+  return encode_pool_tmap_blocked(tk, p.pool.key_pool, rows, p.pool.num_kv_heads, D, kpo / 8) &&
+         encode_pool_tmap_blocked(tv, p.pool.value_pool, rows, p.pool.num_kv_heads, D, kpo / 8);
+}
+
+template <int D, bool KV8>
 cudaError_t launch_prefill_tc(const PrefillParams& p, cudaStream_t s) {
   using C = PCfg<D, KV8>;
   const int ps = p.pool.page_size;
   if (ps < 8 || p.pool.page_shift < 0) return cudaErrorInvalidValue;
   if (KV8 && p.part_o != nullptr) return cudaErrorInvalidValue;  // the cascade prefix pass: bf16 pools
-  const int kpo = ps < kBN ? ps : kBN;  // keys per TMA box
-  const int64_t rows = p.pool.num_pages * (int64_t)ps;
   CUtensorMap tk, tv;
-  if (KV8) {
-    if (!encode_pool_tmap_u8(&tk, p.pool.key_pool, rows, p.pool.num_kv_heads, D, kpo, 1, false) ||
-        !encode_pool_tmap_u8(&tv, p.pool.value_pool, rows, p.pool.num_kv_heads, D, kpo, 1, false))
-      return cudaErrorInvalidValue;
-  } else if (!encode_pool_tmap_blocked(&tk, p.pool.key_pool, rows, p.pool.num_kv_heads, D, kpo / 8) ||
-             !encode_pool_tmap_blocked(&tv, p.pool.value_pool, rows, p.pool.num_kv_heads, D, kpo / 8)) {
-    return cudaErrorInvalidValue;
-  }
-  auto kern = prefill_tc_kernel<D, KV8, WIN>;
+  if (!encode_prefill_tmaps<D, KV8>(p, &tk, &tv)) return cudaErrorInvalidValue;
+  auto kern = prefill_tc_kernel<D, KV8>;
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
   if (e != cudaSuccess) return e;
   const int64_t tiles = ((int64_t)p.max_q_len * p.group + kQT * kBM - 1) / (kQT * kBM);

@@ -1,14 +1,665 @@
-// paged_attention_prefill_window: the sliding-window instantiations of the
-// tensor-core prefill kernel in prefill_tc.cuh, in a translation unit of their
-// own so that they leave the plain ones' code generation untouched.
+// paged_attention_prefill_window: tcgen05 / TMEM varlen causal attention over a
+// sliding window and the first tokens of each sequence, bf16 and e4m3 pools.
+//
+// Row i of sequence b is at position p = L_b - n_b + i and sees the keys
+// j <= p with j > p - window or j < num_sinks.
+//
+// A CTA's work item is what it is in prefill_tc.cuh -- 256 packed rows of one
+// (sequence, KV head) as two 128-row query tiles that share every staged tile of
+// 128 keys, one TMA warp, one MMA thread, two softmax warpgroups (and two
+// converter warps for e4m3 pools) -- with what short key ranges ask for:
+// * The grid is persistent, one CTA per SM, and walks items w = blockIdx.x,
+//   + gridDim.x, ... (KV head fastest, then 256-row tiles, then sequences).
+//   A window of 1024 keys leaves an item ~10 key tiles of 1.9 us, and a CTA that
+//   starts, loads its first tiles and writes its rows alone takes 11 us beside
+//   them.  Here the TMA warp runs ahead into the next item's keys, the query
+//   rows of the next item are copied in while the last key tile's softmax runs,
+//   and its first S is multiplied while this item's rows are written.
+// * Keys are staged as a list of page boxes, not as aligned tiles: the sinks'
+//   boxes, then those from the first key the item's first row sees through
+//   the window on.  A key's place in that list is its "logical" position:
+//   key - gap for keys behind the skipped boxes, the key itself for the sinks;
+//   the masks are ranges of logical positions.  So four sinks cost a box, not a
+//   tile, and a window starts at a box, not at a multiple of 128.
+// * The masks of a row of a 128-key tile are four 32-bit words, built once per
+//   tile that needs any.
+// Boxes whose page holds no key that a row of the sequence sees are never looked
+// up; slots of loaded pages that no row of the sequence sees (between the sinks
+// and the sequence's first window key, or at and past L_b) are zeroed in V.
 #include "prefill_tc.cuh"
 
 namespace pa {
 
-cudaError_t launch_prefill_window(const PrefillParams& p, cudaStream_t s) {
-  if (p.kv8)
-    return p.pool.head_dim == 128 ? launch_prefill_tc<128, true, true>(p, s) : launch_prefill_tc<64, true, true>(p, s);
-  return p.pool.head_dim == 128 ? launch_prefill_tc<128, false, true>(p, s) : launch_prefill_tc<64, false, true>(p, s);
+namespace {
+
+template <int D, bool KV8>
+struct WCfg : PCfg<D, KV8> {
+  using Base = PCfg<D, KV8>;
+  // 8 tiles in flight: {KV head, valid, hid0, hid1} after the first slots of their boxes
+  static constexpr int kMetaOff = Base::kPageOff + 8 * 32 * 4;
+  static constexpr int kWBarOff = kMetaOff + 8 * 16;
+  static constexpr int kWSmem = kWBarOff + kBarSlots * 8 + 16 + 1024;
+};
+
+enum { W_QFULL = 0, W_KFULL = W_QFULL + kQT, W_KEMPTY = W_KFULL + kNSK, W_VFULL = W_KEMPTY + kNSK,
+       W_VEMPTY = W_VFULL + kNSV, W_SFULL = W_VEMPTY + kNSV, W_PFULL = W_SFULL + kQT, W_ODONE = W_PFULL + kQT,
+       W_VLAND = W_ODONE + kQT, W_KREADY = W_VLAND + 1, W_VREADY = W_KREADY + kNSK, W_COUNT = W_VREADY + kNSV };
+static_assert(W_COUNT <= kBarSlots, "barrier slots");
+
+// Sequence b's rows [qs, qs + n) of q; n = 0 where query_start_loc is inconsistent.
+__device__ __forceinline__ int seq_rows(const PrefillParams& p, int b, int* qs) {
+  const int s0 = __ldg(p.query_start_loc + b), s1 = __ldg(p.query_start_loc + b + 1);
+  *qs = s0;
+  return (s0 < 0 || s1 < s0 || (int64_t)s1 > p.total_q) ? 0 : s1 - s0;
+}
+
+__device__ __forceinline__ int row_tiles(int64_t rows) { return (int)((rows + kQT * kBM - 1) / (kQT * kBM)); }
+
+// One work item, as every warp derives it for itself.
+struct Item {
+  int b, hk, n, qs, L;
+  int first;              // position of the sequence's first new row
+  int row0;               // the item's first packed row
+  int head_keys, gap;     // logical position of key j: j below head_keys, else j - gap
+  int seq_start;          // first key that the sequence's first row sees through the window
+  int nt0, nt1;           // key tiles that the query tiles see
+  __device__ int nt() const { return max(nt0, nt1); }
+};
+
+// Walks the items of one CTA in order (whole warps only): 32 sequences at a
+// time, lane i knows the row tiles of sequence base + i.
+struct Walker {
+  int base, total, incl;  // of the chunk; incl: tiles of its sequences up to this lane's
+  int64_t before;         // tiles of the sequences before the chunk
+  int64_t w;              // next item
+
+  __device__ void load(const PrefillParams& p) {
+    const int lane = threadIdx.x & 31, b = base + lane;
+    int qs, c = 0;
+    if (b < p.batch) c = row_tiles((int64_t)min(seq_rows(p, b, &qs), p.max_q_len) * p.group);
+    incl = c;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int t = __shfl_up_sync(0xffffffffu, incl, o);
+      if (lane >= o) incl += t;
+    }
+    total = __shfl_sync(0xffffffffu, incl, 31);
+  }
+  __device__ void start(const PrefillParams& p) {
+    base = 0;
+    before = 0;
+    w = blockIdx.x;
+    load(p);
+  }
+  // The next item; false at the end.
+  __device__ bool next(const PrefillParams& p, int kpo, Item* it) {
+    const int Hkv = p.pool.num_kv_heads;
+    const int64_t gt = w / Hkv;
+    while (gt >= before + total) {
+      if (base + 32 >= p.batch) return false;
+      before += total;
+      base += 32;
+      load(p);
+    }
+    const int rel = (int)(gt - before);
+    const int i = __popc(__ballot_sync(0xffffffffu, incl <= rel));  // < 32: rel < total
+    const int tile = rel - (i > 0 ? __shfl_sync(0xffffffffu, incl, i - 1) : 0);
+    it->b = base + i;
+    it->hk = (int)(w - gt * Hkv);
+    w += gridDim.x;
+    const int ps = p.pool.page_size;
+    it->n = seq_rows(p, it->b, &it->qs);
+    it->L = seq_keys(p.seq_lens, p.kv_indptr, p.kv_last_page_len, p.kv_len, it->b, ps, p.max_blocks * ps, nullptr);
+    it->first = it->L - it->n;
+    it->row0 = tile * kQT * kBM;
+    const int G = p.group;
+    const int rows = it->n * G;
+    const int start = max(0, max(0, it->first + it->row0 / G) - p.window + 1);
+    const int head_boxes = min((p.num_sinks + kpo - 1) / kpo, start / kpo);
+    it->head_keys = head_boxes * kpo;
+    it->gap = start / kpo * kpo - it->head_keys;
+    it->seq_start = max(0, max(0, it->first) - p.window + 1);
+    auto tiles = [&](int r0) {  // tiles up to the last row's own key
+      if (r0 >= rows) return 0;
+      const int pmax = it->first + (min(r0 + kBM, rows) - 1) / G;
+      return pmax < 0 ? 0 : (pmax - it->gap) / kBN + 1;
+    };
+    it->nt0 = tiles(it->row0);
+    it->nt1 = tiles(it->row0 + kBM);
+    return true;
+  }
+};
+
+// Bits 0 .. k of a word (none for k < 0).
+__device__ __forceinline__ uint32_t bits_to(int k) {
+  return k < 0 ? 0u : (k >= 31 ? 0xFFFFFFFFu : 0xFFFFFFFFu >> (31 - k));
+}
+
+template <int D, bool KV8>
+__global__ void __launch_bounds__(PCfg<D, KV8>::kThreads, 1)
+    prefill_window_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_constant__ CUtensorMap tmap_v,
+                          const __grid_constant__ PrefillParams p) {
+  using C = WCfg<D, KV8>;
+  extern __shared__ unsigned char smem_raw[];
+  unsigned char* smem = reinterpret_cast<unsigned char*>(
+      (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
+  const int G = p.group, Hq = p.num_q_heads;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int ps = p.pool.page_size, pshift = p.pool.page_shift;
+  const int kpo = ps < kBN ? ps : kBN;  // keys per box
+  const int ops = kBN / kpo;
+  unsigned char* q_s = smem + C::kQOff;
+  const uint32_t k_base = smem_u32(smem + C::kKOff);
+  const uint32_t v_base = smem_u32(smem + C::kVOff);
+  const uint32_t bars = smem_u32(smem + C::kWBarOff);
+  auto bar = [&](int i) { return bars + 8u * i; };
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + C::kWBarOff + kBarSlots * 8);
+  int* slot_ring = reinterpret_cast<int*>(smem + C::kPageOff);  // [8 tiles][32 lanes] first slot of each box, -1: none
+  int4* meta = reinterpret_cast<int4*>(smem + C::kMetaOff);     // [8 tiles] {KV head, valid, hid0, hid1}
+
+  if (tid == 0) {
+    for (int t = 0; t < kQT; ++t) {
+      mbar_init(bar(W_QFULL + t), kBM);
+      mbar_init(bar(W_SFULL + t), 1);
+      mbar_init(bar(W_PFULL + t), kBM);
+      mbar_init(bar(W_ODONE + t), 1);
+    }
+    for (int s = 0; s < kNSK; ++s) {
+      mbar_init(bar(W_KFULL + s), 1);
+      mbar_init(bar(W_KEMPTY + s), 1);
+      mbar_init(bar(W_KREADY + s), 1);
+    }
+    for (int s = 0; s < kNSV; ++s) {
+      mbar_init(bar(W_VFULL + s), 1);
+      mbar_init(bar(W_VEMPTY + s), 1);
+      mbar_init(bar(W_VREADY + s), 1);
+    }
+    mbar_init(bar(W_VLAND), 1);
+    fence_mbar_init();
+  }
+  if (warp == kMmaWarp) tmem_alloc(smem_u32(tmem_slot), C::kTmemCols);
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+  const float sl2 = p.scale_log2;
+  griddep_launch_dependents();
+  // inconsistent inputs are recorded once, whatever items there are
+  for (int b = blockIdx.x * C::kThreads + tid; b < p.batch; b += gridDim.x * C::kThreads) {
+    int qs;
+    const int n = seq_rows(p, b, &qs);
+    if (n == 0 && qs != __ldg(p.query_start_loc + b + 1)) record_error(p.err, ERR_QUERY_LOC, qs);
+    if (n > p.max_q_len) record_error(p.err, ERR_QUERY_LOC, n);
+    seq_keys(p.seq_lens, p.kv_indptr, p.kv_last_page_len, p.kv_len, b, ps, p.max_blocks * ps, p.err);
+  }
+  bool alive = true;
+  Walker wk;
+  Item it;
+
+  if (warp == kTmaWarp) {
+    // ======================= TMA producer (one warp) =======================
+    // K tiles of all items in order, each as soon as its ring slot is free, and
+    // the V tiles behind them (a V tile reuses the slots its K tile looked up).
+    // The page ids of the next K tile are read while this one is issued.
+    const uint32_t box_bytes = (uint32_t)kpo * D * (KV8 ? 1 : 2);
+    auto box_key = [&](int j) {  // first key of this lane's box of tile j
+      const int l = j * kBN + lane * kpo;
+      return l < it.head_keys ? l : l + it.gap;
+    };
+    auto box_used = [&](int key) {  // a box with a key that some row of the sequence sees
+      return lane < ops && key < it.L && (key < p.num_sinks || key + kpo > it.seq_start);
+    };
+    const int32_t* bt = nullptr;
+    auto fetch = [&](int j) {  // raw block_table entry of this lane's box of tile j
+      const int key = box_key(j);
+      return box_used(key) ? __ldg(bt + (key >> pshift)) : -1;
+    };
+    auto issue = [&](const CUtensorMap* map, uint32_t dst, int hk, int slot, uint32_t full) {
+      const bool ok = slot >= 0;
+      const int cnt = __popc(__ballot_sync(0xffffffffu, ok));
+      if (lane == 0) mbar_arrive_expect_tx(full, (uint32_t)cnt * box_bytes);
+      __syncwarp();
+      if (ok) {
+        if (KV8)  // codes in the ring slot's upper half, [keys][D B]
+          tma_load_3d(dst + (uint32_t)(kBN * D + lane * kpo * D), map, 0, slot, hk, full);
+        else
+          tma_load_5d(dst + (uint32_t)(lane * (kpo / 8)) * C::kRowBlock, map, 0, 0, 0, slot >> 3, hk, full);
+      }
+    };
+    auto phase_done = [&](int b, uint32_t parity) {  // lane 0 polls, the warp agrees
+      int t = 0;
+      if (lane == 0) t = mbar_test(bar(b), parity) ? 1 : 0;
+      return __shfl_sync(0xffffffffu, t, 0) != 0;
+    };
+    wk.start(p);
+    int j = 0, raw = -1;
+    bool more = false;  // `it` has a K tile j left to issue
+    auto to_item = [&]() {  // the next item with keys
+      do {
+        more = wk.next(p, kpo, &it);
+      } while (more && it.nt() == 0);
+      j = 0;
+      if (more) {
+        bt = p.block_table + page_list_start(p.kv_indptr, p.max_blocks, it.b);
+        raw = fetch(0);
+      }
+    };
+    to_item();
+    griddep_wait();  // the pool rows of this step were written by an earlier kernel
+    int kt = 0, vt = 0;  // tiles issued so far, over all items
+    int land_slot = -1;  // ring slot of a V tile whose rows are to be cleared when it has landed
+    int4 land = make_int4(0, 0, 0, 0);
+    uint32_t land_phase = 0;
+    unsigned long long t_last = global_ns();
+    while ((more || vt < kt || land_slot >= 0) && alive) {
+      bool progressed = false;
+      if (more && (kt < kNSK || phase_done(W_KEMPTY + kt % kNSK, (uint32_t)((kt / kNSK - 1) & 1)))) {
+        const int key = box_key(j);
+        int slot = -1;
+        if (box_used(key)) {
+          if (raw < 0 || raw >= p.pool.num_pages)
+            record_error(p.err, ERR_BLOCK_TABLE, raw);
+          else
+            slot = (int)(((int64_t)raw << pshift) + (key & (ps - 1)));
+        }
+        slot_ring[(kt & 7) * 32 + lane] = slot;
+        if (lane == 0) {
+          const int l0 = j * kBN;  // rows of the tile: valid ones, and those no row of the sequence sees
+          const int end = it.seq_start <= it.head_keys ? it.seq_start : max(it.head_keys, it.seq_start - it.gap);
+          meta[kt & 7] = make_int4(it.hk, min(it.L - it.gap - l0, kBN), max(0, p.num_sinks - l0), min(end - l0, kBN));
+        }
+        issue(&tmap_k, k_base + (kt % kNSK) * C::kKVTile, it.hk, slot, bar(W_KFULL + kt % kNSK));
+        ++kt;
+        if (++j < it.nt())
+          raw = fetch(j);
+        else
+          to_item();
+        progressed = true;
+      }
+      if (vt < kt && (vt < kNSV || phase_done(W_VEMPTY + vt % kNSV, (uint32_t)((vt / kNSV - 1) & 1)))) {
+        const int4 m = meta[vt & 7];
+        // rows that may hold anything meet P = 0 and must be zeros (e4m3: the converter writes them)
+        const bool clear = !KV8 && (m.y < kBN || m.z < m.w);
+        if (!clear || land_slot < 0) {
+          const int s = vt % kNSV;
+          issue(&tmap_v, v_base + s * C::kKVTile, m.x, slot_ring[(vt & 7) * 32 + lane],
+                bar(clear ? (int)W_VLAND : W_VFULL + s));
+          if (clear) {
+            land_slot = s;
+            land = m;
+          }
+          ++vt;
+          progressed = true;
+        }
+      }
+      if (land_slot >= 0 && phase_done(W_VLAND, land_phase)) {
+        unsigned char* vtile = smem + C::kVOff + land_slot * C::kKVTile;
+        auto clear_rows = [&](int lo, int hi) {
+          for (int i = lane; i < (hi - lo) * (D / 8); i += 32) {
+            const int k = lo + i / (D / 8), c = i % (D / 8);
+            *reinterpret_cast<uint4*>(vtile + (k >> 3) * C::kRowBlock + (c >> 3) * 1024 + (k & 7) * 128 +
+                                      (c & 7) * 16) = make_uint4(0u, 0u, 0u, 0u);
+          }
+        };
+        clear_rows(land.y, kBN);
+        clear_rows(land.z, land.w);
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar(W_VFULL + land_slot));
+        land_slot = -1;
+        land_phase ^= 1u;
+        progressed = true;
+      }
+      int give_up = 0;
+      if (lane == 0) {
+        const unsigned long long now = global_ns();
+        if (progressed) {
+          t_last = now;
+        } else if (now - t_last > kWaitLimitNs) {
+          record_error(p.err, ERR_TIMEOUT, vt);
+          give_up = 1;
+        }
+      }
+      if (__shfl_sync(0xffffffffu, give_up, 0)) alive = false;
+      if (!progressed) __nanosleep(32);
+    }
+  }
+
+  if (KV8 && (warp == kCvtWarp || warp == kCvtWarp + 1)) {
+    // ======================= e4m3 -> f16 converters (K: warp 10, V: warp 11) =======================
+    const bool isv = warp == kCvtWarp + 1;
+    const int nslots = isv ? kNSV : kNSK;
+    wk.start(p);
+    for (int kt = 0; wk.next(p, kpo, &it) && alive;) {
+      for (int j = 0; j < it.nt() && alive; ++j, ++kt) {
+        const int sl = kt % nslots;
+        alive = __all_sync(0xffffffffu, mbar_wait(bar((isv ? W_VFULL : W_KFULL) + sl),
+                                                  (uint32_t)((kt / nslots) & 1), p.err));
+        const int4 m = meta[kt & 7];
+        convert_tile_e4m3<D>(smem + (isv ? C::kVOff : C::kKOff) + sl * C::kKVTile, m.y, lane, m.z, m.w);
+        fence_proxy_async_smem();  // the f16 tile before the tensor core reads it
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar((isv ? W_VREADY : W_KREADY) + sl));
+      }
+    }
+  }
+
+  if (warp == kMmaWarp) {
+    // ======================= MMA issuer (lane 0) =======================
+    // Per item S_A(0) S_B(0), then per key tile j: PV_A(j) S_A(j+1) PV_B(j)
+    // S_B(j+1), as in prefill_tc.cuh.  tcgen05 operations of one thread execute in
+    // order, so the next item's S may overwrite this item's last P at once; its
+    // first PV overwrites O only after the softmax threads, which write its P,
+    // have read this item's O.
+    constexpr uint32_t idesc_s = KV8 ? umma_idesc_f16(kBM, kBN, false) : umma_idesc_bf16(kBM, kBN, false);
+    constexpr uint32_t idesc_o = KV8 ? umma_idesc_f16(kBM, D, true) : umma_idesc_bf16(kBM, D, true);
+    constexpr int kKWait = KV8 ? W_KREADY : W_KFULL, kVWait = KV8 ? W_VREADY : W_VFULL;
+    const uint64_t q_desc = umma_desc_sw128(smem_u32(q_s), 16, 1024);
+    const uint64_t k_desc = umma_desc_sw128(k_base, 16, C::kRowBlock);
+    const uint64_t v_desc = umma_desc_sw128(v_base, 1024, C::kRowBlock);
+    int kt0 = 0;               // tiles of the items before
+    uint32_t items[kQT] = {0u, 0u}, sp[kQT] = {0u, 0u};  // per query tile: items with keys, P tiles awaited
+    wk.start(p);
+    while (wk.next(p, kpo, &it)) {
+      if (lane == 0) {
+        const int nt0 = it.nt0, nt1 = it.nt1, nt = it.nt();
+        auto issue_s = [&](int t, int j) {
+          const int kt = kt0 + j, sk = kt % kNSK;
+          if (t == 0 || j >= nt0) {  // first S of key tile j
+            if (alive) alive = mbar_wait(bar(kKWait + sk), (uint32_t)((kt / kNSK) & 1), p.err);
+          }
+          tc_fence_after();
+          const uint64_t qd = q_desc + (uint64_t)((t * C::kQBytes) >> 4);
+          const uint64_t kd = k_desc + (uint64_t)((sk * C::kKVTile) >> 4);
+          const uint32_t s_tm = tmem + C::kSCol + t * 128;
+#pragma unroll
+          for (int kk = 0; kk < D / 16; ++kk)  // S_t = Q_t K^T over 16-dim steps
+            umma_bf16(s_tm, qd + (uint64_t)(((kk >> 2) * kSlab + (kk & 3) * 32) >> 4),
+                      kd + (uint64_t)(((kk >> 2) * 1024 + (kk & 3) * 32) >> 4), idesc_s, kk > 0);
+          umma_commit(bar(W_SFULL + t));
+          if (t == 1 || j >= nt1) umma_commit(bar(W_KEMPTY + sk));  // last S of key tile j
+        };
+        auto issue_pv = [&](int t, int j) {
+          const int kt = kt0 + j, sv = kt % kNSV;
+          if (alive) alive = mbar_wait(bar(W_PFULL + t), sp[t] & 1u, p.err);
+          ++sp[t];
+          if (t == 0 || j >= nt0) {  // first PV of key tile j
+            if (alive) alive = mbar_wait(bar(kVWait + sv), (uint32_t)((kt / kNSV) & 1), p.err);
+          }
+          tc_fence_after();
+          const uint64_t vd = v_desc + (uint64_t)((sv * C::kKVTile) >> 4);
+          const uint32_t s_tm = tmem + C::kSCol + t * 128;
+          const uint32_t o_tm = tmem + C::kOCol + t * 128;
+#pragma unroll
+          for (int kk = 0; kk < kBN / 16; ++kk)  // O_t += P_t V over 16-key steps (two 8-key blocks each)
+            umma_bf16_ts(o_tm, s_tm + kk * 8, vd + (uint64_t)((kk * 2 * C::kRowBlock) >> 4), idesc_o,
+                         (j > 0 || kk > 0) ? 1u : 0u);
+          if (j == (t ? nt1 : nt0) - 1) umma_commit(bar(W_ODONE + t));
+          if (t == 1 || j >= nt1) umma_commit(bar(W_VEMPTY + sv));  // last PV of key tile j
+        };
+        auto first_s = [&](int t) {
+          if (alive) alive = mbar_wait(bar(W_QFULL + t), items[t] & 1u, p.err);
+          ++items[t];
+          issue_s(t, 0);
+        };
+        if (nt0 > 0) first_s(0);
+        if (nt1 > 0) first_s(1);
+        for (int j = 0; j < nt; ++j) {
+          if (j < nt0) issue_pv(0, j);
+          if (j + 1 < nt0) issue_s(0, j + 1);
+          if (j < nt1) issue_pv(1, j);
+          if (j + 1 < nt1) issue_s(1, j + 1);
+        }
+        kt0 += nt;
+      }
+      __syncwarp();
+    }
+  }
+
+  if (warp < 4 * kQT) {
+    // ======================= softmax: one TMEM lane (row) per thread =======================
+    const int t = warp >> 2;                 // query tile
+    const int r = tid & (kBM - 1);           // row within the tile == TMEM lane
+    const __nv_bfloat16* qp = static_cast<const __nv_bfloat16*>(p.q);
+    __nv_bfloat16* outp = static_cast<__nv_bfloat16*>(p.out);
+    unsigned char* qt = q_s + t * C::kQBytes;
+    const uint32_t lane_base = tmem + ((uint32_t)((warp & 3) * 32) << 16);
+    const uint32_t s_col = lane_base + C::kSCol + t * 128;
+    const uint32_t o_col = lane_base + C::kOCol + t * 128;
+    auto tiles_of = [&](const Item& x) { return t ? x.nt1 : x.nt0; };
+    auto row_of = [&](const Item& x) { return x.row0 + t * kBM + r; };
+    auto row_off = [&](const Item& x, int R) {  // packed row -> element offset of its q / out row
+      const int i = R / G, g = R - (R / G) * G;
+      return ((int64_t)(x.qs + i) * Hq + (int64_t)x.hk * G + g) * D;
+    };
+    auto q_chunk = [&](int c) { return qt + (c >> 3) * kSlab + r * 128 + (((c & 7) ^ (r & 7)) << 4); };
+    // this thread's Q row into the UMMA A layout (K-major, 128-byte swizzle);
+    // zeros past the last row
+    auto copy_q = [&](const Item& x) {
+      const int R = row_of(x);
+      const bool ok = R < x.n * G;
+      const __nv_bfloat16* src = qp + (ok ? row_off(x, R) : 0);
+#pragma unroll
+      for (int c = 0; c < D / 8; ++c) cp_async_16(smem_u32(q_chunk(c)), src + c * 8, ok ? 16 : 0);
+      cp_async_commit();
+    };
+    auto publish_q = [&]() {
+      cp_async_wait<0>();
+      if (KV8) {  // f16 operands: bf16 -> f16 in place
+#pragma unroll 4
+        for (int c = 0; c < D / 8; ++c) {
+          uint4* x = reinterpret_cast<uint4*>(q_chunk(c));
+          const uint4 v = *x;
+          *x = make_uint4(bf16x2_to_f16x2(v.x), bf16x2_to_f16x2(v.y), bf16x2_to_f16x2(v.z), bf16x2_to_f16x2(v.w));
+        }
+      }
+      fence_proxy_async_smem();
+      mbar_arrive(bar(W_QFULL + t));
+    };
+    wk.start(p);
+    griddep_wait();  // q may come from an earlier kernel; before the first global write
+    Item nx;
+    bool have = wk.next(p, kpo, &nx);
+    if (have && tiles_of(nx) > 0) {
+      copy_q(nx);
+      publish_q();
+    }
+    uint32_t sn = 0, on = 0;  // S tiles and finished O's awaited so far
+    while (have) {
+      it = nx;
+      have = wk.next(p, kpo, &nx);
+      const int ntt = tiles_of(it);
+      const bool next_q = have && tiles_of(nx) > 0;
+      const int R = row_of(it);
+      const int rows = it.n * G;
+      const bool valid_row = R < rows;
+      // logical positions: this row's own key, the first key of its window; the
+      // least own key and the last window start among the tile's rows
+      const int pos = valid_row ? it.first + R / G : -1;
+      const int lim = pos - it.gap;
+      const int wlo = max(0, max(0, pos) - p.window + 1) - it.gap;
+      const int lim_min = it.first + (it.row0 + t * kBM) / G - it.gap;
+      const int pos_max = it.first + (min(it.row0 + (t + 1) * kBM, rows) - 1) / G;
+      const int wlo_max = max(0, max(0, pos_max) - p.window + 1) - it.gap;
+      float m_ref = -INFINITY, l = 0.f;
+      for (int j = 0; j < ntt; ++j) {
+        if (alive) alive = mbar_wait(bar(W_SFULL + t), sn & 1u, p.err);
+        ++sn;
+        tc_fence_after();
+        // every S of this item is done: Q may be replaced
+        if (j == ntt - 1 && next_q) copy_q(nx);
+        const int l0 = j * kBN;
+        // some row does not see some key of the tile
+        const bool masked = l0 + kBN - 1 > lim_min || (l0 < wlo_max && l0 + kBN > p.num_sinks);
+        // x = s * scale * log2(e), -inf where masked.  Unmasked with a positive
+        // scale (the common case) the max is taken over raw S and exp2 takes
+        // one fused multiply-add: no mask, no separate scaling.
+        const bool plain = !masked && sl2 > 0.f;
+        uint32_t see[4] = {0xFFFFFFFFu, 0xFFFFFFFFu, 0xFFFFFFFFu, 0xFFFFFFFFu};
+        if (masked) {
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const int c0 = l0 + 32 * i;
+            see[i] = bits_to(lim - c0) & (~bits_to(wlo - 1 - c0) | bits_to(p.num_sinks - 1 - c0));
+          }
+        }
+        auto scaled = [&](uint32_t raw, uint32_t word, int e) {
+          return ((word >> e) & 1u) ? __uint_as_float(raw) * sl2 : -INFINITY;
+        };
+        // pass 1: the row max, 64 columns at a time
+        float mx[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) mx[i] = -INFINITY;
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          uint32_t v[2][32];
+          tmem_ld32(s_col + h * 64, v[0]);
+          tmem_ld32(s_col + h * 64 + 32, v[1]);
+          tmem_wait_ld();
+          if (plain) {
+#pragma unroll
+            for (int cb = 0; cb < 2; ++cb)
+#pragma unroll
+              for (int e = 0; e < 32; ++e) mx[e & 7] = fmaxf(mx[e & 7], __uint_as_float(v[cb][e]));
+          } else {
+#pragma unroll
+            for (int cb = 0; cb < 2; ++cb)
+#pragma unroll
+              for (int e = 0; e < 32; ++e) mx[e & 7] = fmaxf(mx[e & 7], scaled(v[cb][e], see[2 * h + cb], e));
+          }
+        }
+        float tmax = fmaxf(fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])),
+                           fmaxf(fmaxf(mx[4], mx[5]), fmaxf(mx[6], mx[7])));
+        if (plain) tmax *= sl2;
+        // reference max: moved only when the row max grows by more than 2^8
+        float alpha = 1.f;
+        bool rescale = false;
+        if (tmax > m_ref + kRescaleThreshold) {
+          alpha = m_ref == -INFINITY ? 0.f : fast_exp2(m_ref - tmax);
+          m_ref = tmax;
+          l *= alpha;
+          rescale = j > 0;
+        }
+        const float mbase = m_ref == -INFINITY ? 0.f : m_ref;
+        // pass 2: P = exp2(x - m) as bf16 (f16) pairs, written over the S columns just read
+        float rs[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) rs[i] = 0.f;
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          uint32_t v[2][32];
+          tmem_ld32(s_col + h * 64, v[0]);
+          tmem_ld32(s_col + h * 64 + 32, v[1]);
+          tmem_wait_ld();
+          uint32_t w[32];
+          if (plain) {
+#pragma unroll
+            for (int cb = 0; cb < 2; ++cb)
+#pragma unroll
+              for (int e = 0; e < 32; e += 2) {
+                const float p0 = fast_exp2(fmaf(__uint_as_float(v[cb][e]), sl2, -mbase));
+                const float p1 = fast_exp2(fmaf(__uint_as_float(v[cb][e + 1]), sl2, -mbase));
+                rs[(e >> 1) & 7] += p0 + p1;
+                w[cb * 16 + (e >> 1)] = KV8 ? pack_f16(p0, p1) : pack_bf16(p0, p1);
+              }
+          } else {
+#pragma unroll
+            for (int cb = 0; cb < 2; ++cb)
+#pragma unroll
+              for (int e = 0; e < 32; e += 2) {
+                const float p0 = fast_exp2(scaled(v[cb][e], see[2 * h + cb], e) - mbase);
+                const float p1 = fast_exp2(scaled(v[cb][e + 1], see[2 * h + cb], e + 1) - mbase);
+                rs[(e >> 1) & 7] += p0 + p1;
+                w[cb * 16 + (e >> 1)] = KV8 ? pack_f16(p0, p1) : pack_bf16(p0, p1);
+              }
+          }
+          tmem_st32(s_col + h * 32, w);
+        }
+        l += ((rs[0] + rs[1]) + (rs[2] + rs[3])) + ((rs[4] + rs[5]) + (rs[6] + rs[7]));
+        // O is rescaled in place only when some row of the warp moved its
+        // reference max.  PV_t(j-1) is complete: S_t(j) was issued after it.
+        if (__any_sync(0xffffffffu, rescale)) {
+#pragma unroll 1
+          for (int cb = 0; cb < D / 32; ++cb) {
+            uint32_t o[32];
+            tmem_ld32(o_col + cb * 32, o);
+            tmem_wait_ld();
+#pragma unroll
+            for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * alpha);
+            tmem_st32(o_col + cb * 32, o);
+          }
+        }
+        tmem_wait_st();
+        tc_fence_before();
+        mbar_arrive(bar(W_PFULL + t));
+      }
+      if (next_q) {
+        if (ntt == 0) copy_q(nx);
+        publish_q();
+      }
+      // ---- O / l -> bf16 (zeros for a tile that sees no key) ----
+      if (ntt > 0) {
+        if (alive) alive = mbar_wait(bar(W_ODONE + t), on & 1u, p.err);
+        ++on;
+        tc_fence_after();
+      }
+      const float inv = l > 0.f ? p.v_scale / l : 0.f;  // v_scale: 1 for bf16 pools
+      __nv_bfloat16* orow = outp + (valid_row ? row_off(it, R) : 0);
+#pragma unroll
+      for (int cb = 0; cb < D / 32; ++cb) {
+        uint32_t o[32];
+        if (ntt > 0) {
+          tmem_ld32(o_col + cb * 32, o);
+          tmem_wait_ld();
+        } else {
+#pragma unroll
+          for (int e = 0; e < 32; ++e) o[e] = 0u;
+        }
+        if (valid_row) {
+#pragma unroll
+          for (int q = 0; q < 4; ++q) {
+            uint4 w;
+            w.x = pack_bf16(__uint_as_float(o[8 * q + 0]) * inv, __uint_as_float(o[8 * q + 1]) * inv);
+            w.y = pack_bf16(__uint_as_float(o[8 * q + 2]) * inv, __uint_as_float(o[8 * q + 3]) * inv);
+            w.z = pack_bf16(__uint_as_float(o[8 * q + 4]) * inv, __uint_as_float(o[8 * q + 5]) * inv);
+            w.w = pack_bf16(__uint_as_float(o[8 * q + 6]) * inv, __uint_as_float(o[8 * q + 7]) * inv);
+            *reinterpret_cast<uint4*>(orow + cb * 32 + q * 8) = w;
+          }
+        }
+      }
+      tc_fence_before();  // O is read before this thread's next P lets PV write it again
+    }
+  }
+
+  // ---- teardown: every warp reaches this point; TMEM is freed by its allocator warp ----
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  if (warp == kMmaWarp) tmem_dealloc(tmem, C::kTmemCols);
+}
+
+template <int D, bool KV8>
+cudaError_t launch_window(const PrefillParams& p, int num_sms, cudaStream_t s) {
+  using C = WCfg<D, KV8>;
+  CUtensorMap tk, tv;
+  if (!encode_prefill_tmaps<D, KV8>(p, &tk, &tv)) return cudaErrorInvalidValue;
+  auto kern = prefill_window_kernel<D, KV8>;
+  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kWSmem);
+  if (e != cudaSuccess) return e;
+  // items: at most a partial tile per sequence beside the full ones
+  const int64_t tiles = p.total_q * p.group / (kQT * kBM) + p.batch;
+  const int64_t items = tiles * p.pool.num_kv_heads;
+  const unsigned grid = (unsigned)(items < num_sms ? items : num_sms);
+  return launch_pdl(kern, dim3(grid), dim3(C::kThreads), (size_t)C::kWSmem, s, tk, tv, p);
+}
+
+}  // namespace
+
+cudaError_t launch_prefill_window(const PrefillParams& p, int num_sms, cudaStream_t s) {
+  if (p.max_q_len <= 0 || p.batch <= 0) return cudaSuccess;
+  if (p.pool.page_size < 8 || p.pool.page_shift < 0) return cudaErrorInvalidValue;
+  if (p.kv8) return p.pool.head_dim == 128 ? launch_window<128, true>(p, num_sms, s) : launch_window<64, true>(p, num_sms, s);
+  return p.pool.head_dim == 128 ? launch_window<128, false>(p, num_sms, s) : launch_window<64, false>(p, num_sms, s);
 }
 
 }  // namespace pa

@@ -158,6 +158,25 @@ def test_prefill_rows_without_keys_and_infinities(cuda_device, dtype):
     assert torch.all(out[:10] == 0) and torch.all(out[-9:] == 0)
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "e4m3"])
+@pytest.mark.parametrize("hq,hkv,d", [(8, 8, 64), (16, 4, 128)])
+def test_prefill_many_items(cuda_device, dtype, hq, hkv, d):
+    """Several hundred (sequence, head, row tile) items, so that a CTA walks
+    through several; sequences without new tokens, with fewer keys than rows
+    (tiles that see no key between others) and chunks of more than 32 of them."""
+    rng = np.random.default_rng(21)
+    new = rng.integers(0, 40, 90)
+    cached = rng.integers(-30, 200, 90)
+    new[40:75] = 0                                  # a whole stretch of sequences without rows
+    new[[3, 80]] = [150, 290]
+    Case(new, cached, 24, 3, hq=hq, hkv=hkv, d=d, dtype=dtype, seed=22).check(capi, cuda_device)
+
+
+def test_prefill_long_rows_many_tiles(cuda_device):
+    # hundreds of 256-row tiles of few sequences
+    Case([1500, 700], [100, 2000], 70, 5, hq=32, hkv=2, d=64, seed=23).check(capi, cuda_device)
+
+
 def test_prefill_rows_past_the_batch_are_left(cuda_device):
     c = Case([20, 31], [40, 0], 16, 2, seed=6)
     full = torch.full((60, 8, 64), 7.0, dtype=torch.bfloat16, device=cuda_device)
