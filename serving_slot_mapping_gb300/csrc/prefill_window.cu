@@ -35,6 +35,13 @@ namespace {
 template <int D, bool KV8>
 struct WCfg : PCfg<D, KV8> {
   using Base = PCfg<D, KV8>;
+  // Three warpgroups of 168 registers a thread at launch (two idle warps fill the
+  // third where there are no converters).  The third gives registers to the two
+  // of the softmax, whose threads hold a whole row of S (128 fp32): 2 x 200 + 104
+  // (2 x 192 + 120) = 3 x 168.
+  static constexpr int kThreads = 384;
+  static constexpr int kSoftmaxRegs = KV8 ? 192 : 200, kOtherRegs = KV8 ? 120 : 104;
+  static_assert(2 * kSoftmaxRegs + kOtherRegs <= 3 * 168, "more registers than the launch has");
   // 8 tiles in flight: {KV head, valid, hid0, hid1} after the first slots of their boxes
   static constexpr int kMetaOff = Base::kPageOff + 8 * 32 * 4;
   static constexpr int kWBarOff = kMetaOff + 8 * 16;
@@ -136,7 +143,7 @@ __device__ __forceinline__ uint32_t bits_to(int k) {
 }
 
 template <int D, bool KV8>
-__global__ void __launch_bounds__(PCfg<D, KV8>::kThreads, 1)
+__global__ void __launch_bounds__(WCfg<D, KV8>::kThreads, 1)
     prefill_window_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_constant__ CUtensorMap tmap_v,
                           const __grid_constant__ PrefillParams p) {
   using C = WCfg<D, KV8>;
@@ -194,8 +201,9 @@ __global__ void __launch_bounds__(PCfg<D, KV8>::kThreads, 1)
   }
   bool alive = true;
   Walker wk;
-  Item it;
-
+  Item it = {};
+  if (warp >= 4 * kQT) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;\n" ::"n"(C::kOtherRegs));
   if (warp == kTmaWarp) {
     // ======================= TMA producer (one warp) =======================
     // K tiles of all items in order, each as soon as its ring slot is free, and
@@ -347,25 +355,33 @@ __global__ void __launch_bounds__(PCfg<D, KV8>::kThreads, 1)
   if (warp == kMmaWarp) {
     // ======================= MMA issuer (lane 0) =======================
     // Per item S_A(0) S_B(0), then per key tile j: PV_A(j) S_A(j+1) PV_B(j)
-    // S_B(j+1), as in prefill_tc.cuh.  tcgen05 operations of one thread execute in
-    // order, so the next item's S may overwrite this item's last P at once; its
-    // first PV overwrites O only after the softmax threads, which write its P,
-    // have read this item's O.
+    // S_B(j+1), as in prefill_tc.cuh, with the next item's S_A(0) and S_B(0) in the
+    // places of S_A and S_B past this item's last tiles.  tcgen05 operations of
+    // one thread execute in order, so the next item's S may overwrite this item's
+    // last P; its first PV overwrites O only after the softmax threads, which
+    // write its P, have read this item's O.
     constexpr uint32_t idesc_s = KV8 ? umma_idesc_f16(kBM, kBN, false) : umma_idesc_bf16(kBM, kBN, false);
     constexpr uint32_t idesc_o = KV8 ? umma_idesc_f16(kBM, D, true) : umma_idesc_bf16(kBM, D, true);
     constexpr int kKWait = KV8 ? W_KREADY : W_KFULL, kVWait = KV8 ? W_VREADY : W_VFULL;
     const uint64_t q_desc = umma_desc_sw128(smem_u32(q_s), 16, 1024);
     const uint64_t k_desc = umma_desc_sw128(k_base, 16, C::kRowBlock);
     const uint64_t v_desc = umma_desc_sw128(v_base, 1024, C::kRowBlock);
-    int kt0 = 0;               // tiles of the items before
+    int kt0 = 0;                                         // key tiles of the items before
     uint32_t items[kQT] = {0u, 0u}, sp[kQT] = {0u, 0u};  // per query tile: items with keys, P tiles awaited
+    bool begun[kQT] = {false, false};                    // the item's S_t(0) is issued
+    Item nx;
     wk.start(p);
-    while (wk.next(p, kpo, &it)) {
+    bool have = wk.next(p, kpo, &nx);
+    while (have) {
+      it = nx;
+      have = wk.next(p, kpo, &nx);
       if (lane == 0) {
         const int nt0 = it.nt0, nt1 = it.nt1, nt = it.nt();
-        auto issue_s = [&](int t, int j) {
-          const int kt = kt0 + j, sk = kt % kNSK;
-          if (t == 0 || j >= nt0) {  // first S of key tile j
+        // S_t of key tile j of an item whose tiles start at k0: wait for K where
+        // this is the first S of the tile, free its stage where it is the last
+        auto issue_s = [&](const Item& x, int k0, int t, int j) {
+          const int kt = k0 + j, sk = kt % kNSK;
+          if (t == 0 || j >= x.nt0) {
             if (alive) alive = mbar_wait(bar(kKWait + sk), (uint32_t)((kt / kNSK) & 1), p.err);
           }
           tc_fence_after();
@@ -377,7 +393,7 @@ __global__ void __launch_bounds__(PCfg<D, KV8>::kThreads, 1)
             umma_bf16(s_tm, qd + (uint64_t)(((kk >> 2) * kSlab + (kk & 3) * 32) >> 4),
                       kd + (uint64_t)(((kk >> 2) * 1024 + (kk & 3) * 32) >> 4), idesc_s, kk > 0);
           umma_commit(bar(W_SFULL + t));
-          if (t == 1 || j >= nt1) umma_commit(bar(W_KEMPTY + sk));  // last S of key tile j
+          if (t == 1 || j >= x.nt1) umma_commit(bar(W_KEMPTY + sk));
         };
         auto issue_pv = [&](int t, int j) {
           const int kt = kt0 + j, sv = kt % kNSV;
@@ -397,18 +413,34 @@ __global__ void __launch_bounds__(PCfg<D, KV8>::kThreads, 1)
           if (j == (t ? nt1 : nt0) - 1) umma_commit(bar(W_ODONE + t));
           if (t == 1 || j >= nt1) umma_commit(bar(W_VEMPTY + sv));  // last PV of key tile j
         };
-        auto first_s = [&](int t) {
+        auto begin = [&](const Item& x, int k0, int t) {
           if (alive) alive = mbar_wait(bar(W_QFULL + t), items[t] & 1u, p.err);
           ++items[t];
-          issue_s(t, 0);
+          issue_s(x, k0, t, 0);
         };
-        if (nt0 > 0) first_s(0);
-        if (nt1 > 0) first_s(1);
+        for (int t = 0; t < kQT; ++t) {
+          if (!begun[t] && (t ? nt1 : nt0) > 0) begin(it, kt0, t);
+          begun[t] = false;
+        }
         for (int j = 0; j < nt; ++j) {
-          if (j < nt0) issue_pv(0, j);
-          if (j + 1 < nt0) issue_s(0, j + 1);
-          if (j < nt1) issue_pv(1, j);
-          if (j + 1 < nt1) issue_s(1, j + 1);
+          if (j < nt0) {
+            issue_pv(0, j);
+            if (j + 1 < nt0) {
+              issue_s(it, kt0, 0, j + 1);
+            } else if (have && nx.nt0 > 0) {
+              begin(nx, kt0 + nt, 0);
+              begun[0] = true;
+            }
+          }
+          if (j < nt1) {
+            issue_pv(1, j);
+            if (j + 1 < nt1) {
+              issue_s(it, kt0, 1, j + 1);
+            } else if (have && nx.nt1 > 0 && (begun[0] || nx.nt0 == 0)) {  // never ahead of S_A(0)
+              begin(nx, kt0 + nt, 1);
+              begun[1] = true;
+            }
+          }
         }
         kt0 += nt;
       }
@@ -416,7 +448,8 @@ __global__ void __launch_bounds__(PCfg<D, KV8>::kThreads, 1)
     }
   }
 
-  if (warp < 4 * kQT) {
+  } else {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;\n" ::"n"(C::kSoftmaxRegs));
     // ======================= softmax: one TMEM lane (row) per thread =======================
     const int t = warp >> 2;                 // query tile
     const int r = tid & (kBM - 1);           // row within the tile == TMEM lane
@@ -432,23 +465,28 @@ __global__ void __launch_bounds__(PCfg<D, KV8>::kThreads, 1)
       const int i = R / G, g = R - (R / G) * G;
       return ((int64_t)(x.qs + i) * Hq + (int64_t)x.hk * G + g) * D;
     };
-    auto q_chunk = [&](int c) { return qt + (c >> 3) * kSlab + r * 128 + (((c & 7) ^ (r & 7)) << 4); };
-    // this thread's Q row into the UMMA A layout (K-major, 128-byte swizzle);
-    // zeros past the last row
+    auto q_chunk = [&](int row, int c) { return qt + (c >> 3) * kSlab + row * 128 + (((c & 7) ^ (row & 7)) << 4); };
+    // the warp's 32 Q rows into the UMMA A layout (K-major, 128-byte swizzle),
+    // whole rows of D / 8 chunks a time; zeros past the last row
+    constexpr int kRowLanes = D / 8, kRowsPerCopy = 32 / kRowLanes;
     auto copy_q = [&](const Item& x) {
       const int R = row_of(x);
-      const bool ok = R < x.n * G;
-      const __nv_bfloat16* src = qp + (ok ? row_off(x, R) : 0);
+      const long long off = R < x.n * G ? row_off(x, R) : -1;
 #pragma unroll
-      for (int c = 0; c < D / 8; ++c) cp_async_16(smem_u32(q_chunk(c)), src + c * 8, ok ? 16 : 0);
+      for (int i = 0; i < 32; i += kRowsPerCopy) {
+        const int src_lane = i + lane / kRowLanes, c = lane % kRowLanes;
+        const long long o = __shfl_sync(0xffffffffu, off, src_lane);
+        cp_async_16(smem_u32(q_chunk((warp & 3) * 32 + src_lane, c)), qp + (o < 0 ? 0 : o) + c * 8, o < 0 ? 0 : 16);
+      }
       cp_async_commit();
     };
     auto publish_q = [&]() {
       cp_async_wait<0>();
-      if (KV8) {  // f16 operands: bf16 -> f16 in place
+      if (KV8) {  // f16 operands: bf16 -> f16 in place, each thread its row
+        __syncwarp();
 #pragma unroll 4
         for (int c = 0; c < D / 8; ++c) {
-          uint4* x = reinterpret_cast<uint4*>(q_chunk(c));
+          uint4* x = reinterpret_cast<uint4*>(q_chunk(r, c));
           const uint4 v = *x;
           *x = make_uint4(bf16x2_to_f16x2(v.x), bf16x2_to_f16x2(v.y), bf16x2_to_f16x2(v.z), bf16x2_to_f16x2(v.w));
         }
@@ -506,27 +544,27 @@ __global__ void __launch_bounds__(PCfg<D, KV8>::kThreads, 1)
         auto scaled = [&](uint32_t raw, uint32_t word, int e) {
           return ((word >> e) & 1u) ? __uint_as_float(raw) * sl2 : -INFINITY;
         };
-        // pass 1: the row max, 64 columns at a time
+        // the row of S, and its max
+        uint32_t v[4][32];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) tmem_ld32(s_col + i * 32, v[i]);
+        tmem_wait_ld();
         float mx[8];
 #pragma unroll
         for (int i = 0; i < 8; ++i) mx[i] = -INFINITY;
+        if (plain) {
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          uint32_t v[2][32];
-          tmem_ld32(s_col + h * 64, v[0]);
-          tmem_ld32(s_col + h * 64 + 32, v[1]);
-          tmem_wait_ld();
-          if (plain) {
+          for (int i = 0; i < 4; ++i)
 #pragma unroll
-            for (int cb = 0; cb < 2; ++cb)
+            for (int e = 0; e < 32; ++e) mx[e & 7] = fmaxf(mx[e & 7], __uint_as_float(v[i][e]));
+        } else {
 #pragma unroll
-              for (int e = 0; e < 32; ++e) mx[e & 7] = fmaxf(mx[e & 7], __uint_as_float(v[cb][e]));
-          } else {
+          for (int i = 0; i < 4; ++i)
 #pragma unroll
-            for (int cb = 0; cb < 2; ++cb)
-#pragma unroll
-              for (int e = 0; e < 32; ++e) mx[e & 7] = fmaxf(mx[e & 7], scaled(v[cb][e], see[2 * h + cb], e));
-          }
+            for (int e = 0; e < 32; ++e) {
+              v[i][e] = __float_as_uint(scaled(v[i][e], see[i], e));
+              mx[e & 7] = fmaxf(mx[e & 7], __uint_as_float(v[i][e]));
+            }
         }
         float tmax = fmaxf(fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])),
                            fmaxf(fmaxf(mx[4], mx[5]), fmaxf(mx[6], mx[7])));
@@ -541,38 +579,23 @@ __global__ void __launch_bounds__(PCfg<D, KV8>::kThreads, 1)
           rescale = j > 0;
         }
         const float mbase = m_ref == -INFINITY ? 0.f : m_ref;
-        // pass 2: P = exp2(x - m) as bf16 (f16) pairs, written over the S columns just read
+        // P = exp2(x - m) as bf16 (f16) pairs, written over the S columns
         float rs[8];
 #pragma unroll
         for (int i = 0; i < 8; ++i) rs[i] = 0.f;
+        const float mul = plain ? sl2 : 1.f;
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
-          uint32_t v[2][32];
-          tmem_ld32(s_col + h * 64, v[0]);
-          tmem_ld32(s_col + h * 64 + 32, v[1]);
-          tmem_wait_ld();
           uint32_t w[32];
-          if (plain) {
 #pragma unroll
-            for (int cb = 0; cb < 2; ++cb)
+          for (int cb = 0; cb < 2; ++cb)
 #pragma unroll
-              for (int e = 0; e < 32; e += 2) {
-                const float p0 = fast_exp2(fmaf(__uint_as_float(v[cb][e]), sl2, -mbase));
-                const float p1 = fast_exp2(fmaf(__uint_as_float(v[cb][e + 1]), sl2, -mbase));
-                rs[(e >> 1) & 7] += p0 + p1;
-                w[cb * 16 + (e >> 1)] = KV8 ? pack_f16(p0, p1) : pack_bf16(p0, p1);
-              }
-          } else {
-#pragma unroll
-            for (int cb = 0; cb < 2; ++cb)
-#pragma unroll
-              for (int e = 0; e < 32; e += 2) {
-                const float p0 = fast_exp2(scaled(v[cb][e], see[2 * h + cb], e) - mbase);
-                const float p1 = fast_exp2(scaled(v[cb][e + 1], see[2 * h + cb], e + 1) - mbase);
-                rs[(e >> 1) & 7] += p0 + p1;
-                w[cb * 16 + (e >> 1)] = KV8 ? pack_f16(p0, p1) : pack_bf16(p0, p1);
-              }
-          }
+            for (int e = 0; e < 32; e += 2) {
+              const float p0 = fast_exp2(fmaf(__uint_as_float(v[2 * h + cb][e]), mul, -mbase));
+              const float p1 = fast_exp2(fmaf(__uint_as_float(v[2 * h + cb][e + 1]), mul, -mbase));
+              rs[(e >> 1) & 7] += p0 + p1;
+              w[cb * 16 + (e >> 1)] = KV8 ? pack_f16(p0, p1) : pack_bf16(p0, p1);
+            }
           tmem_st32(s_col + h * 32, w);
         }
         l += ((rs[0] + rs[1]) + (rs[2] + rs[3])) + ((rs[4] + rs[5]) + (rs[6] + rs[7]));
@@ -603,8 +626,14 @@ __global__ void __launch_bounds__(PCfg<D, KV8>::kThreads, 1)
         ++on;
         tc_fence_after();
       }
+      // A quad of lanes holds four rows of 64 bytes per 32 columns; they are
+      // transposed within the quad (16-byte units), so that a store covers 64
+      // contiguous bytes of 8 rows and not 16 of 32.
       const float inv = l > 0.f ? p.v_scale / l : 0.f;  // v_scale: 1 for bf16 pools
-      __nv_bfloat16* orow = outp + (valid_row ? row_off(it, R) : 0);
+      const long long off = valid_row ? row_off(it, R) : -1;
+      long long dst[4];
+#pragma unroll
+      for (int k = 0; k < 4; ++k) dst[k] = __shfl_sync(0xffffffffu, off, (lane & ~3) + k);
 #pragma unroll
       for (int cb = 0; cb < D / 32; ++cb) {
         uint32_t o[32];
@@ -615,17 +644,30 @@ __global__ void __launch_bounds__(PCfg<D, KV8>::kThreads, 1)
 #pragma unroll
           for (int e = 0; e < 32; ++e) o[e] = 0u;
         }
-        if (valid_row) {
+        uint32_t w[4][4];  // unit u: columns 8u .. 8u + 7
 #pragma unroll
-          for (int q = 0; q < 4; ++q) {
-            uint4 w;
-            w.x = pack_bf16(__uint_as_float(o[8 * q + 0]) * inv, __uint_as_float(o[8 * q + 1]) * inv);
-            w.y = pack_bf16(__uint_as_float(o[8 * q + 2]) * inv, __uint_as_float(o[8 * q + 3]) * inv);
-            w.z = pack_bf16(__uint_as_float(o[8 * q + 4]) * inv, __uint_as_float(o[8 * q + 5]) * inv);
-            w.w = pack_bf16(__uint_as_float(o[8 * q + 6]) * inv, __uint_as_float(o[8 * q + 7]) * inv);
-            *reinterpret_cast<uint4*>(orow + cb * 32 + q * 8) = w;
+        for (int u = 0; u < 4; ++u)
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            w[u][i] = pack_bf16(__uint_as_float(o[8 * u + 2 * i]) * inv, __uint_as_float(o[8 * u + 2 * i + 1]) * inv);
+#pragma unroll
+        for (int s = 1; s < 4; s <<= 1) {
+          const bool up = (lane & s) != 0;
+#pragma unroll
+          for (int u = 0; u < 4; ++u) {
+            if (u & s) continue;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              const uint32_t got = __shfl_xor_sync(0xffffffffu, up ? w[u][i] : w[u | s][i], s);
+              if (up) w[u][i] = got; else w[u | s][i] = got;
+            }
           }
         }
+#pragma unroll
+        for (int k = 0; k < 4; ++k)  // row k of the quad, this lane's unit of it
+          if (dst[k] >= 0)
+            *reinterpret_cast<uint4*>(outp + dst[k] + cb * 32 + (lane & 3) * 8) =
+                make_uint4(w[k][0], w[k][1], w[k][2], w[k][3]);
       }
       tc_fence_before();  // O is read before this thread's next P lets PV write it again
     }
