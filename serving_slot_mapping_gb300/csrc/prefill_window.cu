@@ -142,6 +142,34 @@ __device__ __forceinline__ uint32_t bits_to(int k) {
   return k < 0 ? 0u : (k >= 31 ? 0xFFFFFFFFu : 0xFFFFFFFFu >> (31 - k));
 }
 
+// The larger of three; pairs of floats (first in the low half) for the packed
+// fp32 instructions of sm_100+, each half rounded as the scalar one.
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float d;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+  return d;
+}
+__device__ __forceinline__ uint64_t pair(float lo, float hi) {
+  uint64_t d;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(d) : "f"(lo), "f"(hi));
+  return d;
+}
+__device__ __forceinline__ float2 unpair(uint64_t x) {
+  float2 d;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(d.x), "=f"(d.y) : "l"(x));
+  return d;
+}
+__device__ __forceinline__ uint64_t fma_pair(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t d;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+  return d;
+}
+__device__ __forceinline__ uint64_t add_pair(uint64_t a, uint64_t b) {
+  uint64_t d;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
+
 template <int D, bool KV8>
 __global__ void __launch_bounds__(WCfg<D, KV8>::kThreads, 1)
     prefill_window_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_constant__ CUtensorMap tmap_v,
@@ -533,41 +561,30 @@ __global__ void __launch_bounds__(WCfg<D, KV8>::kThreads, 1)
         // scale (the common case) the max is taken over raw S and exp2 takes
         // one fused multiply-add: no mask, no separate scaling.
         const bool plain = !masked && sl2 > 0.f;
-        uint32_t see[4] = {0xFFFFFFFFu, 0xFFFFFFFFu, 0xFFFFFFFFu, 0xFFFFFFFFu};
-        if (masked) {
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const int c0 = l0 + 32 * i;
-            see[i] = bits_to(lim - c0) & (~bits_to(wlo - 1 - c0) | bits_to(p.num_sinks - 1 - c0));
-          }
-        }
-        auto scaled = [&](uint32_t raw, uint32_t word, int e) {
-          return ((word >> e) & 1u) ? __uint_as_float(raw) * sl2 : -INFINITY;
-        };
         // the row of S, and its max
         uint32_t v[4][32];
 #pragma unroll
         for (int i = 0; i < 4; ++i) tmem_ld32(s_col + i * 32, v[i]);
         tmem_wait_ld();
-        float mx[8];
+        if (!plain) {
 #pragma unroll
-        for (int i = 0; i < 8; ++i) mx[i] = -INFINITY;
-        if (plain) {
+          for (int i = 0; i < 4; ++i) {
+            const int c0 = l0 + 32 * i;
+            const uint32_t see = bits_to(lim - c0) & (~bits_to(wlo - 1 - c0) | bits_to(p.num_sinks - 1 - c0));
 #pragma unroll
-          for (int i = 0; i < 4; ++i)
-#pragma unroll
-            for (int e = 0; e < 32; ++e) mx[e & 7] = fmaxf(mx[e & 7], __uint_as_float(v[i][e]));
-        } else {
-#pragma unroll
-          for (int i = 0; i < 4; ++i)
-#pragma unroll
-            for (int e = 0; e < 32; ++e) {
-              v[i][e] = __float_as_uint(scaled(v[i][e], see[i], e));
-              mx[e & 7] = fmaxf(mx[e & 7], __uint_as_float(v[i][e]));
-            }
+            for (int e = 0; e < 32; ++e)
+              v[i][e] = ((see >> e) & 1u) ? __float_as_uint(__uint_as_float(v[i][e]) * sl2) : 0xFF800000u;
+          }
         }
-        float tmax = fmaxf(fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])),
-                           fmaxf(fmaxf(mx[4], mx[5]), fmaxf(mx[6], mx[7])));
+        float mx[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          mx[i] = __uint_as_float(v[i][0]);
+#pragma unroll
+          for (int e = 1; e < 31; e += 2) mx[i] = max3(mx[i], __uint_as_float(v[i][e]), __uint_as_float(v[i][e + 1]));
+          mx[i] = fmaxf(mx[i], __uint_as_float(v[i][31]));
+        }
+        float tmax = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
         if (plain) tmax *= sl2;
         // reference max: moved only when the row max grows by more than 2^8
         float alpha = 1.f;
@@ -580,10 +597,8 @@ __global__ void __launch_bounds__(WCfg<D, KV8>::kThreads, 1)
         }
         const float mbase = m_ref == -INFINITY ? 0.f : m_ref;
         // P = exp2(x - m) as bf16 (f16) pairs, written over the S columns
-        float rs[8];
-#pragma unroll
-        for (int i = 0; i < 8; ++i) rs[i] = 0.f;
-        const float mul = plain ? sl2 : 1.f;
+        const uint64_t mul = plain ? pair(sl2, sl2) : pair(1.f, 1.f), sub = pair(-mbase, -mbase);
+        uint64_t rs[4] = {0ull, 0ull, 0ull, 0ull};
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
           uint32_t w[32];
@@ -591,14 +606,16 @@ __global__ void __launch_bounds__(WCfg<D, KV8>::kThreads, 1)
           for (int cb = 0; cb < 2; ++cb)
 #pragma unroll
             for (int e = 0; e < 32; e += 2) {
-              const float p0 = fast_exp2(fmaf(__uint_as_float(v[2 * h + cb][e]), mul, -mbase));
-              const float p1 = fast_exp2(fmaf(__uint_as_float(v[2 * h + cb][e + 1]), mul, -mbase));
-              rs[(e >> 1) & 7] += p0 + p1;
+              const float2 x = unpair(fma_pair(
+                  pair(__uint_as_float(v[2 * h + cb][e]), __uint_as_float(v[2 * h + cb][e + 1])), mul, sub));
+              const float p0 = fast_exp2(x.x), p1 = fast_exp2(x.y);
+              rs[(e >> 1) & 3] = add_pair(rs[(e >> 1) & 3], pair(p0, p1));
               w[cb * 16 + (e >> 1)] = KV8 ? pack_f16(p0, p1) : pack_bf16(p0, p1);
             }
           tmem_st32(s_col + h * 32, w);
         }
-        l += ((rs[0] + rs[1]) + (rs[2] + rs[3])) + ((rs[4] + rs[5]) + (rs[6] + rs[7]));
+        const float2 sum = unpair(add_pair(add_pair(rs[0], rs[1]), add_pair(rs[2], rs[3])));
+        l += sum.x + sum.y;
         // O is rescaled in place only when some row of the warp moved its
         // reference max.  PV_t(j-1) is complete: S_t(j) was issued after it.
         if (__any_sync(0xffffffffu, rescale)) {
