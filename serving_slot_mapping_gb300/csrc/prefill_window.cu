@@ -32,6 +32,10 @@ namespace pa {
 
 namespace {
 
+constexpr int kItems = 4;        // items whose geometry is in shared memory
+constexpr int kItemBytes = 48;
+constexpr int kWBars = 32;
+
 template <int D, bool KV8>
 struct WCfg : PCfg<D, KV8> {
   using Base = PCfg<D, KV8>;
@@ -44,14 +48,16 @@ struct WCfg : PCfg<D, KV8> {
   static_assert(2 * kSoftmaxRegs + kOtherRegs <= 3 * 168, "more registers than the launch has");
   // 8 tiles in flight: {KV head, valid, hid0, hid1} after the first slots of their boxes
   static constexpr int kMetaOff = Base::kPageOff + 8 * 32 * 4;
-  static constexpr int kWBarOff = kMetaOff + 8 * 16;
-  static constexpr int kWSmem = kWBarOff + kBarSlots * 8 + 16 + 1024;
+  static constexpr int kItemOff = kMetaOff + 8 * 16;
+  static constexpr int kWBarOff = kItemOff + kItems * kItemBytes;
+  static constexpr int kWSmem = kWBarOff + kWBars * 8 + 16 + 1024;
 };
 
 enum { W_QFULL = 0, W_KFULL = W_QFULL + kQT, W_KEMPTY = W_KFULL + kNSK, W_VFULL = W_KEMPTY + kNSK,
        W_VEMPTY = W_VFULL + kNSV, W_SFULL = W_VEMPTY + kNSV, W_PFULL = W_SFULL + kQT, W_ODONE = W_PFULL + kQT,
-       W_VLAND = W_ODONE + kQT, W_KREADY = W_VLAND + 1, W_VREADY = W_KREADY + kNSK, W_COUNT = W_VREADY + kNSV };
-static_assert(W_COUNT <= kBarSlots, "barrier slots");
+       W_VLAND = W_ODONE + kQT, W_KREADY = W_VLAND + 1, W_VREADY = W_KREADY + kNSK, W_IFULL = W_VREADY + kNSV,
+       W_IEMPTY = W_IFULL + kItems, W_COUNT = W_IEMPTY + kItems };
+static_assert(W_COUNT <= kWBars, "barrier slots");
 
 // Sequence b's rows [qs, qs + n) of q; n = 0 where query_start_loc is inconsistent.
 __device__ __forceinline__ int seq_rows(const PrefillParams& p, int b, int* qs) {
@@ -62,9 +68,13 @@ __device__ __forceinline__ int seq_rows(const PrefillParams& p, int b, int* qs) 
 
 __device__ __forceinline__ int row_tiles(int64_t rows) { return (int)((rows + kQT * kBM - 1) / (kQT * kBM)); }
 
-// One work item, as every warp derives it for itself.
+// One work item.  One warp derives it and hands it to the others through a ring
+// in shared memory (deriving it takes ~1.4 us of dependent loads and divisions,
+// which the softmax warps would add to every item): warp 10 for bf16 pools, the
+// TMA warp for e4m3 pools, where warps 10 and 11 convert and clear the tiles.
 struct Item {
-  int b, hk, n, qs, L;
+  int b, hk, qs, L;
+  int n;                  // new rows of the sequence; -1: no more items
   int first;              // position of the sequence's first new row
   int row0;               // the item's first packed row
   int head_keys, gap;     // logical position of key j: j below head_keys, else j - gap
@@ -72,6 +82,7 @@ struct Item {
   int nt0, nt1;           // key tiles that the query tiles see
   __device__ int nt() const { return max(nt0, nt1); }
 };
+static_assert(sizeof(Item) == kItemBytes, "ring entry");
 
 // Walks the items of one CTA in order (whole warps only): 32 sequences at a
 // time, lane i knows the row tiles of sequence base + i.
@@ -190,6 +201,7 @@ __global__ void __launch_bounds__(WCfg<D, KV8>::kThreads, 1)
   auto bar = [&](int i) { return bars + 8u * i; };
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + C::kWBarOff + kBarSlots * 8);
   int* slot_ring = reinterpret_cast<int*>(smem + C::kPageOff);  // [8 tiles][32 lanes] first slot of each box, -1: none
+  volatile Item* item_ring = reinterpret_cast<volatile Item*>(smem + C::kItemOff);
   int4* meta = reinterpret_cast<int4*>(smem + C::kMetaOff);     // [8 tiles] {KV head, valid, hid0, hid1}
 
   if (tid == 0) {
@@ -210,6 +222,10 @@ __global__ void __launch_bounds__(WCfg<D, KV8>::kThreads, 1)
       mbar_init(bar(W_VREADY + s), 1);
     }
     mbar_init(bar(W_VLAND), 1);
+    for (int s = 0; s < kItems; ++s) {
+      mbar_init(bar(W_IFULL + s), 1);
+      mbar_init(bar(W_IEMPTY + s), 4 * kQT + 2 + (KV8 ? 2 : 0));  // each warp with a role
+    }
     fence_mbar_init();
   }
   if (warp == kMmaWarp) tmem_alloc(smem_u32(tmem_slot), C::kTmemCols);
@@ -228,8 +244,34 @@ __global__ void __launch_bounds__(WCfg<D, KV8>::kThreads, 1)
     seq_keys(p.seq_lens, p.kv_indptr, p.kv_last_page_len, p.kv_len, b, ps, p.max_blocks * ps, p.err);
   }
   bool alive = true;
-  Walker wk;
   Item it = {};
+  // The i-th item of this CTA, for a whole warp (in order, each item once).
+  auto read_item = [&](int i, Item* x) {
+    const int s = i % kItems;
+    if (alive) alive = mbar_wait(bar(W_IFULL + s), (uint32_t)((i / kItems) & 1), p.err);
+    const volatile int* src = reinterpret_cast<const volatile int*>(item_ring + s);
+    int* dst = reinterpret_cast<int*>(x);
+#pragma unroll
+    for (int k = 0; k < kItemBytes / 4; ++k) dst[k] = src[k];
+    __syncwarp();
+    if (lane == 0) mbar_arrive(bar(W_IEMPTY + s));
+    return alive && x->n >= 0;
+  };
+  // Derive the next item and hand it out as entry i (whole warp); false at the end.
+  auto publish_next = [&](Walker& wk, int i) {
+    Item x = {};
+    const bool got = wk.next(p, kpo, &x);
+    if (!got) x.n = -1;
+    if (lane == 0) {
+      volatile int* dst = reinterpret_cast<volatile int*>(item_ring + i % kItems);
+      const int* src = reinterpret_cast<const int*>(&x);
+#pragma unroll
+      for (int k = 0; k < kItemBytes / 4; ++k) dst[k] = src[k];
+      mbar_arrive(bar(W_IFULL + i % kItems));
+    }
+    __syncwarp();
+    return got;
+  };
   if (warp >= 4 * kQT) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;\n" ::"n"(C::kOtherRegs));
   if (warp == kTmaWarp) {
@@ -267,28 +309,36 @@ __global__ void __launch_bounds__(WCfg<D, KV8>::kThreads, 1)
       if (lane == 0) t = mbar_test(bar(b), parity) ? 1 : 0;
       return __shfl_sync(0xffffffffu, t, 0) != 0;
     };
-    wk.start(p);
+    Walker wk;
+    if (KV8) wk.start(p);
+    int pub = 0, seen = 0;      // items handed out, items taken for their K tiles
+    bool all_out = !KV8;        // the last entry says that there are no more
     int j = 0, raw = -1;
-    bool more = false;  // `it` has a K tile j left to issue
-    auto to_item = [&]() {  // the next item with keys
-      do {
-        more = wk.next(p, kpo, &it);
-      } while (more && it.nt() == 0);
-      j = 0;
-      if (more) {
-        bt = p.block_table + page_list_start(p.kv_indptr, p.max_blocks, it.b);
-        raw = fetch(0);
-      }
-    };
-    to_item();
+    bool more = false, end = false;  // `it` has a K tile j left to issue; no item is left
     griddep_wait();  // the pool rows of this step were written by an earlier kernel
     int kt = 0, vt = 0;  // tiles issued so far, over all items
     int land_slot = -1;  // ring slot of a V tile whose rows are to be cleared when it has landed
     int4 land = make_int4(0, 0, 0, 0);
     uint32_t land_phase = 0;
     unsigned long long t_last = global_ns();
-    while ((more || vt < kt || land_slot >= 0) && alive) {
+    while ((!end || vt < kt || land_slot >= 0) && alive) {
       bool progressed = false;
+      if (!all_out && (pub < kItems || phase_done(W_IEMPTY + pub % kItems, (uint32_t)((pub / kItems - 1) & 1)))) {
+        all_out = !publish_next(wk, pub);
+        ++pub;
+        progressed = true;
+      }
+      if (!more && !end && (KV8 ? seen < pub : phase_done(W_IFULL + seen % kItems, (uint32_t)((seen / kItems) & 1)))) {
+        end = !read_item(seen, &it);
+        ++seen;
+        more = !end && it.nt() > 0;
+        j = 0;
+        if (more) {
+          bt = p.block_table + page_list_start(p.kv_indptr, p.max_blocks, it.b);
+          raw = fetch(0);
+        }
+        progressed = true;
+      }
       if (more && (kt < kNSK || phase_done(W_KEMPTY + kt % kNSK, (uint32_t)((kt / kNSK - 1) & 1)))) {
         const int key = box_key(j);
         int slot = -1;
@@ -306,10 +356,8 @@ __global__ void __launch_bounds__(WCfg<D, KV8>::kThreads, 1)
         }
         issue(&tmap_k, k_base + (kt % kNSK) * C::kKVTile, it.hk, slot, bar(W_KFULL + kt % kNSK));
         ++kt;
-        if (++j < it.nt())
-          raw = fetch(j);
-        else
-          to_item();
+        more = ++j < it.nt();
+        if (more) raw = fetch(j);
         progressed = true;
       }
       if (vt < kt && (vt < kNSV || phase_done(W_VEMPTY + vt % kNSV, (uint32_t)((vt / kNSV - 1) & 1)))) {
@@ -361,12 +409,22 @@ __global__ void __launch_bounds__(WCfg<D, KV8>::kThreads, 1)
     }
   }
 
+  if (!KV8 && warp == kCvtWarp) {
+    // ======================= items, bf16 pools =======================
+    Walker wk;
+    wk.start(p);
+    for (int i = 0;; ++i) {
+      if (i >= kItems)
+        alive = __all_sync(0xffffffffu, mbar_wait(bar(W_IEMPTY + i % kItems), (uint32_t)((i / kItems - 1) & 1), p.err));
+      if (!publish_next(wk, i) || !alive) break;
+    }
+  }
+
   if (KV8 && (warp == kCvtWarp || warp == kCvtWarp + 1)) {
     // ======================= e4m3 -> f16 converters (K: warp 10, V: warp 11) =======================
     const bool isv = warp == kCvtWarp + 1;
     const int nslots = isv ? kNSV : kNSK;
-    wk.start(p);
-    for (int kt = 0; wk.next(p, kpo, &it) && alive;) {
+    for (int i = 0, kt = 0; read_item(i, &it); ++i) {
       for (int j = 0; j < it.nt() && alive; ++j, ++kt) {
         const int sl = kt % nslots;
         alive = __all_sync(0xffffffffu, mbar_wait(bar((isv ? W_VFULL : W_KFULL) + sl),
@@ -398,11 +456,11 @@ __global__ void __launch_bounds__(WCfg<D, KV8>::kThreads, 1)
     uint32_t items[kQT] = {0u, 0u}, sp[kQT] = {0u, 0u};  // per query tile: items with keys, P tiles awaited
     bool begun[kQT] = {false, false};                    // the item's S_t(0) is issued
     Item nx;
-    wk.start(p);
-    bool have = wk.next(p, kpo, &nx);
+    int taken = 1;
+    bool have = read_item(0, &nx);
     while (have) {
       it = nx;
-      have = wk.next(p, kpo, &nx);
+      have = read_item(taken++, &nx);
       if (lane == 0) {
         const int nt0 = it.nt0, nt1 = it.nt1, nt = it.nt();
         // S_t of key tile j of an item whose tiles start at k0: wait for K where
@@ -522,19 +580,20 @@ __global__ void __launch_bounds__(WCfg<D, KV8>::kThreads, 1)
       fence_proxy_async_smem();
       mbar_arrive(bar(W_QFULL + t));
     };
-    wk.start(p);
     griddep_wait();  // q may come from an earlier kernel; before the first global write
     Item nx;
-    bool have = wk.next(p, kpo, &nx);
+    int taken = 1;
+    bool have = read_item(0, &nx);
     if (have && tiles_of(nx) > 0) {
       copy_q(nx);
       publish_q();
     }
     uint32_t sn = 0, on = 0;  // S tiles and finished O's awaited so far
+    const bool up = sl2 > 0.f;  // the usual scale: the max is taken over raw S and exp2 takes one fused multiply-add
     while (have) {
       it = nx;
-      have = wk.next(p, kpo, &nx);
       const int ntt = tiles_of(it);
+      have = read_item(taken++, &nx);
       const bool next_q = have && tiles_of(nx) > 0;
       const int R = row_of(it);
       const int rows = it.n * G;
@@ -557,23 +616,24 @@ __global__ void __launch_bounds__(WCfg<D, KV8>::kThreads, 1)
         const int l0 = j * kBN;
         // some row does not see some key of the tile
         const bool masked = l0 + kBN - 1 > lim_min || (l0 < wlo_max && l0 + kBN > p.num_sinks);
-        // x = s * scale * log2(e), -inf where masked.  Unmasked with a positive
-        // scale (the common case) the max is taken over raw S and exp2 takes
-        // one fused multiply-add: no mask, no separate scaling.
-        const bool plain = !masked && sl2 > 0.f;
         // the row of S, and its max
         uint32_t v[4][32];
 #pragma unroll
         for (int i = 0; i < 4; ++i) tmem_ld32(s_col + i * 32, v[i]);
         tmem_wait_ld();
-        if (!plain) {
+        if (!up) {
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+#pragma unroll
+            for (int e = 0; e < 32; ++e) v[i][e] = __float_as_uint(__uint_as_float(v[i][e]) * sl2);
+        }
+        if (masked) {
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
             const int c0 = l0 + 32 * i;
             const uint32_t see = bits_to(lim - c0) & (~bits_to(wlo - 1 - c0) | bits_to(p.num_sinks - 1 - c0));
 #pragma unroll
-            for (int e = 0; e < 32; ++e)
-              v[i][e] = ((see >> e) & 1u) ? __float_as_uint(__uint_as_float(v[i][e]) * sl2) : 0xFF800000u;
+            for (int e = 0; e < 32; ++e) v[i][e] = ((see >> e) & 1u) ? v[i][e] : 0xFF800000u;
           }
         }
         float mx[4];
@@ -585,7 +645,7 @@ __global__ void __launch_bounds__(WCfg<D, KV8>::kThreads, 1)
           mx[i] = fmaxf(mx[i], __uint_as_float(v[i][31]));
         }
         float tmax = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
-        if (plain) tmax *= sl2;
+        if (up) tmax *= sl2;
         // reference max: moved only when the row max grows by more than 2^8
         float alpha = 1.f;
         bool rescale = false;
@@ -597,7 +657,7 @@ __global__ void __launch_bounds__(WCfg<D, KV8>::kThreads, 1)
         }
         const float mbase = m_ref == -INFINITY ? 0.f : m_ref;
         // P = exp2(x - m) as bf16 (f16) pairs, written over the S columns
-        const uint64_t mul = plain ? pair(sl2, sl2) : pair(1.f, 1.f), sub = pair(-mbase, -mbase);
+        const uint64_t mul = up ? pair(sl2, sl2) : pair(1.f, 1.f), sub = pair(-mbase, -mbase);
         uint64_t rs[4] = {0ull, 0ull, 0ull, 0ull};
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
@@ -651,16 +711,19 @@ __global__ void __launch_bounds__(WCfg<D, KV8>::kThreads, 1)
       long long dst[4];
 #pragma unroll
       for (int k = 0; k < 4; ++k) dst[k] = __shfl_sync(0xffffffffu, off, (lane & ~3) + k);
+      uint32_t oall[D / 32][32];
 #pragma unroll
-      for (int cb = 0; cb < D / 32; ++cb) {
-        uint32_t o[32];
+      for (int cb = 0; cb < D / 32; ++cb)
         if (ntt > 0) {
-          tmem_ld32(o_col + cb * 32, o);
-          tmem_wait_ld();
+          tmem_ld32(o_col + cb * 32, oall[cb]);
         } else {
 #pragma unroll
-          for (int e = 0; e < 32; ++e) o[e] = 0u;
+          for (int e = 0; e < 32; ++e) oall[cb][e] = 0u;
         }
+      if (ntt > 0) tmem_wait_ld();
+#pragma unroll
+      for (int cb = 0; cb < D / 32; ++cb) {
+        const uint32_t (&o)[32] = oall[cb];
         uint32_t w[4][4];  // unit u: columns 8u .. 8u + 7
 #pragma unroll
         for (int u = 0; u < 4; ++u)
@@ -669,14 +732,14 @@ __global__ void __launch_bounds__(WCfg<D, KV8>::kThreads, 1)
             w[u][i] = pack_bf16(__uint_as_float(o[8 * u + 2 * i]) * inv, __uint_as_float(o[8 * u + 2 * i + 1]) * inv);
 #pragma unroll
         for (int s = 1; s < 4; s <<= 1) {
-          const bool up = (lane & s) != 0;
+          const bool odd = (lane & s) != 0;
 #pragma unroll
           for (int u = 0; u < 4; ++u) {
             if (u & s) continue;
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-              const uint32_t got = __shfl_xor_sync(0xffffffffu, up ? w[u][i] : w[u | s][i], s);
-              if (up) w[u][i] = got; else w[u | s][i] = got;
+              const uint32_t got = __shfl_xor_sync(0xffffffffu, odd ? w[u][i] : w[u | s][i], s);
+              if (odd) w[u][i] = got; else w[u | s][i] = got;
             }
           }
         }
