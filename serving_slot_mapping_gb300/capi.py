@@ -426,16 +426,31 @@ def paged_attention_prefill_csr(key_pool, value_pool, q, query_start_loc, kv_ind
     return out
 
 
-def _here(**tensors):
-    """Refuse tensors that are not on the current CUDA device (the kernels
-    get raw device pointers)."""
-    for name, t in tensors.items():
+# The calls below run at a few microseconds each, where the binding's own work
+# counts: addresses go to ctypes as plain integers, the device is compared by
+# index and the current stream is asked for by device index.
+
+def _here(names, tensors) -> int:
+    """The current CUDA device; refuses tensors that are not on it (the kernels
+    get raw device pointers).  None entries are skipped."""
+    for i, t in enumerate(tensors):
         if t is not None and not t.is_cuda:
-            raise ValueError(f"{name} must be a CUDA tensor")
+            raise ValueError(f"{names.split()[i]} must be a CUDA tensor")
     cur = torch.cuda.current_device()
-    for name, t in tensors.items():
+    for i, t in enumerate(tensors):
         if t is not None and t.get_device() != cur:
-            raise ValueError(f"{name} is on cuda:{t.get_device()}, the current device is cuda:{cur}")
+            raise ValueError(f"{names.split()[i]} is on cuda:{t.get_device()}, the current device is cuda:{cur}")
+    return cur
+
+
+def _addr(t: Optional[torch.Tensor]):
+    return None if t is None else t.data_ptr()
+
+
+def _raw_stream(stream, device: int):
+    if stream is None:
+        return torch._C._cuda_getCurrentRawStream(device)
+    return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 
 
 def _used_on(stream, *tensors):
@@ -450,12 +465,11 @@ def _used_on(stream, *tensors):
             t.record_stream(stream)
 
 
-def _int32(**tensors):
-    for name, t in tensors.items():
-        if t is not None:
-            if t.dtype != torch.int32:
-                raise TypeError(f"{name} must be int32")
-            _contig(t, name)
+def _int32(t, name):
+    if t.dtype != torch.int32:
+        raise TypeError(f"{name} must be int32")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
 
 
 def paged_attention_decode_window(key_pool, value_pool, q, block_table, seq_lens, scale, window, num_sinks=0,
@@ -469,7 +483,8 @@ def paged_attention_decode_window(key_pool, value_pool, q, block_table, seq_lens
     ``block_table`` whose pages hold no visible key are never read (those pages
     may be freed)."""
     pool = make_pool(key_pool, value_pool, k_scale, v_scale)
-    _int32(block_table=block_table, seq_lens=seq_lens)
+    _int32(block_table, "block_table")
+    _int32(seq_lens, "seq_lens")
     made = out is None
     out = _q_out(q, out, key_pool)
     B, hq, _ = q.shape
@@ -478,17 +493,18 @@ def paged_attention_decode_window(key_pool, value_pool, q, block_table, seq_lens
     mb = block_table.shape[1]
     if max_seq_len is None:
         max_seq_len = mb * pool.page_size
-    _here(key_pool=key_pool, value_pool=value_pool, q=q, block_table=block_table, seq_lens=seq_lens, out=out,
-          workspace=workspace)
+    dev = _here("key_pool value_pool q block_table seq_lens out workspace",
+                (key_pool, value_pool, q, block_table, seq_lens, out, workspace))
     if workspace is None:
         workspace = decode_workspace(B, hq, key_pool)
         _used_on(stream, workspace)
     if made:
         _used_on(stream, out)
     wbytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
-    st = lib().paged_attention_decode_window(ctypes.byref(pool), _ptr(q), _ptr(out), B, hq, _ptr(block_table), mb,
-                                             _ptr(seq_lens), int(max_seq_len), float(scale), int(window),
-                                             int(num_sinks), _ptr(workspace), wbytes, _stream(stream))
+    st = lib().paged_attention_decode_window(ctypes.byref(pool), q.data_ptr(), out.data_ptr(), B, hq,
+                                             block_table.data_ptr(), mb, seq_lens.data_ptr(), int(max_seq_len),
+                                             float(scale), int(window), int(num_sinks), _addr(workspace), wbytes,
+                                             _raw_stream(stream, dev))
     _check(st, "paged_attention_decode_window")
     return out
 
@@ -502,7 +518,9 @@ def paged_attention_prefill_window(key_pool, value_pool, q, query_start_loc, blo
     :func:`paged_attention_prefill`; pages without a key that some row of the
     sequence attends to are never read."""
     pool = make_pool(key_pool, value_pool, k_scale, v_scale)
-    _int32(query_start_loc=query_start_loc, block_table=block_table, seq_lens=seq_lens)
+    _int32(query_start_loc, "query_start_loc")
+    _int32(block_table, "block_table")
+    _int32(seq_lens, "seq_lens")
     made = out is None
     out = _q_out(q, out, key_pool)
     T, hq, _ = q.shape
@@ -512,14 +530,14 @@ def paged_attention_prefill_window(key_pool, value_pool, q, query_start_loc, blo
     mb = block_table.shape[1]
     if max_seq_len is None:
         max_seq_len = mb * pool.page_size
-    _here(key_pool=key_pool, value_pool=value_pool, q=q, query_start_loc=query_start_loc, block_table=block_table,
-          seq_lens=seq_lens, out=out)
+    dev = _here("key_pool value_pool q query_start_loc block_table seq_lens out",
+                (key_pool, value_pool, q, query_start_loc, block_table, seq_lens, out))
     if made:
         _used_on(stream, out)
-    st = lib().paged_attention_prefill_window(ctypes.byref(pool), _ptr(q), _ptr(out), B, hq, _ptr(query_start_loc),
-                                              T, int(max_q_len), _ptr(block_table), mb, _ptr(seq_lens),
-                                              int(max_seq_len), float(scale), int(window), int(num_sinks),
-                                              _stream(stream))
+    st = lib().paged_attention_prefill_window(ctypes.byref(pool), q.data_ptr(), out.data_ptr(), B, hq,
+                                              query_start_loc.data_ptr(), T, int(max_q_len), block_table.data_ptr(),
+                                              mb, seq_lens.data_ptr(), int(max_seq_len), float(scale), int(window),
+                                              int(num_sinks), _raw_stream(stream, dev))
     _check(st, "paged_attention_prefill_window")
     return out
 
@@ -528,11 +546,14 @@ def _token_rows(t, name, T, heads, d, dtype):
     """Elements between the tokens of ``t [T, heads, d]`` (heads and dims
     contiguous; the tokens may be slices of longer rows)."""
     if t.dtype != dtype or t.shape != (T, heads, d):
-        raise ValueError(f"{name} must be [T, {heads}, {d}] of {dtype}")
-    s = t.stride()
-    if (d > 1 and s[2] != 1) or (heads > 1 and s[1] != d):
+        raise ValueError(f"{name} must be [{T}, {heads}, {d}] of {dtype}")
+    if T <= 1:
+        s = (heads * d,) + t.stride()[1:]
+    else:
+        s = t.stride()
+    if (s[1] != d and heads > 1) or (s[2] != 1 and d > 1):
         raise ValueError(f"the heads and dims of {name} must be contiguous")
-    return s[0] if T > 1 else heads * d
+    return s[0]
 
 
 def paged_qk_norm_rope_append(key_pool, value_pool, q, key, value, slot_mapping, positions=None, cos_sin=None,
@@ -570,7 +591,7 @@ def paged_qk_norm_rope_append(key_pool, value_pool, q, key, value, slot_mapping,
         max_pos, rot = cos_sin.shape
         if positions is None or positions.numel() != T:
             raise ValueError("a rotation needs one position per token: positions [T]")
-        _int32(positions=positions)
+        _int32(positions, "positions")
     for name, w in (("q_weight", q_weight), ("k_weight", k_weight)):
         if w is not None:
             if w.dtype != row_dtype or w.numel() != d:
@@ -583,14 +604,16 @@ def paged_qk_norm_rope_append(key_pool, value_pool, q, key, value, slot_mapping,
         _contig(out, "out")
         if out.shape != q.shape or out.dtype != q.dtype:
             raise ValueError("out must match q in shape and dtype")
-    _here(key_pool=key_pool, value_pool=value_pool, q=q, key=key, value=value, slot_mapping=slot_mapping,
-          positions=positions if rot else None, cos_sin=cos_sin, q_weight=q_weight, k_weight=k_weight, out=out)
+    if not rot:
+        positions = None
+    dev = _here("key_pool value_pool q key value slot_mapping positions cos_sin q_weight k_weight out",
+                (key_pool, value_pool, q, key, value, slot_mapping, positions, cos_sin, q_weight, k_weight, out))
     if made:
         _used_on(stream, out)
-    st = lib().paged_qk_norm_rope_append(ctypes.byref(pool), _ptr(q), sq, _ptr(key), sk, _ptr(value), sv, _ptr(out),
-                                         hq, _ptr(q_weight), _ptr(k_weight), float(eps),
-                                         _ptr(positions if rot else None), _ptr(cos_sin), max_pos, rot,
-                                         1 if interleaved else 0, _ptr(slot_mapping), T, _stream(stream))
+    st = lib().paged_qk_norm_rope_append(ctypes.byref(pool), q.data_ptr(), sq, key.data_ptr(), sk, value.data_ptr(), sv,
+                                         out.data_ptr(), hq, _addr(q_weight), _addr(k_weight), float(eps),
+                                         _addr(positions), _addr(cos_sin), max_pos, rot, 1 if interleaved else 0,
+                                         slot_mapping.data_ptr(), T, _raw_stream(stream, dev))
     _check(st, "paged_qk_norm_rope_append")
     return out
 
@@ -626,12 +649,14 @@ def paged_kv_copy_pages(pools, src_pages, dst_pages, stream=None):
     (int32 ``[n]``; a negative entry marks a padding pair).  Destinations must be
     distinct and no pair's source."""
     ps = _pools(pools)
-    _int32(src_pages=src_pages, dst_pages=dst_pages)
+    _int32(src_pages, "src_pages")
+    _int32(dst_pages, "dst_pages")
     n = src_pages.numel()
     if dst_pages.numel() != n:
         raise ValueError("src_pages and dst_pages must have the same length")
-    _here(key_pool=ps.tensors[0][0] if ps.count else None, src_pages=src_pages, dst_pages=dst_pages)
-    st = lib().paged_kv_copy_pages(ps.array, ps.count, _ptr(src_pages), _ptr(dst_pages), n, _stream(stream))
+    dev = _here("key_pool src_pages dst_pages", (ps.tensors[0][0] if ps.count else None, src_pages, dst_pages))
+    st = lib().paged_kv_copy_pages(ps.array, ps.count, src_pages.data_ptr(), dst_pages.data_ptr(), n,
+                                   _raw_stream(stream, dev))
     _check(st, "paged_kv_copy_pages")
 
 
@@ -641,21 +666,22 @@ def paged_kv_compact(pools, block_table, seq_lens, keep_indptr, keep, base=None,
     (ascending positions per sequence; ``base`` None: 0).  Returns
     ``new_seq_lens`` int32 ``[B]`` = ``base`` + the number of kept rows."""
     ps = _pools(pools)
-    _int32(block_table=block_table, seq_lens=seq_lens, keep_indptr=keep_indptr, keep=keep, base=base,
-           new_seq_lens=new_seq_lens)
+    for name, t in (("block_table", block_table), ("seq_lens", seq_lens), ("keep_indptr", keep_indptr), ("keep", keep),
+                    ("base", base), ("new_seq_lens", new_seq_lens)):
+        if t is not None:
+            _int32(t, name)
     B = seq_lens.numel()
     if block_table.dim() != 2 or block_table.shape[0] != B or keep_indptr.numel() != B + 1:
         raise ValueError("block_table must be [B, max_blocks], seq_lens [B] and keep_indptr [B + 1]")
-    for name, t in (("base", base), ("new_seq_lens", new_seq_lens)):
-        if t is not None and t.numel() != B:
-            raise ValueError(f"{name} must be [B]")
-    _here(key_pool=ps.tensors[0][0] if ps.count else None, block_table=block_table, seq_lens=seq_lens,
-          keep_indptr=keep_indptr, keep=keep, base=base, new_seq_lens=new_seq_lens)
+    if (base is not None and base.numel() != B) or (new_seq_lens is not None and new_seq_lens.numel() != B):
+        raise ValueError("base and new_seq_lens must be [B]")
+    dev = _here("key_pool block_table seq_lens keep_indptr keep base new_seq_lens",
+                (ps.tensors[0][0] if ps.count else None, block_table, seq_lens, keep_indptr, keep, base, new_seq_lens))
     if new_seq_lens is None:
         new_seq_lens = torch.empty_like(seq_lens)
         _used_on(stream, new_seq_lens)
-    st = lib().paged_kv_compact(ps.array, ps.count, _ptr(block_table), block_table.shape[1], _ptr(seq_lens), B,
-                                _ptr(base), _ptr(keep_indptr), _ptr(keep), keep.numel(), _ptr(new_seq_lens),
-                                _stream(stream))
+    st = lib().paged_kv_compact(ps.array, ps.count, block_table.data_ptr(), block_table.shape[1], seq_lens.data_ptr(), B,
+                                _addr(base), keep_indptr.data_ptr(), keep.data_ptr(), keep.numel(),
+                                new_seq_lens.data_ptr(), _raw_stream(stream, dev))
     _check(st, "paged_kv_compact")
     return new_seq_lens
