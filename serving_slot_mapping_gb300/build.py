@@ -21,7 +21,7 @@ LIB_NAME = "libpagedattn.so"
 LIB_PATH = os.path.join(HERE, LIB_NAME)
 
 SOURCES = ["api.cu", "append.cu", "decode_bf16.cu", "decode_fused.cu", "decode_weighted.cu", "prefill_bf16.cu", "attn_f32.cu",
-           "decode_noalloc.cu", "tmap.cu", "decode_window.cu", "decode_window_e4m3.cu", "prefill_window.cu", "norm_rope.cu",
+           "decode_noalloc.cu", "tmap.cu", "decode_window.cu", "prefill_window.cu", "norm_rope.cu",
            "pages.cu"]
 HEADERS = ["common.cuh", "internal.h", "tma.cuh", "tcgen05.cuh", "decode_split.cuh", "prefill_tc.cuh"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]

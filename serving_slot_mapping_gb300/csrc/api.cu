@@ -268,11 +268,7 @@ pa_status bf16_decode_params(const pa_kv_pool* pool, const void* q, void* out, i
   if (!aligned(q, 16) || !aligned(out, 4)) return PA_ERR_ALIGN;
   const int hb = pa::decode_heads_per_box(pool->num_kv_heads, group, pool->page_size);
   const int sms = num_sms() - reserved_sms;
-  const bool windowed = win.size != INT32_MAX;
-  // keys in the blocks a sequence's units are: a window and sinks that end inside blocks
-  const int64_t used = windowed ? (int64_t)win.size + win.sinks + 48 : INT32_MAX;
-  const int ctas = pa::decode_num_ctas(sms < 1 ? 1 : sms, batch, pool->num_kv_heads,
-                                       (int32_t)std::min<int64_t>(max_seq_len, used), hb);
+  const int ctas = pa::decode_num_ctas(sms < 1 ? 1 : sms, batch, pool->num_kv_heads, max_seq_len, hb);
   const size_t need = decode_ws_bytes(batch, num_q_heads, pool->num_kv_heads, pool->head_dim, ctas, hb);
   if (need > 0 && (workspace == nullptr || workspace_bytes < need)) return PA_ERR_WORKSPACE;
   if (!aligned(workspace, 16)) return PA_ERR_ALIGN;
@@ -311,8 +307,8 @@ pa_status bf16_decode_params(const pa_kv_pool* pool, const void* q, void* out, i
   const int pen = pa::decode_segment_penalty(pool->head_dim, hb, group, kv8(pool), batch, pool->num_kv_heads, ctas);
   const int64_t max_keys = std::max<int64_t>(max_seq_len, (int64_t)t.max_blocks * pool->page_size);
   p->seg_penalty = (int64_t)batch * ((max_keys + 15) / 16 + pen) <= INT32_MAX ? pen : 0;
-  p->window = windowed ? win.size : 0;
-  p->num_sinks = windowed ? win.sinks : 0;
+  p->window = win.size != INT32_MAX ? win.size : 0;
+  p->num_sinks = win.size != INT32_MAX ? win.sinks : 0;
   p->err = error_word();
   return PA_OK;
 }
@@ -401,6 +397,12 @@ pa_status decode_impl(const pa_kv_pool* pool, const void* q, void* out, int32_t 
   st = bf16_decode_params(pool, q, out, batch, num_q_heads, t, max_seq_len, scale, workspace, workspace_bytes, &p, 0,
                           win);
   if (st != PA_OK) return st;
+  if (p.window > 0) {
+    if ((int64_t)batch * pool->num_kv_heads > INT32_MAX / 8) return PA_ERR_RANGE;  // grid x, 8 CTAs each at most
+    const int csize = pa::decode_window_cluster(num_sms(), batch, pool->num_kv_heads, p.group,
+                                                std::min<int64_t>(max_seq_len, (int64_t)win.size + win.sinks));
+    return pa::launch_decode_window(p, csize, s) == cudaSuccess ? PA_OK : PA_ERR_CUDA;
+  }
   return pa::launch_decode_bf16(p, s) == cudaSuccess ? PA_OK : PA_ERR_CUDA;
 }
 

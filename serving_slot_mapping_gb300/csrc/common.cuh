@@ -18,8 +18,6 @@ enum : unsigned long long {
   ERR_SLOT = 2,
   ERR_SEQ_LEN = 3,
   ERR_QUERY_LOC = 4,
-  ERR_POSITION = 6,  // 5: ERR_TIMEOUT (tma.cuh)
-  ERR_KEEP = 7,
 };
 
 __device__ __forceinline__ void record_error(unsigned long long* err, unsigned long long code,

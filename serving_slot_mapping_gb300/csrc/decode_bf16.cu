@@ -219,7 +219,6 @@ cudaError_t launch_split_only(const DecodeParams& p, cudaStream_t s) {
         !encode_pool_tmap_u8(&tv, p.pool.value_pool, rows, p.pool.num_kv_heads, D, R, p.heads_per_box, true))
       return cudaErrorInvalidValue;
     if (p.new_k != nullptr) return launch_split_fused(p, tk, tv, RT, s);
-    if (p.window > 0) return launch_split_window_e4m3(p, tk, tv, RT, s);
     return D == 128 ? launch_split_d<128, true, false>(p, tk, tv, RT, s)
                     : launch_split_d<64, true, false>(p, tk, tv, RT, s);
   }
@@ -228,7 +227,6 @@ cudaError_t launch_split_only(const DecodeParams& p, cudaStream_t s) {
       !encode_pool_tmap(&tv, p.pool.value_pool, rows, p.pool.num_kv_heads, D, R, p.heads_per_box, box_slabs))
     return cudaErrorInvalidValue;
   if (p.new_k != nullptr) return launch_split_fused(p, tk, tv, RT, s);
-  if (p.window > 0) return launch_split_window_bf16(p, tk, tv, RT, s);
   return D == 128 ? launch_split_d<128, false, false>(p, tk, tv, RT, s)
                   : launch_split_d<64, false, false>(p, tk, tv, RT, s);
 }

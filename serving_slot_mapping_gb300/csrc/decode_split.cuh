@@ -1,12 +1,10 @@
 // The split-KV decode kernel of paged_attention_decode (bf16 and e4m3 pools),
 // templated on the shape (head_dim, heads per box, row tiles), the pool
 // element type and FUSED (paged_attention_decode_append: the kernel also
-// writes the step's new K/V rows and attends to them from its input), WC
-// (the weighted cut below for 16-row groups) and WIN
-// (paged_attention_decode_window).  The plain instantiations are compiled in
-// decode_bf16.cu, the fused ones in decode_fused.cu, the WC ones in
-// decode_weighted.cu and the WIN ones in decode_window.cu and
-// decode_window_e4m3.cu, so a plain decode carries none of their code.
+// writes the step's new K/V rows and attends to them from its input) and WC
+// (the weighted cut below for 16-row groups).  The plain instantiations are
+// compiled in decode_bf16.cu, the fused ones in decode_fused.cu, the WC ones in
+// decode_weighted.cu, so a plain decode carries none of the fused code.
 //
 // What is computed (onnxruntime/mobius PR #395 "Add paged / block-table KV
 // cache export", "How it works": Gather(pool, block_table) then Attention
@@ -46,11 +44,6 @@
 //   v_scale into the final normalisation.
 // * Keys at or past L_b are masked in S and their V rows are zeroed in shared
 //   memory, so stale or NaN-poisoned slots never reach the output.
-// * Sliding window (WIN): a sequence's units are the blocks that hold a visible
-//   key -- the sinks' first, then the window's -- and the blocks between them
-//   are skipped (WinSpan): nothing of them is loaded, counted in the cut or
-//   looked up in block_table.  In the blocks at the two edges the hidden keys
-//   are masked in S and zeroed in V as those past L_b are.
 // * At a segment (sequence x head box) end, warps that shared a head merge in
 //   shared memory; a segment covering the whole sequence writes bf16 output,
 //   a segment cut by a range boundary leaves one fp32 partial (m, l, o) per
@@ -76,38 +69,9 @@ namespace pa {
 
 namespace {
 
-// Sliding window: the keys of a sequence of L keys that are visible are those
-// below num_sinks and those from `start` on.  Its units are the 16-key blocks
-// 0 .. head - 1 (the sinks') and then head + gap, head + gap + 1, ... (the
-// window's); gap is 0 where the two meet.
-struct WinSpan {
-  int start, head, gap;
-};
-
-template <bool WIN>
-__device__ __forceinline__ WinSpan win_span(const DecodeParams& p, int L) {
-  WinSpan w = {0, 0, 0};
-  if constexpr (WIN) {
-    w.start = max(0, L - p.window);
-    w.head = (min(p.num_sinks, w.start) + 15) >> 4;
-    w.gap = max(0, (w.start >> 4) - w.head);
-  }
-  return w;
-}
-
-// Block of the sequence that its unit k is.
-template <bool WIN>
-__device__ __forceinline__ int win_block(const WinSpan& w, int k) {
-  if constexpr (WIN) return k < w.head ? k : k + w.gap;
-  return k;
-}
-
-// units of sequence b (either page-table form), recording bad input
-template <bool WIN>
+// keys of sequence b (either page-table form), with / without recording bad input
 __device__ __forceinline__ int nblk_of(const DecodeParams& p, int b, int max_len) {
-  const int L =
-      seq_keys(p.seq_lens, p.kv_indptr, p.kv_last_page_len, p.kv_len, b, p.pool.page_size, max_len, p.err);
-  return ((L + 15) >> 4) - win_span<WIN>(p, L).gap;
+  return (seq_keys(p.seq_lens, p.kv_indptr, p.kv_last_page_len, p.kv_len, b, p.pool.page_size, max_len, p.err) + 15) >> 4;
 }
 
 __device__ __forceinline__ int seq_len_of(const DecodeParams& p, int b, int max_len) {
@@ -128,7 +92,6 @@ __device__ __forceinline__ bool cta_range_empty(int c, int64_t U, int n) {
 struct Cursor {
   int b, hk, k, nblk, L;
   int64_t u;
-  WinSpan win;
 };
 
 // Count one more arrival on a counter word holding (tag << 16) | arrivals in
@@ -373,11 +336,10 @@ __host__ __device__ inline Layout make_layout(int G, int B, int budget) {
   return L;
 }
 
-template <int D, int HB, int RT, bool KV8, bool FUSED, bool WC = false, bool WIN = false>
+template <int D, int HB, int RT, bool KV8, bool FUSED, bool WC = false>
 __global__ void __launch_bounds__(Cfg<D, HB, RT, KV8, WC>::kThreads, 1)
     decode_split_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_constant__ CUtensorMap tmap_v,
                         DecodeParams p) {
-  static_assert(!(FUSED && WIN), "the fused step has no windowed form");
   using C = Cfg<D, HB, RT, KV8, WC>;
   constexpr int NBS = C::NBS, BPW = C::BPW, NW = C::NW;
   extern __shared__ unsigned char smem_raw[];
@@ -451,7 +413,7 @@ __global__ void __launch_bounds__(Cfg<D, HB, RT, KV8, WC>::kThreads, 1)
       else __syncthreads();  // every thread has read the first pass's total
     }
     for (int b = tid; b < B; b += C::kThreads) {
-      const int nb = nblk_of<WIN>(p, b, max_len);
+      const int nb = nblk_of(p, b, max_len);
       prefix[b + 1] = C::kCostlyChange && nb > 0 ? nb + P : nb;
     }
     if (tid == 0) prefix[0] = 0;
@@ -568,7 +530,6 @@ __global__ void __launch_bounds__(Cfg<D, HB, RT, KV8, WC>::kThreads, 1)
       cur.u = u;
     }
     cur.L = seq_len_of(p, cur.b, max_len);
-    cur.win = win_span<WIN>(p, cur.L);
     return cur;
   };
   auto advance = [&](Cursor& cur, int nb) {
@@ -583,7 +544,6 @@ __global__ void __launch_bounds__(Cfg<D, HB, RT, KV8, WC>::kThreads, 1)
         if (cur.b < B) {
           cur.nblk = prefix[cur.b + 1] - prefix[cur.b] - (C::kCostlyChange ? P : 0);
           cur.L = seq_len_of(p, cur.b, max_len);
-          cur.win = win_span<WIN>(p, cur.L);
         }
       }
     }
@@ -713,22 +673,14 @@ __global__ void __launch_bounds__(Cfg<D, HB, RT, KV8, WC>::kThreads, 1)
     OpGeom full_geom[kOpsPerLane];
 #pragma unroll
     for (int x = 0; x < kOpsPerLane; ++x) full_geom[x] = geom(NBS, lane + 32 * x);
-    // first key of op g's box in the stage at cu, and whether the box is loaded:
-    // it holds keys of the sequence, and (sliding window; boxes of 8 rows, half
-    // a block, may lie outside) a visible one
-    auto box_key = [&](const Cursor& cu, const OpGeom& g) { return win_block<WIN>(cu.win, cu.k + g.jj) * 16 + g.q * R; };
-    auto box_used = [&](const Cursor& cu, int kk) {
-      if constexpr (WIN) return kk < cu.L && (kk < p.num_sinks || kk + R > cu.win.start);
-      return kk < cu.L;
-    };
     // raw block_table entries of this lane's ops in the stage at cu (loads only)
     auto fetch = [&](const Cursor& cu, int nbs, int (&pg)[kOpsPerLane]) {
       const int32_t* bt = p.block_table + page_list_start(p.kv_indptr, p.max_blocks, cu.b);
 #pragma unroll
       for (int x = 0; x < kOpsPerLane; ++x) {
         const OpGeom g = nbs == NBS ? full_geom[x] : geom(nbs, lane + 32 * x);
-        const int kk = box_key(cu, g);
-        pg[x] = (g.on && nbs > 0 && box_used(cu, kk)) ? __ldg(bt + (kk >> pshift)) : 0;
+        const int kk = (cu.k + g.jj) * 16 + g.q * R;
+        pg[x] = (g.on && nbs > 0 && kk < cu.L) ? __ldg(bt + (kk >> pshift)) : 0;
       }
     };
     // the stage after the one at (c, nb); nb = 0 past the CTA's range
@@ -768,10 +720,10 @@ __global__ void __launch_bounds__(Cfg<D, HB, RT, KV8, WC>::kThreads, 1)
 #pragma unroll
       for (int x = 0; x < kOpsPerLane; ++x) {
         const OpGeom g = nbs == NBS ? full_geom[x] : geom(nbs, lane + 32 * x);
-        const int kk = box_key(cur, g);
+        const int kk = (cur.k + g.jj) * 16 + g.q * R;
         row[x] = -1;
         dst[x] = sbase + g.off;
-        if (g.on && box_used(cur, kk)) {
+        if (g.on && kk < cur.L) {
           const int page = pg[x];
           if (page < 0 || page >= p.pool.num_pages) {
             if (g.sl == 0 && g.TT == 0) record_error(p.err, ERR_BLOCK_TABLE, page);
@@ -883,7 +835,6 @@ __global__ void __launch_bounds__(Cfg<D, HB, RT, KV8, WC>::kThreads, 1)
         unsigned char* st = ring + slot * C::kStageBytes;
         float s[2 * BPW][4];
         int valid[BPW];
-        int hid0[BPW], hid1[BPW];  // (WIN) rows hid0 .. hid1 - 1 lie between the sinks and the window
         uint32_t vbase[BPW];
         bool touched = false;  // shared-memory stores this warp made into the stage
 #pragma unroll
@@ -891,13 +842,7 @@ __global__ void __launch_bounds__(Cfg<D, HB, RT, KV8, WC>::kThreads, 1)
           const int jb = jw * BPW + bb;  // block within the stage
           s[2 * bb][0] = s[2 * bb][1] = s[2 * bb][2] = s[2 * bb][3] = 0.f;
           s[2 * bb + 1][0] = s[2 * bb + 1][1] = s[2 * bb + 1][2] = s[2 * bb + 1][3] = 0.f;
-          const int key0 = win_block<WIN>(cc.win, first_k + done + jb) * 16;  // the block's first key
-          valid[bb] = jb < nbs ? cc.L - key0 : 0;  // >= 1 for a block of the stage
-          hid0[bb] = hid1[bb] = 0;
-          if constexpr (WIN) {
-            hid0[bb] = max(0, p.num_sinks - key0);
-            hid1[bb] = min(16, cc.win.start - key0);
-          }
+          valid[bb] = jb < nbs ? cc.L - (first_k + done + jb) * 16 : 0;  // >= 1 for a block of the stage
           unsigned char* kt = st + (jb * C::kSlabs) * C::kBoxBytes + h * C::kHeadTile;
           unsigned char* vt = st + ((NBS + jb) * C::kSlabs) * C::kBoxBytes + h * C::kHeadTile;
           vbase[bb] = smem_u32(vt);
@@ -915,20 +860,6 @@ __global__ void __launch_bounds__(Cfg<D, HB, RT, KV8, WC>::kThreads, 1)
             }
             __syncwarp();
             touched = true;
-          }
-          if constexpr (WIN) {
-            // likewise the rows of V between the sinks and the window
-            constexpr int kCh = C::kRowBytes / 16;
-            for (int e = lane; e < (hid1[bb] - hid0[bb]) * C::kSlabs * kCh; e += 32) {
-              const int row = hid0[bb] + e / (C::kSlabs * kCh);
-              const int rem = e % (C::kSlabs * kCh);
-              *reinterpret_cast<uint4*>(vt + (rem / kCh) * C::kBoxBytes + row * C::kRowBytes + (rem % kCh) * 16) =
-                  make_uint4(0, 0, 0, 0);
-            }
-            if (hid1[bb] > hid0[bb]) {
-              __syncwarp();
-              touched = true;
-            }
           }
           if (bb == new_bb) {
             // the new token's K and V rows (row L_b - 1 of this block) come from
@@ -975,9 +906,7 @@ __global__ void __launch_bounds__(Cfg<D, HB, RT, KV8, WC>::kThreads, 1)
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
             const int key = (t & 1) * 8 + (lane & 3) * 2 + (e & 1);
-            bool see = key < valid[t >> 1];
-            if constexpr (WIN) see = see && (key < hid0[t >> 1] || key >= hid1[t >> 1]);
-            s[t][e] = see ? s[t][e] * sl2 : -INFINITY;
+            s[t][e] = key < valid[t >> 1] ? s[t][e] * sl2 : -INFINITY;
           }
         float mx0 = -INFINITY, mx1 = -INFINITY;
 #pragma unroll
@@ -1289,12 +1218,12 @@ cudaError_t launch_split_weighted(const DecodeParams& p, const CUtensorMap& tk, 
 
 namespace {
 
-template <int D, int HB, int RT, bool KV8, bool FUSED, bool WC = false, bool WIN = false>
+template <int D, int HB, int RT, bool KV8, bool FUSED, bool WC = false>
 cudaError_t launch_split(const DecodeParams& p, const CUtensorMap& tk, const CUtensorMap& tv, cudaStream_t s) {
   using C = Cfg<D, HB, RT, KV8, WC>;
   const Layout lay = make_layout<D, HB, RT, KV8, WC>(p.group, p.batch, p.smem_budget);
   if (lay.stages < 2) return cudaErrorInvalidConfiguration;
-  auto kern = decode_split_kernel<D, HB, RT, KV8, FUSED, WC, WIN>;
+  auto kern = decode_split_kernel<D, HB, RT, KV8, FUSED, WC>;
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, lay.total);
   if (e != cudaSuccess) return e;
   // Plain decode: a co-resident (cooperative) grid lets every CTA of a cut
@@ -1321,27 +1250,22 @@ cudaError_t launch_split(const DecodeParams& p, const CUtensorMap& tk, const CUt
   return launch_pdl(kern, dim3(p.num_ctas), dim3(C::kThreads), (size_t)lay.total, s, tk, tv, p);
 }
 
-template <int D, bool KV8, bool FUSED, bool WIN = false>
+template <int D, bool KV8, bool FUSED>
 cudaError_t launch_split_d(const DecodeParams& p, const CUtensorMap& tk, const CUtensorMap& tv, int rt,
                            cudaStream_t s) {
   switch (p.heads_per_box * 10 + rt) {
     case 81:
       // 16-row groups in boxes of 8 heads with a segment penalty: the WC
-      // instantiation (decode_weighted.cu; the windowed ones beside their plain cut)
-      if constexpr (D == 128) {
-        if constexpr (WIN) {
-          if (p.seg_penalty > 0) return launch_split<D, 8, 1, KV8, FUSED, true, true>(p, tk, tv, s);
-        } else if (p.seg_penalty > 0) {
-          return launch_split_weighted(p, tk, tv, KV8, FUSED, s);
-        }
-      }
-      return launch_split<D, 8, 1, KV8, FUSED, false, WIN>(p, tk, tv, s);
-    case 41: return launch_split<D, 4, 1, KV8, FUSED, false, WIN>(p, tk, tv, s);
-    case 21: return launch_split<D, 2, 1, KV8, FUSED, false, WIN>(p, tk, tv, s);
-    case 11: return launch_split<D, 1, 1, KV8, FUSED, false, WIN>(p, tk, tv, s);
-    case 42: return launch_split<D, 4, 2, KV8, FUSED, false, WIN>(p, tk, tv, s);
-    case 22: return launch_split<D, 2, 2, KV8, FUSED, false, WIN>(p, tk, tv, s);
-    case 12: return launch_split<D, 1, 2, KV8, FUSED, false, WIN>(p, tk, tv, s);
+      // instantiation (decode_weighted.cu)
+      if constexpr (D == 128)
+        if (p.seg_penalty > 0) return launch_split_weighted(p, tk, tv, KV8, FUSED, s);
+      return launch_split<D, 8, 1, KV8, FUSED>(p, tk, tv, s);
+    case 41: return launch_split<D, 4, 1, KV8, FUSED>(p, tk, tv, s);
+    case 21: return launch_split<D, 2, 1, KV8, FUSED>(p, tk, tv, s);
+    case 11: return launch_split<D, 1, 1, KV8, FUSED>(p, tk, tv, s);
+    case 42: return launch_split<D, 4, 2, KV8, FUSED>(p, tk, tv, s);
+    case 22: return launch_split<D, 2, 2, KV8, FUSED>(p, tk, tv, s);
+    case 12: return launch_split<D, 1, 2, KV8, FUSED>(p, tk, tv, s);
     default: return cudaErrorInvalidValue;
   }
 }

@@ -7,6 +7,9 @@
 
 namespace pa {
 
+// Codes of the device error word beside those of common.cuh and tma.cuh.
+enum : unsigned long long { ERR_POSITION = 6, ERR_KEEP = 7 };
+
 // Geometry of one layer's pool, as the kernels see it.
 struct PoolGeom {
   const void* key_pool;
@@ -165,7 +168,7 @@ struct DecodeParams {
   // blocks of the box (decode_segment_penalty).  0 for cascade decode, whose
   // combine kernel recomputes the plain cut.
   int32_t seg_penalty;
-  // sliding window (the WIN instantiations): the last `window` keys and the
+  // sliding window (decode_window.cu; 0: none): the last `window` keys and the
   // first `num_sinks` are attended to
   int32_t window;
   int32_t num_sinks;
@@ -183,11 +186,11 @@ cudaError_t launch_decode_bf16(const DecodeParams& p, cudaStream_t s);
 // Cascade: split kernel on s, then the combine after `prefix_done` (an event
 // recorded once the prefix partials are written) has completed.
 cudaError_t launch_decode_cascade_bf16(const DecodeParams& p, cudaStream_t s, cudaEvent_t prefix_done);
-// Launch the sliding-window instantiations (decode_window.cu, decode_window_e4m3.cu).
-cudaError_t launch_split_window_bf16(const DecodeParams& p, const CUtensorMap& tk, const CUtensorMap& tv, int rt,
-                                     cudaStream_t s);
-cudaError_t launch_split_window_e4m3(const DecodeParams& p, const CUtensorMap& tk, const CUtensorMap& tv, int rt,
-                                     cudaStream_t s);
+// The sliding-window decode (decode_window.cu), window > 0.  csize: CTAs of a
+// (sequence, KV head), decode_window_cluster's choice for sequences of at most
+// max_keys visible keys.
+int decode_window_cluster(int num_sms, int32_t batch, int32_t num_kv_heads, int32_t group, int64_t max_keys);
+cudaError_t launch_decode_window(const DecodeParams& p, int csize, cudaStream_t s);
 // Dynamic shared memory the bf16 decode split kernel needs.
 // (size_t)-1 when no stage ring of >= 2 stages fits the budget.
 size_t decode_smem_bytes(int head_dim, int group, int batch, int heads_per_box, int budget, bool kv8);
