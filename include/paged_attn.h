@@ -436,8 +436,8 @@ pa_status paged_attention_prefill_window(const pa_kv_pool* pool, const void* q, 
  * rotary_dim     a multiple of 8, at most head_dim; 0: no rotation (positions
  *                and cos_sin may be NULL).
  * slot_mapping   as for paged_kv_append; a negative entry marks a padding
- *                token, of which nothing is read or written (its q_out row is
- *                left as it was).
+ *                token: its position may be anything and nothing of it is
+ *                written (its q_out row is left as it was).
  * A slot or position out of range is recorded in the device error word (codes
  * 2 and 6) and that token is skipped like a padding token.
  * head_dim a multiple of 8, at most 256 (PA_ERR_UNSUPPORTED); any alignment

@@ -567,7 +567,7 @@ def paged_qk_norm_rope_append(key_pool, value_pool, q, key, value, slot_mapping,
     ``[D]`` of the rows' dtype (None: no norm); ``cos_sin`` float32
     ``[max_position, rotary_dim]``, cosines then sines (None: no rotation), read
     at ``positions`` int32 ``[T]``; ``slot_mapping`` int64 ``[T]``, negative for
-    a padding token (nothing of it is read or written).  Returns the rotated
+    a padding token (its position may be anything, nothing of it is written).  Returns the rotated
     queries ``[T, Hq, D]`` (``out``, which may be ``q`` itself when contiguous);
     the pools are updated in place."""
     pool = make_pool(key_pool, value_pool, k_scale, v_scale)

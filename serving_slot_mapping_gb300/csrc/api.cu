@@ -774,10 +774,11 @@ pa_status paged_qk_norm_rope_append(const pa_kv_pool* pool, const void* q, int64
            aligned(k_weight, a) && aligned(pool->key_pool, pa_) && aligned(pool->value_pool, pa_) &&
            (num_tokens == 1 || (q_stride % n == 0 && key_stride % n == 0 && value_stride % n == 0));
   };
-  if (!p.f32 && D % 16 == 0 && rotary_dim % 16 == 0 && rows_aligned(8))
+  if (!p.f32 && D % 16 == 0 && rotary_dim % 16 == 0 && aligned(cos_sin, 16) && rows_aligned(8))
     p.vec = 8;
   else
     p.vec = rows_aligned(4) ? 4 : 0;
+  p.bulk = aligned(cos_sin, 16) && rotary_dim % 4 == 0 && rows_aligned(16 / (int)es) && D * es % 16 == 0 ? 1 : 0;
   return pa::launch_qk_norm_rope_append(p, num_sms(), static_cast<cudaStream_t>(stream)) == cudaSuccess ? PA_OK
                                                                                                        : PA_ERR_CUDA;
 }

@@ -62,7 +62,12 @@ struct NormRopeParams {
   int32_t kv8;              // bf16 rows, e4m3 pools
   float k_scale, v_scale;
   int32_t vec;              // elements per vector access (8 or 4); 0: addresses not aligned to 4 elements
-  int32_t lanes_per_head;   // set by the launcher
+  int32_t bulk;             // every row (of the table too) starts on 16 bytes
+  // set by the launcher
+  int32_t lanes_per_head;
+  int32_t slices;           // warps a token's heads are spread over
+  int32_t stage_bytes;      // shared memory of a token
+  float inv_dim;            // 1 / head_dim
   unsigned long long* err;
 };
 cudaError_t launch_qk_norm_rope_append(const NormRopeParams& p, int num_sms, cudaStream_t s);

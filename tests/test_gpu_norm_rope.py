@@ -129,6 +129,33 @@ def test_token_counts(cuda_device, T, packed):
     _check(_inputs(cuda_device, T, 32, 8, 128, "bf16", packed=packed, pad=T // 7, seed=T), "bf16")
 
 
+@pytest.mark.parametrize("dtype,hq,hkv,d,rot,interleaved", [("bf16", 8, 2, 128, 128, False), ("bf16", 4, 4, 64, 32, True),
+                                                            ("f32", 4, 2, 64, 64, False), ("f32", 2, 1, 40, 24, True),
+                                                            ("e4m3", 6, 2, 96, 96, False), ("bf16", 3, 1, 256, 0, False)])
+def test_many_tokens(cuda_device, dtype, hq, hkv, d, rot, interleaved):
+    """Thousands of tokens: the kernel that copies token rows through shared
+    memory, with padding tokens between."""
+    s = _inputs(cuda_device, 6001, hq, hkv, d, dtype, rot=rot, pad=700, seed=d)
+    _check(s, dtype, interleaved, scale=0.02 if dtype == "e4m3" else 1.0)
+
+
+def test_many_tokens_in_place_and_all_padding(cuda_device):
+    s = _inputs(cuda_device, 5000, 8, 2, 64, "bf16", packed=False, seed=4)
+    expect = _call(s)
+    got = _call(s, out=s["q"])
+    torch.cuda.synchronize()
+    assert torch.equal(got.view(torch.int16), expect.view(torch.int16))
+    before = s["kp"].clone()
+    s["slots"][:] = -1
+    out = _call(s, out=torch.full_like(expect, 3.0))
+    torch.cuda.synchronize()
+    assert torch.all(out == 3.0) and torch.equal(s["kp"].view(torch.int16), before.view(torch.int16))
+    s["slots"][:5] = torch.arange(5)
+    s["pos"][3] = -7
+    _call(s)
+    assert capi.device_error() == (6, -7)
+
+
 @pytest.mark.parametrize("dtype", ["bf16", "f32", "e4m3"])
 def test_without_norm_or_rotation(cuda_device, dtype):
     scale = 0.02 if dtype == "e4m3" else 1.0
