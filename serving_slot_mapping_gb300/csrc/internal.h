@@ -68,6 +68,7 @@ struct NormRopeParams {
   int32_t slices;           // warps a token's heads are spread over
   int32_t stage_bytes;      // shared memory of a token
   float inv_dim;            // 1 / head_dim
+  float k_inv, v_inv;       // reciprocals of the scales (0: divide)
   unsigned long long* err;
 };
 cudaError_t launch_qk_norm_rope_append(const NormRopeParams& p, int num_sms, cudaStream_t s);

@@ -22,6 +22,8 @@
 //   multiplied into four factors per dim pair once per token, and a head costs two
 //   packed fp32 instructions per pair and one more for 1 / sqrt(mean).
 // * Few tokens: the passes over a token's heads are spread over several warps.
+#include <cmath>
+
 #include "common.cuh"
 #include "internal.h"
 #include "tma.cuh"
@@ -131,14 +133,33 @@ __device__ __forceinline__ void set_pair(Raw<float, V>& r, int i, uint64_t x) {
   r.w[2 * i + 1] = __float_as_uint(v.y);
 }
 
-// V values as e4m3 codes of x / scale (IEEE division, nearest even, saturating)
+// V values as e4m3 codes of x / scale (the correctly rounded quotient, nearest
+// even, saturating).  With inv = the rounded reciprocal of the scale, q = x inv
+// and q + (x - q scale) inv, both fused, is the correctly rounded quotient unless
+// the scale's significand is all ones (Markstein, IBM J. Res. Dev. 34, 1990); the
+// host gives inv = 0 for those scales and for ones near the ends of fp32's range.
+// Quotients outside 2^-12 .. 2^12 round to 0 or saturate as they stand (and
+// infinities and NaN pass).  A division each took the e4m3 append from 61 to 72 us
+// for 10,496 tokens.
 template <int V, bool VEC>
-__device__ __forceinline__ void store_codes(unsigned char* dst, const uint64_t (&x)[V / 2], float scale) {
+__device__ __forceinline__ void store_codes(unsigned char* dst, const uint64_t (&x)[V / 2], float scale, float inv) {
   uint32_t c[V / 2];
+  auto quotient = [&](float v) {
+    const float q = v * inv, r = fmaf(fmaf(-q, scale, v), inv, q);
+    return fabsf(q) >= 0x1p-12f && fabsf(q) <= 0x1p12f ? r : q;
+  };
+  if (inv != 0.f) {
 #pragma unroll
-  for (int i = 0; i < V / 2; ++i) {
-    const float2 v = unpair(x[i]);
-    c[i] = f32x2_to_e4m3x2(__fdiv_rn(v.x, scale), __fdiv_rn(v.y, scale));
+    for (int i = 0; i < V / 2; ++i) {
+      const float2 v = unpair(x[i]);
+      c[i] = f32x2_to_e4m3x2(quotient(v.x), quotient(v.y));
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < V / 2; ++i) {
+      const float2 v = unpair(x[i]);
+      c[i] = f32x2_to_e4m3x2(__fdiv_rn(v.x, scale), __fdiv_rn(v.y, scale));
+    }
   }
   if constexpr (VEC) {
     const uint32_t lo = c[0] | (c[1] << 16);
@@ -315,8 +336,8 @@ template <typename T, bool KV8, int V, bool VEC>
 __device__ __forceinline__ void store_key(const NormRopeParams& p, const Lane<V>& ln, int64_t at,
                                           const uint64_t (&za)[V / 2], const uint64_t (&zb)[V / 2]) {
   if constexpr (KV8) {
-    store_codes<V, VEC>(static_cast<unsigned char*>(p.key_pool) + at + ln.a, za, p.k_scale);
-    store_codes<V, VEC>(static_cast<unsigned char*>(p.key_pool) + at + ln.b, zb, p.k_scale);
+    store_codes<V, VEC>(static_cast<unsigned char*>(p.key_pool) + at + ln.a, za, p.k_scale, p.k_inv);
+    store_codes<V, VEC>(static_cast<unsigned char*>(p.key_pool) + at + ln.b, zb, p.k_scale, p.k_inv);
   } else {
     store_pairs<T, V, VEC>(static_cast<T*>(p.key_pool) + at + ln.a, za);
     store_pairs<T, V, VEC>(static_cast<T*>(p.key_pool) + at + ln.b, zb);
@@ -333,8 +354,8 @@ __device__ __forceinline__ void store_value(const NormRopeParams& p, const Lane<
       za[e] = get_pair(xa, e);
       zb[e] = get_pair(xb, e);
     }
-    store_codes<V, VEC>(static_cast<unsigned char*>(p.value_pool) + at + ln.a, za, p.v_scale);
-    store_codes<V, VEC>(static_cast<unsigned char*>(p.value_pool) + at + ln.b, zb, p.v_scale);
+    store_codes<V, VEC>(static_cast<unsigned char*>(p.value_pool) + at + ln.a, za, p.v_scale, p.v_inv);
+    store_codes<V, VEC>(static_cast<unsigned char*>(p.value_pool) + at + ln.b, zb, p.v_scale, p.v_inv);
   } else {
     store_raw<T, V, VEC>(static_cast<T*>(p.value_pool) + at + ln.a, xa);
     store_raw<T, V, VEC>(static_cast<T*>(p.value_pool) + at + ln.b, xb);
@@ -539,6 +560,13 @@ cudaError_t launch_style(NormRopeParams p, int num_sms, cudaStream_t s) {
   while (lph < p.head_dim / (2 * V)) lph *= 2;
   p.lanes_per_head = lph;
   p.inv_dim = 1.f / (float)p.head_dim;
+  auto reciprocal = [](float scale) {
+    int e = 0;
+    const float f = std::frexp(scale, &e);  // in [1/2, 1)
+    return e > -100 && e < 100 && f != 1.f - 0x1p-24f ? 1.f / scale : 0.f;
+  };
+  p.k_inv = KV8 ? reciprocal(p.k_scale) : 0.f;
+  p.v_inv = KV8 ? reciprocal(p.v_scale) : 0.f;
   if constexpr (VEC && V * sizeof(T) == 16) {
     // bulk copies: 16-byte rows, two blocks an SM, and tokens for at least two
     // laps of every warp

@@ -180,6 +180,23 @@ def test_odd_strides_and_addresses(cuda_device, dtype, odd):
     _check(s, dtype, scale=0.02 if dtype == "e4m3" else 1.0)
 
 
+@pytest.mark.parametrize("scale", [0.02, 1.0, 1 / 3, 0.0078125, 0.013824462890625, 3.7e-5, 1234.5, 1e-37, 1e37,
+                                   float(np.float32(1) - np.float32(2 ** -24)), float(np.float32(0.5) - np.float32(2 ** -25))])
+def test_codes_are_those_of_the_division(cuda_device, scale):
+    """Every bf16 value (infinities and NaN too) as a value row: the code is that
+    of the correctly rounded quotient, as paged_kv_append stores it."""
+    x = torch.arange(1 << 16, dtype=torch.int32).to(torch.int16).view(torch.bfloat16).view(512, 1, 128).to(cuda_device)
+    f8 = torch.float8_e4m3fn
+    a = [torch.zeros(32, 16, 1, 128, device=cuda_device).to(f8) for _ in range(4)]
+    slots = torch.arange(512, device=cuda_device)
+    # keys without norm or rotation go through the same store
+    capi.paged_qk_norm_rope_append(a[0], a[1], x, x, x, slots, k_scale=scale, v_scale=scale)
+    capi.paged_kv_append(a[2], a[3], x, x, slots, k_scale=scale, v_scale=scale)
+    torch.cuda.synchronize()
+    for i in (0, 1):
+        assert torch.equal(a[i].view(torch.uint8), a[2 + i].view(torch.uint8))
+
+
 def test_in_place(cuda_device):
     s = _inputs(cuda_device, 50, 16, 4, 128, "bf16", packed=False, seed=3)
     expect = _call(s)
