@@ -10,9 +10,10 @@
 // (e4m3 pools: the IEEE quotient by the scale, as paged_kv_append).
 //
 // Bound by memory: each row is read once and written once, and by the
-// instructions between (a first form with a thread's heads converted, normed and
+// instructions between: a first form with a thread's heads converted, normed and
 // rotated one operation at a time issued 315 instructions per 4 heads and ran at
-// half the copy rate, 75 us for 10,496 tokens of 48 heads; this one DONE_FIGURE).
+// half the copy rate.  On a GB300, 10,496 tokens of 32 + 8 + 8 heads of 128 bf16
+// dims (262 MB): 45 us, 5.8 TB/s (75 us in the first form); one token: 2.3 us.
 // * A thread holds V elements of each half of a head (16-byte accesses for bf16 V
 //   = 8 and fp32 V = 4), placed so that both elements of every rotated pair are
 //   its own; a head takes LPH lanes (8 for 128 bf16 dims), its sum of squares
@@ -450,29 +451,36 @@ __global__ void __launch_bounds__(kThreads) qk_norm_rope_append_kernel(const __g
   }
 }
 
-// Many tokens: each warp walks tokens w, w + warps, ... through a ring of its own of
-// kSlots tokens in shared memory, filled by bulk copies of the token's q, k, v and
-// cos / sin rows, so that a warp always has a token's 12 KB in flight (in
-// registers the bytes in flight cost occupancy: 55 us at best for the same rows).
+// Many tokens: a team of two warps walks tokens w, w + teams, ... through a ring of
+// its own of kSlots tokens in shared memory, filled by bulk copies of the token's
+// q, k, v and cos / sin rows, so that every team always has a token's 12 KB in
+// flight (in registers the bytes in flight cost occupancy: 55 us at best for the
+// same rows).  The warps share a token's passes: one warp a token left 8 warps an
+// SM, whose latency bound the call (49 us).
 constexpr int kSlots = 2;
+constexpr int kTeamWarps = 2;
+constexpr int kTeams = 4;  // a block
+constexpr int kBulkThreads = 32 * kTeamWarps * kTeams;
 
 template <typename T, bool KV8, int V, bool INTER>
-__global__ void __launch_bounds__(kThreads) qk_norm_rope_append_bulk_kernel(const __grid_constant__ NormRopeParams p) {
+__global__ void __launch_bounds__(kBulkThreads, 2) qk_norm_rope_append_bulk_kernel(const __grid_constant__ NormRopeParams p) {
   extern __shared__ __align__(128) unsigned char smem[];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int team = warp / kTeamWarps, part = warp % kTeamWarps;  // this warp's passes: part, part + kTeamWarps, ...
+  const bool leads = part == 0 && lane == 0;                     // issues the team's copies, records errors
   const int D = p.head_dim, rot = p.rotary_dim, hpw = 32 / p.lanes_per_head;
   const Lane<V> ln(p, lane);
   const int q_bytes = p.num_q_heads * D * (int)sizeof(T), kv_bytes = p.num_kv_heads * D * (int)sizeof(T);
   const int stage = p.stage_bytes;
-  unsigned char* ring = smem + warp * kSlots * stage;
-  const uint32_t bars = smem_u32(smem + (kThreads / 32) * kSlots * stage) + 8u * (warp * kSlots);
-  if (lane < kSlots) {
-    mbar_init(bars + 8u * lane, 1);
+  unsigned char* ring = smem + team * kSlots * stage;
+  const uint32_t bars = smem_u32(smem + kTeams * kSlots * stage) + 8u * (team * kSlots);
+  if (threadIdx.x < kTeams * kSlots) {
+    mbar_init(smem_u32(smem + kTeams * kSlots * stage) + 8u * threadIdx.x, 1);
     fence_mbar_init();
   }
-  __syncwarp();
-  const int64_t warps = (int64_t)gridDim.x * (kThreads / 32);
-  int64_t t = (int64_t)blockIdx.x * (kThreads / 32) + warp;
+  __syncthreads();
+  const int64_t teams = (int64_t)gridDim.x * kTeams;
+  int64_t t = (int64_t)blockIdx.x * kTeams + team;
   griddep_wait();
   // slot and position of a token (every lane the same)
   auto look_up = [&](int64_t x, int64_t* slot, int* pos) {
@@ -482,7 +490,7 @@ __global__ void __launch_bounds__(kThreads) qk_norm_rope_append_bulk_kernel(cons
     *slot = __ldg(p.slot_mapping + x);
     if (rot > 0) *pos = __ldg(p.positions + x);
   };
-  auto issue = [&](int64_t x, int pos, int s) {  // lane 0
+  auto issue = [&](int64_t x, int pos, int s) {  // one thread
     const uint32_t dst = smem_u32(ring + s * stage), bar = bars + 8u * s;
     mbar_arrive_expect_tx(bar, (uint32_t)(q_bytes + 2 * kv_bytes + rot * 4));
     bulk_load(dst, static_cast<const T*>(p.q) + x * p.q_stride, q_bytes, bar);
@@ -491,19 +499,18 @@ __global__ void __launch_bounds__(kThreads) qk_norm_rope_append_bulk_kernel(cons
     if (rot > 0) bulk_load(dst + q_bytes + 2 * kv_bytes, p.cos_sin + (int64_t)pos * rot, rot * 4, bar);
   };
   int64_t slot, next_slot, raw;
-  int pos, next_pos, raw_pos;
+  int raw_pos;
   look_up(t, &raw, &raw_pos);
-  slot = live_slot(p, raw, raw_pos, lane == 0 ? p.err : nullptr);
-  if (slot >= 0 && lane == 0) issue(t, raw_pos, 0);
-  look_up(t + warps, &raw, &raw_pos);
+  slot = live_slot(p, raw, raw_pos, leads ? p.err : nullptr);
+  if (slot >= 0 && leads) issue(t, raw_pos, 0);
+  look_up(t + teams, &raw, &raw_pos);
   uint32_t phases = 0;  // bit s: parity of slot s's next phase
   bool alive = true;
-  for (int s = 0; t < p.num_tokens; t += warps, s ^= 1) {
+  for (int s = 0; t < p.num_tokens; t += teams, s ^= 1) {
     // the next token's copies, the one after's slot and position
-    next_pos = raw_pos;
-    next_slot = t + warps < p.num_tokens ? live_slot(p, raw, next_pos, lane == 0 ? p.err : nullptr) : -1;
-    if (next_slot >= 0 && lane == 0) issue(t + warps, next_pos, s ^ 1);
-    look_up(t + 2 * warps, &raw, &raw_pos);
+    next_slot = t + teams < p.num_tokens ? live_slot(p, raw, raw_pos, leads ? p.err : nullptr) : -1;
+    if (next_slot >= 0 && leads) issue(t + teams, raw_pos, s ^ 1);
+    look_up(t + 2 * teams, &raw, &raw_pos);
     if (slot >= 0) {
       if (alive) alive = mbar_wait(bars + 8u * s, (phases >> s) & 1u, p.err);
       phases ^= 1u << s;
@@ -524,7 +531,7 @@ __global__ void __launch_bounds__(kThreads) qk_norm_rope_append_bulk_kernel(cons
       };
       f.set(p, ln, tr, static_cast<const T*>(p.q_weight));
 #pragma unroll 2
-      for (int h0 = 0; h0 < p.num_q_heads; h0 += hpw) {
+      for (int h0 = part * hpw; h0 < p.num_q_heads; h0 += kTeamWarps * hpw) {
         const int h = min(h0 + ln.g, p.num_q_heads - 1);
         uint64_t za[V / 2], zb[V / 2];
         f.apply(p, ln, p.q_weight != nullptr, half(q, h, ln.a), half(q, h, ln.b), za, zb);
@@ -535,7 +542,7 @@ __global__ void __launch_bounds__(kThreads) qk_norm_rope_append_bulk_kernel(cons
       }
       const int64_t pool_row = slot * (int64_t)p.num_kv_heads * D;
       f.set(p, ln, tr, static_cast<const T*>(p.k_weight));
-      for (int h0 = 0; h0 < p.num_kv_heads; h0 += hpw) {
+      for (int h0 = part * hpw; h0 < p.num_kv_heads; h0 += kTeamWarps * hpw) {
         const int h = min(h0 + ln.g, p.num_kv_heads - 1);
         const bool mine = h0 + ln.g < p.num_kv_heads && ln.on;
         const int64_t at = pool_row + (int64_t)h * D;
@@ -546,12 +553,10 @@ __global__ void __launch_bounds__(kThreads) qk_norm_rope_append_bulk_kernel(cons
           store_value<T, KV8, V, true>(p, ln, at, half(v, h, ln.a), half(v, h, ln.b));
         }
       }
-      __syncwarp();  // the token is read: its slot may be filled again
+      named_barrier(1 + team, 32 * kTeamWarps);  // the token is read: its slot may be filled again
     }
     slot = next_slot;
-    pos = next_pos;
   }
-  (void)pos;
 }
 
 template <typename T, bool KV8, int V, bool VEC, bool INTER>
@@ -568,18 +573,19 @@ cudaError_t launch_style(NormRopeParams p, int num_sms, cudaStream_t s) {
   p.k_inv = KV8 ? reciprocal(p.k_scale) : 0.f;
   p.v_inv = KV8 ? reciprocal(p.v_scale) : 0.f;
   if constexpr (VEC && V * sizeof(T) == 16) {
-    // bulk copies: 16-byte rows, two blocks an SM, and tokens for at least two
-    // laps of every warp
+    // bulk copies: 16-byte rows, two blocks an SM, and tokens for half the teams
+    // (2048 tokens of 48 bf16 heads of 128: 9.7 us, straight to registers 14.0; 512
+    // tokens, fewer than half: 6.4 us straight)
     const int64_t row = (int64_t)(p.num_q_heads + 2 * p.num_kv_heads) * p.head_dim * (int)sizeof(T) + p.rotary_dim * 4;
     const int64_t stage = (row + 127) / 128 * 128;
-    const int64_t smem = (kThreads / 32) * kSlots * (stage + 8);
-    const int64_t warps = 2 * (int64_t)num_sms * (kThreads / 32);
-    if (p.bulk && smem <= 113 * 1024 && p.num_tokens >= 2 * warps) {
+    const int64_t smem = kTeams * kSlots * (stage + 8);
+    const int64_t teams = 2 * (int64_t)num_sms * kTeams;
+    if (p.bulk && smem <= 113 * 1024 && p.num_tokens >= teams / 2) {
       p.stage_bytes = (int32_t)stage;
       auto kern = qk_norm_rope_append_bulk_kernel<T, KV8, V, INTER>;
       const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
       if (e != cudaSuccess) return e;
-      return launch_pdl(kern, dim3((unsigned)(2 * num_sms)), dim3(kThreads), (size_t)smem, s, p);
+      return launch_pdl(kern, dim3((unsigned)(2 * num_sms)), dim3(kBulkThreads), (size_t)smem, s, p);
     }
   }
   const int hpw = 32 / lph;
