@@ -433,13 +433,18 @@ def paged_attention_prefill_csr(key_pool, value_pool, q, query_start_loc, kv_ind
 def _here(names, tensors) -> int:
     """The current CUDA device; refuses tensors that are not on it (the kernels
     get raw device pointers).  None entries are skipped."""
-    for i, t in enumerate(tensors):
-        if t is not None and not t.is_cuda:
-            raise ValueError(f"{names.split()[i]} must be a CUDA tensor")
-    cur = torch.cuda.current_device()
-    for i, t in enumerate(tensors):
+    cur = torch.cuda.current_device() if torch.cuda.is_initialized() or torch.cuda.is_available() else -2
+    for t in tensors:
         if t is not None and t.get_device() != cur:
-            raise ValueError(f"{names.split()[i]} is on cuda:{t.get_device()}, the current device is cuda:{cur}")
+            break
+    else:
+        return cur
+    for name, t in zip(names.split(), tensors):
+        if t is not None and not t.is_cuda:
+            raise ValueError(f"{name} must be a CUDA tensor")
+    for name, t in zip(names.split(), tensors):
+        if t is not None and t.get_device() != cur:
+            raise ValueError(f"{name} is on cuda:{t.get_device()}, the current device is cuda:{cur}")
     return cur
 
 
@@ -666,10 +671,14 @@ def paged_kv_compact(pools, block_table, seq_lens, keep_indptr, keep, base=None,
     (ascending positions per sequence; ``base`` None: 0).  Returns
     ``new_seq_lens`` int32 ``[B]`` = ``base`` + the number of kept rows."""
     ps = _pools(pools)
-    for name, t in (("block_table", block_table), ("seq_lens", seq_lens), ("keep_indptr", keep_indptr), ("keep", keep),
-                    ("base", base), ("new_seq_lens", new_seq_lens)):
-        if t is not None:
-            _int32(t, name)
+    _int32(block_table, "block_table")
+    _int32(seq_lens, "seq_lens")
+    _int32(keep_indptr, "keep_indptr")
+    _int32(keep, "keep")
+    if base is not None:
+        _int32(base, "base")
+    if new_seq_lens is not None:
+        _int32(new_seq_lens, "new_seq_lens")
     B = seq_lens.numel()
     if block_table.dim() != 2 or block_table.shape[0] != B or keep_indptr.numel() != B + 1:
         raise ValueError("block_table must be [B, max_blocks], seq_lens [B] and keep_indptr [B + 1]")
