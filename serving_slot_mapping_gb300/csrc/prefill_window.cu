@@ -21,11 +21,18 @@
 //   key - gap for keys behind the skipped boxes, the key itself for the sinks;
 //   the masks are ranges of logical positions.  So four sinks cost a box, not a
 //   tile, and a window starts at a box, not at a multiple of 128.
+// * Few items (a short chunk of one request): the SPLIT instantiations give an item
+//   to a cluster of CTAs, each a part of its key tiles, and merge their rows
+//   through distributed shared memory (see window_split).
 // * The masks of a row of a 128-key tile are four 32-bit words, built once per
 //   tile that needs any.
 // Boxes whose page holds no key that a row of the sequence sees are never looked
 // up; slots of loaded pages that no row of the sequence sees (between the sinks
 // and the sequence's first window key, or at and past L_b) are zeroed in V.
+#include <algorithm>
+#include <type_traits>
+
+#include "cluster.cuh"
 #include "prefill_tc.cuh"
 
 namespace pa {
@@ -33,7 +40,7 @@ namespace pa {
 namespace {
 
 constexpr int kItems = 4;        // items whose geometry is in shared memory
-constexpr int kItemBytes = 48;
+constexpr int kItemBytes = 52;
 constexpr int kWBars = 32;
 
 template <int D, bool KV8>
@@ -51,6 +58,11 @@ struct WCfg : PCfg<D, KV8> {
   static constexpr int kItemOff = kMetaOff + 8 * 16;
   static constexpr int kWBarOff = kItemOff + kItems * kItemBytes;
   static constexpr int kWSmem = kWBarOff + kWBars * 8 + 16 + 1024;
+  // SPLIT, once the item's products are done: its rows of O, fp32, padded against
+  // bank conflicts, and their (reference max, sum) over the K and V rings
+  static constexpr int kPartRow = D + 4;
+  static constexpr int kPartMl = kQT * kBM * kPartRow * 4;
+  static_assert(kPartMl + kQT * kBM * 8 <= (kNSK + kNSV) * Base::kKVTile, "an item's rows fit over the rings");
 };
 
 enum { W_QFULL = 0, W_KFULL = W_QFULL + kQT, W_KEMPTY = W_KFULL + kNSK, W_VFULL = W_KEMPTY + kNSK,
@@ -66,7 +78,7 @@ __device__ __forceinline__ int seq_rows(const PrefillParams& p, int b, int* qs) 
   return (s0 < 0 || s1 < s0 || (int64_t)s1 > p.total_q) ? 0 : s1 - s0;
 }
 
-__device__ __forceinline__ int row_tiles(int64_t rows) { return (int)((rows + kQT * kBM - 1) / (kQT * kBM)); }
+__host__ __device__ __forceinline__ int row_tiles(int64_t rows) { return (int)((rows + kQT * kBM - 1) / (kQT * kBM)); }
 
 // One work item.  One warp derives it and hands it to the others through a ring
 // in shared memory (deriving it takes ~1.4 us of dependent loads and divisions,
@@ -80,6 +92,7 @@ struct Item {
   int head_keys, gap;     // logical position of key j: j below head_keys, else j - gap
   int seq_start;          // first key that the sequence's first row sees through the window
   int nt0, nt1;           // key tiles that the query tiles see
+  int base;               // logical position of the first (SPLIT: this CTA's part of them)
   __device__ int nt() const { return max(nt0, nt1); }
 };
 static_assert(sizeof(Item) == kItemBytes, "ring entry");
@@ -103,14 +116,14 @@ struct Walker {
     }
     total = __shfl_sync(0xffffffffu, incl, 31);
   }
-  __device__ void start(const PrefillParams& p) {
+  __device__ void start(const PrefillParams& p, int csize) {
     base = 0;
     before = 0;
-    w = blockIdx.x;
+    w = blockIdx.x / csize;
     load(p);
   }
   // The next item; false at the end.
-  __device__ bool next(const PrefillParams& p, int kpo, Item* it) {
+  __device__ bool next(const PrefillParams& p, int kpo, int csize, Item* it) {
     const int Hkv = p.pool.num_kv_heads;
     const int64_t gt = w / Hkv;
     while (gt >= before + total) {
@@ -124,7 +137,7 @@ struct Walker {
     const int tile = rel - (i > 0 ? __shfl_sync(0xffffffffu, incl, i - 1) : 0);
     it->b = base + i;
     it->hk = (int)(w - gt * Hkv);
-    w += gridDim.x;
+    w += gridDim.x / csize;
     const int ps = p.pool.page_size;
     it->n = seq_rows(p, it->b, &it->qs);
     it->L = seq_keys(p.seq_lens, p.kv_indptr, p.kv_last_page_len, p.kv_len, it->b, ps, p.max_blocks * ps, nullptr);
@@ -144,6 +157,13 @@ struct Walker {
     };
     it->nt0 = tiles(it->row0);
     it->nt1 = tiles(it->row0 + kBM);
+    it->base = 0;
+    if (csize > 1) {  // this CTA's part of the key tiles
+      const int per = (it->nt() + csize - 1) / csize, j0 = (int)(blockIdx.x % csize) * per;
+      it->nt0 = min(max(it->nt0 - j0, 0), per);
+      it->nt1 = min(max(it->nt1 - j0, 0), per);
+      it->base = j0 * kBN;
+    }
     return true;
   }
 };
@@ -181,10 +201,13 @@ __device__ __forceinline__ uint64_t add_pair(uint64_t a, uint64_t b) {
   return d;
 }
 
-template <int D, bool KV8>
+// SPLIT: csize CTAs of a cluster share an item, and there are clusters for all
+// items (a CTA has one item at most); else csize is 1.
+template <int D, bool KV8, bool SPLIT>
 __global__ void __launch_bounds__(WCfg<D, KV8>::kThreads, 1)
     prefill_window_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_constant__ CUtensorMap tmap_v,
-                          const __grid_constant__ PrefillParams p) {
+                          const __grid_constant__ PrefillParams p, int csize_arg) {
+  const int csize = SPLIT ? csize_arg : 1;
   using C = WCfg<D, KV8>;
   extern __shared__ unsigned char smem_raw[];
   unsigned char* smem = reinterpret_cast<unsigned char*>(
@@ -260,7 +283,7 @@ __global__ void __launch_bounds__(WCfg<D, KV8>::kThreads, 1)
   // Derive the next item and hand it out as entry i (whole warp); false at the end.
   auto publish_next = [&](Walker& wk, int i) {
     Item x = {};
-    const bool got = wk.next(p, kpo, &x);
+    const bool got = (!SPLIT || i == 0) && wk.next(p, kpo, csize, &x);
     if (!got) x.n = -1;
     if (lane == 0) {
       volatile int* dst = reinterpret_cast<volatile int*>(item_ring + i % kItems);
@@ -281,7 +304,7 @@ __global__ void __launch_bounds__(WCfg<D, KV8>::kThreads, 1)
     // The page ids of the next K tile are read while this one is issued.
     const uint32_t box_bytes = (uint32_t)kpo * D * (KV8 ? 1 : 2);
     auto box_key = [&](int j) {  // first key of this lane's box of tile j
-      const int l = j * kBN + lane * kpo;
+      const int l = it.base + j * kBN + lane * kpo;
       return l < it.head_keys ? l : l + it.gap;
     };
     auto box_used = [&](int key) {  // a box with a key that some row of the sequence sees
@@ -310,7 +333,7 @@ __global__ void __launch_bounds__(WCfg<D, KV8>::kThreads, 1)
       return __shfl_sync(0xffffffffu, t, 0) != 0;
     };
     Walker wk;
-    if (KV8) wk.start(p);
+    if (KV8) wk.start(p, csize);
     int pub = 0, seen = 0;      // items handed out, items taken for their K tiles
     bool all_out = !KV8;        // the last entry says that there are no more
     int j = 0, raw = -1;
@@ -350,7 +373,7 @@ __global__ void __launch_bounds__(WCfg<D, KV8>::kThreads, 1)
         }
         slot_ring[(kt & 7) * 32 + lane] = slot;
         if (lane == 0) {
-          const int l0 = j * kBN;  // rows of the tile: valid ones, and those no row of the sequence sees
+          const int l0 = it.base + j * kBN;  // rows of the tile: valid ones, and those no row of the sequence sees
           const int end = it.seq_start <= it.head_keys ? it.seq_start : max(it.head_keys, it.seq_start - it.gap);
           meta[kt & 7] = make_int4(it.hk, min(it.L - it.gap - l0, kBN), max(0, p.num_sinks - l0), min(end - l0, kBN));
         }
@@ -412,7 +435,7 @@ __global__ void __launch_bounds__(WCfg<D, KV8>::kThreads, 1)
   if (!KV8 && warp == kCvtWarp) {
     // ======================= items, bf16 pools =======================
     Walker wk;
-    wk.start(p);
+    wk.start(p, csize);
     for (int i = 0;; ++i) {
       if (i >= kItems)
         alive = __all_sync(0xffffffffu, mbar_wait(bar(W_IEMPTY + i % kItems), (uint32_t)((i / kItems - 1) & 1), p.err));
@@ -613,7 +636,7 @@ __global__ void __launch_bounds__(WCfg<D, KV8>::kThreads, 1)
         tc_fence_after();
         // every S of this item is done: Q may be replaced
         if (j == ntt - 1 && next_q) copy_q(nx);
-        const int l0 = j * kBN;
+        const int l0 = it.base + j * kBN;
         // some row does not see some key of the tile
         const bool masked = l0 + kBN - 1 > lim_min || (l0 < wlo_max && l0 + kBN > p.num_sinks);
         // the row of S, and its max
@@ -703,6 +726,25 @@ __global__ void __launch_bounds__(WCfg<D, KV8>::kThreads, 1)
         ++on;
         tc_fence_after();
       }
+      if constexpr (SPLIT) {
+        // the row unnormalised over the rings, once the other query tile's
+        // products have read them too
+        named_barrier(1, kQT * kBM);
+        float* row = reinterpret_cast<float*>(smem + C::kKOff) + (t * kBM + r) * C::kPartRow;
+        reinterpret_cast<float2*>(smem + C::kKOff + C::kPartMl)[t * kBM + r] = make_float2(m_ref, l);
+        if (ntt > 0) {
+#pragma unroll
+          for (int cb = 0; cb < D / 32; ++cb) {
+            uint32_t o[32];
+            tmem_ld32(o_col + cb * 32, o);
+            tmem_wait_ld();
+#pragma unroll
+            for (int e = 0; e < 32; e += 4)
+              *reinterpret_cast<uint4*>(row + cb * 32 + e) = make_uint4(o[e], o[e + 1], o[e + 2], o[e + 3]);
+          }
+        }
+        continue;
+      }
       // A quad of lanes holds four rows of 64 bytes per 32 columns; they are
       // transposed within the quad (16-byte units), so that a store covers 64
       // contiguous bytes of 8 rows and not 16 of 32.
@@ -758,21 +800,100 @@ __global__ void __launch_bounds__(WCfg<D, KV8>::kThreads, 1)
   __syncthreads();
   tc_fence_after();
   if (warp == kMmaWarp) tmem_dealloc(tmem, C::kTmemCols);
+  if constexpr (SPLIT) {
+    // ======================= the cluster's parts joined =======================
+    // o = v_scale sum_c 2^(m_c - M) o_c / sum_c 2^(m_c - M) l_c; each CTA a part of
+    // the item's rows, 4 dims a thread.
+    cluster_sync();
+    const Item x = *const_cast<const Item*>(item_ring);
+    const int rank = (int)(blockIdx.x % csize);
+    if (x.n >= 0) {
+      const uint32_t part = smem_u32(smem + C::kKOff), part_ml = part + C::kPartMl;
+      const int rows = min(kQT * kBM, x.n * G - x.row0);
+      // 16 loads of a thread in flight whatever the cluster's size
+      auto join = [&](auto size) {
+        constexpr int N = decltype(size)::value, U = 8 / N;
+        const int total = rows * (D / 4), step = N * C::kThreads;
+        for (int i0 = rank * C::kThreads + tid; i0 < total; i0 += U * step) {
+          float2 ml[U][N];
+          float4 v[U][N];
+#pragma unroll
+          for (int k = 0; k < U; ++k) {
+            const int i = min(i0 + k * step, total - 1), r = i / (D / 4), c = i - r * (D / 4);
+#pragma unroll
+            for (int q = 0; q < N; ++q) {
+              ml[k][q] = ld_cluster2(map_rank(part_ml + 8u * r, q));
+              v[k][q] = ld_cluster4(map_rank(part + 4u * (r * C::kPartRow + 4 * c), q));
+            }
+          }
+#pragma unroll
+          for (int k = 0; k < U; ++k) {
+            const int i = i0 + k * step, r = i / (D / 4), c = i - r * (D / 4);
+            if (i >= total) break;
+            float M = -INFINITY, den = 0.f;
+            float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+            for (int q = 0; q < N; ++q) M = fmaxf(M, ml[k][q].x);
+#pragma unroll
+            for (int q = 0; q < N; ++q) {
+              if (ml[k][q].x == -INFINITY) continue;  // a part without a visible key: its row is not written
+              const float f = fast_exp2(ml[k][q].x - M);
+              den += f * ml[k][q].y;
+              acc.x += f * v[k][q].x; acc.y += f * v[k][q].y; acc.z += f * v[k][q].z; acc.w += f * v[k][q].w;
+            }
+            const float inv = den > 0.f ? p.v_scale / den : 0.f;
+            const int R = x.row0 + r, tok = R / G;
+            const int64_t at = ((int64_t)(x.qs + tok) * Hq + (int64_t)x.hk * G + (R - tok * G)) * D + 4 * c;
+            *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(p.out) + at) =
+                make_uint2(pack_bf16(acc.x * inv, acc.y * inv), pack_bf16(acc.z * inv, acc.w * inv));
+          }
+        }
+      };
+      if (csize == 2) join(std::integral_constant<int, 2>());
+      else if (csize == 4) join(std::integral_constant<int, 4>());
+      else join(std::integral_constant<int, 8>());
+    }
+    cluster_sync();  // no CTA leaves while another reads its memory
+  }
+}
+
+// CTAs of an item: one where the items fill the SMs; else as many (a power of two
+// up to 8, with two key tiles each at least) as the SMs hold at once (four fifths
+// of them for clusters of 4 and 8, which do not fill every SM).  32 / 8 heads of 128 on one CTA an item
+// and so split: 512 tokens, window 1024 23.7 and 21.7 us (2 CTAs); 128 tokens 23.6
+// and 16.6 us (4); 64 tokens, window 4096 71 and 21 us (4).
+int window_split(int num_sms, int64_t items, int64_t max_keys) {
+  const int64_t tiles = (max_keys + kBN - 1) / kBN;
+  int c = 1;
+  while (c < 8 && items * 2 * c <= (c == 1 ? (int64_t)num_sms : (int64_t)num_sms * 4 / 5) && tiles >= 4 * c) c *= 2;
+  return c;
+}
+
+template <int D, bool KV8, bool SPLIT>
+cudaError_t launch_items(const PrefillParams& p, const CUtensorMap& tk, const CUtensorMap& tv, unsigned grid, int csize,
+                         cudaStream_t s) {
+  using C = WCfg<D, KV8>;
+  auto kern = prefill_window_kernel<D, KV8, SPLIT>;
+  const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kWSmem);
+  if (e != cudaSuccess) return e;
+  if (!SPLIT) return launch_pdl(kern, dim3(grid), dim3(C::kThreads), (size_t)C::kWSmem, s, tk, tv, p, 1);
+  return launch_pdl_cluster(kern, dim3(grid), dim3(C::kThreads), (size_t)C::kWSmem, csize, s, tk, tv, p, csize);
 }
 
 template <int D, bool KV8>
 cudaError_t launch_window(const PrefillParams& p, int num_sms, cudaStream_t s) {
-  using C = WCfg<D, KV8>;
   CUtensorMap tk, tv;
   if (!encode_prefill_tmaps<D, KV8>(p, &tk, &tv)) return cudaErrorInvalidValue;
-  auto kern = prefill_window_kernel<D, KV8>;
-  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kWSmem);
-  if (e != cudaSuccess) return e;
-  // items: at most a partial tile per sequence beside the full ones
-  const int64_t tiles = p.total_q * p.group / (kQT * kBM) + p.batch;
+  // items: at most a partial tile per sequence beside the full ones, and at most
+  // the longest sequence's for each
+  const int64_t tiles = std::min<int64_t>(p.total_q * p.group / (kQT * kBM) + p.batch,
+                                          (int64_t)p.batch * row_tiles((int64_t)p.max_q_len * p.group));
   const int64_t items = tiles * p.pool.num_kv_heads;
-  const unsigned grid = (unsigned)(items < num_sms ? items : num_sms);
-  return launch_pdl(kern, dim3(grid), dim3(C::kThreads), (size_t)C::kWSmem, s, tk, tv, p);
+  const int64_t keys = std::min<int64_t>((int64_t)p.max_blocks * p.pool.page_size,
+                                         (int64_t)p.window + p.num_sinks + kQT * kBM / p.group);
+  const int csize = window_split(num_sms, items, keys);
+  if (csize > 1) return launch_items<D, KV8, true>(p, tk, tv, (unsigned)(items * csize), csize, s);
+  return launch_items<D, KV8, false>(p, tk, tv, (unsigned)(items < num_sms ? items : num_sms), 1, s);
 }
 
 }  // namespace

@@ -144,6 +144,16 @@ def test_prefill_layouts(cuda_device, dtype, hq, hkv, d, ps):
         capi, cuda_device)
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "e4m3"])
+@pytest.mark.parametrize("hq,hkv,d,ps", [(8, 2, 128, 16), (2, 2, 64, 8), (4, 1, 128, 128), (5, 1, 64, 32), (16, 1, 128, 256)])
+def test_prefill_few_rows_long_windows(cuda_device, dtype, hq, hkv, d, ps):
+    """Few items with many key tiles each: their parts are computed by the CTAs of
+    a cluster and joined (some CTAs of a cluster without a tile, rows without a key)."""
+    Case([33, 1, 70, 12], [900, 1500, 0, -12], 1300, 40, hq=hq, hkv=hkv, d=d, ps=ps, dtype=dtype, seed=d + ps).check(
+        capi, cuda_device)
+    Case([64], [5000], 3000, 4, hq=hq, hkv=hkv, d=d, ps=ps, dtype=dtype, seed=d + ps + 1).check(capi, cuda_device)
+
+
 @pytest.mark.parametrize("dtype,ps", [("bf16", 1), ("bf16", 12), ("f32", 16)])
 def test_prefill_core_path(cuda_device, dtype, ps):
     Case([20, 1, 50], [60, 0, 10], 30, 3, dtype=dtype, ps=ps, seed=ps).check(capi, cuda_device)
