@@ -382,7 +382,9 @@ pa_status paged_attention_prefill(const pa_kv_pool* pool, const void* q, void* o
  * to must be finite, as for the plain calls.
  * Every other argument, limit, type, the workspace and the results are those
  * of the plain calls; where the window reaches every key (window or num_sinks
- * >= max_seq_len) the plain kernels run.
+ * >= max_seq_len) the plain kernels run, and only there is the workspace used.
+ * Tensor-core pools: out is 8-byte aligned (decode), q and out are 16-byte
+ * aligned (prefill, which takes at most 2^31 - 1 slots per pool).
  */
 pa_status paged_attention_decode_window(const pa_kv_pool* pool, const void* q, void* out,
                                         int32_t batch, int32_t num_q_heads,
@@ -427,8 +429,8 @@ pa_status paged_attention_prefill_window(const pa_kv_pool* pool, const void* q, 
  *                least a row long.
  * q_out          device [num_tokens, num_q_heads, head_dim], the rows' type; q
  *                itself when its rows are contiguous, else memory that no row
- *                of q overlaps (PA_ERR_SHAPE); no input overlaps q_out or the
- *                pools otherwise.
+ *                of q, key or value overlaps (PA_ERR_SHAPE).  No input overlaps
+ *                the pools.
  * q_weight, k_weight  device [head_dim], the rows' type, or NULL: no norm.
  * eps            >= 0, finite.
  * positions      device int32 [num_tokens], each in [0, max_position).

@@ -234,6 +234,20 @@ Table dense_table(const int32_t* block_table, int32_t max_blocks, const int32_t*
   return t;
 }
 
+// The status of a launch; a refused one leaves no error behind for the caller's
+// next CUDA call to find.
+pa_status launched(cudaError_t e) {
+  if (e == cudaSuccess) return PA_OK;
+  (void)cudaGetLastError();
+  return PA_ERR_CUDA;
+}
+
+// Whether [a, a + na) and [b, b + nb) bytes meet.
+bool meet(const void* a, int64_t na, const void* b, int64_t nb) {
+  const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+  return x < y + (uintptr_t)nb && y < x + (uintptr_t)na;
+}
+
 // Sliding window of the _window calls: position p sees keys j <= p with
 // j > p - size or j < sinks.
 struct Window {
@@ -393,6 +407,7 @@ pa_status decode_impl(const pa_kv_pool* pool, const void* q, void* out, int32_t 
     p.err = error_word();
     return pa::launch_attn_f32(p, num_sms(), s) == cudaSuccess ? PA_OK : PA_ERR_CUDA;
   }
+  if (win.size != INT32_MAX && !aligned(out, 8)) return PA_ERR_ALIGN;
   pa::DecodeParams p;
   st = bf16_decode_params(pool, q, out, batch, num_q_heads, t, max_seq_len, scale, workspace, workspace_bytes, &p, 0,
                           win);
@@ -401,7 +416,7 @@ pa_status decode_impl(const pa_kv_pool* pool, const void* q, void* out, int32_t 
     if ((int64_t)batch * pool->num_kv_heads > INT32_MAX / 8) return PA_ERR_RANGE;  // grid x, 8 CTAs each at most
     const int csize = pa::decode_window_cluster(num_sms(), batch, pool->num_kv_heads, p.group,
                                                 std::min<int64_t>(max_seq_len, (int64_t)win.size + win.sinks));
-    return pa::launch_decode_window(p, csize, s) == cudaSuccess ? PA_OK : PA_ERR_CUDA;
+    return launched(pa::launch_decode_window(p, csize, s));
   }
   return pa::launch_decode_bf16(p, s) == cudaSuccess ? PA_OK : PA_ERR_CUDA;
 }
@@ -473,8 +488,13 @@ pa_status prefill_impl(const pa_kv_pool* pool, const void* q, void* out, int32_t
   p.window = win.size != INT32_MAX ? win.size : 0;
   p.num_sinks = win.size != INT32_MAX ? win.sinks : 0;
   p.err = error_word();
-  const cudaError_t e = p.window > 0 ? pa::launch_prefill_window(p, num_sms(), s) : pa::launch_prefill_bf16(p, s);
-  return e == cudaSuccess ? PA_OK : PA_ERR_CUDA;
+  if (p.window > 0) {
+    // q rows are read and out rows written 16 bytes at a time; a slot is 32 bits
+    if (!aligned(q, 16) || !aligned(out, 16)) return PA_ERR_ALIGN;
+    if (pool->num_pages * (int64_t)pool->page_size > INT32_MAX) return PA_ERR_RANGE;
+    return launched(pa::launch_prefill_window(p, num_sms(), s));
+  }
+  return pa::launch_prefill_bf16(p, s) == cudaSuccess ? PA_OK : PA_ERR_CUDA;
 }
 
 // The CSR form as a Table; max_seq_len bounds every sequence's keys.
@@ -723,6 +743,7 @@ pa_status paged_qk_norm_rope_append(const pa_kv_pool* pool, const void* q, int64
   if (q_row > INT32_MAX || kv_row > INT32_MAX || num_tokens > INT32_MAX || max_position > INT32_MAX)
     return PA_ERR_RANGE;
   if (num_tokens > 1 && (q_stride < q_row || key_stride < kv_row || value_stride < kv_row)) return PA_ERR_SHAPE;
+  if (num_tokens > 1 && std::max(q_stride, std::max(key_stride, value_stride)) > INT32_MAX) return PA_ERR_RANGE;
   if (num_tokens == 0) return PA_OK;
   if (q == nullptr || key == nullptr || value == nullptr || q_out == nullptr || slot_mapping == nullptr)
     return PA_ERR_NULL;
@@ -731,11 +752,13 @@ pa_status paged_qk_norm_rope_append(const pa_kv_pool* pool, const void* q, int64
   if (!aligned(q, es) || !aligned(key, es) || !aligned(value, es) || !aligned(q_out, es) || !aligned(q_weight, es) ||
       !aligned(k_weight, es) || !aligned(slot_mapping, 8) || !aligned(positions, 4) || !aligned(cos_sin, 4))
     return PA_ERR_ALIGN;
-  // q_out is q itself, row for row, or memory that no row of q reaches
-  const uintptr_t q0 = reinterpret_cast<uintptr_t>(q), o0 = reinterpret_cast<uintptr_t>(q_out);
-  const uintptr_t q1 = q0 + (uintptr_t)(((num_tokens - 1) * q_stride + q_row) * (int64_t)es);
-  const uintptr_t o1 = o0 + (uintptr_t)(num_tokens * q_row * (int64_t)es);
-  if (q0 < o1 && o0 < q1 && !(q0 == o0 && (num_tokens == 1 || q_stride == q_row))) return PA_ERR_SHAPE;
+  // q_out is q itself, row for row, or memory that no row reaches
+  auto span = [&](int64_t stride, int64_t row) { return ((num_tokens - 1) * stride + row) * (int64_t)es; };
+  const int64_t out_bytes = num_tokens * q_row * (int64_t)es;
+  const bool in_place = q == q_out && (num_tokens == 1 || q_stride == q_row);
+  if ((!in_place && meet(q, span(q_stride, q_row), q_out, out_bytes)) ||
+      meet(key, span(key_stride, kv_row), q_out, out_bytes) || meet(value, span(value_stride, kv_row), q_out, out_bytes))
+    return PA_ERR_SHAPE;
   pa::NormRopeParams p{};
   p.key_pool = pool->key_pool;
   p.value_pool = pool->value_pool;
@@ -779,8 +802,7 @@ pa_status paged_qk_norm_rope_append(const pa_kv_pool* pool, const void* q, int64
   else
     p.vec = rows_aligned(4) ? 4 : 0;
   p.bulk = aligned(cos_sin, 16) && rotary_dim % 4 == 0 && rows_aligned(16 / (int)es) && D * es % 16 == 0 ? 1 : 0;
-  return pa::launch_qk_norm_rope_append(p, num_sms(), static_cast<cudaStream_t>(stream)) == cudaSuccess ? PA_OK
-                                                                                                       : PA_ERR_CUDA;
+  return launched(pa::launch_qk_norm_rope_append(p, num_sms(), static_cast<cudaStream_t>(stream)));
 }
 
 namespace {
@@ -851,7 +873,8 @@ pa_status paged_kv_copy_pages(const pa_kv_pool* pools, int32_t num_pools, const 
   const int vec = pools_vec(pools, num_pools, p.page_bytes);
   for (int32_t i = 0; i < num_pools; i += pa::kMaxPoolsPerLaunch) {
     fill_pools(&p.pools, pools, i, num_pools);
-    if (pa::launch_copy_pages(p, vec, static_cast<cudaStream_t>(stream)) != cudaSuccess) return PA_ERR_CUDA;
+    const pa_status launch = launched(pa::launch_copy_pages(p, vec, static_cast<cudaStream_t>(stream)));
+    if (launch != PA_OK) return launch;
   }
   return PA_OK;
 }
@@ -895,7 +918,8 @@ pa_status paged_kv_compact(const pa_kv_pool* pools, int32_t num_pools, const int
   const int vec = pools_vec(pools, num_pools, p.row_bytes);
   for (int32_t i = 0; i < num_pools; i += pa::kMaxPoolsPerLaunch) {
     fill_pools(&p.pools, pools, i, num_pools);
-    if (pa::launch_compact(p, vec, num_sms(), static_cast<cudaStream_t>(stream)) != cudaSuccess) return PA_ERR_CUDA;
+    const pa_status launch = launched(pa::launch_compact(p, vec, num_sms(), static_cast<cudaStream_t>(stream)));
+    if (launch != PA_OK) return launch;
     p.new_seq_lens = nullptr;  // written by the first launch
   }
   return PA_OK;

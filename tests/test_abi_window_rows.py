@@ -37,21 +37,24 @@ def test_decode_window_validation(L):
     assert call(out=FAKE) == capi.PA_ERR_SHAPE
     assert call(msl=65) == capi.PA_ERR_SHAPE
     assert call(pool=_pool(d=96)) == capi.PA_ERR_UNSUPPORTED
+    assert call(out=ctypes.c_void_p(0x8000004)) == capi.PA_ERR_ALIGN
     assert call(ws=None, wsb=0) == capi.PA_ERR_WORKSPACE
     assert L.paged_attention_decode_window(None, FAKE, OUT, 2, 32, FAKE, 4, FAKE, 64, 0.1, 8, 0, FAKE, 1, None) \
         == capi.PA_ERR_NULL
 
 
 def test_prefill_window_validation(L):
-    def call(window=10, sinks=4, total=10, mql=5, q=FAKE):
-        p = _pool()
-        return L.paged_attention_prefill_window(ctypes.byref(p), q, OUT, 2, 32, FAKE, total, mql, FAKE, 4, FAKE, 64,
+    def call(window=10, sinks=4, total=10, mql=5, q=FAKE, out=OUT, p=_pool()):
+        return L.paged_attention_prefill_window(ctypes.byref(p), q, out, 2, 32, FAKE, total, mql, FAKE, 4, FAKE, 64,
                                                 0.1, window, sinks, None)
     assert call(window=0) == capi.PA_ERR_SHAPE
     assert call(sinks=-1) == capi.PA_ERR_SHAPE
     assert call(total=0) == capi.PA_OK
     assert call(mql=0) == capi.PA_ERR_SHAPE
     assert call(q=None) == capi.PA_ERR_NULL
+    assert call(q=ctypes.c_void_p(0x40008)) == capi.PA_ERR_ALIGN
+    assert call(out=ctypes.c_void_p(0x8000008)) == capi.PA_ERR_ALIGN
+    assert call(p=_pool(P=1 << 27)) == capi.PA_ERR_RANGE             # 2^31 slots
 
 
 def test_norm_rope_append_validation(L):
@@ -85,7 +88,9 @@ def test_norm_rope_append_validation(L):
     assert call(out=ctypes.c_void_p(0x40010)) == capi.PA_ERR_SHAPE
     assert call(out=ctypes.c_void_p(0x40000 - 16)) == capi.PA_ERR_SHAPE
     assert call(out=FAKE, qs=6144) == capi.PA_ERR_SHAPE             # strided q cannot be written in place
+    assert call(out=ctypes.c_void_p(0x40000), q=ctypes.c_void_p(0x90000)) == capi.PA_ERR_SHAPE    # over key and value
     assert call(T=1 << 32) == capi.PA_ERR_RANGE
+    assert call(vstr=1 << 40) == capi.PA_ERR_RANGE
     assert call(pool=_pool(dtype=capi.PA_DTYPE_FP8_E4M3, ks=0.0)) == capi.PA_ERR_RANGE
 
 

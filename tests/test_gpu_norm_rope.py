@@ -239,6 +239,13 @@ def test_bad_slots_and_positions_are_recorded_and_skipped(cuda_device):
         assert torch.equal(t["kp"].view(-1, 2, 64)[s["slots"][3]], s["kp"].view(-1, 2, 64)[s["slots"][3]])
 
 
+def test_no_tokens(cuda_device):
+    s = _inputs(cuda_device, 1, 4, 2, 64, "bf16")
+    for k in ("q", "k", "v", "slots", "pos"):
+        s[k] = s[k][:0]
+    assert _call(s).shape == (0, 4, 64)
+
+
 def test_captured_and_replayed(cuda_device):
     s = _inputs(cuda_device, 12, 8, 2, 128, "bf16", seed=10)
     eager = _call(s)

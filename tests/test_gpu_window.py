@@ -64,6 +64,13 @@ def test_decode_infinities_in_hidden_slots(cuda_device):
     _decode(LENS, 40, 3, seed=6, ps=8, poison=-float("inf")).check(capi, cuda_device)
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "e4m3", "f32"])
+@pytest.mark.parametrize("scale", [0.0, -0.2, 1.5])
+def test_scales(cuda_device, dtype, scale):
+    _decode([0, 1, 40, 333, 77, 600], 90, 5, hq=6, hkv=2, dtype=dtype, seed=31, scale=scale).check(capi, cuda_device)
+    Case([60, 1, 30], [300, 0, 70], 90, 5, hq=6, hkv=2, dtype=dtype, seed=32, scale=scale).check(capi, cuda_device)
+
+
 def test_decode_a_wide_window_is_the_plain_call(cuda_device):
     c = _decode([1, 50, 400], 400, 0, seed=2)
     out = c.run(capi, cuda_device)
