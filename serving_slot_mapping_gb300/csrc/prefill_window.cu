@@ -256,7 +256,10 @@ __global__ void __launch_bounds__(WCfg<D, KV8>::kThreads, 1)
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
-  const float sl2 = p.scale_log2;
+  // A scale below 0 is taken by the queries (negated as they are staged), a scale
+  // of 0 too (zeros): the softmax then always has a positive one, and takes the max
+  // over raw S and one fused multiply-add per exponential.
+  const float sl2 = p.scale_log2 == 0.f ? 1.f : fabsf(p.scale_log2);
   griddep_launch_dependents();
   // inconsistent inputs are recorded once, whatever items there are
   for (int b = blockIdx.x * C::kThreads + tid; b < p.batch; b += gridDim.x * C::kThreads) {
@@ -600,6 +603,16 @@ __global__ void __launch_bounds__(WCfg<D, KV8>::kThreads, 1)
           *x = make_uint4(bf16x2_to_f16x2(v.x), bf16x2_to_f16x2(v.y), bf16x2_to_f16x2(v.z), bf16x2_to_f16x2(v.w));
         }
       }
+      if (p.scale_log2 <= 0.f) {
+        __syncwarp();
+#pragma unroll 1
+        for (int c = 0; c < D / 8; ++c) {
+          uint4* x = reinterpret_cast<uint4*>(q_chunk(r, c));
+          const uint32_t keep = p.scale_log2 < 0.f ? 0xFFFFFFFFu : 0u, flip = p.scale_log2 < 0.f ? 0x80008000u : 0u;
+          const uint4 v = *x;
+          *x = make_uint4((v.x & keep) ^ flip, (v.y & keep) ^ flip, (v.z & keep) ^ flip, (v.w & keep) ^ flip);
+        }
+      }
       fence_proxy_async_smem();
       mbar_arrive(bar(W_QFULL + t));
     };
@@ -612,7 +625,6 @@ __global__ void __launch_bounds__(WCfg<D, KV8>::kThreads, 1)
       publish_q();
     }
     uint32_t sn = 0, on = 0;  // S tiles and finished O's awaited so far
-    const bool up = sl2 > 0.f;  // the usual scale: the max is taken over raw S and exp2 takes one fused multiply-add
     while (have) {
       it = nx;
       const int ntt = tiles_of(it);
@@ -644,12 +656,6 @@ __global__ void __launch_bounds__(WCfg<D, KV8>::kThreads, 1)
 #pragma unroll
         for (int i = 0; i < 4; ++i) tmem_ld32(s_col + i * 32, v[i]);
         tmem_wait_ld();
-        if (!up) {
-#pragma unroll
-          for (int i = 0; i < 4; ++i)
-#pragma unroll
-            for (int e = 0; e < 32; ++e) v[i][e] = __float_as_uint(__uint_as_float(v[i][e]) * sl2);
-        }
         if (masked) {
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
@@ -668,7 +674,7 @@ __global__ void __launch_bounds__(WCfg<D, KV8>::kThreads, 1)
           mx[i] = fmaxf(mx[i], __uint_as_float(v[i][31]));
         }
         float tmax = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
-        if (up) tmax *= sl2;
+        tmax *= sl2;
         // reference max: moved only when the row max grows by more than 2^8
         float alpha = 1.f;
         bool rescale = false;
@@ -680,7 +686,7 @@ __global__ void __launch_bounds__(WCfg<D, KV8>::kThreads, 1)
         }
         const float mbase = m_ref == -INFINITY ? 0.f : m_ref;
         // P = exp2(x - m) as bf16 (f16) pairs, written over the S columns
-        const uint64_t mul = up ? pair(sl2, sl2) : pair(1.f, 1.f), sub = pair(-mbase, -mbase);
+        const uint64_t mul = pair(sl2, sl2), sub = pair(-mbase, -mbase);
         uint64_t rs[4] = {0ull, 0ull, 0ull, 0ull};
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
