@@ -416,7 +416,7 @@ pa_status decode_impl(const pa_kv_pool* pool, const void* q, void* out, int32_t 
     if ((int64_t)batch * pool->num_kv_heads > INT32_MAX / 8) return PA_ERR_RANGE;  // grid x, 8 CTAs each at most
     const int csize = pa::decode_window_cluster(num_sms(), batch, pool->num_kv_heads, p.group,
                                                 std::min<int64_t>(max_seq_len, (int64_t)win.size + win.sinks));
-    return launched(pa::launch_decode_window(p, csize, s));
+    return launched(pa::launch_decode_window(p, num_sms(), csize, s));
   }
   return pa::launch_decode_bf16(p, s) == cudaSuccess ? PA_OK : PA_ERR_CUDA;
 }

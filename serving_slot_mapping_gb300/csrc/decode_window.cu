@@ -59,13 +59,20 @@ __device__ __forceinline__ uint32_t code_chunk(int row, int chunk) {
   return D == 128 ? row * 128 + ((chunk ^ (row & 7)) << 4) : row * 64 + ((chunk ^ ((row >> 1) & 3)) << 4);
 }
 
-// CTAs of an SM that the ring of a team is sized for: 125 registers a thread
+// CTAs of an SM that the ring of a team is sized for: 128 registers a thread
 // leave room for three of 160 threads (up to 8 query heads per KV head), 168 for
 // two of 160 (16) or one of 288 (32).
 __host__ __device__ constexpr int ctas_per_sm(int heads) { return heads <= 8 ? 3 : (heads <= 16 ? 2 : 1); }
 
-// RT: warps per team, each with NT tiles of 8 query heads of the group.
-template <int D, bool KV8, int RT, int NT>
+// Up to 8 heads: with up to 4 CTAs for each SM, a ring half as long again and two
+// CTAs an SM (32 sequences, 8 KV heads, a window of 1024: 23.4 against 27.4 us out
+// of HBM; 64 sequences: 43.4 against 49.6 us); with more, the third CTA hides
+// more than the ring (256 sequences, a window of 128: 38.3 against 42.8 us).
+bool deep_rings(int num_sms, int64_t ctas) { return ctas <= 4 * (int64_t)num_sms; }
+
+// RT: warps per team, each with NT tiles of 8 query heads of the group; DEEP: see
+// deep_rings.
+template <int D, bool KV8, int RT, int NT, bool DEEP>
 struct DCfg {
   static constexpr int kConsumers = kTeams * RT;           // warps
   static constexpr int kThreads = 32 * (kConsumers + 1);   // + the producer warp
@@ -75,7 +82,7 @@ struct DCfg {
   static constexpr int kTensorBytes = kSlabs * kSlabBytes;  // K or V of one block
   static constexpr int kBlockBytes = 2 * kTensorBytes;
   static constexpr int kHeads = 8 * NT * RT;
-  static constexpr int kPerSm = ctas_per_sm(kHeads);
+  static constexpr int kPerSm = DEEP ? 2 : ctas_per_sm(kHeads);
   static constexpr int kTeamRing = (kPerSm == 3 ? 16 : (kPerSm == 2 ? 24 : 40)) * 1024;
   static constexpr int kStages = kTeamRing / kBlockBytes;
   static constexpr int kRing = kTeams * kStages * kBlockBytes;
@@ -98,11 +105,11 @@ __device__ __forceinline__ uint32_t transpose8(uint32_t x) {
   return d;
 }
 
-template <int D, bool KV8, int RT, int NT>
-__global__ void __launch_bounds__(DCfg<D, KV8, RT, NT>::kThreads, DCfg<D, KV8, RT, NT>::kPerSm)
+template <int D, bool KV8, int RT, int NT, bool DEEP>
+__global__ void __launch_bounds__(DCfg<D, KV8, RT, NT, DEEP>::kThreads, DCfg<D, KV8, RT, NT, DEEP>::kPerSm)
     decode_window_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_constant__ CUtensorMap tmap_v,
                           const __grid_constant__ DecodeParams p, int csize) {
-  using C = DCfg<D, KV8, RT, NT>;
+  using C = DCfg<D, KV8, RT, NT, DEEP>;
   constexpr int S = C::kStages;
   extern __shared__ unsigned char smem_raw[];
   unsigned char* smem = reinterpret_cast<unsigned char*>(
@@ -492,11 +499,11 @@ __global__ void __launch_bounds__(DCfg<D, KV8, RT, NT>::kThreads, DCfg<D, KV8, R
   }
 }
 
-template <int D, bool KV8, int RT, int NT>
+template <int D, bool KV8, int RT, int NT, bool DEEP>
 cudaError_t launch_window(const DecodeParams& p, const CUtensorMap& tk, const CUtensorMap& tv, int csize,
                            cudaStream_t s) {
-  using C = DCfg<D, KV8, RT, NT>;
-  auto kern = decode_window_kernel<D, KV8, RT, NT>;
+  using C = DCfg<D, KV8, RT, NT, DEEP>;
+  auto kern = decode_window_kernel<D, KV8, RT, NT, DEEP>;
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
   if (e != cudaSuccess) return e;
   const unsigned grid = (unsigned)((int64_t)p.batch * p.pool.num_kv_heads * csize);
@@ -504,11 +511,14 @@ cudaError_t launch_window(const DecodeParams& p, const CUtensorMap& tk, const CU
 }
 
 template <int D, bool KV8>
-cudaError_t launch_group(const DecodeParams& p, const CUtensorMap& tk, const CUtensorMap& tv, int csize,
-                              cudaStream_t s) {
-  if (p.group <= 8) return launch_window<D, KV8, 1, 1>(p, tk, tv, csize, s);
-  return p.group <= 16 ? launch_window<D, KV8, 1, 2>(p, tk, tv, csize, s)
-                       : launch_window<D, KV8, 2, 2>(p, tk, tv, csize, s);
+cudaError_t launch_group(const DecodeParams& p, const CUtensorMap& tk, const CUtensorMap& tv, int num_sms, int csize,
+                         cudaStream_t s) {
+  if (p.group <= 8)
+    return deep_rings(num_sms, (int64_t)p.batch * p.pool.num_kv_heads * csize)
+               ? launch_window<D, KV8, 1, 1, true>(p, tk, tv, csize, s)
+               : launch_window<D, KV8, 1, 1, false>(p, tk, tv, csize, s);
+  return p.group <= 16 ? launch_window<D, KV8, 1, 2, false>(p, tk, tv, csize, s)
+                       : launch_window<D, KV8, 2, 2, false>(p, tk, tv, csize, s);
 }
 
 }  // namespace
@@ -526,7 +536,7 @@ int decode_window_cluster(int num_sms, int32_t batch, int32_t num_kv_heads, int3
   return c;
 }
 
-cudaError_t launch_decode_window(const DecodeParams& p, int csize, cudaStream_t s) {
+cudaError_t launch_decode_window(const DecodeParams& p, int num_sms, int csize, cudaStream_t s) {
   const int D = p.pool.head_dim;
   const int R = p.pool.page_size < 16 ? p.pool.page_size : 16;
   const int64_t rows = p.pool.num_pages * (int64_t)p.pool.page_size;
@@ -535,13 +545,13 @@ cudaError_t launch_decode_window(const DecodeParams& p, int csize, cudaStream_t 
     if (!encode_pool_tmap_u8(&tk, p.pool.key_pool, rows, p.pool.num_kv_heads, D, R, 1, true) ||
         !encode_pool_tmap_u8(&tv, p.pool.value_pool, rows, p.pool.num_kv_heads, D, R, 1, true))
       return cudaErrorInvalidValue;
-    return D == 128 ? launch_group<128, true>(p, tk, tv, csize, s) : launch_group<64, true>(p, tk, tv, csize, s);
+    return D == 128 ? launch_group<128, true>(p, tk, tv, num_sms, csize, s) : launch_group<64, true>(p, tk, tv, num_sms, csize, s);
   }
   const int slabs = R == 16 ? D / 64 : 1;
   if (!encode_pool_tmap(&tk, p.pool.key_pool, rows, p.pool.num_kv_heads, D, R, 1, slabs) ||
       !encode_pool_tmap(&tv, p.pool.value_pool, rows, p.pool.num_kv_heads, D, R, 1, slabs))
     return cudaErrorInvalidValue;
-  return D == 128 ? launch_group<128, false>(p, tk, tv, csize, s) : launch_group<64, false>(p, tk, tv, csize, s);
+  return D == 128 ? launch_group<128, false>(p, tk, tv, num_sms, csize, s) : launch_group<64, false>(p, tk, tv, num_sms, csize, s);
 }
 
 }  // namespace pa

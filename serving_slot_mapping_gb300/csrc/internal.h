@@ -196,7 +196,7 @@ cudaError_t launch_decode_cascade_bf16(const DecodeParams& p, cudaStream_t s, cu
 // (sequence, KV head), decode_window_cluster's choice for sequences of at most
 // max_keys visible keys.
 int decode_window_cluster(int num_sms, int32_t batch, int32_t num_kv_heads, int32_t group, int64_t max_keys);
-cudaError_t launch_decode_window(const DecodeParams& p, int csize, cudaStream_t s);
+cudaError_t launch_decode_window(const DecodeParams& p, int num_sms, int csize, cudaStream_t s);
 // Dynamic shared memory the bf16 decode split kernel needs.
 // (size_t)-1 when no stage ring of >= 2 stages fits the budget.
 size_t decode_smem_bytes(int head_dim, int group, int batch, int heads_per_box, int budget, bool kv8);

@@ -53,8 +53,10 @@ def test_decode_core_path(cuda_device, ps, dtype):
 @pytest.mark.parametrize("dtype", ["bf16", "e4m3"])
 def test_decode_many_short_and_few_long(cuda_device, dtype):
     rng = np.random.default_rng(3)
-    # 300 sequences: more segments than CTAs; 3 long ones: each cut over many CTAs (the weighted cut)
+    # hundreds of sequences, one CTA each; 3 long ones: clusters of 8
     _decode(rng.integers(0, 400, 300), 64, 4, hq=8, hkv=2, d=64, dtype=dtype, seed=9).check(capi, cuda_device)
+    # over 608 CTAs: three of them an SM, with shorter rings
+    _decode(rng.integers(0, 300, 420), 100, 4, hq=8, hkv=2, d=128, dtype=dtype, seed=12).check(capi, cuda_device)
     _decode([5000, 4000, 3], 2500, 20, hq=32, hkv=8, d=128, dtype=dtype, seed=10).check(capi, cuda_device)
     _decode([5000, 4000, 3], 2500, 20, hq=32, hkv=1, d=128, dtype=dtype, seed=11).check(capi, cuda_device)
 
