@@ -448,6 +448,19 @@ def _here(names, tensors) -> int:
     return cur
 
 
+_POOL_CODES = {torch.float32: PA_DTYPE_F32, torch.bfloat16: PA_DTYPE_BF16, torch.float8_e4m3fn: PA_DTYPE_FP8_E4M3}
+
+
+def _pool_of(key_pool, value_pool, k_scale, v_scale) -> PaKvPool:
+    """make_pool, with its checks in one expression (make_pool says what is wrong)."""
+    shape, dtype = key_pool.shape, key_pool.dtype
+    if (len(shape) != 4 or dtype not in _POOL_CODES or value_pool.dtype != dtype or value_pool.shape != shape
+            or not key_pool.is_contiguous() or not value_pool.is_contiguous()):
+        return make_pool(key_pool, value_pool, k_scale, v_scale)
+    P, ps, hkv, d = shape
+    return PaKvPool(key_pool.data_ptr(), value_pool.data_ptr(), P, ps, hkv, d, _POOL_CODES[dtype], k_scale, v_scale)
+
+
 def _addr(t: Optional[torch.Tensor]):
     return None if t is None else t.data_ptr()
 
@@ -487,7 +500,7 @@ def paged_attention_decode_window(key_pool, value_pool, q, block_table, seq_lens
     Arguments otherwise as for :func:`paged_attention_decode`; entries of
     ``block_table`` whose pages hold no visible key are never read (those pages
     may be freed)."""
-    pool = make_pool(key_pool, value_pool, k_scale, v_scale)
+    pool = _pool_of(key_pool, value_pool, k_scale, v_scale)
     _int32(block_table, "block_table")
     _int32(seq_lens, "seq_lens")
     made = out is None
@@ -510,7 +523,8 @@ def paged_attention_decode_window(key_pool, value_pool, q, block_table, seq_lens
                                              block_table.data_ptr(), mb, seq_lens.data_ptr(), int(max_seq_len),
                                              float(scale), int(window), int(num_sinks), _addr(workspace), wbytes,
                                              _raw_stream(stream, dev))
-    _check(st, "paged_attention_decode_window")
+    if st != PA_OK:
+        raise PagedAttnError(st, "paged_attention_decode_window")
     return out
 
 
@@ -522,7 +536,7 @@ def paged_attention_prefill_window(key_pool, value_pool, q, query_start_loc, blo
     or ``j < num_sinks``.  Arguments otherwise as for
     :func:`paged_attention_prefill`; pages without a key that some row of the
     sequence attends to are never read."""
-    pool = make_pool(key_pool, value_pool, k_scale, v_scale)
+    pool = _pool_of(key_pool, value_pool, k_scale, v_scale)
     _int32(query_start_loc, "query_start_loc")
     _int32(block_table, "block_table")
     _int32(seq_lens, "seq_lens")
@@ -543,7 +557,8 @@ def paged_attention_prefill_window(key_pool, value_pool, q, query_start_loc, blo
                                               query_start_loc.data_ptr(), T, int(max_q_len), block_table.data_ptr(),
                                               mb, seq_lens.data_ptr(), int(max_seq_len), float(scale), int(window),
                                               int(num_sinks), _raw_stream(stream, dev))
-    _check(st, "paged_attention_prefill_window")
+    if st != PA_OK:
+        raise PagedAttnError(st, "paged_attention_prefill_window")
     return out
 
 
@@ -575,11 +590,11 @@ def paged_qk_norm_rope_append(key_pool, value_pool, q, key, value, slot_mapping,
     a padding token (its position may be anything, nothing of it is written).  Returns the rotated
     queries ``[T, Hq, D]`` (``out``, which may be ``q`` itself when contiguous);
     the pools are updated in place."""
-    pool = make_pool(key_pool, value_pool, k_scale, v_scale)
+    pool = _pool_of(key_pool, value_pool, k_scale, v_scale)
     if q.dim() != 3:
         raise ValueError("q must be [T, num_q_heads, head_dim]")
     T, hq, d = q.shape
-    row_dtype = torch.bfloat16 if key_pool.dtype == torch.float8_e4m3fn else key_pool.dtype
+    row_dtype = torch.float32 if pool.dtype == PA_DTYPE_F32 else torch.bfloat16
     sq = _token_rows(q, "q", T, hq, pool.head_dim, row_dtype)
     sk = _token_rows(key, "key", T, pool.num_kv_heads, pool.head_dim, row_dtype)
     sv = _token_rows(value, "value", T, pool.num_kv_heads, pool.head_dim, row_dtype)
@@ -619,7 +634,8 @@ def paged_qk_norm_rope_append(key_pool, value_pool, q, key, value, slot_mapping,
                                          out.data_ptr(), hq, _addr(q_weight), _addr(k_weight), float(eps),
                                          _addr(positions), _addr(cos_sin), max_pos, rot, 1 if interleaved else 0,
                                          slot_mapping.data_ptr(), T, _raw_stream(stream, dev))
-    _check(st, "paged_qk_norm_rope_append")
+    if st != PA_OK:
+        raise PagedAttnError(st, "paged_qk_norm_rope_append")
     return out
 
 
@@ -662,7 +678,8 @@ def paged_kv_copy_pages(pools, src_pages, dst_pages, stream=None):
     dev = _here("key_pool src_pages dst_pages", (ps.tensors[0][0] if ps.count else None, src_pages, dst_pages))
     st = lib().paged_kv_copy_pages(ps.array, ps.count, src_pages.data_ptr(), dst_pages.data_ptr(), n,
                                    _raw_stream(stream, dev))
-    _check(st, "paged_kv_copy_pages")
+    if st != PA_OK:
+        raise PagedAttnError(st, "paged_kv_copy_pages")
 
 
 def paged_kv_compact(pools, block_table, seq_lens, keep_indptr, keep, base=None, new_seq_lens=None, stream=None):
@@ -692,5 +709,6 @@ def paged_kv_compact(pools, block_table, seq_lens, keep_indptr, keep, base=None,
     st = lib().paged_kv_compact(ps.array, ps.count, block_table.data_ptr(), block_table.shape[1], seq_lens.data_ptr(), B,
                                 _addr(base), keep_indptr.data_ptr(), keep.data_ptr(), keep.numel(),
                                 new_seq_lens.data_ptr(), _raw_stream(stream, dev))
-    _check(st, "paged_kv_compact")
+    if st != PA_OK:
+        raise PagedAttnError(st, "paged_kv_compact")
     return new_seq_lens
