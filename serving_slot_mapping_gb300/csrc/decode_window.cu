@@ -299,7 +299,8 @@ __global__ void __launch_bounds__(DCfg<D, KV8, RT, NT, DEEP>::kThreads, DCfg<D, 
     // S^T = K Q^T: keys are the rows of the product and query heads its 8 columns
     // a tile, so a group of up to 8 heads costs one tile (heads as the 16 rows
     // would leave most of them empty).  All K fragments are loaded before the
-    // first product, all V fragments before the softmax.
+    // first product; V's as they are used (loaded before the softmax their
+    // registers cost more than the wait: MQA, 256 x 4096 keys 107 against 120 us).
     float s[NT][4];
     uint32_t f[kFrags][4];
 #pragma unroll
@@ -324,9 +325,6 @@ __global__ void __launch_bounds__(DCfg<D, KV8, RT, NT, DEEP>::kThreads, DCfg<D, 
 #pragma unroll
       for (int e = 0; e < 4; ++e) s[n][e] = up ? s0[e] + s1[e] : (s0[e] + s1[e]) * sl2;
     }
-#pragma unroll
-    for (int x = 0; x < kFrags; ++x)
-      ldmatrix_x4_trans(vbase + voff[x % kOffs] + (x / kOffs) * C::kSlabBytes, f[x][0], f[x][1], f[x][2], f[x][3]);
     if (edge) {
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
@@ -379,6 +377,7 @@ __global__ void __launch_bounds__(DCfg<D, KV8, RT, NT, DEEP>::kThreads, DCfg<D, 
     }
 #pragma unroll
     for (int x = 0; x < kFrags; ++x) {
+      ldmatrix_x4_trans(vbase + voff[x % kOffs] + (x / kOffs) * C::kSlabBytes, f[x][0], f[x][1], f[x][2], f[x][3]);
       if (KV8) {
         // codes of keys 2c, 2c + 1 and dims 2j, 2j + 1 (j = lane / 4), regrouped by dim:
         // the even dims of the chunk are the tile's rows 0 - 7, the odd ones 8 - 15
