@@ -524,9 +524,9 @@ cudaError_t launch_group(const DecodeParams& p, const CUtensorMap& tk, const CUt
 
 // As many CTAs a (sequence, KV head) as are resident at once, and each with a
 // block at least for every team: a cluster whose CTAs wait for a second wave
-// loses more than the shorter parts gain (64 segments of 1024 keys: 13.2, 9.2,
-// 6.8 and 10.6 us on clusters of 1, 2, 4 and 8; 256 segments: 23.8, 30.9, 33.2,
-// 45.8 us).
+// loses more than the shorter parts gain (1024 keys, on clusters of 1, 2, 4 and
+// 8 CTAs: 32 sequences of 2 KV heads of 64 dims 12.9, 9.2, 6.8 and 10.6 us; of 8
+// heads of 128 dims 23.8, 30.9, 33.2 and 45.8 us).
 int decode_window_cluster(int num_sms, int32_t batch, int32_t num_kv_heads, int32_t group, int64_t max_keys) {
   const int64_t segments = (int64_t)batch * num_kv_heads, slots = (int64_t)num_sms * ctas_per_sm(group);
   const int64_t blocks = (max_keys + 15) / 16;

@@ -10,9 +10,9 @@
 // converter warps for e4m3 pools) -- with what short key ranges ask for:
 // * The grid is persistent, one CTA per SM, and walks items w = blockIdx.x,
 //   + gridDim.x, ... (KV head fastest, then 256-row tiles, then sequences).
-//   A window of 1024 keys leaves an item ~10 key tiles of 1.9 us, and a CTA that
-//   starts, loads its first tiles and writes its rows alone takes 11 us beside
-//   them.  Here the TMA warp runs ahead into the next item's keys, the query
+//   A window of 1024 keys leaves an item ~10 key tiles; with a CTA for each item,
+//   as the plain kernel has it, its start, first loads and last writes took 11 us
+//   beside tiles of 1.9 us.  Here the TMA warp runs ahead into the next item's keys, the query
 //   rows of the next item are copied in while the last key tile's softmax runs,
 //   and its first S is multiplied while this item's rows are written.
 // * Keys are staged as a list of page boxes, not as aligned tiles: the sinks'
