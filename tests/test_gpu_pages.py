@@ -189,3 +189,27 @@ def test_compact_captured_and_replayed(cuda_device):
     for x, y in zip(a, b):
         assert all(np.array_equal(_bytes(s), _bytes(t)) for s, t in zip(x, y))
     assert new.tolist() == np.diff(ptr).tolist()
+
+
+def test_copy_captured_and_replayed(cuda_device):
+    pairs = [tuple(torch.randn(12, 16, 2, 64, device=cuda_device).to(torch.bfloat16) for _ in range(2)) for _ in range(3)]
+    pools = capi.make_pools(pairs)
+    src = torch.tensor([0, 1, 2], dtype=torch.int32, device=cuda_device)
+    dst = torch.tensor([6, 7, -1], dtype=torch.int32, device=cuda_device)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        capi.paged_kv_copy_pages(pools, src, dst)
+    for s, d in (([0, 1, 2], [6, 7, -1]), ([3, 4, 5], [9, -1, 11])):   # the same graph serves other pairs
+        before = [[x.clone() for x in p] for p in pairs]
+        src.copy_(torch.tensor(s, dtype=torch.int32))
+        dst.copy_(torch.tensor(d, dtype=torch.int32))
+        graph.replay()
+        torch.cuda.synchronize()
+        for p, old in zip(pairs, before):
+            for x, o in zip(p, old):
+                want = o.clone()
+                for a, b in zip(s, d):
+                    if b >= 0:
+                        want[b] = o[a]
+                assert torch.equal(x.view(torch.int16), want.view(torch.int16))
+    assert capi.device_error() == (0, 0)

@@ -231,3 +231,82 @@ def test_on_a_stream_of_its_own_without_buffers(cuda_device):
     torch.cuda.synchronize()
     for out in outs:
         assert (np.abs(out.float().cpu().numpy().astype(np.float64) - y) <= tol).all()
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "e4m3"])
+@pytest.mark.parametrize("bad", [1 << 29, -7])
+def test_prefill_bad_pages_are_recorded(cuda_device, dtype, bad):
+    def case():
+        return Case([60, 300, 20], [0, 200, 5], 70, 4, dtype=dtype, seed=41)
+
+    good = case().check(capi, cuda_device)
+    c = case()
+    c.table[1, 0] = bad                           # a sink's page of the middle sequence
+    out = c.run(capi, cuda_device)
+    torch.cuda.synchronize()
+    assert capi.device_error() == (1, bad)
+    # the sequences beside it are what they were, and so is the next call
+    assert torch.equal(out[:60].view(torch.int16), good[:60].view(torch.int16))
+    assert torch.equal(out[360:].view(torch.int16), good[360:].view(torch.int16))
+    again = case().check(capi, cuda_device)
+    assert torch.equal(again.view(torch.int16), good.view(torch.int16))
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "e4m3"])
+@pytest.mark.parametrize("new,cached", [([130, 40, 300], [0, 900, 128]), ([20], [2000])])   # persistent grid; clusters
+def test_prefill_captured_and_replayed(cuda_device, dtype, new, cached):
+    c = Case(new, cached, 333, 7, hq=8, hkv=2, d=128, dtype=dtype, seed=42)
+    eager = c.check(capi, cuda_device)
+    dev = lambda a: torch.from_numpy(a).to(cuda_device)
+    kp, vp, q = c.args
+    qsl, table, lens, out = dev(c.qsl), dev(c.table), dev(c.lens), torch.zeros_like(q)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        capi.paged_attention_prefill_window(kp, vp, q, qsl, table, lens, c.scale, int(c.n.max()), 333, 7,
+                                            max_seq_len=int(c.lens.max()), out=out, k_scale=c.k_scale,
+                                            v_scale=c.v_scale)
+    for _ in range(3):
+        out.fill_(float("nan"))
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(out.view(torch.int16), eager.view(torch.int16))
+    # the same graph serves a batch whose last sequence has no rows
+    last = int(c.n[-1])
+    out.fill_(7.0)
+    qsl[-1] = qsl[-2]
+    graph.replay()
+    torch.cuda.synchronize()
+    rows = int(c.n[:-1].sum())
+    assert torch.equal(out[:rows].view(torch.int16), eager[:rows].view(torch.int16))
+    assert torch.all(out[rows:rows + last] == 7.0)
+    assert capi.device_error() == (0, 0)
+
+
+def test_two_calls_at_once(cuda_device):
+    """Decodes and prefills on two streams at a time, each with clusters or a grid
+    that fills the GPU, give what they give alone, bit for bit."""
+    cases = [_decode([3000, 2000, 5], 1500, 4, hq=32, hkv=8, d=128, seed=43),
+             Case([300, 40, 700], [200, 1000, 0], 200, 4, hq=16, hkv=4, d=128, seed=44)]
+    alone = [c.check(capi, cuda_device) for c in cases]
+    calls = []
+    for c in cases:
+        dev = lambda a: torch.from_numpy(a).to(cuda_device)
+        kp, vp, q = c.args
+        msl = int(c.lens.max())
+        if c.is_decode:
+            args = (kp, vp, q, dev(c.table), dev(c.lens), c.scale, c.window, c.sinks)
+            calls.append((capi.paged_attention_decode_window, args, dict(max_seq_len=msl)))
+        else:
+            args = (kp, vp, q, dev(c.qsl), dev(c.table), dev(c.lens), c.scale, int(c.n.max()), c.window, c.sinks)
+            calls.append((capi.paged_attention_prefill_window, args, dict(max_seq_len=msl)))
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    torch.cuda.synchronize()
+    outs = []
+    for i in range(20):
+        for k, st in enumerate(streams):
+            f, args, kw = calls[(k + i) % 2]
+            outs.append(((k + i) % 2, f(*args, stream=st, **kw)))
+    torch.cuda.synchronize()
+    assert capi.device_error() == (0, 0)
+    for k, out in outs:
+        assert torch.equal(out.view(torch.int16), alone[k].view(torch.int16))
