@@ -43,6 +43,12 @@ constexpr int kItems = 4;        // items whose geometry is in shared memory
 constexpr int kItemBytes = 52;
 constexpr int kWBars = 32;
 
+enum { W_QFULL = 0, W_KFULL = W_QFULL + kQT, W_KEMPTY = W_KFULL + kNSK, W_VFULL = W_KEMPTY + kNSK,
+       W_VEMPTY = W_VFULL + kNSV, W_SFULL = W_VEMPTY + kNSV, W_PFULL = W_SFULL + kQT, W_ODONE = W_PFULL + kQT,
+       W_VLAND = W_ODONE + kQT, W_KREADY = W_VLAND + 1, W_VREADY = W_KREADY + kNSK, W_IFULL = W_VREADY + kNSV,
+       W_IEMPTY = W_IFULL + kItems, W_COUNT = W_IEMPTY + kItems };
+static_assert(W_COUNT <= kWBars, "barrier slots");
+
 template <int D, bool KV8>
 struct WCfg : PCfg<D, KV8> {
   using Base = PCfg<D, KV8>;
@@ -57,19 +63,15 @@ struct WCfg : PCfg<D, KV8> {
   static constexpr int kMetaOff = Base::kPageOff + 8 * 32 * 4;
   static constexpr int kItemOff = kMetaOff + 8 * 16;
   static constexpr int kWBarOff = kItemOff + kItems * kItemBytes;
-  static constexpr int kWSmem = kWBarOff + kWBars * 8 + 16 + 1024;
+  static constexpr int kTmemOff = kWBarOff + kWBars * 8;  // the word that tcgen05.alloc writes, behind every barrier
+  static_assert(kTmemOff >= kWBarOff + 8 * W_COUNT, "the TMEM base lies on a barrier");
+  static constexpr int kWSmem = kTmemOff + 16 + 1024;
   // SPLIT, once the item's products are done: its rows of O, fp32, padded against
   // bank conflicts, and their (reference max, sum) over the K and V rings
   static constexpr int kPartRow = D + 4;
   static constexpr int kPartMl = kQT * kBM * kPartRow * 4;
   static_assert(kPartMl + kQT * kBM * 8 <= (kNSK + kNSV) * Base::kKVTile, "an item's rows fit over the rings");
 };
-
-enum { W_QFULL = 0, W_KFULL = W_QFULL + kQT, W_KEMPTY = W_KFULL + kNSK, W_VFULL = W_KEMPTY + kNSK,
-       W_VEMPTY = W_VFULL + kNSV, W_SFULL = W_VEMPTY + kNSV, W_PFULL = W_SFULL + kQT, W_ODONE = W_PFULL + kQT,
-       W_VLAND = W_ODONE + kQT, W_KREADY = W_VLAND + 1, W_VREADY = W_KREADY + kNSK, W_IFULL = W_VREADY + kNSV,
-       W_IEMPTY = W_IFULL + kItems, W_COUNT = W_IEMPTY + kItems };
-static_assert(W_COUNT <= kWBars, "barrier slots");
 
 // Sequence b's rows [qs, qs + n) of q; n = 0 where query_start_loc is inconsistent.
 __device__ __forceinline__ int seq_rows(const PrefillParams& p, int b, int* qs) {
@@ -222,7 +224,7 @@ __global__ void __launch_bounds__(WCfg<D, KV8>::kThreads, 1)
   const uint32_t v_base = smem_u32(smem + C::kVOff);
   const uint32_t bars = smem_u32(smem + C::kWBarOff);
   auto bar = [&](int i) { return bars + 8u * i; };
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + C::kWBarOff + kBarSlots * 8);
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + C::kTmemOff);
   int* slot_ring = reinterpret_cast<int*>(smem + C::kPageOff);  // [8 tiles][32 lanes] first slot of each box, -1: none
   volatile Item* item_ring = reinterpret_cast<volatile Item*>(smem + C::kItemOff);
   int4* meta = reinterpret_cast<int4*>(smem + C::kMetaOff);     // [8 tiles] {KV head, valid, hid0, hid1}
