@@ -17,7 +17,13 @@
 // * Per block S^T = K Q^T and O^T += V^T P^T with mma.sync m16n8k16 (keys, then
 //   dims, as the 16 rows, query heads as the 8 columns), online softmax in the
 //   log2 domain; e4m3 codes become f16 fragments in registers.
-// * Keys hidden by the window or past L_b are masked in S and zeroed in V.
+// * Keys hidden by the window or past L_b are masked in S and zeroed in V.  A
+//   block_table entry out of range is noted by the producer, and a CTA that met
+//   one computes its part again without the keys of such pages (skip_bad_pages).
+//   The loop itself knows nothing of them: a word that says which keys of a block
+//   are there, read for each block or for each 8, took 117 and 113.5 us for 256 MQA
+//   sequences with a window of 4096 (so: 110.6) and 40.3 and 40.8 us for 256
+//   sequences with a window of 128 (37.5; with no such check 107.2 and 37.2).
 // * End: teams merge in shared memory, then each CTA of the cluster finishes a
 //   slice of the G x D outputs over the c partial rows.
 #include <math.h>
@@ -105,6 +111,61 @@ __device__ __forceinline__ uint32_t transpose8(uint32_t x) {
   return d;
 }
 
+// The part of a CTA over the keys whose pages are in range, a warp a query head and
+// a key at a time: team 0's partial rows and (m, l), the other teams' empty.  An
+// error path, slow, which works out its blocks anew so that the loop before it holds
+// no register for it.
+template <int D, bool KV8, int HEADS, int ROW>
+__device__ __forceinline__ void skip_bad_pages(const DecodeParams& p, int csize, float* part, float2* part_ml) {
+  constexpr int E = D / 32;  // a lane's dims
+  const int lane = threadIdx.x & 31, ps = p.pool.page_size, G = p.group;
+  const int seg = blockIdx.x / csize, rank = blockIdx.x - seg * csize;
+  const int b = seg / p.pool.num_kv_heads, hk = seg - b * p.pool.num_kv_heads;
+  const int L = seq_keys(p.seq_lens, p.kv_indptr, p.kv_last_page_len, p.kv_len, b, ps, p.max_blocks * ps, nullptr);
+  const WinSpan win = win_span(p, L);
+  const int nblk = ((L + 15) >> 4) - win.gap, per = (nblk + csize - 1) / csize;
+  const int k0 = rank * per, k1 = min(nblk, k0 + per);
+  const int32_t* bt = p.block_table + page_list_start(p.kv_indptr, p.max_blocks, b);
+  for (int i = threadIdx.x; i < kTeams * HEADS * ROW; i += blockDim.x) part[i] = 0.f;
+  for (int i = threadIdx.x; i < kTeams * HEADS; i += blockDim.x) part_ml[i] = make_float2(-INFINITY, 0.f);
+  __syncthreads();
+  auto element = [&](const void* pool, int64_t at) {
+    if (KV8) {
+      const uint32_t f = e4m3x2_lo_to_f16x2(static_cast<const unsigned char*>(pool)[at]);
+      return __half2float(__ushort_as_half((unsigned short)(f & 0xFFFFu)));
+    }
+    return __bfloat162float(static_cast<const __nv_bfloat16*>(pool)[at]);
+  };
+  for (int head = threadIdx.x >> 5; head < G; head += blockDim.x >> 5) {
+    const __nv_bfloat16* q =
+        static_cast<const __nv_bfloat16*>(p.q) + ((int64_t)b * p.num_q_heads + (int64_t)hk * G + head) * D;
+    float qv[E], o[E] = {}, m = -INFINITY, l = 0.f;
+#pragma unroll
+    for (int e = 0; e < E; ++e) qv[e] = __bfloat162float(q[lane * E + e]) * p.scale_log2;
+#pragma unroll 1
+    for (int i = k0 * 16; i < k1 * 16; ++i) {
+      const int j = win_block(win, i >> 4) * 16 + (i & 15);
+      if (j >= L || (j >= p.num_sinks && j < win.start)) continue;
+      const int page = __ldg(bt + (j >> p.pool.page_shift));
+      if (page < 0 || page >= p.pool.num_pages) continue;
+      const int64_t at = (((int64_t)page * ps + (j & (ps - 1))) * p.pool.num_kv_heads + hk) * D + lane * E;
+      float s = 0.f;
+#pragma unroll
+      for (int e = 0; e < E; ++e) s = fmaf(qv[e], element(p.pool.key_pool, at + e), s);
+#pragma unroll
+      for (int x = 16; x > 0; x >>= 1) s += __shfl_xor_sync(0xffffffffu, s, x);
+      const float mn = fmaxf(m, s), a = fast_exp2(m - mn), w = fast_exp2(s - mn);
+      m = mn;
+      l = fmaf(l, a, w);
+#pragma unroll
+      for (int e = 0; e < E; ++e) o[e] = fmaf(o[e], a, w * element(p.pool.value_pool, at + e));
+    }
+#pragma unroll
+    for (int e = 0; e < E; ++e) part[head * ROW + lane * E + e] = o[e];
+    if (lane == 0) part_ml[head] = make_float2(m, l);
+  }
+}
+
 template <int D, bool KV8, int RT, int NT, bool DEEP>
 __global__ void __launch_bounds__(DCfg<D, KV8, RT, NT, DEEP>::kThreads, DCfg<D, KV8, RT, NT, DEEP>::kPerSm)
     decode_window_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_constant__ CUtensorMap tmap_v,
@@ -122,6 +183,8 @@ __global__ void __launch_bounds__(DCfg<D, KV8, RT, NT, DEEP>::kThreads, DCfg<D, 
   const uint32_t bars = smem_u32(smem + C::kBarOff);
   auto full_bar = [&](int team, int s) { return bars + 8u * (team * S + s); };
   auto empty_bar = [&](int team, int s) { return bars + 8u * ((kTeams + team) * S + s); };
+  __shared__ volatile int bad_page;  // one out of range was met
+  if (tid == 0) bad_page = 0;
   if (tid < kTeams * S) {
     mbar_init(bars + 8u * tid, 2);  // full: the lanes that issue K and V
     mbar_init(bars + 8u * (kTeams * S + tid), RT);  // empty: the team's warps
@@ -182,7 +245,10 @@ __global__ void __launch_bounds__(DCfg<D, KV8, RT, NT, DEEP>::kThreads, DCfg<D, 
           const int kk = kk0 + h * 8;
           if ((h == 1 && R == 16) || !half_used(kk)) continue;
           if (pages[h] < 0 || pages[h] >= p.pool.num_pages) {
-            if (T == 0) record_error(p.err, ERR_BLOCK_TABLE, pages[h]);
+            if (T == 0) {
+              record_error(p.err, ERR_BLOCK_TABLE, pages[h]);
+              bad_page = 1;
+            }
             continue;
           }
           rows[h] = pages[h] * ps + (kk & (ps - 1));
@@ -435,6 +501,10 @@ __global__ void __launch_bounds__(DCfg<D, KV8, RT, NT, DEEP>::kThreads, DCfg<D, 
       }
   }
   __syncthreads();
+  if (__builtin_expect(bad_page != 0, 0)) {
+    skip_bad_pages<D, KV8, C::kHeads, C::kRow>(p, csize, part, part_ml);
+    __syncthreads();
+  }
   const int items = G * (D / 4);  // float4s of the output
   __nv_bfloat16* out = static_cast<__nv_bfloat16*>(p.out) + ((int64_t)b * Hq + (int64_t)hk * G) * D;
   auto store = [&](int x, float4 acc, float den) {
