@@ -376,7 +376,10 @@ pa_status paged_attention_prefill(const pa_kv_pool* pool, const void* q, void* o
  * block_table   as for the plain calls, with one difference: an entry whose
  *               page holds no key that some query row of the sequence attends
  *               to is never read, so the pages between the sinks and the
- *               window may have been freed (any value, -1 included).
+ *               window may have been freed (any value, -1 included).  An
+ *               entry out of range elsewhere is recorded (code 1) and the keys
+ *               of its page take no part (slower; a row without a key left
+ *               gives 0).
  * Slots of read pages that no query row of the sequence attends to may hold
  * anything, NaN included.  Keys and values that a row of the sequence attends
  * to must be finite, as for the plain calls.

@@ -29,6 +29,10 @@
 // Boxes whose page holds no key that a row of the sequence sees are never looked
 // up; slots of loaded pages that no row of the sequence sees (between the sinks
 // and the sequence's first window key, or at and past L_b) are zeroed in V.
+// A block_table entry out of range is noted by the TMA warp; a CTA that met one
+// computes the rows of its items with such a page again at its end, without their
+// keys (redo_bad_items).  The loop knows nothing of them: masks told to the softmax by
+// tile took 12 % (8 chunks of 512-2048, window 1024: 220 against 196 us).
 #include <algorithm>
 #include <type_traits>
 
@@ -65,6 +69,7 @@ struct WCfg : PCfg<D, KV8> {
   static constexpr int kWBarOff = kItemOff + kItems * kItemBytes;
   static constexpr int kTmemOff = kWBarOff + kWBars * 8;  // the word that tcgen05.alloc writes, behind every barrier
   static_assert(kTmemOff >= kWBarOff + 8 * W_COUNT, "the TMEM base lies on a barrier");
+  static constexpr int kBadOff = kTmemOff + 8;  // a page out of range was met
   static constexpr int kWSmem = kTmemOff + 16 + 1024;
   // SPLIT, once the item's products are done: its rows of O, fp32, padded against
   // bank conflicts, and their (reference max, sum) over the K and V rings
@@ -203,6 +208,71 @@ __device__ __forceinline__ uint64_t add_pair(uint64_t a, uint64_t b) {
   return d;
 }
 
+// The items of this CTA (SPLIT: of its cluster) that have a page out of range in one
+// of their key tiles, once all their rows are written: each row anew over the keys
+// whose pages are in range, a warp a row and a key at a time.  An error path, slow.
+template <int D, bool KV8>
+__device__ __forceinline__ void redo_bad_items(const PrefillParams& p, int kpo, int csize) {
+  constexpr int E = D / 32;  // a lane's dims
+  const int lane = threadIdx.x & 31, warps = blockDim.x >> 5, ps = p.pool.page_size, G = p.group;
+  const int worker = (int)(blockIdx.x % csize) * warps + (threadIdx.x >> 5), workers = csize * warps;
+  auto element = [&](const void* pool, int64_t at) {
+    if (KV8) {
+      const uint32_t f = e4m3x2_lo_to_f16x2(static_cast<const unsigned char*>(pool)[at]);
+      return __half2float(__ushort_as_half((unsigned short)(f & 0xFFFFu)));
+    }
+    return __bfloat162float(static_cast<const __nv_bfloat16*>(pool)[at]);
+  };
+  Walker wk;
+  wk.start(p, csize);
+  Item x;
+  while (wk.next(p, kpo, csize, &x)) {
+    const int32_t* bt = p.block_table + page_list_start(p.kv_indptr, p.max_blocks, x.b);
+    auto in_range = [&](int key) {
+      const int page = __ldg(bt + (key >> p.pool.page_shift));
+      return page >= 0 && page < p.pool.num_pages;
+    };
+    const int rows = min(kQT * kBM, x.n * G - x.row0);
+    // its key tiles reach from the window of the first row to less than a tile past
+    // the last row's own key; the keys there are seen by later rows at least
+    const int lo = x.first + x.row0 / G, hi = x.first + (x.row0 + rows - 1) / G;
+    bool bad = false;
+    for (int m = lane; hi >= 0 && m * ps < min(x.L, hi + kBN); m += 32) {
+      const int key = m * ps;
+      if (key < p.num_sinks || key + ps > max(0, lo) - p.window + 1) bad |= !in_range(key);
+    }
+    if (!__any_sync(0xffffffffu, bad)) continue;
+#pragma unroll 1
+    for (int r = worker; r < rows; r += workers) {
+      const int R = x.row0 + r, tok = R / G, pos = x.first + tok;
+      const int64_t row = ((int64_t)(x.qs + tok) * p.num_q_heads + (int64_t)x.hk * G + (R - tok * G)) * D + lane * E;
+      float q[E], o[E] = {}, m = -INFINITY, l = 0.f;
+#pragma unroll
+      for (int e = 0; e < E; ++e) q[e] = __bfloat162float(static_cast<const __nv_bfloat16*>(p.q)[row + e]) * p.scale_log2;
+#pragma unroll 1
+      for (int j = 0; j <= pos; ++j) {
+        if (j >= p.num_sinks && j <= pos - p.window) j = pos - p.window + 1;
+        if (!in_range(j)) continue;
+        const int64_t page = __ldg(bt + (j >> p.pool.page_shift));
+        const int64_t at = ((page * ps + (j & (ps - 1))) * p.pool.num_kv_heads + x.hk) * D + lane * E;
+        float s = 0.f;
+#pragma unroll
+        for (int e = 0; e < E; ++e) s = fmaf(q[e], element(p.pool.key_pool, at + e), s);
+#pragma unroll
+        for (int i = 16; i > 0; i >>= 1) s += __shfl_xor_sync(0xffffffffu, s, i);
+        const float mn = fmaxf(m, s), a = fast_exp2(m - mn), w = fast_exp2(s - mn);
+        m = mn;
+        l = fmaf(l, a, w);
+#pragma unroll
+        for (int e = 0; e < E; ++e) o[e] = fmaf(o[e], a, w * element(p.pool.value_pool, at + e));
+      }
+      const float inv = l > 0.f ? p.v_scale / l : 0.f;
+#pragma unroll
+      for (int e = 0; e < E; ++e) static_cast<__nv_bfloat16*>(p.out)[row + e] = __float2bfloat16_rn(o[e] * inv);
+    }
+  }
+}
+
 // SPLIT: csize CTAs of a cluster share an item, and there are clusters for all
 // items (a CTA has one item at most); else csize is 1.
 template <int D, bool KV8, bool SPLIT>
@@ -229,7 +299,10 @@ __global__ void __launch_bounds__(WCfg<D, KV8>::kThreads, 1)
   volatile Item* item_ring = reinterpret_cast<volatile Item*>(smem + C::kItemOff);
   int4* meta = reinterpret_cast<int4*>(smem + C::kMetaOff);     // [8 tiles] {KV head, valid, hid0, hid1}
 
+  volatile int* bad_page = reinterpret_cast<volatile int*>(smem + C::kBadOff);
+
   if (tid == 0) {
+    *bad_page = 0;
     for (int t = 0; t < kQT; ++t) {
       mbar_init(bar(W_QFULL + t), kBM);
       mbar_init(bar(W_SFULL + t), 1);
@@ -371,10 +444,12 @@ __global__ void __launch_bounds__(WCfg<D, KV8>::kThreads, 1)
         const int key = box_key(j);
         int slot = -1;
         if (box_used(key)) {
-          if (raw < 0 || raw >= p.pool.num_pages)
+          if (raw < 0 || raw >= p.pool.num_pages) {
             record_error(p.err, ERR_BLOCK_TABLE, raw);
-          else
+            *bad_page = 1;
+          } else {
             slot = (int)(((int64_t)raw << pshift) + (key & (ps - 1)));
+          }
         }
         slot_ring[(kt & 7) * 32 + lane] = slot;
         if (lane == 0) {
@@ -808,6 +883,7 @@ __global__ void __launch_bounds__(WCfg<D, KV8>::kThreads, 1)
   __syncthreads();
   tc_fence_after();
   if (warp == kMmaWarp) tmem_dealloc(tmem, C::kTmemCols);
+  bool redo = *bad_page != 0;
   if constexpr (SPLIT) {
     // ======================= the cluster's parts joined =======================
     // o = v_scale sum_c 2^(m_c - M) o_c / sum_c 2^(m_c - M) l_c; each CTA a part of
@@ -861,8 +937,10 @@ __global__ void __launch_bounds__(WCfg<D, KV8>::kThreads, 1)
       else if (csize == 4) join(std::integral_constant<int, 4>());
       else join(std::integral_constant<int, 8>());
     }
-    cluster_sync();  // no CTA leaves while another reads its memory
+    for (int c = 0; c < csize; ++c) redo |= ld_cluster(map_rank(smem_u32(smem + C::kBadOff), c)) != 0u;
+    cluster_sync();  // no CTA leaves while another reads its memory; every row of the item is written
   }
+  if (__builtin_expect(redo, 0)) redo_bad_items<D, KV8>(p, kpo, csize);
 }
 
 // CTAs of an item: one where the items fill the SMs; else as many (a power of two

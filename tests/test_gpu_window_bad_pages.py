@@ -109,3 +109,37 @@ def test_decode_bad_pages_on_clusters_and_short_rings(cuda_device):
     lens = np.random.default_rng(3).integers(1, 300, 420)  # over 608 CTAs
     make = lambda: Case(np.ones(420, dtype=int), lens - 1, 100, 4, hq=8, hkv=2, d=128, seed=12)
     _run(make, cuda_device, {(b, int(lens[b] - 1) // 16): BAD for b in range(0, 420, 7)})
+
+
+NEW, CACHED = [60, 300, 20, 9, 130], [0, 200, 5, 900, 300]
+
+
+# page sizes below, at and above a tile of 128 keys
+@pytest.mark.parametrize("dtype,hq,hkv,d,ps", [
+    ("bf16", 8, 2, 64, 16), ("bf16", 8, 2, 128, 8), ("bf16", 5, 1, 128, 64), ("bf16", 4, 2, 64, 128),
+    ("bf16", 4, 2, 64, 256), ("e4m3", 8, 2, 64, 16), ("e4m3", 8, 2, 128, 8), ("e4m3", 4, 1, 128, 128),
+    ("bf16", 4, 2, 64, 12)])
+def test_prefill_skips_the_keys_of_bad_pages(cuda_device, dtype, hq, hkv, d, ps):
+    make = lambda: Case(NEW, CACHED, 70, 4, hq=hq, hkv=hkv, d=d, ps=ps, dtype=dtype, seed=hq + d + ps)
+    _run(make, cuda_device, _pages(ps, (1, 0, BAD)))                                 # the sinks' page
+    _run(make, cuda_device, _pages(ps, (1, 333, -7), (0, 59, BAD), (4, 429, -1)))    # inside the window; the last pages
+    _run(make, cuda_device, _pages(ps, *((2, j, BAD) for j in range(25))))           # every key: the rows give 0
+    _run(make, cuda_device, _pages(ps, *((4, j, BAD) for j in [0, *range(250, 430, 8)])))
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "e4m3"])
+def test_prefill_bad_pages_on_clusters_and_many_items(cuda_device, dtype):
+    make = lambda: Case([33, 1, 70], [900, 1500, 0], 1300, 40, hq=8, hkv=2, d=128, dtype=dtype, seed=51)
+    _run(make, cuda_device, _pages(16, (0, 0, BAD), *((0, j, -3) for j in range(400, 700, 16)), (2, 69, BAD)))
+    _run(make, cuda_device, _pages(16, *((0, j, BAD) for j in range(0, 933, 16))))   # every key of the first sequence
+    make = lambda: Case(np.full(90, 25), np.full(90, 150), 100, 4, hq=16, hkv=4, d=128, dtype=dtype, seed=52)
+    _run(make, cuda_device, {(b, m): BAD for b in range(0, 90, 5) for m in (0, 7, 10)})
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "e4m3"])
+def test_prefill_bad_pages_behind_an_items_last_key(cuda_device, dtype):
+    """A page that only later rows of the sequence see, in the last key tile of the
+    rows before them (64 tokens of 4 heads are one item)."""
+    make = lambda: Case([300, 40], [0, 100], 70, 4, hq=8, hkv=2, d=128, dtype=dtype, seed=53)
+    for j in (64, 80, 112, 130, 191, 256):
+        _run(make, cuda_device, _pages(16, (0, j, BAD)))
