@@ -28,6 +28,8 @@
 //   slice of the G x D outputs over the c partial rows.
 #include <math.h>
 
+#include <algorithm>
+
 #include "cluster.cuh"
 #include "common.cuh"
 #include "internal.h"
@@ -596,9 +598,12 @@ cudaError_t launch_group(const DecodeParams& p, const CUtensorMap& tk, const CUt
 // block at least for every team: a cluster whose CTAs wait for a second wave
 // loses more than the shorter parts gain (1024 keys, on clusters of 1, 2, 4 and
 // 8 CTAs: 32 sequences of 2 KV heads of 64 dims 12.9, 9.2, 6.8 and 10.6 us; of 8
-// heads of 128 dims 23.8, 30.9, 33.2 and 45.8 us).
+// heads of 128 dims 23.8, 30.9, 33.2 and 45.8 us).  Clusters get the deep rings (a
+// grid of them is never past deep_rings' bound), so two CTAs are resident on an SM
+// at most: counted as three, 12 and 24 sequences of 8 heads of 128 dims got clusters
+// of 4 and 2 and took 17.1 and 25.8 us; on 2 and 1 they take 12.3 and 18.7 us.
 int decode_window_cluster(int num_sms, int32_t batch, int32_t num_kv_heads, int32_t group, int64_t max_keys) {
-  const int64_t segments = (int64_t)batch * num_kv_heads, slots = (int64_t)num_sms * ctas_per_sm(group);
+  const int64_t segments = (int64_t)batch * num_kv_heads, slots = (int64_t)num_sms * std::min(2, ctas_per_sm(group));
   const int64_t blocks = (max_keys + 15) / 16;
   int c = 1;
   while (c < 8 && segments * 2 * c <= slots && blocks >= 2 * kTeams * c) c *= 2;
