@@ -490,6 +490,19 @@ def _int32(t, name):
         raise ValueError(f"{name} must be contiguous")
 
 
+def _reach(n) -> int:
+    """A window or a number of sinks as the C call's int32 (ctypes keeps the low 32
+    bits of an integer without a word): no sequence has more keys than the bound."""
+    return max(-1, min(int(n), 2 ** 31 - 1))
+
+
+def _bound(n, name) -> int:
+    n = int(n)
+    if not -2 ** 31 <= n < 2 ** 31:
+        raise ValueError(f"{name} is beyond 32 bits")
+    return n
+
+
 def paged_attention_decode_window(key_pool, value_pool, q, block_table, seq_lens, scale, window, num_sinks=0,
                                   max_seq_len=None, out=None, workspace=None, stream=None, k_scale=1.0,
                                   v_scale=1.0):
@@ -520,8 +533,9 @@ def paged_attention_decode_window(key_pool, value_pool, q, block_table, seq_lens
         _used_on(stream, out)
     wbytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
     st = lib().paged_attention_decode_window(ctypes.byref(pool), q.data_ptr(), out.data_ptr(), B, hq,
-                                             block_table.data_ptr(), mb, seq_lens.data_ptr(), int(max_seq_len),
-                                             float(scale), int(window), int(num_sinks), _addr(workspace), wbytes,
+                                             block_table.data_ptr(), mb, seq_lens.data_ptr(),
+                                             _bound(max_seq_len, "max_seq_len"), float(scale), _reach(window),
+                                             _reach(num_sinks), _addr(workspace), wbytes,
                                              _raw_stream(stream, dev))
     if st != PA_OK:
         raise PagedAttnError(st, "paged_attention_decode_window")
@@ -554,9 +568,10 @@ def paged_attention_prefill_window(key_pool, value_pool, q, query_start_loc, blo
     if made:
         _used_on(stream, out)
     st = lib().paged_attention_prefill_window(ctypes.byref(pool), q.data_ptr(), out.data_ptr(), B, hq,
-                                              query_start_loc.data_ptr(), T, int(max_q_len), block_table.data_ptr(),
-                                              mb, seq_lens.data_ptr(), int(max_seq_len), float(scale), int(window),
-                                              int(num_sinks), _raw_stream(stream, dev))
+                                              query_start_loc.data_ptr(), T, _bound(max_q_len, "max_q_len"),
+                                              block_table.data_ptr(), mb, seq_lens.data_ptr(),
+                                              _bound(max_seq_len, "max_seq_len"), float(scale), _reach(window),
+                                              _reach(num_sinks), _raw_stream(stream, dev))
     if st != PA_OK:
         raise PagedAttnError(st, "paged_attention_prefill_window")
     return out
