@@ -471,16 +471,23 @@ def _raw_stream(stream, device: int):
     return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 
 
-def _used_on(stream, *tensors):
-    """Tensors allocated here and used on a stream other than the current one:
-    their memory is not handed out again before that stream's work is done."""
+def _fresh(stream, make):
+    """``make()``, a tensor that a call on ``stream`` writes.  It is allocated for that
+    stream: memory that the current stream freed may still be in use by kernels queued
+    there, which the call does not wait for.  The caller reads it on the current
+    stream, which therefore counts as a user until it is freed."""
     if stream is None:
-        return
+        return make()
     if not hasattr(stream, "cuda_stream"):
         stream = torch.cuda.ExternalStream(int(stream))
-    for t in tensors:
-        if t is not None:
-            t.record_stream(stream)
+    current = torch.cuda.current_stream()
+    if stream.cuda_stream == current.cuda_stream:
+        return make()
+    with torch.cuda.stream(stream):
+        t = make()
+    if t is not None:
+        t.record_stream(current)
+    return t
 
 
 def _int32(t, name):
@@ -516,8 +523,7 @@ def paged_attention_decode_window(key_pool, value_pool, q, block_table, seq_lens
     pool = _pool_of(key_pool, value_pool, k_scale, v_scale)
     _int32(block_table, "block_table")
     _int32(seq_lens, "seq_lens")
-    made = out is None
-    out = _q_out(q, out, key_pool)
+    out = _fresh(stream, lambda: _q_out(q, None, key_pool)) if out is None else _q_out(q, out, key_pool)
     B, hq, _ = q.shape
     if block_table.dim() != 2 or block_table.shape[0] != B or seq_lens.numel() != B:
         raise ValueError("block_table must be [B, max_blocks] and seq_lens [B]")
@@ -527,10 +533,7 @@ def paged_attention_decode_window(key_pool, value_pool, q, block_table, seq_lens
     dev = _here("key_pool value_pool q block_table seq_lens out workspace",
                 (key_pool, value_pool, q, block_table, seq_lens, out, workspace))
     if workspace is None:
-        workspace = decode_workspace(B, hq, key_pool)
-        _used_on(stream, workspace)
-    if made:
-        _used_on(stream, out)
+        workspace = _fresh(stream, lambda: decode_workspace(B, hq, key_pool))
     wbytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
     st = lib().paged_attention_decode_window(ctypes.byref(pool), q.data_ptr(), out.data_ptr(), B, hq,
                                              block_table.data_ptr(), mb, seq_lens.data_ptr(),
@@ -554,8 +557,7 @@ def paged_attention_prefill_window(key_pool, value_pool, q, query_start_loc, blo
     _int32(query_start_loc, "query_start_loc")
     _int32(block_table, "block_table")
     _int32(seq_lens, "seq_lens")
-    made = out is None
-    out = _q_out(q, out, key_pool)
+    out = _fresh(stream, lambda: _q_out(q, None, key_pool)) if out is None else _q_out(q, out, key_pool)
     T, hq, _ = q.shape
     B = query_start_loc.numel() - 1
     if block_table.dim() != 2 or block_table.shape[0] != B or seq_lens.numel() != B:
@@ -565,8 +567,6 @@ def paged_attention_prefill_window(key_pool, value_pool, q, query_start_loc, blo
         max_seq_len = mb * pool.page_size
     dev = _here("key_pool value_pool q query_start_loc block_table seq_lens out",
                 (key_pool, value_pool, q, query_start_loc, block_table, seq_lens, out))
-    if made:
-        _used_on(stream, out)
     st = lib().paged_attention_prefill_window(ctypes.byref(pool), q.data_ptr(), out.data_ptr(), B, hq,
                                               query_start_loc.data_ptr(), T, _bound(max_q_len, "max_q_len"),
                                               block_table.data_ptr(), mb, seq_lens.data_ptr(),
@@ -632,9 +632,8 @@ def paged_qk_norm_rope_append(key_pool, value_pool, q, key, value, slot_mapping,
             if w.dtype != row_dtype or w.numel() != d:
                 raise ValueError(f"{name} must be [{d}] of {row_dtype}")
             _contig(w, name)
-    made = out is None
-    if made:
-        out = torch.empty((T, hq, d), dtype=row_dtype, device=q.device)
+    if out is None:
+        out = _fresh(stream, lambda: torch.empty((T, hq, d), dtype=row_dtype, device=q.device))
     else:
         _contig(out, "out")
         if out.shape != q.shape or out.dtype != q.dtype:
@@ -643,8 +642,6 @@ def paged_qk_norm_rope_append(key_pool, value_pool, q, key, value, slot_mapping,
         positions = None
     dev = _here("key_pool value_pool q key value slot_mapping positions cos_sin q_weight k_weight out",
                 (key_pool, value_pool, q, key, value, slot_mapping, positions, cos_sin, q_weight, k_weight, out))
-    if made:
-        _used_on(stream, out)
     st = lib().paged_qk_norm_rope_append(ctypes.byref(pool), q.data_ptr(), sq, key.data_ptr(), sk, value.data_ptr(), sv,
                                          out.data_ptr(), hq, _addr(q_weight), _addr(k_weight), float(eps),
                                          _addr(positions), _addr(cos_sin), max_pos, rot, 1 if interleaved else 0,
@@ -719,8 +716,7 @@ def paged_kv_compact(pools, block_table, seq_lens, keep_indptr, keep, base=None,
     dev = _here("key_pool block_table seq_lens keep_indptr keep base new_seq_lens",
                 (ps.tensors[0][0] if ps.count else None, block_table, seq_lens, keep_indptr, keep, base, new_seq_lens))
     if new_seq_lens is None:
-        new_seq_lens = torch.empty_like(seq_lens)
-        _used_on(stream, new_seq_lens)
+        new_seq_lens = _fresh(stream, lambda: torch.empty_like(seq_lens))
     st = lib().paged_kv_compact(ps.array, ps.count, block_table.data_ptr(), block_table.shape[1], seq_lens.data_ptr(), B,
                                 _addr(base), keep_indptr.data_ptr(), keep.data_ptr(), keep.numel(),
                                 new_seq_lens.data_ptr(), _raw_stream(stream, dev))
