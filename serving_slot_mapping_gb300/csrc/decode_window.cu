@@ -192,6 +192,12 @@ __global__ void __launch_bounds__(DCfg<D, KV8, RT, NT, DEEP>::kThreads, DCfg<D, 
     mbar_init(bars + 8u * (kTeams * S + tid), RT);  // empty: the team's warps
     fence_mbar_init();
   }
+  griddep_launch_dependents();
+  // Before the first read of an input: any of them, the lengths and the table too,
+  // may come from the kernel before.  Read ahead of this wait they save 0.4 to 0.9 us
+  // a call among decodes alone and nothing behind an append (32 sequences, append and
+  // decode 26.3 us either way).
+  griddep_wait();
   const int L = seq_keys(p.seq_lens, p.kv_indptr, p.kv_last_page_len, p.kv_len, b, ps, p.max_blocks * ps,
                          tid == 0 && rank == 0 && hk == 0 ? p.err : nullptr);
   const WinSpan win = win_span(p, L);
@@ -201,7 +207,6 @@ __global__ void __launch_bounds__(DCfg<D, KV8, RT, NT, DEEP>::kThreads, DCfg<D, 
   // the sequence's k0 + t + i * kTeams
   const int k0 = rank * per, k1 = min(nblk, k0 + per);
   auto team_blocks = [&](int team) { return max(0, (k1 - k0 - team + kTeams - 1) / kTeams); };
-  griddep_launch_dependents();
   __syncthreads();  // the barriers are set up
   bool alive = true;
 
@@ -224,8 +229,7 @@ __global__ void __launch_bounds__(DCfg<D, KV8, RT, NT, DEEP>::kThreads, DCfg<D, 
       if (half_used(kk)) next0 = __ldg(bt + (kk >> pshift));
       if (R < 16 && half_used(kk + 8)) next1 = __ldg(bt + ((kk + 8) >> pshift));
     };
-    fetch(0);        // block_table is an input, not written by the append kernel
-    griddep_wait();  // the pool rows of this step may come from an earlier kernel
+    fetch(0);
     const CUtensorMap* map = T ? &tmap_v : &tmap_k;
     const uint32_t ring = smem_u32(smem) + (uint32_t)(team * S * C::kBlockBytes + T * C::kTensorBytes);
     int slot = 0;
@@ -285,7 +289,6 @@ __global__ void __launch_bounds__(DCfg<D, KV8, RT, NT, DEEP>::kThreads, DCfg<D, 
   const bool consumer = warp < C::kConsumers;
   const int mine = consumer ? team_blocks(team) : 0;
   unsigned char* ring = smem + team * S * C::kBlockBytes;
-  if (consumer) griddep_wait();  // q may come from an earlier kernel; before the first global write
   // ---- queries: B fragments of m16n8k16 (columns are heads; those >= G are zero) ----
   const int c4 = lane & 3, r8 = lane >> 2;
   uint32_t qf[NT][D / 16][2];
