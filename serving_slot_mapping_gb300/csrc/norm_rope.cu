@@ -138,7 +138,8 @@ __device__ __forceinline__ void set_pair(Raw<float, V>& r, int i, uint64_t x) {
 // even, saturating).  With inv = the rounded reciprocal of the scale, q = x inv
 // and q + (x - q scale) inv, both fused, is the correctly rounded quotient unless
 // the scale's significand is all ones (Markstein, IBM J. Res. Dev. 34, 1990); the
-// host gives inv = 0 for those scales and for ones near the ends of fp32's range.
+// host gives inv = 0 for those scales and for ones so small (below 2^-90) that the
+// remainder x - q scale would not be exact, or near the other end of fp32's range.
 // Quotients outside 2^-12 .. 2^12 round to 0 or saturate as they stand (and
 // infinities and NaN pass).  A division each took the e4m3 append from 61 to 72 us
 // for 10,496 tokens.
@@ -568,7 +569,8 @@ cudaError_t launch_style(NormRopeParams p, int num_sms, cudaStream_t s) {
   auto reciprocal = [](float scale) {
     int e = 0;
     const float f = std::frexp(scale, &e);  // in [1/2, 1)
-    return e > -100 && e < 100 && f != 1.f - 0x1p-24f ? 1.f / scale : 0.f;
+    // q >= 2^-12 ends at 2^-35 and scale at 2^(e - 24): their product at 2^-149 or above
+    return e > -90 && e < 100 && f != 1.f - 0x1p-24f ? 1.f / scale : 0.f;
   };
   p.k_inv = KV8 ? reciprocal(p.k_scale) : 0.f;
   p.v_inv = KV8 ? reciprocal(p.v_scale) : 0.f;
