@@ -25,6 +25,14 @@
  * - Calls are asynchronous on `stream` (a cudaStream_t; NULL = the legacy
  *   default stream).  Host-side argument checks run before any launch; on a
  *   non-PA_OK return nothing was launched.
+ * - Kernels are launched with programmatic stream serialization, and wait for
+ *   the kernel before them (griddepcontrol.wait) ahead of every read, with one
+ *   exception: the paged_attention_decode and paged_attention_prefill calls
+ *   without a window (and their other forms) read lengths and page tables, and
+ *   the prefills queries, ahead of it.  A caller's kernel directly before such a
+ *   call that writes one of these must not let its dependents start early
+ *   (griddepcontrol.launch_dependents); the library's kernels that write them do
+ *   not.
  * - Pool layout (NHD): key_pool and value_pool are each
  *   [num_pages, page_size, num_kv_heads, head_dim], contiguous, element type
  *   `dtype`.  The flat slot s = page_id * page_size + offset addresses row s
@@ -347,8 +355,9 @@ pa_status paged_attention_decode_static_scratch(const pa_kv_pool* pool, const vo
  * e4m3 pools: the bf16 limits, q 16-byte aligned; q and out are bf16; the
  * attention is that of the values the codes stand for (scale * k_scale *
  * q . e4m3(K), outputs times v_scale), computed with f16 products: q is
- * rounded to f16 (exact for bf16 values of magnitude 2^-14 .. 65504), the
- * codes are exact in f16, and the softmax weights are rounded to f16;
+ * rounded to f16 (exact for bf16 values of magnitude 2^-14 .. 65504; larger
+ * ones become infinite), the codes are exact in f16, and the softmax weights are
+ * rounded to f16;
  * CUDA-core path (fp32 arithmetic): f32 pools, and bf16 pools of any other
  * page_size; head_dim <= 256.
  */
@@ -387,7 +396,10 @@ pa_status paged_attention_prefill(const pa_kv_pool* pool, const void* q, void* o
  * of the plain calls; where the window reaches every key (window or num_sinks
  * >= max_seq_len) the plain kernels run, and only there is the workspace used.
  * Tensor-core pools: out is 8-byte aligned (decode), q and out are 16-byte
- * aligned (prefill, which takes at most 2^31 - 1 slots per pool).
+ * aligned (prefill, which takes at most 2^31 - 1 slots per pool).  As in the
+ * plain calls the softmax weights go into the second product as bf16 (e4m3
+ * pools: f16), and the queries of an e4m3 pool into the first as f16: they are
+ * at most 65504 in magnitude.
  */
 pa_status paged_attention_decode_window(const pa_kv_pool* pool, const void* q, void* out,
                                         int32_t batch, int32_t num_q_heads,
@@ -446,8 +458,11 @@ pa_status paged_attention_prefill_window(const pa_kv_pool* pool, const void* q, 
  * A slot or position out of range is recorded in the device error word (codes
  * 2 and 6) and that token is skipped like a padding token.
  * head_dim a multiple of 8, at most 256 (PA_ERR_UNSUPPORTED); any alignment
- * of the element type (16-byte aligned rows of bf16 heads whose head_dim and
- * rotary_dim are multiples of 16 are the fast path).
+ * of the element type.  The fast path: 16-byte aligned rows of f32 heads, or of
+ * bf16 heads whose head_dim and rotary_dim are multiples of 16; for many tokens
+ * (four an SM or more) also a token's rows of q, key, value and cos_sin of at most
+ * 14,336 bytes together (32 + 8 + 8 bf16 heads of 128 take 12,800; wider ones run
+ * at 0.71 to 0.87 of the copy rate, not 0.85).
  */
 pa_status paged_qk_norm_rope_append(const pa_kv_pool* pool, const void* q, int64_t q_stride,
                                     const void* key, int64_t key_stride, const void* value,
@@ -520,7 +535,8 @@ pa_status paged_kv_compact(const pa_kv_pool* pools, int32_t num_pools, const int
  * else 1 = block_table / kv_indices entry out of range, 2 = slot out of
  * range, 3 = seq_len (or CSR kv_indptr / kv_last_page_len) out of range,
  * 4 = query_start_loc inconsistent, 5 = a bounded wait inside a kernel gave
- * up, 6 = position out of range, 7 = compaction list inconsistent; *detail holds the offending value.  Either pointer may be NULL.
+ * up, 6 = position out of range, 7 = compaction list inconsistent; *detail
+ * holds the offending value.  Either pointer may be NULL.
  */
 pa_status paged_device_error(int64_t* code, int64_t* detail);
 

@@ -73,9 +73,9 @@ __device__ __forceinline__ uint32_t code_chunk(int row, int chunk) {
 __host__ __device__ constexpr int ctas_per_sm(int heads) { return heads <= 8 ? 3 : (heads <= 16 ? 2 : 1); }
 
 // Up to 8 heads: with up to 4 CTAs for each SM, a ring half as long again and two
-// CTAs an SM (32 sequences, 8 KV heads, a window of 1024: 23.4 against 27.4 us out
-// of HBM; 64 sequences: 43.4 against 49.6 us); with more, the third CTA hides
-// more than the ring (256 sequences, a window of 128: 38.3 against 42.8 us).
+// CTAs an SM (32 sequences, 8 KV heads, a window of 1024: 23.4 against 24.2 us; 64
+// sequences: 43.1 against 46.6 us); with more, the third CTA hides more than the
+// ring (256 sequences, a window of 128: 38.1 against 43.9 us).
 bool deep_rings(int num_sms, int64_t ctas) { return ctas <= 4 * (int64_t)num_sms; }
 
 // RT: warps per team, each with NT tiles of 8 query heads of the group; DEEP: see
@@ -371,7 +371,7 @@ __global__ void __launch_bounds__(DCfg<D, KV8, RT, NT, DEEP>::kThreads, DCfg<D, 
     // a tile, so a group of up to 8 heads costs one tile (heads as the 16 rows
     // would leave most of them empty).  All K fragments are loaded before the
     // first product; V's as they are used (loaded before the softmax their
-    // registers cost more than the wait: MQA, 256 x 4096 keys 107 against 120 us).
+    // registers cost more than the wait: 12 % for MQA, 256 x 4096 keys, 111.6 us now).
     float s[NT][4];
     uint32_t f[kFrags][4];
 #pragma unroll
@@ -434,7 +434,11 @@ __global__ void __launch_bounds__(DCfg<D, KV8, RT, NT, DEEP>::kThreads, DCfg<D, 
         }
       }
     }
-    // O^T += V^T P^T; P^T is the transpose of the weights as they stand
+    // O^T += V^T P^T; P^T is the transpose of the weights as they stand.  They are
+    // rounded to V's type (f16 for codes), the one that the matrix instruction takes
+    // beside it; their sum is of the fp32 ones.  Against 64 bits an output is off by
+    // 0.0021 to 0.0022 of its norm so (codes: 0.0017), by 0.0017 with its own
+    // rounding alone.
     uint32_t pb[NT][2];
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
@@ -600,11 +604,11 @@ cudaError_t launch_group(const DecodeParams& p, const CUtensorMap& tk, const CUt
 // As many CTAs a (sequence, KV head) as are resident at once, and each with a
 // block at least for every team: a cluster whose CTAs wait for a second wave
 // loses more than the shorter parts gain (1024 keys, on clusters of 1, 2, 4 and
-// 8 CTAs: 32 sequences of 2 KV heads of 64 dims 12.9, 9.2, 6.8 and 10.6 us; of 8
-// heads of 128 dims 23.8, 30.9, 33.2 and 45.8 us).  Clusters get the deep rings (a
+// 8 CTAs: 32 sequences of 2 KV heads of 64 dims 14.7, 10.5, 7.7 and 12.5 us; of 8
+// heads of 128 dims 24.6, 29.3, 33.8 and 45.0 us).  Clusters get the deep rings (a
 // grid of them is never past deep_rings' bound), so two CTAs are resident on an SM
 // at most: counted as three, 12 and 24 sequences of 8 heads of 128 dims got clusters
-// of 4 and 2 and took 17.1 and 25.8 us; on 2 and 1 they take 12.3 and 18.7 us.
+// of 4 and 2 and took 17.8 and 26.4 us; on 2 and 1 they take 12.9 and 19.3 us.
 int decode_window_cluster(int num_sms, int32_t batch, int32_t num_kv_heads, int32_t group, int64_t max_keys) {
   const int64_t segments = (int64_t)batch * num_kv_heads, slots = (int64_t)num_sms * std::min(2, ctas_per_sm(group));
   const int64_t blocks = (max_keys + 15) / 16;

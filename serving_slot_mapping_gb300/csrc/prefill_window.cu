@@ -763,7 +763,9 @@ __global__ void __launch_bounds__(WCfg<D, KV8>::kThreads, 1)
           rescale = j > 0;
         }
         const float mbase = m_ref == -INFINITY ? 0.f : m_ref;
-        // P = exp2(x - m) as bf16 (f16) pairs, written over the S columns
+        // P = exp2(x - m) as bf16 (f16) pairs, written over the S columns: V's type, the one that the product takes
+        // beside it; l sums the fp32 ones.  Against 64 bits an output is off by 0.0023 of its norm so (codes:
+        // 0.0017), by 0.0017 with its own rounding alone
         const uint64_t mul = pair(sl2, sl2), sub = pair(-mbase, -mbase);
         uint64_t rs[4] = {0ull, 0ull, 0ull, 0ull};
 #pragma unroll
@@ -947,8 +949,8 @@ __global__ void __launch_bounds__(WCfg<D, KV8>::kThreads, 1)
 // CTAs of an item: one where the items fill the SMs; else as many (a power of two
 // up to 8, with two key tiles each at least) as the SMs hold at once (four fifths
 // of them for clusters of 4 and 8, which do not fill every SM).  32 / 8 heads of 128 on one CTA an item
-// and so split: 512 tokens, window 1024 23.7 and 21.7 us (2 CTAs); 128 tokens 23.6
-// and 16.6 us (4); 64 tokens, window 4096 71 and 21 us (4).
+// and so split: 512 tokens, window 1024 25.2 and 22.8 us (2 CTAs); 128 tokens 25.0
+// and 18.4 us (4); 64 tokens, window 4096 71.7 and 22.7 us (4).
 int window_split(int num_sms, int64_t items, int64_t max_keys) {
   const int64_t tiles = (max_keys + kBN - 1) / kBN;
   int c = 1;
