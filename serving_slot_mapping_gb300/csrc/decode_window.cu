@@ -32,6 +32,7 @@
 
 #include "cluster.cuh"
 #include "common.cuh"
+#include "inputs.cuh"
 #include "internal.h"
 #include "tma.cuh"
 
@@ -123,11 +124,11 @@ __device__ __forceinline__ void skip_bad_pages(const DecodeParams& p, int csize,
   const int lane = threadIdx.x & 31, ps = p.pool.page_size, G = p.group;
   const int seg = blockIdx.x / csize, rank = blockIdx.x - seg * csize;
   const int b = seg / p.pool.num_kv_heads, hk = seg - b * p.pool.num_kv_heads;
-  const int L = seq_keys(p.seq_lens, p.kv_indptr, p.kv_last_page_len, p.kv_len, b, ps, p.max_blocks * ps, nullptr);
+  const int L = ld_seq_len(p.seq_lens, b, p.max_blocks * ps, nullptr);
   const WinSpan win = win_span(p, L);
   const int nblk = ((L + 15) >> 4) - win.gap, per = (nblk + csize - 1) / csize;
   const int k0 = rank * per, k1 = min(nblk, k0 + per);
-  const int32_t* bt = p.block_table + page_list_start(p.kv_indptr, p.max_blocks, b);
+  const int32_t* bt = p.block_table + (int64_t)b * p.max_blocks;
   for (int i = threadIdx.x; i < kTeams * HEADS * ROW; i += blockDim.x) part[i] = 0.f;
   for (int i = threadIdx.x; i < kTeams * HEADS; i += blockDim.x) part_ml[i] = make_float2(-INFINITY, 0.f);
   __syncthreads();
@@ -148,7 +149,7 @@ __device__ __forceinline__ void skip_bad_pages(const DecodeParams& p, int csize,
     for (int i = k0 * 16; i < k1 * 16; ++i) {
       const int j = win_block(win, i >> 4) * 16 + (i & 15);
       if (j >= L || (j >= p.num_sinks && j < win.start)) continue;
-      const int page = __ldg(bt + (j >> p.pool.page_shift));
+      const int page = ld_input(bt + (j >> p.pool.page_shift));
       if (page < 0 || page >= p.pool.num_pages) continue;
       const int64_t at = (((int64_t)page * ps + (j & (ps - 1))) * p.pool.num_kv_heads + hk) * D + lane * E;
       float s = 0.f;
@@ -198,8 +199,7 @@ __global__ void __launch_bounds__(DCfg<D, KV8, RT, NT, DEEP>::kThreads, DCfg<D, 
   // a call among decodes alone and nothing behind an append (32 sequences, append and
   // decode 26.3 us either way).
   griddep_wait();
-  const int L = seq_keys(p.seq_lens, p.kv_indptr, p.kv_last_page_len, p.kv_len, b, ps, p.max_blocks * ps,
-                         tid == 0 && rank == 0 && hk == 0 ? p.err : nullptr);
+  const int L = ld_seq_len(p.seq_lens, b, p.max_blocks * ps, tid == 0 && rank == 0 && hk == 0 ? p.err : nullptr);
   const WinSpan win = win_span(p, L);
   const int nblk = ((L + 15) >> 4) - win.gap;  // the sequence's blocks with a visible key
   const int per = (nblk + csize - 1) / csize;
@@ -215,7 +215,7 @@ __global__ void __launch_bounds__(DCfg<D, KV8, RT, NT, DEEP>::kThreads, DCfg<D, 
     // Lane t + kTeams * r knows the page (of each half, 8-slot pages) of block
     // i0 + r of team t; the next 8 blocks' are read while these are issued.  Two
     // lanes a team issue its K and its V box.
-    const int32_t* bt = p.block_table + page_list_start(p.kv_indptr, p.max_blocks, b);
+    const int32_t* bt = p.block_table + (int64_t)b * p.max_blocks;
     const int R = ps < 16 ? ps : 16;  // rows per box (page_size >= 8)
     constexpr int kAhead = 32 / kTeams;
     auto half_used = [&](int kk) { return kk < L && (kk < p.num_sinks || kk + R > win.start); };
@@ -226,8 +226,8 @@ __global__ void __launch_bounds__(DCfg<D, KV8, RT, NT, DEEP>::kThreads, DCfg<D, 
       const int k = k0 + team + (i0 + lane / kTeams) * kTeams;
       if (k >= k1) return;
       const int kk = win_block(win, k) * 16;
-      if (half_used(kk)) next0 = __ldg(bt + (kk >> pshift));
-      if (R < 16 && half_used(kk + 8)) next1 = __ldg(bt + ((kk + 8) >> pshift));
+      if (half_used(kk)) next0 = ld_input(bt + (kk >> pshift));
+      if (R < 16 && half_used(kk + 8)) next1 = ld_input(bt + ((kk + 8) >> pshift));
     };
     fetch(0);
     const CUtensorMap* map = T ? &tmap_v : &tmap_k;
@@ -298,7 +298,7 @@ __global__ void __launch_bounds__(DCfg<D, KV8, RT, NT, DEEP>::kThreads, DCfg<D, 
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
       const int head = (rt * NT + n) * 8 + r8;
-      auto ld = [&](int d) { return head < G && mine > 0 ? __ldg(qg + ((head * D + d) >> 1)) : 0u; };
+      auto ld = [&](int d) { return head < G && mine > 0 ? ld_input(qg + ((head * D + d) >> 1)) : 0u; };
 #pragma unroll
       for (int kk = 0; kk < D / 16; ++kk) {
         // e4m3 pools: f16, dims permuted to match the K fragments: MMA k = 2c, 2c + 1

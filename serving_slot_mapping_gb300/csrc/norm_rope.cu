@@ -30,6 +30,7 @@
 #include <cmath>
 
 #include "common.cuh"
+#include "inputs.cuh"
 #include "internal.h"
 #include "tma.cuh"
 
@@ -81,11 +82,11 @@ __device__ __forceinline__ Raw<T, V> load_raw(const T* src) {
   Raw<T, V> r;
   if constexpr (VEC && Raw<T, V>::kWords == 4) {
     const uint4* s = reinterpret_cast<const uint4*>(src);
-    const uint4 v = STREAM ? __ldcs(s) : __ldg(s);
+    const uint4 v = STREAM ? ld_stream(s) : ld_input(s);
     r.w[0] = v.x; r.w[1] = v.y; r.w[2] = v.z; r.w[3] = v.w;
   } else if constexpr (VEC) {
     const uint2* s = reinterpret_cast<const uint2*>(src);
-    const uint2 v = STREAM ? __ldcs(s) : __ldg(s);
+    const uint2 v = STREAM ? ld_stream(s) : ld_input(s);
     r.w[0] = v.x; r.w[1] = v.y;
   } else if constexpr (sizeof(T) == 4) {
 #pragma unroll
@@ -406,9 +407,9 @@ __global__ void __launch_bounds__(kThreads) qk_norm_rope_append_kernel(const __g
   auto first_pass = [&](int before) { return (slice - before % p.slices + p.slices) % p.slices; };
   const int q0 = slice, k0 = first_pass(q_passes), v0 = first_pass(q_passes + kv_passes);
   if (q0 < q_passes) load(q, p.num_q_heads, q0);  // in flight while slot, position and table are read
-  const int pos = p.rotary_dim > 0 ? __ldg(p.positions + t) : 0;
+  const int pos = p.rotary_dim > 0 ? ld_input(p.positions + t) : 0;
   const int64_t slot =
-      live_slot(p, __ldg(p.slot_mapping + t), pos, slice == 0 && (threadIdx.x & 31) == 0 ? p.err : nullptr);
+      live_slot(p, ld_input(p.slot_mapping + t), pos, slice == 0 && (threadIdx.x & 31) == 0 ? p.err : nullptr);
   if (slot < 0) return;
   const Turn<V, VEC, INTER> tr(p, ln, p.cos_sin + (int64_t)pos * p.rotary_dim);
   Factors<T, V, VEC, INTER> f;
@@ -492,8 +493,8 @@ __global__ void __launch_bounds__(kBulkThreads, 2) qk_norm_rope_append_bulk_kern
     *slot = -1;
     *pos = 0;
     if (x >= p.num_tokens) return;
-    *slot = __ldg(p.slot_mapping + x);
-    if (rot > 0) *pos = __ldg(p.positions + x);
+    *slot = ld_input(p.slot_mapping + x);
+    if (rot > 0) *pos = ld_input(p.positions + x);
   };
   auto issue = [&](int64_t x, int pos, int s) {  // one thread
     const uint32_t dst = smem_u32(ring + s * stage), bar = bars + 8u * s;

@@ -12,6 +12,7 @@
 // layers: 149 us, 6.7 TB/s; half of 16 sequences of 1024 - 4096 keys moved in 4
 // layers: 99 us, 6.1 TB/s (the barrier between a tile's reads and its writes).
 #include "common.cuh"
+#include "inputs.cuh"
 #include "internal.h"
 
 namespace pa {
@@ -36,7 +37,7 @@ __global__ void __launch_bounds__(kCopyThreads) copy_pages_kernel(const __grid_c
     const int chunk = (int)(w - pt * chunks);
     const int64_t i = pt / tensors;
     const int tensor = (int)(pt - i * tensors);
-    const int src = __ldg(p.src + i), dst = __ldg(p.dst + i);
+    const int src = ld_input(p.src + i), dst = ld_input(p.dst + i);
     if (src < 0 || dst < 0 || src == dst) continue;  // padding pair, or nothing to do
     if (src >= p.num_pages || dst >= p.num_pages) {
       if (threadIdx.x == 0 && tensor == 0 && chunk == 0)
@@ -50,7 +51,7 @@ __global__ void __launch_bounds__(kCopyThreads) copy_pages_kernel(const __grid_c
     V v[kCopyAhead];
 #pragma unroll
     for (int k = 0; k < kCopyAhead; ++k)
-      if (x0 + k * blockDim.x < nvec) v[k] = __ldcs(s + x0 + k * blockDim.x);
+      if (x0 + k * blockDim.x < nvec) v[k] = ld_stream(s + x0 + k * blockDim.x);
 #pragma unroll
     for (int k = 0; k < kCopyAhead; ++k)
       if (x0 + k * blockDim.x < nvec) d[x0 + k * blockDim.x] = v[k];
@@ -95,9 +96,9 @@ __global__ void __launch_bounds__(kCompactThreads) compact_kernel(const __grid_c
   griddep_wait();
   const bool first = blockIdx.x == 0 && tensor == 0;  // records errors, writes the new length
   const int max_len = p.max_blocks * p.page_size;
-  const int L0 = __ldg(p.seq_lens + b);
-  const int base = p.base != nullptr ? __ldg(p.base + b) : 0;
-  const int s0 = __ldg(p.keep_indptr + b), s1 = __ldg(p.keep_indptr + b + 1);
+  const int L0 = ld_input(p.seq_lens + b);
+  const int base = p.base != nullptr ? ld_input(p.base + b) : 0;
+  const int s0 = ld_input(p.keep_indptr + b), s1 = ld_input(p.keep_indptr + b + 1);
   const bool bad_len = L0 < 0 || L0 > max_len || base < 0 || base > L0;
   const bool bad_list = s0 < 0 || s1 < s0 || s1 > p.num_keep || (!bad_len && s1 - s0 > L0 - base);
   if (bad_len || bad_list) {
@@ -117,12 +118,12 @@ __global__ void __launch_bounds__(kCompactThreads) compact_kernel(const __grid_c
       int64_t f = -1, d = -1;
       const int i = i0 + r;
       if (i < count) {
-        const int old = __ldg(p.keep + s0 + i), now = base + i;
-        const int before = i > 0 ? __ldg(p.keep + s0 + i - 1) : now - 1;
+        const int old = ld_input(p.keep + s0 + i), now = base + i;
+        const int before = i > 0 ? ld_input(p.keep + s0 + i - 1) : now - 1;
         if (old < now || old >= L0 || old <= before) {
           if (first) record_error(p.err, ERR_KEEP, old);
         } else if (old != now) {
-          const int pf = __ldg(bt + old / p.page_size), pt = __ldg(bt + now / p.page_size);
+          const int pf = ld_input(bt + old / p.page_size), pt = ld_input(bt + now / p.page_size);
           if (pf < 0 || pf >= p.num_pages || pt < 0 || pt >= p.num_pages) {
             if (first) record_error(p.err, ERR_BLOCK_TABLE, pf < 0 || pf >= p.num_pages ? pf : pt);
           } else {

@@ -37,6 +37,7 @@
 #include <type_traits>
 
 #include "cluster.cuh"
+#include "inputs.cuh"
 #include "prefill_tc.cuh"
 
 namespace pa {
@@ -80,7 +81,7 @@ struct WCfg : PCfg<D, KV8> {
 
 // Sequence b's rows [qs, qs + n) of q; n = 0 where query_start_loc is inconsistent.
 __device__ __forceinline__ int seq_rows(const PrefillParams& p, int b, int* qs) {
-  const int s0 = __ldg(p.query_start_loc + b), s1 = __ldg(p.query_start_loc + b + 1);
+  const int s0 = ld_input(p.query_start_loc + b), s1 = ld_input(p.query_start_loc + b + 1);
   *qs = s0;
   return (s0 < 0 || s1 < s0 || (int64_t)s1 > p.total_q) ? 0 : s1 - s0;
 }
@@ -147,7 +148,7 @@ struct Walker {
     w += gridDim.x / csize;
     const int ps = p.pool.page_size;
     it->n = seq_rows(p, it->b, &it->qs);
-    it->L = seq_keys(p.seq_lens, p.kv_indptr, p.kv_last_page_len, p.kv_len, it->b, ps, p.max_blocks * ps, nullptr);
+    it->L = ld_seq_len(p.seq_lens, it->b, p.max_blocks * ps, nullptr);
     it->first = it->L - it->n;
     it->row0 = tile * kQT * kBM;
     const int G = p.group;
@@ -227,9 +228,9 @@ __device__ __forceinline__ void redo_bad_items(const PrefillParams& p, int kpo, 
   wk.start(p, csize);
   Item x;
   while (wk.next(p, kpo, csize, &x)) {
-    const int32_t* bt = p.block_table + page_list_start(p.kv_indptr, p.max_blocks, x.b);
+    const int32_t* bt = p.block_table + (int64_t)x.b * p.max_blocks;
     auto in_range = [&](int key) {
-      const int page = __ldg(bt + (key >> p.pool.page_shift));
+      const int page = ld_input(bt + (key >> p.pool.page_shift));
       return page >= 0 && page < p.pool.num_pages;
     };
     const int rows = min(kQT * kBM, x.n * G - x.row0);
@@ -253,7 +254,7 @@ __device__ __forceinline__ void redo_bad_items(const PrefillParams& p, int kpo, 
       for (int j = 0; j <= pos; ++j) {
         if (j >= p.num_sinks && j <= pos - p.window) j = pos - p.window + 1;
         if (!in_range(j)) continue;
-        const int64_t page = __ldg(bt + (j >> p.pool.page_shift));
+        const int64_t page = ld_input(bt + (j >> p.pool.page_shift));
         const int64_t at = ((page * ps + (j & (ps - 1))) * p.pool.num_kv_heads + x.hk) * D + lane * E;
         float s = 0.f;
 #pragma unroll
@@ -343,9 +344,9 @@ __global__ void __launch_bounds__(WCfg<D, KV8>::kThreads, 1)
   for (int b = blockIdx.x * C::kThreads + tid; b < p.batch; b += gridDim.x * C::kThreads) {
     int qs;
     const int n = seq_rows(p, b, &qs);
-    if (n == 0 && qs != __ldg(p.query_start_loc + b + 1)) record_error(p.err, ERR_QUERY_LOC, qs);
+    if (n == 0 && qs != ld_input(p.query_start_loc + b + 1)) record_error(p.err, ERR_QUERY_LOC, qs);
     if (n > p.max_q_len) record_error(p.err, ERR_QUERY_LOC, n);
-    seq_keys(p.seq_lens, p.kv_indptr, p.kv_last_page_len, p.kv_len, b, ps, p.max_blocks * ps, p.err);
+    ld_seq_len(p.seq_lens, b, p.max_blocks * ps, p.err);
   }
   bool alive = true;
   Item it = {};
@@ -394,7 +395,7 @@ __global__ void __launch_bounds__(WCfg<D, KV8>::kThreads, 1)
     const int32_t* bt = nullptr;
     auto fetch = [&](int j) {  // raw block_table entry of this lane's box of tile j
       const int key = box_key(j);
-      return box_used(key) ? __ldg(bt + (key >> pshift)) : -1;
+      return box_used(key) ? ld_input(bt + (key >> pshift)) : -1;
     };
     auto issue = [&](const CUtensorMap* map, uint32_t dst, int hk, int slot, uint32_t full) {
       const bool ok = slot >= 0;
@@ -437,7 +438,7 @@ __global__ void __launch_bounds__(WCfg<D, KV8>::kThreads, 1)
         more = !end && it.nt() > 0;
         j = 0;
         if (more) {
-          bt = p.block_table + page_list_start(p.kv_indptr, p.max_blocks, it.b);
+          bt = p.block_table + (int64_t)it.b * p.max_blocks;
           raw = fetch(0);
         }
         progressed = true;
