@@ -76,8 +76,13 @@ typedef enum pa_status {
 typedef enum pa_dtype {
   PA_DTYPE_F32 = 0,        /* float32 pool, q and out                           */
   PA_DTYPE_BF16 = 1,       /* bfloat16 pool, q and out; fp32 accumulation       */
-  PA_DTYPE_FP8_E4M3 = 2    /* e4m3 pool with k_scale / v_scale; bf16 q, out and
+  PA_DTYPE_FP8_E4M3 = 2,   /* e4m3 pool with k_scale / v_scale; bf16 q, out and
                               appended rows                                     */
+  PA_DTYPE_INT8 = 3        /* int8 pool with a scale for each block of tokens and
+                              KV head (pa_kv_scales); bf16 q, out and appended
+                              rows.  Taken by the _int8 calls,
+                              paged_attention_decode_mass and
+                              paged_kv_copy_pages only                          */
 } pa_dtype;
 
 /* One layer's KV page pool (mobius PR #395 "ONNX I/O contract":
@@ -528,6 +533,178 @@ pa_status paged_kv_compact(const pa_kv_pool* pools, int32_t num_pools, const int
                            int32_t max_blocks_per_seq, const int32_t* seq_lens, int32_t batch,
                            const int32_t* base, const int32_t* keep_indptr, const int32_t* keep,
                            int64_t num_keep, int32_t* new_seq_lens, void* stream);
+
+/*
+ * int8 pools.  key_pool and value_pool hold int8 codes (PA_DTYPE_INT8, the
+ * layout of every pool); code c of slot s and KV head h stands for
+ *
+ *   c * scales[s / block_tokens, h],
+ *
+ * with scales of their own for keys and values.  A scale counts as
+ * min(max(scale, 2^-40), 2^40).  The pages have no counterpart of these calls.
+ *
+ * key_scales, value_scales  device f32 [num_pages * page_size / block_tokens,
+ *               num_kv_heads], 16-byte aligned.
+ * block_tokens  a power of two, 16 .. page_size.
+ * All calls on int8 pools: page_size a power of two >= 16, head_dim in
+ * {64, 128} (PA_ERR_UNSUPPORTED else), at most 2^31 - 1 slots, pools 16-byte
+ * aligned.  paged_kv_copy_pages copies their pages; their scales are a pool of
+ * dtype f32, page_size page_size / block_tokens and head_dim 1 to it.
+ * paged_kv_compact refuses them: rows that share a scale cannot move alone
+ * (paged_kv_evict_pages drops whole pages).
+ */
+typedef struct pa_kv_scales {
+  float* key_scales;
+  float* value_scales;
+  int32_t block_tokens;
+} pa_kv_scales;
+
+/*
+ * paged_kv_append_int8 -- write each token's K/V rows into an int8 pool and keep
+ * the scales of the blocks that they lie in.  For a block of which this call
+ * writes rows, a KV head and a tensor, with a the largest magnitude of those rows
+ * (NaN aside) in that head:
+ *
+ *   n = min(max(a / 127, 2^-40), 2^40)
+ *   new scale s = n                when the call writes the block's first slot,
+ *               = max(scale, n)    else;
+ *   the rows written get the codes rint(x / s), at most 127 in magnitude (NaN
+ *   becomes 0); where s is larger than the scale before, the codes c of the
+ *   block's other rows become rint(c * (scale / s)).
+ *
+ * Arithmetic is fp32 (one division, rounding to nearest even).  A block's first
+ * slot is the first that a sequence writes, so a page taken into use again
+ * starts anew; its slots not yet written may hold anything, and are left or
+ * re-encoded.
+ *
+ * key, value    device bf16 rows of num_kv_heads heads of head_dim contiguous
+ *               elements, 16-byte aligned; token t starts at t * key_stride
+ *               (value_stride) elements, multiples of 8, at least a row.
+ * slot_mapping  as for paged_kv_append.  The tokens of one block must follow one
+ *               another in the call (as those of a sequence do; up to 31 padding
+ *               tokens may stand between two): else which of their scales the
+ *               block keeps is unspecified.
+ */
+pa_status paged_kv_append_int8(const pa_kv_pool* pool, const pa_kv_scales* scales, const void* key,
+                               int64_t key_stride, const void* value, int64_t value_stride,
+                               const int64_t* slot_mapping, int64_t num_tokens, void* stream);
+
+/*
+ * paged_attention_decode_int8 / paged_attention_prefill_int8 --
+ * paged_attention_decode / paged_attention_prefill over an int8 pool: the
+ * attention of the values that the codes stand for.  Products are f16 with fp32
+ * sums: the codes are exact, the queries are rounded to f16 (exact for bf16 values
+ * of magnitude 2^-14 .. 65504, their largest), the softmax weights too; the prefill
+ * also rounds each code times its scale, relative to the largest scale of its tile
+ * of 128 keys, to f16.  The keys of a page that is out of range take no part.
+ * out is 8-byte aligned (decode), q and out are 16-byte aligned (prefill).  Every
+ * other argument, limit, the workspace (dtype PA_DTYPE_INT8) and the results are
+ * those of the plain calls.
+ */
+pa_status paged_attention_decode_int8(const pa_kv_pool* pool, const pa_kv_scales* scales,
+                                      const void* q, void* out, int32_t batch, int32_t num_q_heads,
+                                      const int32_t* block_table, int32_t max_blocks_per_seq,
+                                      const int32_t* seq_lens, int32_t max_seq_len, float scale,
+                                      void* workspace, size_t workspace_bytes, void* stream);
+
+pa_status paged_attention_prefill_int8(const pa_kv_pool* pool, const pa_kv_scales* scales,
+                                       const void* q, void* out, int32_t batch, int32_t num_q_heads,
+                                       const int32_t* query_start_loc, int64_t total_q,
+                                       int32_t max_q_len, const int32_t* block_table,
+                                       int32_t max_blocks_per_seq, const int32_t* seq_lens,
+                                       int32_t max_seq_len, float scale, void* stream);
+
+/*
+ * paged_attention_decode_mass -- a decode that also gives the attention weight of
+ * every key, summed over the query heads and added to what the key had:
+ *
+ *   mass_out[b, j] = decay * mass_in[b, j] + sum_h softmax_j(scale * q[b,h] . K_b[j, h/G]),
+ *   j in [0, seq_lens[b]); entries at and past seq_lens[b] are left as they were.
+ *
+ * Summed over the layers or steps that share a block table, it says which keys
+ * the queries still look at (paged_kv_evict_rows, paged_kv_evict_pages).  The sum
+ * is fp32, heads in ascending order, the same on every run.  The pages have no
+ * counterpart of this call.
+ *
+ * pool, scales  bf16, e4m3 (scales NULL) or int8 pools, with the limits of their
+ *               decode calls; PA_ERR_UNSUPPORTED for f32 pools and for pages that
+ *               the tensor-core kernels do not take.
+ * mass_in       device f32 [batch, mass_stride] rows, mass_out itself, or NULL: 0.
+ *               Rows that overlap mass_out otherwise are refused (PA_ERR_SHAPE).
+ * decay         finite; 1 adds, 0 forgets, between them old weights fade.
+ * mass_out      device f32, rows mass_stride >= max_seq_len apart.
+ * max_seq_len   a longer sequence is cut to it and recorded (code 3).
+ * workspace     paged_attention_decode_mass_workspace_size(...) bytes, 16-byte
+ *               aligned, contents need no initialisation.
+ * out is 8-byte aligned.  Every other argument is as for paged_attention_decode.
+ */
+size_t paged_attention_decode_mass_workspace_size(int32_t batch, int32_t num_q_heads,
+                                                  int32_t num_kv_heads, int32_t head_dim,
+                                                  int32_t dtype, int32_t max_seq_len);
+
+pa_status paged_attention_decode_mass(const pa_kv_pool* pool, const pa_kv_scales* scales,
+                                      const void* q, void* out, int32_t batch, int32_t num_q_heads,
+                                      const int32_t* block_table, int32_t max_blocks_per_seq,
+                                      const int32_t* seq_lens, int32_t max_seq_len, float scale,
+                                      const float* mass_in, float decay, float* mass_out,
+                                      int64_t mass_stride, void* workspace, size_t workspace_bytes,
+                                      void* stream);
+
+/*
+ * paged_kv_evict_rows -- choose the rows that stay, by their accumulated weight:
+ * a sequence of more than `budget` rows keeps its first num_sinks, its last
+ * num_recent and, of the others, the heaviest budget - num_sinks - num_recent
+ * (equal ones by the lower position; NaN counts as the lightest).  The result is
+ * what paged_kv_compact takes:
+ *
+ *   base[b] = num_sinks and keep[keep_indptr[b] ..] = the other rows that stay,
+ *   ascending (budget - num_sinks of them), for a sequence over its budget;
+ *   base[b] = seq_lens[b] and an empty list for one that stays whole;
+ *   new_mass[b, :] = the masses of the rows that stay, in order, then zeros up to
+ *   `width`: what the next steps add to.
+ *
+ * The pages have no counterpart of these calls.
+ *
+ * mass, new_mass  device f32 [batch, width], rows mass_stride / new_mass_stride >=
+ *               width apart; a sequence longer than width is cut to it and
+ *               recorded (code 3).
+ * budget        >= num_sinks + num_recent (PA_ERR_SHAPE).
+ * keep_indptr   device int32 [batch + 1], written.   base  device int32 [batch], written.
+ * keep          device int32 [num_keep], num_keep >= batch * (budget - num_sinks) (0
+ *               when width <= budget); entries past keep_indptr[batch] are left.
+ * Outputs overlap neither inputs nor one another (PA_ERR_SHAPE).
+ */
+pa_status paged_kv_evict_rows(const float* mass, int64_t mass_stride, const int32_t* seq_lens,
+                              int32_t batch, int32_t width, int32_t budget, int32_t num_sinks,
+                              int32_t num_recent, int32_t* keep_indptr, int32_t* keep,
+                              int64_t num_keep, int32_t* base, float* new_mass,
+                              int64_t new_mass_stride, void* stream);
+
+/*
+ * paged_kv_evict_pages -- the same by whole pages, for pools of any type; no row is
+ * moved.  A sequence of more than `budget` pages keeps those that hold its first
+ * num_sinks and its last max(num_recent, 1) rows and the heaviest of the others, a
+ * page's weight being the sum of its rows' (x[0 .. n/2) + x[n/2 .. n) again and
+ * again, rows at and past seq_lens[b] counting 0).
+ *
+ *   new_block_table[b, :] = the pages that stay, in order, then those that go, in
+ *   order, then the entries behind the sequence as they were;
+ *   new_seq_lens[b] = seq_lens[b] - page_size * (pages that go): entries from
+ *   ceil(new_seq_lens[b] / page_size) to the old number of pages are free;
+ *   new_mass as above.
+ *
+ * Keys keep the rotation of their old position, as with paged_kv_compact.
+ * page_size     a power of two, at most 1024 (PA_ERR_UNSUPPORTED).
+ * budget        in pages, at least ceil(num_sinks / page_size) + 1 +
+ *               (max(num_recent, 1) + page_size - 2) / page_size (PA_ERR_SHAPE): the most
+ *               pages that the rows kept in any case lie in.
+ * At most 327,424 pages a sequence (PA_ERR_RANGE).
+ */
+pa_status paged_kv_evict_pages(const float* mass, int64_t mass_stride, const int32_t* block_table,
+                               int32_t max_blocks_per_seq, const int32_t* seq_lens, int32_t batch,
+                               int32_t width, int32_t page_size, int32_t budget, int32_t num_sinks,
+                               int32_t num_recent, int32_t* new_block_table, int32_t* new_seq_lens,
+                               float* new_mass, int64_t new_mass_stride, void* stream);
 
 /*
  * paged_device_error -- read and clear the device error word of the current

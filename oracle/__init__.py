@@ -35,6 +35,9 @@ What it follows:
   (:mod:`oracle.window`), the norm and rotation of queries and keys, page
   copies and the compaction of a sequence's rows (:mod:`oracle.rows`): not on
   the pages, defined plainly in those modules;
+* int8 pools with a scale for each block of tokens and KV head
+  (:mod:`oracle.kv_int8`), the attention weight of cached keys and the choice
+  of what to evict by it (:mod:`oracle.evict`): not on the pages either;
 * one decode step as one call: the append of the step's rows followed by
   the decode that attends to them (mobius page, "How it works (per
   attention layer)", steps 1 and 2).
@@ -70,4 +73,4 @@ from .rows import (  # noqa: F401,E402
     rope_table,
     rotate,
 )
-from . import kv_fp8  # noqa: F401,E402
+from . import evict, kv_fp8, kv_int8  # noqa: F401,E402

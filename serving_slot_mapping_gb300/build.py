@@ -22,9 +22,10 @@ LIB_PATH = os.path.join(HERE, LIB_NAME)
 
 SOURCES = ["api.cu", "append.cu", "decode_bf16.cu", "decode_fused.cu", "decode_weighted.cu", "prefill_bf16.cu", "attn_f32.cu",
            "decode_noalloc.cu", "tmap.cu", "decode_window.cu", "prefill_window.cu", "norm_rope.cu",
-           "pages.cu"]
+           "pages.cu", "decode_int8.cu", "decode_mass.cu", "decode_mass_bf16.cu", "decode_mass_e4m3.cu",
+           "decode_mass_int8.cu", "append_int8.cu", "evict.cu"]
 HEADERS = ["common.cuh", "internal.h", "tma.cuh", "tcgen05.cuh", "decode_split.cuh", "prefill_tc.cuh", "cluster.cuh",
-           "inputs.cuh"]
+           "inputs.cuh", "decode_ext.cuh"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ARCH + ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC",
                      "-I", os.path.join(ROOT, "include"), "--expt-relaxed-constexpr"]

@@ -28,6 +28,7 @@ PA_ERR_ALIGN = 8
 PA_DTYPE_F32 = 0
 PA_DTYPE_BF16 = 1
 PA_DTYPE_FP8_E4M3 = 2
+PA_DTYPE_INT8 = 3
 
 # Every symbol include/paged_attn.h declares, with (restype, argtypes).
 _c_void_p = ctypes.c_void_p
@@ -41,6 +42,13 @@ class PaKvPool(ctypes.Structure):
 
 
 _PPOOL = ctypes.POINTER(PaKvPool)
+
+
+class PaKvScales(ctypes.Structure):
+    _fields_ = [("key_scales", _c_void_p), ("value_scales", _c_void_p), ("block_tokens", _i32)]
+
+
+_PSCALES = ctypes.POINTER(PaKvScales)
 
 SIGNATURES = {
     "paged_kv_append": (_i32, [_PPOOL, _c_void_p, _c_void_p, _c_void_p, _i64, _c_void_p]),
@@ -75,6 +83,19 @@ SIGNATURES = {
     "paged_kv_copy_pages": (_i32, [_PPOOL, _i32, _c_void_p, _c_void_p, _i64, _c_void_p]),
     "paged_kv_compact": (_i32, [_PPOOL, _i32, _c_void_p, _i32, _c_void_p, _i32, _c_void_p, _c_void_p, _c_void_p,
                                 _i64, _c_void_p, _c_void_p]),
+    "paged_kv_append_int8": (_i32, [_PPOOL, _PSCALES, _c_void_p, _i64, _c_void_p, _i64, _c_void_p, _i64, _c_void_p]),
+    "paged_attention_decode_int8": (_i32, [_PPOOL, _PSCALES, _c_void_p, _c_void_p, _i32, _i32, _c_void_p, _i32,
+                                           _c_void_p, _i32, _f32, _c_void_p, _sz, _c_void_p]),
+    "paged_attention_prefill_int8": (_i32, [_PPOOL, _PSCALES, _c_void_p, _c_void_p, _i32, _i32, _c_void_p, _i64, _i32,
+                                            _c_void_p, _i32, _c_void_p, _i32, _f32, _c_void_p]),
+    "paged_attention_decode_mass_workspace_size": (_sz, [_i32, _i32, _i32, _i32, _i32, _i32]),
+    "paged_attention_decode_mass": (_i32, [_PPOOL, _PSCALES, _c_void_p, _c_void_p, _i32, _i32, _c_void_p, _i32,
+                                           _c_void_p, _i32, _f32, _c_void_p, _f32, _c_void_p, _i64, _c_void_p, _sz,
+                                           _c_void_p]),
+    "paged_kv_evict_rows": (_i32, [_c_void_p, _i64, _c_void_p, _i32, _i32, _i32, _i32, _i32, _c_void_p, _c_void_p, _i64,
+                                   _c_void_p, _c_void_p, _i64, _c_void_p]),
+    "paged_kv_evict_pages": (_i32, [_c_void_p, _i64, _c_void_p, _i32, _c_void_p, _i32, _i32, _i32, _i32, _i32, _i32,
+                                    _c_void_p, _c_void_p, _c_void_p, _i64, _c_void_p]),
     "pa_testing_decode_part_wait": (_i32, [_PPOOL, _c_void_p, _c_void_p, _i32, _i32, _c_void_p, _i32,
                                            _c_void_p, _i32, _f32, _c_void_p, _sz, ctypes.c_uint64, _i32,
                                            _c_void_p]),
@@ -119,6 +140,8 @@ def _dtype_code(t: torch.dtype) -> int:
         return PA_DTYPE_F32
     if t == torch.float8_e4m3fn:
         return PA_DTYPE_FP8_E4M3
+    if t == torch.int8:
+        return PA_DTYPE_INT8
     raise TypeError(f"unsupported pool dtype {t}")
 
 
@@ -146,7 +169,8 @@ def _contig(t: torch.Tensor, name: str):
 def make_pool(key_pool: torch.Tensor, value_pool: torch.Tensor, k_scale: float = 1.0,
               v_scale: float = 1.0) -> PaKvPool:
     """Describe a [num_pages, page_size, num_kv_heads, head_dim] K/V pool pair
-    (float32, bfloat16, or float8_e4m3fn with per-tensor k_scale / v_scale)."""
+    (float32, bfloat16, float8_e4m3fn with per-tensor k_scale / v_scale, or int8 for
+    the calls that take its scales and for page copies)."""
     if key_pool.shape != value_pool.shape or key_pool.dtype != value_pool.dtype:
         raise ValueError("key_pool and value_pool must match in shape and dtype")
     if key_pool.dim() != 4:
@@ -159,10 +183,10 @@ def make_pool(key_pool: torch.Tensor, value_pool: torch.Tensor, k_scale: float =
 
 
 def _q_out(q, out, key_pool):
-    """Check ``q [rows, Hq, D]`` against the pool (bf16 for bf16 and e4m3
+    """Check ``q [rows, Hq, D]`` against the pool (bf16 for bf16, e4m3 and int8
     pools, f32 for f32 pools) and return ``out`` of the same shape and dtype
     (allocated when None)."""
-    want = torch.bfloat16 if key_pool.dtype in (torch.bfloat16, torch.float8_e4m3fn) else key_pool.dtype
+    want = torch.bfloat16 if key_pool.dtype in (torch.bfloat16, torch.float8_e4m3fn, torch.int8) else key_pool.dtype
     _contig(q, "q")
     if q.dim() != 3 or q.dtype != want or q.shape[2] != key_pool.shape[3]:
         raise ValueError(f"q must be [rows, num_q_heads, {key_pool.shape[3]}] of {want}")
@@ -448,7 +472,8 @@ def _here(names, tensors) -> int:
     return cur
 
 
-_POOL_CODES = {torch.float32: PA_DTYPE_F32, torch.bfloat16: PA_DTYPE_BF16, torch.float8_e4m3fn: PA_DTYPE_FP8_E4M3}
+_POOL_CODES = {torch.float32: PA_DTYPE_F32, torch.bfloat16: PA_DTYPE_BF16, torch.float8_e4m3fn: PA_DTYPE_FP8_E4M3,
+               torch.int8: PA_DTYPE_INT8}
 
 
 def _pool_of(key_pool, value_pool, k_scale, v_scale) -> PaKvPool:
@@ -723,3 +748,235 @@ def paged_kv_compact(pools, block_table, seq_lens, keep_indptr, keep, base=None,
     if st != PA_OK:
         raise PagedAttnError(st, "paged_kv_compact")
     return new_seq_lens
+
+
+# ---- int8 pools with a scale for each block of tokens and KV head; attention weights; eviction ----
+
+def _scales_of(pool: PaKvPool, key_scales, value_scales) -> PaKvScales:
+    """The scales ``[num_pages, page_size / block_tokens, Hkv]`` float32 of an int8 pool."""
+    if pool.dtype != PA_DTYPE_INT8:
+        raise ValueError("key_pool and value_pool must be int8")
+    shape = key_scales.shape
+    if (len(shape) != 3 or shape != value_scales.shape or shape[0] != pool.num_pages or shape[2] != pool.num_kv_heads
+            or shape[1] <= 0 or pool.page_size % shape[1] != 0 or key_scales.dtype != torch.float32
+            or value_scales.dtype != torch.float32):
+        raise ValueError("key_scales and value_scales must be float32 [num_pages, page_size / block_tokens, num_kv_heads]")
+    if not key_scales.is_contiguous() or not value_scales.is_contiguous():
+        raise ValueError("key_scales and value_scales must be contiguous")
+    return PaKvScales(key_scales.data_ptr(), value_scales.data_ptr(), pool.page_size // shape[1])
+
+
+def paged_kv_append_int8(key_pool, value_pool, key_scales, value_scales, key, value, slot_mapping, stream=None):
+    """Write ``key/value [T, Hkv, D]`` (bf16; heads and dims contiguous, any token
+    stride) into int8 pools at ``slot_mapping`` (int64 ``[T]``, negative: padding),
+    keeping ``key_scales`` / ``value_scales`` (float32 ``[num_pages, page_size /
+    block_tokens, Hkv]``) of the blocks that they lie in: a block's scale is its
+    largest magnitude / 127; where it grows, the block's earlier codes are encoded
+    anew.  The tokens of one block must follow one another in the call (padding aside)."""
+    pool = _pool_of(key_pool, value_pool, 1.0, 1.0)
+    sc = _scales_of(pool, key_scales, value_scales)
+    T = slot_mapping.numel()
+    if slot_mapping.dtype != torch.int64:
+        raise TypeError("slot_mapping must be int64")
+    _contig(slot_mapping, "slot_mapping")
+    sk = _token_rows(key, "key", T, pool.num_kv_heads, pool.head_dim, torch.bfloat16)
+    sv = _token_rows(value, "value", T, pool.num_kv_heads, pool.head_dim, torch.bfloat16)
+    dev = _here("key_pool value_pool key_scales value_scales key value slot_mapping",
+                (key_pool, value_pool, key_scales, value_scales, key, value, slot_mapping))
+    st = lib().paged_kv_append_int8(ctypes.byref(pool), ctypes.byref(sc), key.data_ptr(), sk, value.data_ptr(), sv,
+                                    slot_mapping.data_ptr(), T, _raw_stream(stream, dev))
+    if st != PA_OK:
+        raise PagedAttnError(st, "paged_kv_append_int8")
+
+
+def _tables(q, block_table, seq_lens, page_size, max_seq_len):
+    """Checks of a decode's tables; max_seq_len (default: what the table holds)."""
+    _int32(block_table, "block_table")
+    _int32(seq_lens, "seq_lens")
+    B = q.shape[0]
+    if block_table.dim() != 2 or block_table.shape[0] != B or seq_lens.numel() != B:
+        raise ValueError("block_table must be [B, max_blocks] and seq_lens [B]")
+    return block_table.shape[1] * page_size if max_seq_len is None else _bound(max_seq_len, "max_seq_len")
+
+
+def paged_attention_decode_int8(key_pool, value_pool, key_scales, value_scales, q, block_table, seq_lens, scale,
+                                max_seq_len=None, out=None, workspace=None, stream=None):
+    """:func:`paged_attention_decode` over int8 pools with a scale for each block of
+    tokens and KV head (see :func:`paged_kv_append_int8`); ``q`` and ``out`` bf16."""
+    pool = _pool_of(key_pool, value_pool, 1.0, 1.0)
+    sc = _scales_of(pool, key_scales, value_scales)
+    out = _fresh(stream, lambda: _q_out(q, None, key_pool)) if out is None else _q_out(q, out, key_pool)
+    msl = _tables(q, block_table, seq_lens, pool.page_size, max_seq_len)
+    B, hq, _ = q.shape
+    dev = _here("key_pool value_pool key_scales value_scales q block_table seq_lens out workspace",
+                (key_pool, value_pool, key_scales, value_scales, q, block_table, seq_lens, out, workspace))
+    if workspace is None:
+        workspace = _fresh(stream, lambda: decode_workspace(B, hq, key_pool))
+    wbytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
+    st = lib().paged_attention_decode_int8(ctypes.byref(pool), ctypes.byref(sc), q.data_ptr(), out.data_ptr(), B, hq,
+                                           block_table.data_ptr(), block_table.shape[1], seq_lens.data_ptr(), msl,
+                                           float(scale), _addr(workspace), wbytes, _raw_stream(stream, dev))
+    if st != PA_OK:
+        raise PagedAttnError(st, "paged_attention_decode_int8")
+    return out
+
+
+def paged_attention_prefill_int8(key_pool, value_pool, key_scales, value_scales, q, query_start_loc, block_table,
+                                 seq_lens, scale, max_q_len, max_seq_len=None, out=None, stream=None):
+    """:func:`paged_attention_prefill` over int8 pools with a scale for each block of
+    tokens and KV head (see :func:`paged_kv_append_int8`); ``q`` and ``out`` bf16."""
+    pool = _pool_of(key_pool, value_pool, 1.0, 1.0)
+    sc = _scales_of(pool, key_scales, value_scales)
+    _int32(query_start_loc, "query_start_loc")
+    _int32(block_table, "block_table")
+    _int32(seq_lens, "seq_lens")
+    out = _fresh(stream, lambda: _q_out(q, None, key_pool)) if out is None else _q_out(q, out, key_pool)
+    T, hq, _ = q.shape
+    B = query_start_loc.numel() - 1
+    if block_table.dim() != 2 or block_table.shape[0] != B or seq_lens.numel() != B:
+        raise ValueError("block_table must be [B, max_blocks] and seq_lens [B], with query_start_loc [B + 1]")
+    mb = block_table.shape[1]
+    msl = mb * pool.page_size if max_seq_len is None else _bound(max_seq_len, "max_seq_len")
+    dev = _here("key_pool value_pool key_scales value_scales q query_start_loc block_table seq_lens out",
+                (key_pool, value_pool, key_scales, value_scales, q, query_start_loc, block_table, seq_lens, out))
+    st = lib().paged_attention_prefill_int8(ctypes.byref(pool), ctypes.byref(sc), q.data_ptr(), out.data_ptr(), B, hq,
+                                            query_start_loc.data_ptr(), T, _bound(max_q_len, "max_q_len"),
+                                            block_table.data_ptr(), mb, seq_lens.data_ptr(), msl, float(scale),
+                                            _raw_stream(stream, dev))
+    if st != PA_OK:
+        raise PagedAttnError(st, "paged_attention_prefill_int8")
+    return out
+
+
+def decode_mass_workspace(batch, num_q_heads, key_pool, max_seq_len, device=None) -> Optional[torch.Tensor]:
+    """Allocate (with torch) the scratch buffer paged_attention_decode_mass needs."""
+    n = int(lib().paged_attention_decode_mass_workspace_size(batch, num_q_heads, key_pool.shape[2], key_pool.shape[3],
+                                                             _dtype_code(key_pool.dtype),
+                                                             _bound(max_seq_len, "max_seq_len")))
+    if n == 0:
+        return None
+    return torch.empty(n, dtype=torch.uint8, device=device or key_pool.device)
+
+
+def _mass_rows(t, name, B, width):
+    """Floats between the rows of ``t [B, width or more]`` float32 (entries of a row contiguous)."""
+    if t.dtype != torch.float32 or t.dim() != 2 or t.shape[0] != B or t.shape[1] < width:
+        raise ValueError(f"{name} must be float32 [{B}, {width} or more]")
+    if t.shape[1] > 1 and t.stride(1) != 1:
+        raise ValueError(f"the rows of {name} must be contiguous")
+    return t.stride(0) if B > 1 else max(t.shape[1], 1)
+
+
+def paged_attention_decode_mass(key_pool, value_pool, q, block_table, seq_lens, scale, mass_out, mass_in=None, decay=1.0,
+                                max_seq_len=None, out=None, workspace=None, stream=None, k_scale=1.0, v_scale=1.0,
+                                key_scales=None, value_scales=None):
+    """Decode attention that also gives every key's attention weight, summed over the
+    query heads: ``mass_out[b, j] = decay * mass_in[b, j] + sum of its weights`` for
+    ``j < seq_lens[b]`` (float32 ``[B, max_seq_len or more]``; ``mass_in`` None: 0, or
+    ``mass_out`` itself).  ``k_scale`` / ``v_scale`` apply to e4m3 pools,
+    ``key_scales`` / ``value_scales`` to int8 pools.  Returns ``out [B, Hq, D]``."""
+    pool = _pool_of(key_pool, value_pool, k_scale, v_scale)
+    if (key_scales is None) != (value_scales is None) or (key_scales is not None) != (pool.dtype == PA_DTYPE_INT8):
+        raise ValueError("key_scales and value_scales belong to int8 pools")
+    sc = None if key_scales is None else ctypes.byref(_scales_of(pool, key_scales, value_scales))
+    out = _fresh(stream, lambda: _q_out(q, None, key_pool)) if out is None else _q_out(q, out, key_pool)
+    msl = _tables(q, block_table, seq_lens, pool.page_size, max_seq_len)
+    B, hq, _ = q.shape
+    stride = _mass_rows(mass_out, "mass_out", B, msl)
+    if mass_in is not None and _mass_rows(mass_in, "mass_in", B, msl) != stride:
+        raise ValueError("mass_in and mass_out must have the same row stride")
+    dev = _here("key_pool value_pool key_scales value_scales q block_table seq_lens mass_out mass_in out workspace",
+                (key_pool, value_pool, key_scales, value_scales, q, block_table, seq_lens, mass_out, mass_in, out, workspace))
+    if workspace is None:
+        workspace = _fresh(stream, lambda: decode_mass_workspace(B, hq, key_pool, msl))
+    wbytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
+    st = lib().paged_attention_decode_mass(ctypes.byref(pool), sc, q.data_ptr(), out.data_ptr(), B, hq,
+                                           block_table.data_ptr(), block_table.shape[1], seq_lens.data_ptr(), msl,
+                                           float(scale), _addr(mass_in), float(decay), mass_out.data_ptr(), stride,
+                                           _addr(workspace), wbytes, _raw_stream(stream, dev))
+    if st != PA_OK:
+        raise PagedAttnError(st, "paged_attention_decode_mass")
+    return out
+
+
+def paged_kv_evict_rows(mass, seq_lens, budget, num_sinks=0, num_recent=0, keep_indptr=None, keep=None, base=None,
+                        new_mass=None, stream=None):
+    """Choose the rows that stay by their accumulated weight ``mass`` float32 ``[B,
+    width]``: a sequence of more than ``budget`` rows keeps its first ``num_sinks``, its
+    last ``num_recent`` and the heaviest of the others (ties: the lower position).
+
+    Returns ``(keep_indptr [B + 1], keep, base [B], new_mass [B, width])``: the first
+    three are what :func:`paged_kv_compact` takes (``keep`` has room for ``B * (budget -
+    num_sinks)`` rows, entries past ``keep_indptr[B]`` are left), ``new_mass`` the masses
+    of the rows that stay, zeros behind them."""
+    if mass.dim() != 2:
+        raise ValueError("mass must be float32 [B, width]")
+    B, width = mass.shape
+    ms = _mass_rows(mass, "mass", B, width)
+    _int32(seq_lens, "seq_lens")
+    budget, num_sinks, num_recent = (_bound(v, n) for v, n in ((budget, "budget"), (num_sinks, "num_sinks"),
+                                                               (num_recent, "num_recent")))
+    if seq_lens.numel() != B:
+        raise ValueError("seq_lens must be [B]")
+    dev = _here("mass seq_lens keep_indptr keep base new_mass", (mass, seq_lens, keep_indptr, keep, base, new_mass))
+    int32 = lambda n: _fresh(stream, lambda: torch.empty(n, dtype=torch.int32, device=mass.device))
+    for name, t, n in (("keep_indptr", keep_indptr, B + 1), ("keep", keep, None), ("base", base, B)):
+        if t is not None:
+            _int32(t, name)
+            if n is not None and t.numel() != n:
+                raise ValueError(f"{name} must be [{n}]")
+    if keep_indptr is None:
+        keep_indptr = int32(B + 1)
+    if keep is None:
+        keep = int32(0 if budget >= width else max(0, B * (budget - num_sinks)))
+    if base is None:
+        base = int32(B)
+    if new_mass is None:
+        new_mass = _fresh(stream, lambda: torch.empty((B, width), dtype=torch.float32, device=mass.device))
+    ns = _mass_rows(new_mass, "new_mass", B, width)
+    st = lib().paged_kv_evict_rows(mass.data_ptr(), ms, seq_lens.data_ptr(), B, width, budget, num_sinks, num_recent,
+                                   keep_indptr.data_ptr(), keep.data_ptr(), keep.numel(), base.data_ptr(),
+                                   new_mass.data_ptr(), ns, _raw_stream(stream, dev))
+    if st != PA_OK:
+        raise PagedAttnError(st, "paged_kv_evict_rows")
+    return keep_indptr, keep, base, new_mass
+
+
+def paged_kv_evict_pages(mass, block_table, seq_lens, page_size, budget, num_sinks=0, num_recent=0, new_block_table=None,
+                         new_seq_lens=None, new_mass=None, stream=None):
+    """The same by whole pages, ``budget`` of them a sequence, for pools of any type:
+    the pages that hold the first ``num_sinks`` and the last ``num_recent`` rows stay,
+    and the heaviest of the others by the sum of their rows' ``mass`` float32 ``[B,
+    width]``.  Returns ``(new_block_table [B, max_blocks], new_seq_lens [B], new_mass [B,
+    width])``: a row of the table lists the pages that stay and behind them those that
+    go (free from ``ceil(new_seq_lens / page_size)`` on)."""
+    if mass.dim() != 2:
+        raise ValueError("mass must be float32 [B, width]")
+    B, width = mass.shape
+    ms = _mass_rows(mass, "mass", B, width)
+    _int32(block_table, "block_table")
+    _int32(seq_lens, "seq_lens")
+    if block_table.dim() != 2 or block_table.shape[0] != B or seq_lens.numel() != B:
+        raise ValueError("block_table must be [B, max_blocks] and seq_lens [B]")
+    for name, t, like in (("new_block_table", new_block_table, block_table), ("new_seq_lens", new_seq_lens, seq_lens)):
+        if t is not None:
+            _int32(t, name)
+            if t.shape != like.shape:
+                raise ValueError(f"{name} must have the shape of {name[4:]}")
+    dev = _here("mass block_table seq_lens new_block_table new_seq_lens new_mass",
+                (mass, block_table, seq_lens, new_block_table, new_seq_lens, new_mass))
+    if new_block_table is None:
+        new_block_table = _fresh(stream, lambda: torch.empty_like(block_table))
+    if new_seq_lens is None:
+        new_seq_lens = _fresh(stream, lambda: torch.empty_like(seq_lens))
+    if new_mass is None:
+        new_mass = _fresh(stream, lambda: torch.empty((B, width), dtype=torch.float32, device=mass.device))
+    ns = _mass_rows(new_mass, "new_mass", B, width)
+    st = lib().paged_kv_evict_pages(mass.data_ptr(), ms, block_table.data_ptr(), block_table.shape[1],
+                                    seq_lens.data_ptr(), B, width, _bound(page_size, "page_size"),
+                                    _bound(budget, "budget"), _bound(num_sinks, "num_sinks"),
+                                    _bound(num_recent, "num_recent"), new_block_table.data_ptr(),
+                                    new_seq_lens.data_ptr(), new_mass.data_ptr(), ns, _raw_stream(stream, dev))
+    if st != PA_OK:
+        raise PagedAttnError(st, "paged_kv_evict_pages")
+    return new_block_table, new_seq_lens, new_mass

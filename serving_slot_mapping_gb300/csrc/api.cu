@@ -59,9 +59,12 @@ bool is_pow2(int64_t x) { return x > 0 && (x & (x - 1)) == 0; }
 
 bool aligned(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
 
-size_t elem_size(int32_t dtype) { return dtype == PA_DTYPE_F32 ? 4 : (dtype == PA_DTYPE_FP8_E4M3 ? 1 : 2); }
+size_t elem_size(int32_t dtype) {
+  return dtype == PA_DTYPE_F32 ? 4 : (dtype == PA_DTYPE_FP8_E4M3 || dtype == PA_DTYPE_INT8 ? 1 : 2);
+}
 
 bool kv8(const pa_kv_pool* pool) { return pool->dtype == PA_DTYPE_FP8_E4M3; }
+bool int8(const pa_kv_pool* pool) { return pool->dtype == PA_DTYPE_INT8; }
 
 // Pages the TMA boxes of the tensor-core kernels take: whole 8-slot blocks.
 bool tma_pages(const pa_kv_pool* pool) { return is_pow2(pool->page_size) && pool->page_size >= 8; }
@@ -72,9 +75,12 @@ bool core_path(const pa_kv_pool* pool) {
   return pool->dtype == PA_DTYPE_F32 || (pool->dtype == PA_DTYPE_BF16 && !tma_pages(pool));
 }
 
-pa_status check_pool(const pa_kv_pool* pool) {
+// int8_ok: int8 pools too, which only the calls that take their scales (and page
+// copies) know.
+pa_status check_pool(const pa_kv_pool* pool, bool int8_ok = false) {
   if (pool == nullptr || pool->key_pool == nullptr || pool->value_pool == nullptr) return PA_ERR_NULL;
-  if (pool->dtype != PA_DTYPE_F32 && pool->dtype != PA_DTYPE_BF16 && pool->dtype != PA_DTYPE_FP8_E4M3)
+  if (pool->dtype != PA_DTYPE_F32 && pool->dtype != PA_DTYPE_BF16 && pool->dtype != PA_DTYPE_FP8_E4M3 &&
+      !(int8_ok && int8(pool)))
     return PA_ERR_DTYPE;
   if (kv8(pool) && !(std::isfinite(pool->k_scale) && pool->k_scale > 0.f && std::isfinite(pool->v_scale) &&
                      pool->v_scale > 0.f))
@@ -101,8 +107,8 @@ pa::PoolGeom geom(const pa_kv_pool* pool) {
 
 // Shape checks common to decode and prefill.
 pa_status check_attention(const pa_kv_pool* pool, int32_t batch, int32_t num_q_heads,
-                          int32_t max_blocks_per_seq, int32_t max_seq_len, float scale) {
-  pa_status st = check_pool(pool);
+                          int32_t max_blocks_per_seq, int32_t max_seq_len, float scale, bool int8_ok = false) {
+  pa_status st = check_pool(pool, int8_ok);
   if (st != PA_OK) return st;
   if (batch < 0 || num_q_heads <= 0 || max_blocks_per_seq <= 0 || max_seq_len < 0) return PA_ERR_SHAPE;
   if (num_q_heads % pool->num_kv_heads != 0) return PA_ERR_SHAPE;
@@ -118,6 +124,22 @@ pa_status check_attention(const pa_kv_pool* pool, int32_t batch, int32_t num_q_h
   } else {
     if (pool->head_dim > 256) return PA_ERR_UNSUPPORTED;
   }
+  return PA_OK;
+}
+
+// An int8 pool and its scales: what every call on them asks for.
+pa_status check_int8(const pa_kv_pool* pool, const pa_kv_scales* scales) {
+  if (pool != nullptr && !int8(pool)) return PA_ERR_DTYPE;
+  const pa_status st = check_pool(pool, true);
+  if (st != PA_OK) return st;
+  if (scales == nullptr || scales->key_scales == nullptr || scales->value_scales == nullptr) return PA_ERR_NULL;
+  if (scales->block_tokens <= 0 || scales->block_tokens > pool->page_size) return PA_ERR_SHAPE;
+  if (!is_pow2(pool->page_size) || !is_pow2(scales->block_tokens) || scales->block_tokens < 16) return PA_ERR_UNSUPPORTED;
+  if (pool->head_dim != 64 && pool->head_dim != 128) return PA_ERR_UNSUPPORTED;
+  if (pool->num_pages * (int64_t)pool->page_size > INT32_MAX) return PA_ERR_RANGE;
+  if (!aligned(pool->key_pool, 16) || !aligned(pool->value_pool, 16) || !aligned(scales->key_scales, 16) ||
+      !aligned(scales->value_scales, 16))
+    return PA_ERR_ALIGN;
   return PA_OK;
 }
 
@@ -195,7 +217,7 @@ pa_status paged_kv_append(const pa_kv_pool* pool, const void* key, const void* v
 
 size_t paged_attention_decode_workspace_size(int32_t batch, int32_t num_q_heads, int32_t num_kv_heads,
                                              int32_t head_dim, int32_t dtype) {
-  if (dtype != PA_DTYPE_BF16 && dtype != PA_DTYPE_FP8_E4M3) return 0;
+  if (dtype != PA_DTYPE_BF16 && dtype != PA_DTYPE_FP8_E4M3 && dtype != PA_DTYPE_INT8) return 0;
   if (num_kv_heads <= 0 || num_q_heads <= 0) return 0;
   // heads per box for page_size >= 16 is an upper bound for every page size
   const int hb = pa::decode_heads_per_box(num_kv_heads, num_q_heads / num_kv_heads, 16);
@@ -287,7 +309,8 @@ pa_status bf16_decode_params(const pa_kv_pool* pool, const void* q, void* out, i
   if (need > 0 && (workspace == nullptr || workspace_bytes < need)) return PA_ERR_WORKSPACE;
   if (!aligned(workspace, 16)) return PA_ERR_ALIGN;
   const int budget = max_smem_optin();
-  if (pa::decode_smem_bytes(pool->head_dim, group, batch, hb, budget, kv8(pool)) > (size_t)budget)
+  const bool codes = kv8(pool) || int8(pool);
+  if (pa::decode_smem_bytes(pool->head_dim, group, batch, hb, budget, codes, int8(pool)) > (size_t)budget)
     return PA_ERR_UNSUPPORTED;
   const int64_t slots = pa::decode_partial_slots(batch, pool->num_kv_heads, ctas, hb);
   *p = pa::DecodeParams{};
@@ -313,12 +336,12 @@ pa_status bf16_decode_params(const pa_kv_pool* pool, const void* q, void* out, i
   p->heads_per_box = hb;
   p->smem_budget = budget;
   // e4m3 pools: S = scale * k_scale * q . e4m3(K), O = v_scale * softmax(S) e4m3(V)
-  p->kv8 = kv8(pool) ? 1 : 0;
+  p->kv8 = codes ? 1 : 0;
   p->scale_log2 = (float)((double)scale * (kv8(pool) ? (double)pool->k_scale : 1.0) * kLog2e);
   p->v_scale = kv8(pool) ? pool->v_scale : 1.f;
   // segment changes weigh in the cut (32-row groups; 16-row groups of few long
   // sequences); positions are counted in 32 bits
-  const int pen = pa::decode_segment_penalty(pool->head_dim, hb, group, kv8(pool), batch, pool->num_kv_heads, ctas);
+  const int pen = pa::decode_segment_penalty(pool->head_dim, hb, group, codes, batch, pool->num_kv_heads, ctas);
   const int64_t max_keys = std::max<int64_t>(max_seq_len, (int64_t)t.max_blocks * pool->page_size);
   p->seg_penalty = (int64_t)batch * ((max_keys + 15) / 16 + pen) <= INT32_MAX ? pen : 0;
   p->window = win.size != INT32_MAX ? win.size : 0;
@@ -423,8 +446,9 @@ pa_status decode_impl(const pa_kv_pool* pool, const void* q, void* out, int32_t 
 
 pa_status prefill_impl(const pa_kv_pool* pool, const void* q, void* out, int32_t batch, int32_t num_q_heads,
                        const int32_t* query_start_loc, int64_t total_q, int32_t max_q_len, const Table& t,
-                       int32_t max_seq_len, float scale, void* stream, const Window& win = Window{}) {
-  pa_status st = check_attention(pool, batch, num_q_heads, t.max_blocks, max_seq_len, scale);
+                       int32_t max_seq_len, float scale, void* stream, const Window& win = Window{},
+                       const pa_kv_scales* scales = nullptr) {
+  pa_status st = check_attention(pool, batch, num_q_heads, t.max_blocks, max_seq_len, scale, scales != nullptr);
   if (st != PA_OK) return st;
   if (total_q < 0 || max_q_len < 0 || total_q > INT32_MAX) return PA_ERR_SHAPE;
   if (batch == 0 || total_q == 0) return PA_OK;
@@ -482,12 +506,18 @@ pa_status prefill_impl(const pa_kv_pool* pool, const void* q, void* out, int32_t
   p.max_blocks = t.max_blocks;
   p.max_q_len = max_q_len;
   // e4m3 pools: S = scale * k_scale * q . e4m3(K), O = v_scale * softmax(S) e4m3(V)
-  p.kv8 = kv8(pool) ? 1 : 0;
+  p.kv8 = kv8(pool) || int8(pool) ? 1 : 0;
   p.scale_log2 = (float)((double)scale * (kv8(pool) ? (double)pool->k_scale : 1.0) * kLog2e);
   p.v_scale = kv8(pool) ? pool->v_scale : 1.f;
+  if (scales != nullptr) {
+    p.key_scales = scales->key_scales;
+    p.value_scales = scales->value_scales;
+    p.scale_shift = pa::ilog2_pow2(scales->block_tokens);
+  }
   p.window = win.size != INT32_MAX ? win.size : 0;
   p.num_sinks = win.size != INT32_MAX ? win.sinks : 0;
   p.err = error_word();
+  if (scales != nullptr) p.window = INT32_MAX;  // the windowed kernel, every key in the window
   if (p.window > 0) {
     // q rows are read and out rows written 16 bytes at a time; a slot is 32 bits
     if (!aligned(q, 16) || !aligned(out, 16)) return PA_ERR_ALIGN;
@@ -812,14 +842,14 @@ constexpr int32_t kMaxPools = 1024;
 // The pools of one call over all layers: each valid, all of one geometry and
 // element type, and no two tensors of them overlapping (a row would be moved
 // twice).
-pa_status check_pools(const pa_kv_pool* pools, int32_t num_pools) {
+pa_status check_pools(const pa_kv_pool* pools, int32_t num_pools, bool int8_ok = false) {
   if (num_pools < 0) return PA_ERR_SHAPE;
   if (num_pools > kMaxPools) return PA_ERR_RANGE;
   if (num_pools == 0) return PA_OK;
   if (pools == nullptr) return PA_ERR_NULL;
   uintptr_t starts[2 * kMaxPools];
   for (int32_t i = 0; i < num_pools; ++i) {
-    const pa_status st = check_pool(pools + i);
+    const pa_status st = check_pool(pools + i, int8_ok);
     if (st != PA_OK) return st;
     if (pools[i].num_pages != pools[0].num_pages || pools[i].page_size != pools[0].page_size ||
         pools[i].num_kv_heads != pools[0].num_kv_heads || pools[i].head_dim != pools[0].head_dim ||
@@ -856,7 +886,7 @@ void fill_pools(pa::PoolList* list, const pa_kv_pool* pools, int32_t first, int3
 
 pa_status paged_kv_copy_pages(const pa_kv_pool* pools, int32_t num_pools, const int32_t* src_pages,
                               const int32_t* dst_pages, int64_t num_copies, void* stream) {
-  const pa_status st = check_pools(pools, num_pools);
+  const pa_status st = check_pools(pools, num_pools, true);
   if (st != PA_OK) return st;
   if (num_copies < 0) return PA_ERR_SHAPE;
   if (num_copies > INT32_MAX) return PA_ERR_RANGE;
@@ -923,6 +953,273 @@ pa_status paged_kv_compact(const pa_kv_pool* pools, int32_t num_pools, const int
     p.new_seq_lens = nullptr;  // written by the first launch
   }
   return PA_OK;
+}
+
+pa_status paged_kv_append_int8(const pa_kv_pool* pool, const pa_kv_scales* scales, const void* key, int64_t key_stride,
+                               const void* value, int64_t value_stride, const int64_t* slot_mapping,
+                               int64_t num_tokens, void* stream) {
+  const pa_status st = check_int8(pool, scales);
+  if (st != PA_OK) return st;
+  if (num_tokens < 0) return PA_ERR_SHAPE;
+  const int64_t row = (int64_t)pool->num_kv_heads * pool->head_dim;
+  if (row > INT32_MAX || num_tokens > INT32_MAX) return PA_ERR_RANGE;
+  if (num_tokens > 1 && (key_stride < row || value_stride < row)) return PA_ERR_SHAPE;
+  if (num_tokens > 1 && std::max(key_stride, value_stride) > INT32_MAX) return PA_ERR_RANGE;
+  if (num_tokens == 0) return PA_OK;
+  if (key == nullptr || value == nullptr || slot_mapping == nullptr) return PA_ERR_NULL;
+  if (!aligned(slot_mapping, 8) || !aligned(key, 16) || !aligned(value, 16) ||
+      (num_tokens > 1 && (key_stride % 8 != 0 || value_stride % 8 != 0)))
+    return PA_ERR_ALIGN;
+  pa::AppendInt8Params p{};
+  p.key_pool = pool->key_pool;
+  p.value_pool = pool->value_pool;
+  p.key_scales = scales->key_scales;
+  p.value_scales = scales->value_scales;
+  p.key = key;
+  p.value = value;
+  p.key_stride = key_stride;
+  p.value_stride = value_stride;
+  p.slot_mapping = slot_mapping;
+  p.num_tokens = num_tokens;
+  p.num_slots = pool->num_pages * (int64_t)pool->page_size;
+  p.num_kv_heads = pool->num_kv_heads;
+  p.head_dim = pool->head_dim;
+  p.scale_shift = pa::ilog2_pow2(scales->block_tokens);
+  p.err = error_word();
+  return launched(pa::launch_append_int8(p, num_sms(), static_cast<cudaStream_t>(stream)));
+}
+
+namespace {
+
+// The launch parameters of a decode over an int8 pool (scales given) or another
+// tensor-core pool, after every check that the two calls below share.
+pa_status ext_decode_params(const pa_kv_pool* pool, const pa_kv_scales* scales, const void* q, void* out, int32_t batch,
+                            int32_t num_q_heads, const Table& t, int32_t max_seq_len, float scale, void* workspace,
+                            size_t workspace_bytes, pa::DecodeParams* p) {
+  if (q == nullptr || out == nullptr) return PA_ERR_NULL;
+  pa_status st = check_table(t);
+  if (st != PA_OK) return st;
+  if (q == out) return PA_ERR_SHAPE;
+  if (!aligned(out, 8)) return PA_ERR_ALIGN;
+  st = bf16_decode_params(pool, q, out, batch, num_q_heads, t, max_seq_len, scale, workspace, workspace_bytes, p);
+  if (st != PA_OK || scales == nullptr) return st;
+  p->key_scales = scales->key_scales;
+  p->value_scales = scales->value_scales;
+  p->scale_shift = pa::ilog2_pow2(scales->block_tokens);
+  return PA_OK;
+}
+
+// Bytes of the scores and sums behind a decode's own workspace.
+int64_t score_stride(int32_t max_seq_len) { return align_up((size_t)max_seq_len, 16); }
+size_t lse_bytes(int32_t batch, int32_t num_q_heads) { return align_up((size_t)batch * num_q_heads * 4, 256); }
+
+}  // namespace
+
+pa_status paged_attention_decode_int8(const pa_kv_pool* pool, const pa_kv_scales* scales, const void* q, void* out,
+                                      int32_t batch, int32_t num_q_heads, const int32_t* block_table,
+                                      int32_t max_blocks_per_seq, const int32_t* seq_lens, int32_t max_seq_len,
+                                      float scale, void* workspace, size_t workspace_bytes, void* stream) {
+  pa_status st = check_int8(pool, scales);
+  if (st != PA_OK) return st;
+  st = check_attention(pool, batch, num_q_heads, max_blocks_per_seq, max_seq_len, scale, true);
+  if (st != PA_OK) return st;
+  if (batch == 0) return PA_OK;
+  pa::DecodeParams p;
+  st = ext_decode_params(pool, scales, q, out, batch, num_q_heads, dense_table(block_table, max_blocks_per_seq, seq_lens),
+                         max_seq_len, scale, workspace, workspace_bytes, &p);
+  if (st != PA_OK) return st;
+  return launched(pa::launch_decode_int8(p, static_cast<cudaStream_t>(stream)));
+}
+
+pa_status paged_attention_prefill_int8(const pa_kv_pool* pool, const pa_kv_scales* scales, const void* q, void* out,
+                                       int32_t batch, int32_t num_q_heads, const int32_t* query_start_loc,
+                                       int64_t total_q, int32_t max_q_len, const int32_t* block_table,
+                                       int32_t max_blocks_per_seq, const int32_t* seq_lens, int32_t max_seq_len,
+                                       float scale, void* stream) {
+  const pa_status st = check_int8(pool, scales);
+  if (st != PA_OK) return st;
+  return prefill_impl(pool, q, out, batch, num_q_heads, query_start_loc, total_q, max_q_len,
+                      dense_table(block_table, max_blocks_per_seq, seq_lens), max_seq_len, scale, stream, Window{}, scales);
+}
+
+size_t paged_attention_decode_mass_workspace_size(int32_t batch, int32_t num_q_heads, int32_t num_kv_heads,
+                                                  int32_t head_dim, int32_t dtype, int32_t max_seq_len) {
+  const size_t own = paged_attention_decode_workspace_size(batch, num_q_heads, num_kv_heads, head_dim, dtype);
+  if (own == 0 || max_seq_len < 0) return 0;
+  return align_up(own, 256) + lse_bytes(batch, num_q_heads) +
+         (size_t)batch * num_q_heads * (size_t)score_stride(max_seq_len) * 4;
+}
+
+pa_status paged_attention_decode_mass(const pa_kv_pool* pool, const pa_kv_scales* scales, const void* q, void* out,
+                                      int32_t batch, int32_t num_q_heads, const int32_t* block_table,
+                                      int32_t max_blocks_per_seq, const int32_t* seq_lens, int32_t max_seq_len,
+                                      float scale, const float* mass_in, float decay, float* mass_out,
+                                      int64_t mass_stride, void* workspace, size_t workspace_bytes, void* stream) {
+  const bool codes8 = pool != nullptr && int8(pool);
+  pa_status st = codes8 ? check_int8(pool, scales) : PA_OK;
+  if (st != PA_OK) return st;
+  st = check_attention(pool, batch, num_q_heads, max_blocks_per_seq, max_seq_len, scale, true);
+  if (st != PA_OK) return st;
+  if (core_path(pool)) return PA_ERR_UNSUPPORTED;  // the scores are those of the tensor-core kernel
+  if (batch > 65535) return PA_ERR_RANGE;          // grid y
+  if (!std::isfinite(decay)) return PA_ERR_RANGE;
+  if (mass_stride < max_seq_len) return PA_ERR_SHAPE;
+  if (mass_stride > INT32_MAX) return PA_ERR_RANGE;
+  if (batch == 0) return PA_OK;
+  if (mass_out == nullptr) return PA_ERR_NULL;
+  if (!aligned(mass_in, 4) || !aligned(mass_out, 4)) return PA_ERR_ALIGN;
+  // the same rows, or others
+  const int64_t mass_bytes = ((batch - 1) * mass_stride + max_seq_len) * 4;
+  if (mass_in != nullptr && mass_in != mass_out && meet(mass_in, mass_bytes, mass_out, mass_bytes)) return PA_ERR_SHAPE;
+  const size_t need = paged_attention_decode_mass_workspace_size(batch, num_q_heads, pool->num_kv_heads, pool->head_dim,
+                                                                 pool->dtype, max_seq_len);
+  if (workspace == nullptr || workspace_bytes < need) return PA_ERR_WORKSPACE;
+  const size_t own = paged_attention_decode_workspace_size(batch, num_q_heads, pool->num_kv_heads, pool->head_dim, pool->dtype);
+  pa::DecodeParams p;
+  st = ext_decode_params(pool, codes8 ? scales : nullptr, q, out, batch, num_q_heads,
+                         dense_table(block_table, max_blocks_per_seq, seq_lens), max_seq_len, scale, workspace, own, &p);
+  if (st != PA_OK) return st;
+  char* ws = static_cast<char*>(workspace) + align_up(own, 256);
+  p.lse = reinterpret_cast<float*>(ws);
+  p.scores = reinterpret_cast<float*>(ws + lse_bytes(batch, num_q_heads));
+  p.score_stride = score_stride(max_seq_len);
+  p.max_keys = max_seq_len;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  st = launched(pa::launch_decode_scores(p, s));
+  if (st != PA_OK) return st;
+  pa::KeyMassParams m{};
+  m.scores = p.scores;
+  m.lse = p.lse;
+  m.score_stride = p.score_stride;
+  m.seq_lens = seq_lens;
+  m.mass_in = mass_in;
+  m.mass_out = mass_out;
+  m.mass_stride = mass_stride;
+  m.decay = decay;
+  m.batch = batch;
+  m.num_q_heads = num_q_heads;
+  m.max_keys = max_seq_len;
+  m.max_len = std::min<int32_t>(max_seq_len, max_blocks_per_seq * pool->page_size);
+  return launched(pa::launch_key_mass(m, s));
+}
+
+namespace {
+
+// What the two forms of eviction share; the caller has set its own arrays.
+pa_status check_evict(const float* mass, int64_t mass_stride, const int32_t* seq_lens, int32_t batch, int32_t width,
+                      int32_t budget, int32_t num_sinks, int32_t num_recent, const float* new_mass,
+                      int64_t new_mass_stride, int32_t protect) {
+  if (batch < 0 || width < 0 || budget < 0 || num_sinks < 0 || num_recent < 0) return PA_ERR_SHAPE;
+  if (mass_stride < width || new_mass_stride < width || protect > budget) return PA_ERR_SHAPE;
+  if (batch > INT32_MAX / 8 || mass_stride > INT32_MAX || new_mass_stride > INT32_MAX) return PA_ERR_RANGE;
+  if (batch == 0) return PA_OK;
+  if (seq_lens == nullptr || (width > 0 && (mass == nullptr || new_mass == nullptr))) return PA_ERR_NULL;
+  if (!aligned(mass, 4) || !aligned(new_mass, 4) || !aligned(seq_lens, 4)) return PA_ERR_ALIGN;
+  return PA_OK;
+}
+
+// Whether an output meets one of the inputs of n entries of 4 bytes each.
+struct Span {
+  const void* at;
+  int64_t n;
+};
+bool any_meet(const Span* outs, int n_outs, const Span* ins, int n_ins) {
+  for (int i = 0; i < n_outs; ++i) {
+    if (outs[i].n <= 0) continue;
+    for (int k = 0; k < n_ins; ++k)
+      if (ins[k].n > 0 && meet(outs[i].at, outs[i].n * 4, ins[k].at, ins[k].n * 4)) return true;
+    for (int k = 0; k < i; ++k)
+      if (outs[k].n > 0 && meet(outs[i].at, outs[i].n * 4, outs[k].at, outs[k].n * 4)) return true;
+  }
+  return false;
+}
+
+}  // namespace
+
+pa_status paged_kv_evict_rows(const float* mass, int64_t mass_stride, const int32_t* seq_lens, int32_t batch,
+                              int32_t width, int32_t budget, int32_t num_sinks, int32_t num_recent,
+                              int32_t* keep_indptr, int32_t* keep, int64_t num_keep, int32_t* base, float* new_mass,
+                              int64_t new_mass_stride, void* stream) {
+  const int64_t protect = (int64_t)std::max(num_sinks, 0) + std::max(num_recent, 0);
+  const pa_status st = check_evict(mass, mass_stride, seq_lens, batch, width, budget, num_sinks, num_recent, new_mass,
+                                   new_mass_stride, (int32_t)std::min<int64_t>(protect, INT32_MAX));
+  if (st != PA_OK) return st;
+  const int64_t list = (int64_t)batch * (budget - num_sinks);
+  if (num_keep < 0) return PA_ERR_SHAPE;
+  // no sequence is over a budget that its row cannot hold: nothing is listed then
+  const int64_t need = budget >= width ? 0 : list;
+  if (need > INT32_MAX) return PA_ERR_RANGE;
+  if (num_keep < need) return PA_ERR_SHAPE;
+  if (batch == 0) return PA_OK;
+  if (keep_indptr == nullptr || base == nullptr || (keep == nullptr && need > 0)) return PA_ERR_NULL;
+  if (!aligned(keep_indptr, 4) || !aligned(keep, 4) || !aligned(base, 4)) return PA_ERR_ALIGN;
+  const Span outs[] = {{keep_indptr, batch + 1}, {keep, need}, {base, batch},
+                       {new_mass, width > 0 ? (batch - 1) * new_mass_stride + width : 0}};
+  const Span ins[] = {{mass, width > 0 ? (batch - 1) * mass_stride + width : 0}, {seq_lens, batch}};
+  if (any_meet(outs, 4, ins, 2)) return PA_ERR_SHAPE;
+  pa::EvictParams p{};
+  p.mass = mass;
+  p.new_mass = new_mass;
+  p.mass_stride = mass_stride;
+  p.new_mass_stride = new_mass_stride;
+  p.seq_lens = seq_lens;
+  p.batch = batch;
+  p.width = width;
+  p.max_len = width;
+  p.budget = budget;
+  p.num_sinks = num_sinks;
+  p.num_recent = num_recent;
+  p.keep_indptr = keep_indptr;
+  p.keep = keep;
+  p.base = base;
+  p.page_size = 1;
+  p.err = error_word();
+  return launched(pa::launch_evict(p, false, num_sms(), static_cast<cudaStream_t>(stream)));
+}
+
+pa_status paged_kv_evict_pages(const float* mass, int64_t mass_stride, const int32_t* block_table,
+                               int32_t max_blocks_per_seq, const int32_t* seq_lens, int32_t batch, int32_t width,
+                               int32_t page_size, int32_t budget, int32_t num_sinks, int32_t num_recent,
+                               int32_t* new_block_table, int32_t* new_seq_lens, float* new_mass,
+                               int64_t new_mass_stride, void* stream) {
+  if (page_size <= 0 || max_blocks_per_seq <= 0) return PA_ERR_SHAPE;
+  if (!is_pow2(page_size) || page_size > 1024) return PA_ERR_UNSUPPORTED;
+  if ((int64_t)max_blocks_per_seq * page_size > INT32_MAX) return PA_ERR_RANGE;
+  // pages that hold sinks, and the most that the last max(num_recent, 1) rows lie in
+  const int64_t recent = std::max(num_recent, 1);
+  const int64_t protect = ((int64_t)std::max(num_sinks, 0) + page_size - 1) / page_size + (recent + page_size - 2) / page_size + 1;
+  const pa_status st = check_evict(mass, mass_stride, seq_lens, batch, width, budget, num_sinks, num_recent, new_mass,
+                                   new_mass_stride, (int32_t)std::min<int64_t>(protect, INT32_MAX));
+  if (st != PA_OK) return st;
+  const int32_t max_len = (int32_t)std::min<int64_t>(width, (int64_t)max_blocks_per_seq * page_size);
+  if ((max_len + (int64_t)page_size - 1) / page_size > pa::kMaxEvictPages) return PA_ERR_RANGE;
+  if (batch == 0) return PA_OK;
+  if (block_table == nullptr || new_block_table == nullptr || new_seq_lens == nullptr) return PA_ERR_NULL;
+  if (!aligned(block_table, 4) || !aligned(new_block_table, 4) || !aligned(new_seq_lens, 4)) return PA_ERR_ALIGN;
+  const int64_t table = (int64_t)batch * max_blocks_per_seq;
+  const Span outs[] = {{new_block_table, table}, {new_seq_lens, batch},
+                       {new_mass, width > 0 ? (batch - 1) * new_mass_stride + width : 0}};
+  const Span ins[] = {{mass, width > 0 ? (batch - 1) * mass_stride + width : 0}, {seq_lens, batch}, {block_table, table}};
+  if (any_meet(outs, 3, ins, 3)) return PA_ERR_SHAPE;
+  pa::EvictParams p{};
+  p.mass = mass;
+  p.new_mass = new_mass;
+  p.mass_stride = mass_stride;
+  p.new_mass_stride = new_mass_stride;
+  p.seq_lens = seq_lens;
+  p.batch = batch;
+  p.width = width;
+  p.max_len = max_len;
+  p.budget = budget;
+  p.num_sinks = num_sinks;
+  p.num_recent = num_recent;
+  p.block_table = block_table;
+  p.new_block_table = new_block_table;
+  p.new_seq_lens = new_seq_lens;
+  p.max_blocks = max_blocks_per_seq;
+  p.page_size = page_size;
+  p.err = error_word();
+  return launched(pa::launch_evict(p, true, num_sms(), static_cast<cudaStream_t>(stream)));
 }
 
 pa_status paged_device_error(int64_t* code, int64_t* detail) {

@@ -110,6 +110,39 @@ __device__ __forceinline__ uint32_t e4m3x2_hi_to_f16x2(uint32_t w) {
   return d;
 }
 
+// int8 codes A and B (bytes of w) as an f16 pair, exact: the code plus 128 is put
+// into the low bits of 1024 (steps of 1 there), and 1024 + 128 taken off.
+template <int A, int B>
+__device__ __forceinline__ uint32_t i8x2_to_f16x2(uint32_t w) {
+  const uint32_t u = __byte_perm(w ^ 0x80808080u, 0x64646464u, A | 0x40 | (B << 8) | 0x4000);
+  __half2 v = __hsub2(*reinterpret_cast<const __half2*>(&u), __half2half2(__ushort_as_half((unsigned short)0x6480)));
+  return *reinterpret_cast<uint32_t*>(&v);
+}
+
+// int8 pools: the value that a block's scale counts as (NaN as the least).
+constexpr float kScaleMin = 0x1p-40f, kScaleMax = 0x1p40f;
+__device__ __forceinline__ float clamp_scale(float s) { return fminf(fmaxf(s, kScaleMin), kScaleMax); }
+
+// N consecutive floats to shared memory, asynchronously; both sides aligned to
+// min(N, 4) floats.
+template <int N>
+__device__ __forceinline__ void cp_async_floats(uint32_t dst, const float* src) {
+  if constexpr (N >= 4) {
+#pragma unroll
+    for (int i = 0; i < N; i += 4) cp_async_16(dst + 4 * i, src + i, 16);
+  } else if constexpr (N == 2) {
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 8;\n" ::"r"(dst), "l"(src) : "memory");
+  } else {
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 4;\n" ::"r"(dst), "l"(src) : "memory");
+  }
+}
+
+// Arrive on an mbarrier (whose count includes this thread) once this thread's
+// cp.async so far have landed.
+__device__ __forceinline__ void cp_async_arrive(uint32_t bar) {
+  asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];\n" ::"r"(bar) : "memory");
+}
+
 // Two floats (first in the low byte) as e4m3 codes: round to nearest even,
 // finite magnitudes past 448 saturate, NaN stays NaN.
 __device__ __forceinline__ uint32_t f32x2_to_e4m3x2(float lo, float hi) {

@@ -179,11 +179,13 @@ int decode_num_ctas(int num_sms, int32_t batch, int32_t num_kv_heads, int32_t ma
   return (int)n;
 }
 
-size_t decode_smem_bytes(int head_dim, int group, int batch, int heads_per_box, int budget, bool kv8) {
+size_t decode_smem_bytes(int head_dim, int group, int batch, int heads_per_box, int budget, bool kv8, bool scales) {
   const int rt = group <= 16 ? 1 : 2;
   Layout L;
 #define PA_LAYOUT(DD, HH, RR) \
-  L = kv8 ? make_layout<DD, HH, RR, true>(group, batch, budget) : make_layout<DD, HH, RR, false>(group, batch, budget)
+  L = scales ? make_layout<DD, HH, RR, true, false, true>(group, batch, budget)  \
+      : kv8  ? make_layout<DD, HH, RR, true>(group, batch, budget)               \
+             : make_layout<DD, HH, RR, false>(group, batch, budget)
   const int key = (head_dim == 128 ? 1000 : 0) + heads_per_box * 10 + rt;
   switch (key) {
     case 1081: PA_LAYOUT(128, 8, 1); break;

@@ -1,0 +1,11 @@
+// paged_attention_decode_mass, int8 pools: the split-KV decode kernel of decode_split.cuh
+// that also keeps its scores.
+#include "decode_ext.cuh"
+
+namespace pa {
+
+cudaError_t launch_decode_scores_int8(const DecodeParams& p, cudaStream_t s) {
+  return launch_decode_ext<true, kExtScales | kExtMass>(p, s);
+}
+
+}  // namespace pa

@@ -2,9 +2,11 @@
 // templated on the shape (head_dim, heads per box, row tiles), the pool
 // element type and FUSED (paged_attention_decode_append: the kernel also
 // writes the step's new K/V rows and attends to them from its input) and WC
-// (the weighted cut below for 16-row groups).  The plain instantiations are
-// compiled in decode_bf16.cu, the fused ones in decode_fused.cu, the WC ones in
-// decode_weighted.cu, so a plain decode carries none of the fused code.
+// (the weighted cut below for 16-row groups) and EXT (int8 codes with block
+// scales, attention weights: below).  The plain instantiations are compiled in
+// decode_bf16.cu, the fused ones in decode_fused.cu, the WC ones in
+// decode_weighted.cu, those with EXT in decode_int8.cu and decode_mass*.cu, so a
+// plain decode carries none of their code.
 //
 // What is computed (onnxruntime/mobius PR #395 "Add paged / block-table KV
 // cache export", "How it works": Gather(pool, block_table) then Attention
@@ -42,6 +44,22 @@
 //   the f16 B fragments of mma.sync m16n8k16 f16 (Q's dims and the output
 //   columns are permuted to match); k_scale is folded into the softmax scale,
 //   v_scale into the final normalisation.
+// * int8 pools (EXT & kExtScales): the codes come like e4m3 ones and become f16
+//   exactly.  A 16-key block of a head has one scale a tensor, k and v (a scale's
+//   block is 16 tokens or more).  The producers bring the stage's scales with
+//   4- to 16-byte cp.async beside its boxes.  k goes into the factor that S is
+//   multiplied by anyway.  v goes into the exponent: with y = x + log2 v the
+//   running max m follows y, p' = 2^(y - m) <= 1 is the f16 operand beside the raw
+//   codes, and l sums p' / v, so that o / l = sum 2^x v c / sum 2^x, merges of
+//   (m, l, o) stay as they are, and a block whose v is small loses no bits of p'.
+//   That costs an FFMA in place of S's FMUL and two more products a row.  Scales
+//   count as min(max(s, 2^-40), 2^40), so that 2^(x + log2 v) stays far from the
+//   ends of fp32.  The keys of a page out of range take no part.
+// * EXT & kExtMass: each warp also stores its x (scaled scores, log2 units) as fp32
+//   into a scratch [B, Hq, keys], and every finished row its log2 of the sum of
+//   2^x; key_mass_kernel (decode_mass.cu) makes weights of them.  4 Hq bytes a key
+//   written and read, 6 % of a bf16 GQA key's bytes, against half of them for
+//   multiplying q and K again.
 // * Keys at or past L_b are masked in S and their V rows are zeroed in shared
 //   memory, so stale or NaN-poisoned slots never reach the output.
 // * At a segment (sequence x head box) end, warps that shared a head merge in
@@ -62,12 +80,15 @@
 #include <math.h>
 
 #include "common.cuh"
+#include "inputs.cuh"
 #include "internal.h"
 #include "tma.cuh"
 
 namespace pa {
 
 namespace {
+
+constexpr int kExtScales = 1, kExtMass = 2;  // bits of EXT
 
 // keys of sequence b (either page-table form), with / without recording bad input
 __device__ __forceinline__ int nblk_of(const DecodeParams& p, int b, int max_len) {
@@ -132,6 +153,9 @@ __device__ __forceinline__ unsigned long long ld_acquire_gpu(const unsigned long
   return v;
 }
 
+// log2 of a row's sum of 2^x, from its (m, l); +inf without a key (its weights are 0).
+__device__ __forceinline__ float row_lse(float m, float l) { return l > 0.f ? m + log2f(l) : INFINITY; }
+
 // One warp merges query row (head h of the box, row g) of segment `seg`, cut
 // into parts by CTAs c0 .. c0 + nparts - 1 (a CTA that owns no unit, only
 // possible when U < n, wrote nothing and weighs 0), and writes the bf16
@@ -139,9 +163,10 @@ __device__ __forceinline__ unsigned long long ld_acquire_gpu(const unsigned long
 // Lane q holds part q's (m, l); each lane accumulates 4 dims.  The first 8
 // parts' rows are loaded together with the (m, l) (one round trip), later
 // parts one by one.
+template <bool MASS>
 __device__ __noinline__ void merge_segment_row(const DecodeParams& p, int64_t seg, int HB, int G, int h, int g,
                                                int c0, int nparts, int64_t U, int n, int D,
-                                               __nv_bfloat16* outrow) {
+                                               __nv_bfloat16* outrow, float* lse) {
   const int lane = threadIdx.x & 31;
   const bool some_empty = U < n;
   const bool dims = 4 * lane < D;
@@ -171,6 +196,7 @@ __device__ __noinline__ void merge_segment_row(const DecodeParams& p, int64_t se
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) den += __shfl_xor_sync(0xffffffffu, den, o);
   const float inv = den > 0.f ? p.v_scale / den : 0.f;
+  if (MASS && lane == 0) *lse = row_lse(M, den);
   float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
   for (int q = 0; q < kRegParts; ++q) {
@@ -204,7 +230,7 @@ __device__ __noinline__ void merge_segment_row(const DecodeParams& p, int64_t se
 // parts -- and every thread then merges 4 dims of a row:
 //   o = v_scale * sum_q 2^(m_q - M) o_q / sum_q 2^(m_q - M) l_q.
 // Parts that do not fit in the ring are merged warp by warp from global memory.
-template <int D>
+template <int D, bool MASS>
 __device__ __noinline__ void merge_segment(const DecodeParams& p, int b, int hkb, int c0, int span, int HB, int Hg,
                                            int64_t U, int n, int row_lo, int row_hi, unsigned char* scratch,
                                            int scratch_bytes, int tid, int nthreads, int bar_id) {
@@ -216,12 +242,14 @@ __device__ __noinline__ void merge_segment(const DecodeParams& p, int b, int hkb
   const int64_t Hq = p.num_q_heads;
   __nv_bfloat16* out =
       static_cast<__nv_bfloat16*>(p.out) + ((int64_t)b * Hq + (int64_t)hkb * HB * G + row_lo) * D;
+  float* lse = MASS ? p.lse + (int64_t)b * Hq + (int64_t)hkb * HB * G + row_lo : nullptr;
   const int o_bytes = rows * D * 4;
   if ((int64_t)span * (o_bytes + rows * 8) > scratch_bytes) {
     const int warp = tid >> 5;
     for (int t = warp; t < rows; t += nthreads / 32) {
       const int r = row_lo + t;
-      merge_segment_row(p, seg, HB, G, r / G, r - (r / G) * G, c0, span, U, n, D, out + (int64_t)t * D);
+      merge_segment_row<MASS>(p, seg, HB, G, r / G, r - (r / G) * G, c0, span, U, n, D, out + (int64_t)t * D,
+                              MASS ? lse + t : nullptr);
     }
     return;
   }
@@ -261,6 +289,7 @@ __device__ __noinline__ void merge_segment(const DecodeParams& p, int b, int hkb
       acc.x += f * v.x; acc.y += f * v.y; acc.z += f * v.z; acc.w += f * v.w;
     }
     const float inv = den > 0.f ? p.v_scale / den : 0.f;
+    if (MASS && c4 == 0) lse[r] = row_lse(M, den);
     uint2 packed;
     packed.x = pack_bf16(acc.x * inv, acc.y * inv);
     packed.y = pack_bf16(acc.z * inv, acc.w * inv);
@@ -315,33 +344,41 @@ __device__ __forceinline__ uint32_t sw_e4m3(int row, int chunk) {
 
 // Runtime shared-memory layout (stage count depends on G and B).
 struct Layout {
-  int stages, qslot, bar_off, mrg_off, prefix_off, total;
+  int stages, qslot, bar_off, mrg_off, prefix_off, scale_off, total;
 };
 
-template <int D, int HB, int RT, bool KV8 = false, bool WC = false>
+// Scales of a stage: [K, V][block of the stage][head of the box] fp32, 8 a tensor; then
+// a word with a bit for each block whose page is out of range.
+constexpr int kStageScales = 80;
+
+template <int D, int HB, int RT, bool KV8 = false, bool WC = false, bool SC = false>
 __host__ __device__ inline Layout make_layout(int G, int B, int budget) {
   using C = Cfg<D, HB, RT, KV8, WC>;
   Layout L;
   L.qslot = ((HB * G * D * 2) + 127) / 128 * 128;
   const int merge = C::NW > 1 ? HB * G * (D + 2) * 4 : 0;  // one slot: the chained merge below
   const int prefix = ((B + 1) * 4 + 127) / 128 * 128;
-  const int fixed = 2 * L.qslot + (2 * kMaxStages + C::kBars) * 8 + 128 + merge + prefix + 128 + 1024;
+  const int scales = SC ? kMaxStages * kStageScales + 128 : 0;
+  const int fixed = 2 * L.qslot + (2 * kMaxStages + C::kBars) * 8 + 128 + merge + prefix + 128 + 1024 + scales;
   int s = (budget - fixed) / C::kStageBytes;
   if (s > kMaxStages) s = kMaxStages;
   L.stages = s;
   L.bar_off = s * C::kStageBytes + 2 * L.qslot;
   L.mrg_off = L.bar_off + (2 * s + C::kBars) * 8 + 128;  // + the pending-merge list
   L.prefix_off = L.mrg_off + merge;
-  L.total = L.prefix_off + prefix + 1024;
+  L.scale_off = (L.prefix_off + prefix + 127) / 128 * 128;
+  L.total = SC ? L.scale_off + kMaxStages * kStageScales + 1024 : L.prefix_off + prefix + 1024;
   return L;
 }
 
-template <int D, int HB, int RT, bool KV8, bool FUSED, bool WC = false>
+template <int D, int HB, int RT, bool KV8, bool FUSED, bool WC = false, int EXT = 0>
 __global__ void __launch_bounds__(Cfg<D, HB, RT, KV8, WC>::kThreads, 1)
     decode_split_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_constant__ CUtensorMap tmap_v,
                         DecodeParams p) {
   using C = Cfg<D, HB, RT, KV8, WC>;
   constexpr int NBS = C::NBS, BPW = C::BPW, NW = C::NW;
+  constexpr bool SC = (EXT & kExtScales) != 0, MASS = (EXT & kExtMass) != 0;
+  static_assert(!SC || (KV8 && !FUSED && NBS * HB == 8), "int8 codes come as e4m3 ones do, 8 scales a stage and tensor");
   extern __shared__ unsigned char smem_raw[];
   unsigned char* smem = reinterpret_cast<unsigned char*>(
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
@@ -350,7 +387,7 @@ __global__ void __launch_bounds__(Cfg<D, HB, RT, KV8, WC>::kThreads, 1)
   const int Hkv = p.pool.num_kv_heads;
   const int Hg = Hkv / HB;  // head boxes per sequence
   const int Hq = p.num_q_heads;
-  const Layout lay = make_layout<D, HB, RT, KV8, WC>(G, B, p.smem_budget);
+  const Layout lay = make_layout<D, HB, RT, KV8, WC, SC>(G, B, p.smem_budget);
   const int S = lay.stages;
   unsigned char* ring = smem;
   unsigned char* qring = smem + S * C::kStageBytes;
@@ -376,12 +413,12 @@ __global__ void __launch_bounds__(Cfg<D, HB, RT, KV8, WC>::kThreads, 1)
 
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int ps = p.pool.page_size, pshift = p.pool.page_shift;
-  const int max_len = p.max_blocks * ps;
+  const int max_len = MASS ? min(p.max_blocks * ps, p.max_keys) : p.max_blocks * ps;
 
   // ---- set-up: barriers and the per-sequence block prefix (reads seq_lens only) ----
   if (tid == 0) {
     for (int s = 0; s < S; ++s) {
-      mbar_init(full_bar(s), 1);
+      mbar_init(full_bar(s), SC ? 33 : 1);  // SC: each producer lane's scales too
       mbar_init(empty_bar(s), C::kConsumers);
     }
     for (int s = 0; s < 2; ++s) {
@@ -396,6 +433,8 @@ __global__ void __launch_bounds__(Cfg<D, HB, RT, KV8, WC>::kThreads, 1)
     fence_mbar_init();
   }
   const int n = p.num_ctas, c = blockIdx.x;
+  // these calls wait for the kernel before them ahead of every read
+  if constexpr (EXT != 0) griddep_wait();
   // Units: (b, head box hg, 16-key block k), sequence-major, cut into one
   // range per CTA.  Plainly, the U units in n equal ranges.  With
   // kCostlyChange they are laid out on a line of positions on which each
@@ -413,7 +452,7 @@ __global__ void __launch_bounds__(Cfg<D, HB, RT, KV8, WC>::kThreads, 1)
       else __syncthreads();  // every thread has read the first pass's total
     }
     for (int b = tid; b < B; b += C::kThreads) {
-      const int nb = nblk_of(p, b, max_len);
+      const int nb = EXT != 0 ? (ld_seq_len(p.seq_lens, b, max_len, p.err) + 15) >> 4 : nblk_of(p, b, max_len);
       prefix[b + 1] = C::kCostlyChange && nb > 0 ? nb + P : nb;
     }
     if (tid == 0) prefix[0] = 0;
@@ -504,6 +543,10 @@ __global__ void __launch_bounds__(Cfg<D, HB, RT, KV8, WC>::kThreads, 1)
   }
   if (u0 >= u1) return;
 
+  auto keys_of = [&](int b) {
+    if constexpr (EXT != 0) return ld_seq_len(p.seq_lens, b, max_len, nullptr);
+    else return seq_len_of(p, b, max_len);
+  };
   // the first unit at position u or after it (u in a header: the segment's
   // first unit); cur.u is the unit's position
   auto locate = [&](int64_t u) {
@@ -529,7 +572,7 @@ __global__ void __launch_bounds__(Cfg<D, HB, RT, KV8, WC>::kThreads, 1)
       cur.k = r - cur.hk * cur.nblk;
       cur.u = u;
     }
-    cur.L = seq_len_of(p, cur.b, max_len);
+    cur.L = keys_of(cur.b);
     return cur;
   };
   auto advance = [&](Cursor& cur, int nb) {
@@ -543,7 +586,7 @@ __global__ void __launch_bounds__(Cfg<D, HB, RT, KV8, WC>::kThreads, 1)
         do { ++cur.b; } while (cur.b < B && prefix[cur.b + 1] == prefix[cur.b]);
         if (cur.b < B) {
           cur.nblk = prefix[cur.b + 1] - prefix[cur.b] - (C::kCostlyChange ? P : 0);
-          cur.L = seq_len_of(p, cur.b, max_len);
+          cur.L = keys_of(cur.b);
         }
       }
     }
@@ -675,12 +718,14 @@ __global__ void __launch_bounds__(Cfg<D, HB, RT, KV8, WC>::kThreads, 1)
     for (int x = 0; x < kOpsPerLane; ++x) full_geom[x] = geom(NBS, lane + 32 * x);
     // raw block_table entries of this lane's ops in the stage at cu (loads only)
     auto fetch = [&](const Cursor& cu, int nbs, int (&pg)[kOpsPerLane]) {
-      const int32_t* bt = p.block_table + page_list_start(p.kv_indptr, p.max_blocks, cu.b);
+      const int32_t* bt =
+          p.block_table + (EXT != 0 ? (int64_t)cu.b * p.max_blocks : page_list_start(p.kv_indptr, p.max_blocks, cu.b));
 #pragma unroll
       for (int x = 0; x < kOpsPerLane; ++x) {
         const OpGeom g = nbs == NBS ? full_geom[x] : geom(nbs, lane + 32 * x);
         const int kk = (cu.k + g.jj) * 16 + g.q * R;
-        pg[x] = (g.on && nbs > 0 && kk < cu.L) ? __ldg(bt + (kk >> pshift)) : 0;
+        if constexpr (EXT != 0) pg[x] = (g.on && nbs > 0 && kk < cu.L) ? ld_input(bt + (kk >> pshift)) : 0;
+        else pg[x] = (g.on && nbs > 0 && kk < cu.L) ? __ldg(bt + (kk >> pshift)) : 0;
       }
     };
     // the stage after the one at (c, nb); nb = 0 past the CTA's range
@@ -736,6 +781,22 @@ __global__ void __launch_bounds__(Cfg<D, HB, RT, KV8, WC>::kThreads, 1)
       const int issued = __reduce_add_sync(0xffffffffu, mine);
       if (lane == 0 && lap > 0 && alive) alive = mbar_wait(empty_bar(slot), (uint32_t)((lap - 1) & 1), p.err);
       alive = __shfl_sync(0xffffffffu, alive ? 1 : 0, 0) != 0;
+      if constexpr (SC) {
+        // this lane's op is one block of one tensor for all heads of the box (pages
+        // of 16 slots or more: one box a block), so it brings that block's scales
+        const OpGeom g = nbs == NBS ? full_geom[0] : geom(nbs, lane);
+        if (g.on && (cur.k + g.jj) * 16 < cur.L) {
+          const uint32_t sdst = smem_u32(smem + lay.scale_off) + slot * kStageScales + g.TT * 32 + g.jj * HB * 4;
+          if (row[0] >= 0)
+            cp_async_floats<HB>(sdst, (g.TT ? p.value_scales : p.key_scales) +
+                                          (int64_t)(row[0] >> p.scale_shift) * Hkv + cur.hk * HB);
+        }
+        const unsigned bad =
+            __ballot_sync(0xffffffffu, g.on && g.TT == 0 && (cur.k + g.jj) * 16 < cur.L && row[0] < 0);
+        if (lane == 0)  // lanes 0 .. nbs - 1 have the blocks of K
+          *reinterpret_cast<volatile uint32_t*>(smem + lay.scale_off + slot * kStageScales + 64) = bad;
+        cp_async_arrive(full_bar(slot));
+      }
       if (lane == 0) mbar_arrive_expect_tx(full_bar(slot), (uint32_t)(issued * R * C::kRowBytes * HB * slabs_per_op));
       __syncwarp();
 #pragma unroll
@@ -835,6 +896,7 @@ __global__ void __launch_bounds__(Cfg<D, HB, RT, KV8, WC>::kThreads, 1)
         unsigned char* st = ring + slot * C::kStageBytes;
         float s[2 * BPW][4];
         int valid[BPW];
+        float kf[BPW], lv[BPW], iv[BPW];  // SC: S's factor, log2 of V's scale and its inverse
         uint32_t vbase[BPW];
         bool touched = false;  // shared-memory stores this warp made into the stage
 #pragma unroll
@@ -846,7 +908,18 @@ __global__ void __launch_bounds__(Cfg<D, HB, RT, KV8, WC>::kThreads, 1)
           unsigned char* kt = st + (jb * C::kSlabs) * C::kBoxBytes + h * C::kHeadTile;
           unsigned char* vt = st + ((NBS + jb) * C::kSlabs) * C::kBoxBytes + h * C::kHeadTile;
           vbase[bb] = smem_u32(vt);
+          kf[bb] = sl2;
+          lv[bb] = 0.f;
+          iv[bb] = 1.f;
           if (jb >= nbs) continue;
+          if constexpr (SC) {
+            const float* sc = reinterpret_cast<const float*>(smem + lay.scale_off + slot * kStageScales);
+            const float ks = sc[jb * HB + h], vs = sc[8 + jb * HB + h];
+            if ((reinterpret_cast<const uint32_t*>(sc)[16] >> jb) & 1u) valid[bb] = 0;  // a page out of range
+            kf[bb] = sl2 * clamp_scale(ks);
+            lv[bb] = __log2f(clamp_scale(vs));
+            iv[bb] = fast_exp2(-lv[bb]);  // of the very power that p' carries
+          }
           if (valid[bb] < 16) {
             // rows past L_b may hold stale or poisoned data (NaN would survive
             // P = 0): zero them in V; K is masked below.  A row's chunks stay in
@@ -886,6 +959,13 @@ __global__ void __launch_bounds__(Cfg<D, HB, RT, KV8, WC>::kThreads, 1)
             for (int q2 = 0; q2 < D / 32; ++q2) {
               uint32_t r0, r1, r2, r3;
               ldmatrix_x4(kbase + sw_e4m3<D>((mi & 1) * 8 + rr, 2 * q2 + (mi >> 1)), r0, r1, r2, r3);
+              if constexpr (SC) {
+                mma_f16_16816(s[2 * bb], qf[2 * q2], i8x2_to_f16x2<0, 1>(r0), i8x2_to_f16x2<2, 3>(r0));
+                mma_f16_16816(s[2 * bb + 1], qf[2 * q2], i8x2_to_f16x2<0, 1>(r1), i8x2_to_f16x2<2, 3>(r1));
+                mma_f16_16816(s[2 * bb], qf[2 * q2 + 1], i8x2_to_f16x2<0, 1>(r2), i8x2_to_f16x2<2, 3>(r2));
+                mma_f16_16816(s[2 * bb + 1], qf[2 * q2 + 1], i8x2_to_f16x2<0, 1>(r3), i8x2_to_f16x2<2, 3>(r3));
+                continue;
+              }
               mma_f16_16816(s[2 * bb], qf[2 * q2], e4m3x2_lo_to_f16x2(r0), e4m3x2_hi_to_f16x2(r0));
               mma_f16_16816(s[2 * bb + 1], qf[2 * q2], e4m3x2_lo_to_f16x2(r1), e4m3x2_hi_to_f16x2(r1));
               mma_f16_16816(s[2 * bb], qf[2 * q2 + 1], e4m3x2_lo_to_f16x2(r2), e4m3x2_hi_to_f16x2(r2));
@@ -901,13 +981,34 @@ __global__ void __launch_bounds__(Cfg<D, HB, RT, KV8, WC>::kThreads, 1)
             }
           }
         }
+        float score[MASS ? 2 * BPW : 1][4];
 #pragma unroll
         for (int t = 0; t < 2 * BPW; ++t)
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
             const int key = (t & 1) * 8 + (lane & 3) * 2 + (e & 1);
-            s[t][e] = key < valid[t >> 1] ? s[t][e] * sl2 : -INFINITY;
+            if constexpr (MASS) {
+              // the score itself, kept for key_mass_kernel
+              const float x = key < valid[t >> 1] ? s[t][e] * (SC ? kf[t >> 1] : sl2) : -INFINITY;
+              score[t][e] = x;
+              if constexpr (!SC) s[t][e] = x;
+            }
+            if constexpr (SC)
+              s[t][e] = key < valid[t >> 1] ? fmaf(s[t][e], kf[t >> 1], lv[t >> 1]) : -INFINITY;
+            else if constexpr (!MASS)
+              s[t][e] = key < valid[t >> 1] ? s[t][e] * sl2 : -INFINITY;
           }
+        if constexpr (MASS) {
+          // whole 16-key blocks (rows of the scratch are padded to them)
+#pragma unroll
+          for (int t = 0; t < 2 * BPW; ++t) {
+            if (jw * BPW + (t >> 1) >= nbs) continue;
+            const int64_t key = (int64_t)(first_k + done + jw * BPW + (t >> 1)) * 16 + (t & 1) * 8 + (lane & 3) * 2;
+            float* x = p.scores + ((int64_t)cc.b * Hq + (int64_t)hk * G) * p.score_stride + key;
+            if (rA < G) *reinterpret_cast<float2*>(x + rA * p.score_stride) = make_float2(score[t][0], score[t][1]);
+            if (rB < G) *reinterpret_cast<float2*>(x + rB * p.score_stride) = make_float2(score[t][2], score[t][3]);
+          }
+        }
         float mx0 = -INFINITY, mx1 = -INFINITY;
 #pragma unroll
         for (int t = 0; t < 2 * BPW; ++t) {
@@ -918,7 +1019,11 @@ __global__ void __launch_bounds__(Cfg<D, HB, RT, KV8, WC>::kThreads, 1)
         mx0 = fmaxf(mx0, __shfl_xor_sync(0xffffffffu, mx0, 2));
         mx1 = fmaxf(mx1, __shfl_xor_sync(0xffffffffu, mx1, 1));
         mx1 = fmaxf(mx1, __shfl_xor_sync(0xffffffffu, mx1, 2));
-        const float mn0 = fmaxf(m0, mx0), mn1 = fmaxf(m1, mx1);
+        float mn0 = fmaxf(m0, mx0), mn1 = fmaxf(m1, mx1);
+        if constexpr (SC) {  // no key yet (a page out of range): any finite reference
+          mn0 = mn0 == -INFINITY ? -1e30f : mn0;
+          mn1 = mn1 == -INFINITY ? -1e30f : mn1;
+        }
         const float al0 = fast_exp2(m0 - mn0), al1 = fast_exp2(m1 - mn1);
         float p_[2 * BPW][4];
         float rs0 = 0.f, rs1 = 0.f;
@@ -928,8 +1033,13 @@ __global__ void __launch_bounds__(Cfg<D, HB, RT, KV8, WC>::kThreads, 1)
           p_[t][1] = fast_exp2(s[t][1] - mn0);
           p_[t][2] = fast_exp2(s[t][2] - mn1);
           p_[t][3] = fast_exp2(s[t][3] - mn1);
-          rs0 += p_[t][0] + p_[t][1];
-          rs1 += p_[t][2] + p_[t][3];
+          if constexpr (SC) {
+            rs0 = fmaf(p_[t][0] + p_[t][1], iv[t >> 1], rs0);
+            rs1 = fmaf(p_[t][2] + p_[t][3], iv[t >> 1], rs1);
+          } else {
+            rs0 += p_[t][0] + p_[t][1];
+            rs1 += p_[t][2] + p_[t][3];
+          }
         }
         l0 = l0 * al0 + rs0;
         l1 = l1 * al1 + rs1;
@@ -966,6 +1076,13 @@ __global__ void __launch_bounds__(Cfg<D, HB, RT, KV8, WC>::kThreads, 1)
             for (int q2 = 0; q2 < D / 32; ++q2) {
               uint32_t r0, r1, r2, r3;
               ldmatrix_x4_trans(vbase[bb] + sw_e4m3<D>((mi & 1) * 8 + rr, 2 * q2 + (mi >> 1)), r0, r1, r2, r3);
+              if constexpr (SC) {  // the even and odd dims' key pairs picked as they become f16
+                mma_f16_16816(o[4 * q2], pa, i8x2_to_f16x2<0, 2>(r0), i8x2_to_f16x2<0, 2>(r1));
+                mma_f16_16816(o[4 * q2 + 1], pa, i8x2_to_f16x2<1, 3>(r0), i8x2_to_f16x2<1, 3>(r1));
+                mma_f16_16816(o[4 * q2 + 2], pa, i8x2_to_f16x2<0, 2>(r2), i8x2_to_f16x2<0, 2>(r3));
+                mma_f16_16816(o[4 * q2 + 3], pa, i8x2_to_f16x2<1, 3>(r2), i8x2_to_f16x2<1, 3>(r3));
+                continue;
+              }
               r0 = __byte_perm(r0, 0u, 0x3120);  // (key 2c, key 2c+1) of dim 2j | same of dim 2j+1
               r1 = __byte_perm(r1, 0u, 0x3120);
               r2 = __byte_perm(r2, 0u, 0x3120);
@@ -1105,6 +1222,11 @@ __global__ void __launch_bounds__(Cfg<D, HB, RT, KV8, WC>::kThreads, 1)
           if (rB < G) *reinterpret_cast<float2*>(p.part_o + (pslot * G + rB) * D + col) = vb;
         }
       }
+      if (MASS && complete && (lane & 3) == 0) {
+        float* lse = p.lse + (int64_t)cc.b * Hq + (int64_t)hk * G;
+        if (rA < G) lse[rA] = row_lse(m0, la);
+        if (rB < G) lse[rB] = row_lse(m1, lb);
+      }
       if (!complete && (lane & 3) == 0) {
         if (rA < G) p.part_ml[pslot * G + rA] = make_float2(m0, la);
         if (rB < G) p.part_ml[pslot * G + rB] = make_float2(m1, lb);
@@ -1197,7 +1319,7 @@ __global__ void __launch_bounds__(Cfg<D, HB, RT, KV8, WC>::kThreads, 1)
       named_barrier(bar_id, gsize);
       // merge rows [mine, mine + 1) * rows / parts of the segment
       const int rows = HB * p.group;
-      merge_segment<D>(p, b, hkb, c0, span, HB, Hg, W, n, mine * rows / parts, (mine + 1) * rows / parts,
+      merge_segment<D, MASS>(p, b, hkb, c0, span, HB, Hg, W, n, mine * rows / parts, (mine + 1) * rows / parts,
                        ring + grp * scratch_bytes, scratch_bytes, gtid, gsize, bar_id);
       named_barrier(bar_id, gsize);  // before a next merge reuses the scratch
     }
@@ -1218,12 +1340,12 @@ cudaError_t launch_split_weighted(const DecodeParams& p, const CUtensorMap& tk, 
 
 namespace {
 
-template <int D, int HB, int RT, bool KV8, bool FUSED, bool WC = false>
+template <int D, int HB, int RT, bool KV8, bool FUSED, bool WC = false, int EXT = 0>
 cudaError_t launch_split(const DecodeParams& p, const CUtensorMap& tk, const CUtensorMap& tv, cudaStream_t s) {
   using C = Cfg<D, HB, RT, KV8, WC>;
-  const Layout lay = make_layout<D, HB, RT, KV8, WC>(p.group, p.batch, p.smem_budget);
+  const Layout lay = make_layout<D, HB, RT, KV8, WC, (EXT & kExtScales) != 0>(p.group, p.batch, p.smem_budget);
   if (lay.stages < 2) return cudaErrorInvalidConfiguration;
-  auto kern = decode_split_kernel<D, HB, RT, KV8, FUSED, WC>;
+  auto kern = decode_split_kernel<D, HB, RT, KV8, FUSED, WC, EXT>;
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, lay.total);
   if (e != cudaSuccess) return e;
   // Plain decode: a co-resident (cooperative) grid lets every CTA of a cut
@@ -1250,22 +1372,24 @@ cudaError_t launch_split(const DecodeParams& p, const CUtensorMap& tk, const CUt
   return launch_pdl(kern, dim3(p.num_ctas), dim3(C::kThreads), (size_t)lay.total, s, tk, tv, p);
 }
 
-template <int D, bool KV8, bool FUSED>
+template <int D, bool KV8, bool FUSED, int EXT = 0>
 cudaError_t launch_split_d(const DecodeParams& p, const CUtensorMap& tk, const CUtensorMap& tv, int rt,
                            cudaStream_t s) {
   switch (p.heads_per_box * 10 + rt) {
     case 81:
       // 16-row groups in boxes of 8 heads with a segment penalty: the WC
       // instantiation (decode_weighted.cu)
-      if constexpr (D == 128)
+      if constexpr (D == 128 && EXT != 0)
+        if (p.seg_penalty > 0) return launch_split<D, 8, 1, KV8, FUSED, true, EXT>(p, tk, tv, s);
+      if constexpr (D == 128 && EXT == 0)
         if (p.seg_penalty > 0) return launch_split_weighted(p, tk, tv, KV8, FUSED, s);
-      return launch_split<D, 8, 1, KV8, FUSED>(p, tk, tv, s);
-    case 41: return launch_split<D, 4, 1, KV8, FUSED>(p, tk, tv, s);
-    case 21: return launch_split<D, 2, 1, KV8, FUSED>(p, tk, tv, s);
-    case 11: return launch_split<D, 1, 1, KV8, FUSED>(p, tk, tv, s);
-    case 42: return launch_split<D, 4, 2, KV8, FUSED>(p, tk, tv, s);
-    case 22: return launch_split<D, 2, 2, KV8, FUSED>(p, tk, tv, s);
-    case 12: return launch_split<D, 1, 2, KV8, FUSED>(p, tk, tv, s);
+      return launch_split<D, 8, 1, KV8, FUSED, false, EXT>(p, tk, tv, s);
+    case 41: return launch_split<D, 4, 1, KV8, FUSED, false, EXT>(p, tk, tv, s);
+    case 21: return launch_split<D, 2, 1, KV8, FUSED, false, EXT>(p, tk, tv, s);
+    case 11: return launch_split<D, 1, 1, KV8, FUSED, false, EXT>(p, tk, tv, s);
+    case 42: return launch_split<D, 4, 2, KV8, FUSED, false, EXT>(p, tk, tv, s);
+    case 22: return launch_split<D, 2, 2, KV8, FUSED, false, EXT>(p, tk, tv, s);
+    case 12: return launch_split<D, 1, 2, KV8, FUSED, false, EXT>(p, tk, tv, s);
     default: return cudaErrorInvalidValue;
   }
 }

@@ -38,6 +38,48 @@ struct AppendParams {
 };
 cudaError_t launch_append(const AppendParams& p, int vec_bytes, int num_sms, cudaStream_t s);
 
+// ---- append into int8 pools (append_int8.cu) ----------------------------------
+struct AppendInt8Params {
+  void* key_pool;           // codes [slots, num_kv_heads, head_dim]
+  void* value_pool;
+  float* key_scales;        // [slots >> scale_shift, num_kv_heads]
+  float* value_scales;
+  const void* key;          // bf16; token t's rows at key + t * key_stride (elements)
+  const void* value;
+  int64_t key_stride, value_stride;
+  const int64_t* slot_mapping;
+  int64_t num_tokens;
+  int64_t num_slots;
+  int32_t num_kv_heads, head_dim;
+  int32_t scale_shift;      // log2 of the tokens of a scale's block
+  unsigned long long* err;
+};
+cudaError_t launch_append_int8(const AppendInt8Params& p, int num_sms, cudaStream_t s);
+
+// ---- eviction by accumulated attention weight (evict.cu) -----------------------
+constexpr int kMaxEvictPages = 8 * 40928;  // of a sequence: their weights stay in shared memory
+struct EvictParams {
+  const float* mass;        // [B, width], rows mass_stride apart
+  float* new_mass;
+  int64_t mass_stride, new_mass_stride;
+  const int32_t* seq_lens;
+  int32_t batch, width;
+  int32_t max_len;          // bound of seq_lens
+  int32_t budget;           // rows, or pages
+  int32_t num_sinks, num_recent;
+  // rows
+  int32_t* keep_indptr;
+  int32_t* keep;
+  int32_t* base;
+  // pages
+  const int32_t* block_table;
+  int32_t* new_block_table;
+  int32_t* new_seq_lens;
+  int32_t max_blocks, page_size;
+  unsigned long long* err;
+};
+cudaError_t launch_evict(const EvictParams& p, bool pages, int num_sms, cudaStream_t s);
+
 // ---- norm, rotation and append (norm_rope.cu) --------------------------------
 struct NormRopeParams {
   void* key_pool;
@@ -178,6 +220,17 @@ struct DecodeParams {
   // first `num_sinks` are attended to
   int32_t window;
   int32_t num_sinks;
+  // int8 pools: codes of one byte (kv8 is set too) and their scales
+  // [slots >> scale_shift, num_kv_heads]; nullptr: not int8
+  const float* key_scales;
+  const float* value_scales;
+  int32_t scale_shift;
+  // attention weights wanted: scaled scores (log2 units) [B, Hq, score_stride], the
+  // stride a multiple of 16, and log2 of each row's sum of 2^score [B, Hq]; nullptr: no
+  float* scores;
+  int64_t score_stride;
+  int32_t max_keys;        // with scores: keys of a sequence that have a place there
+  float* lse;
 };
 // Number of partial slots the split kernel may write for this launch.
 int decode_heads_per_box(int32_t num_kv_heads, int32_t group, int32_t page_size);
@@ -189,6 +242,27 @@ int decode_num_ctas(int num_sms, int32_t batch, int32_t num_kv_heads, int32_t ma
 cudaError_t launch_split_fused(const DecodeParams& p, const CUtensorMap& tk, const CUtensorMap& tv, int rt,
                                cudaStream_t s);
 cudaError_t launch_decode_bf16(const DecodeParams& p, cudaStream_t s);
+// int8 pools (decode_int8.cu), and any tensor-core pool with p.scores
+// (decode_mass.cu and the instantiations of decode_mass_*.cu).
+cudaError_t launch_decode_int8(const DecodeParams& p, cudaStream_t s);
+cudaError_t launch_decode_scores(const DecodeParams& p, cudaStream_t s);
+cudaError_t launch_decode_scores_bf16(const DecodeParams& p, cudaStream_t s);
+cudaError_t launch_decode_scores_e4m3(const DecodeParams& p, cudaStream_t s);
+cudaError_t launch_decode_scores_int8(const DecodeParams& p, cudaStream_t s);
+// mass_out[b, j] = decay * mass_in[b, j] + sum_h 2^(score[b, h, j] - lse[b, h]) for
+// j < seq_lens[b] (mass_in nullptr: 0).
+struct KeyMassParams {
+  const float* scores;
+  const float* lse;
+  int64_t score_stride;
+  const int32_t* seq_lens;
+  const float* mass_in;
+  float* mass_out;
+  int64_t mass_stride;
+  float decay;
+  int32_t batch, num_q_heads, max_keys, max_len;
+};
+cudaError_t launch_key_mass(const KeyMassParams& p, cudaStream_t s);
 // Cascade: split kernel on s, then the combine after `prefix_done` (an event
 // recorded once the prefix partials are written) has completed.
 cudaError_t launch_decode_cascade_bf16(const DecodeParams& p, cudaStream_t s, cudaEvent_t prefix_done);
@@ -199,7 +273,7 @@ int decode_window_cluster(int num_sms, int32_t batch, int32_t num_kv_heads, int3
 cudaError_t launch_decode_window(const DecodeParams& p, int num_sms, int csize, cudaStream_t s);
 // Dynamic shared memory the bf16 decode split kernel needs.
 // (size_t)-1 when no stage ring of >= 2 stages fits the budget.
-size_t decode_smem_bytes(int head_dim, int group, int batch, int heads_per_box, int budget, bool kv8);
+size_t decode_smem_bytes(int head_dim, int group, int batch, int heads_per_box, int budget, bool kv8, bool scales);
 
 // TMA descriptor of a bf16 pool viewed as {64, rows, num_kv_heads,
 // head_dim/64} (strides num_kv_heads*head_dim*2, head_dim*2 and 128 bytes),
@@ -258,6 +332,11 @@ struct PrefillParams {
   // or j < num_sinks
   int32_t window;
   int32_t num_sinks;
+  // int8 pools (kv8 is set too; the sliding-window kernel, with a window that
+  // reaches every key): scales [slots >> scale_shift, num_kv_heads]; nullptr: not int8
+  const float* key_scales;
+  const float* value_scales;
+  int32_t scale_shift;
 };
 cudaError_t launch_prefill_bf16(const PrefillParams& p, cudaStream_t s);
 // The sliding-window kernel (prefill_window.cu), window > 0.

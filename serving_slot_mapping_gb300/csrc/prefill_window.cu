@@ -29,6 +29,18 @@
 // Boxes whose page holds no key that a row of the sequence sees are never looked
 // up; slots of loaded pages that no row of the sequence sees (between the sinks
 // and the sequence's first window key, or at and past L_b) are zeroed in V.
+// int8 pools (SC; paged_attention_prefill_int8, a window that reaches every key): the
+// codes land like e4m3 ones.  A tile's 16-key blocks each have a scale; with R the
+// largest of the tile, for K and for V:
+// * warp 10 looks the scales up ahead and hands out, per tile, the f16 ratios s / R
+//   of the 8 blocks and R_k, log2 R_v, 1 / R_v (a ring of four tiles);
+// * four converter warps take a whole tile of codes into registers, meet, and write
+//   f16(code * ratio) over it (code exact, ratio and product rounded: 2^-11 of a
+//   value at most, beside 2^-8 of its own rounding to 8 bits);
+// * R_k goes into the factor of S that the softmax has anyway, log2 R_v into the
+//   reference max (y = x + log2 R_v; P = 2^(y - m) stays in f16's range whatever the
+//   scales are), and l sums P / R_v.  No work is added for an element of S.
+// Sixteen warps for that: 2 x 192 + 2 x 64 registers a thread.
 // A block_table entry out of range is noted by the TMA warp; a CTA that met one
 // computes the rows of its items with such a page again at its end, without their
 // keys (redo_bad_items).  The loop knows nothing of them: masks told to the softmax by
@@ -46,24 +58,30 @@ namespace {
 
 constexpr int kItems = 4;        // items whose geometry is in shared memory
 constexpr int kItemBytes = 52;
-constexpr int kWBars = 32;
+constexpr int kWBars = 40;
+constexpr int kScaleTiles = 4;   // int8: tiles whose scales are in shared memory
+constexpr int kScaleBytes = 48;
+constexpr int kI8Warps = 4;      // int8: converter warps 12 .. 15; warp 10 hands out items and scales
 
 enum { W_QFULL = 0, W_KFULL = W_QFULL + kQT, W_KEMPTY = W_KFULL + kNSK, W_VFULL = W_KEMPTY + kNSK,
        W_VEMPTY = W_VFULL + kNSV, W_SFULL = W_VEMPTY + kNSV, W_PFULL = W_SFULL + kQT, W_ODONE = W_PFULL + kQT,
        W_VLAND = W_ODONE + kQT, W_KREADY = W_VLAND + 1, W_VREADY = W_KREADY + kNSK, W_IFULL = W_VREADY + kNSV,
-       W_IEMPTY = W_IFULL + kItems, W_COUNT = W_IEMPTY + kItems };
+       W_IEMPTY = W_IFULL + kItems, W_CFULL = W_IEMPTY + kItems, W_CEMPTY = W_CFULL + kScaleTiles,
+       W_COUNT = W_CEMPTY + kScaleTiles };
 static_assert(W_COUNT <= kWBars, "barrier slots");
 
-template <int D, bool KV8>
+template <int D, bool KV8, bool SC = false>
 struct WCfg : PCfg<D, KV8> {
   using Base = PCfg<D, KV8>;
   // Three warpgroups of 168 registers a thread at launch (two idle warps fill the
   // third where there are no converters).  The third gives registers to the two
   // of the softmax, whose threads hold a whole row of S (128 fp32): 2 x 200 + 104
   // (2 x 192 + 120) = 3 x 168.
-  static constexpr int kThreads = 384;
-  static constexpr int kSoftmaxRegs = KV8 ? 192 : 200, kOtherRegs = KV8 ? 120 : 104;
-  static_assert(2 * kSoftmaxRegs + kOtherRegs <= 3 * 168, "more registers than the launch has");
+  // int8: a fourth one, 128 registers a thread at launch.
+  static constexpr int kThreads = SC ? 512 : 384;
+  static constexpr int kSoftmaxRegs = KV8 ? 192 : 200, kOtherRegs = SC ? 64 : (KV8 ? 120 : 104);
+  static_assert(SC ? 2 * kSoftmaxRegs + 2 * kOtherRegs <= 4 * 128 : 2 * kSoftmaxRegs + kOtherRegs <= 3 * 168,
+                "more registers than the launch has");
   // 8 tiles in flight: {KV head, valid, hid0, hid1} after the first slots of their boxes
   static constexpr int kMetaOff = Base::kPageOff + 8 * 32 * 4;
   static constexpr int kItemOff = kMetaOff + 8 * 16;
@@ -71,7 +89,9 @@ struct WCfg : PCfg<D, KV8> {
   static constexpr int kTmemOff = kWBarOff + kWBars * 8;  // the word that tcgen05.alloc writes, behind every barrier
   static_assert(kTmemOff >= kWBarOff + 8 * W_COUNT, "the TMEM base lies on a barrier");
   static constexpr int kBadOff = kTmemOff + 8;  // a page out of range was met
-  static constexpr int kWSmem = kTmemOff + 16 + 1024;
+  static constexpr int kScaleOff = kTmemOff + 16;
+  static constexpr int kWSmem = kScaleOff + (SC ? kScaleTiles * kScaleBytes : 0) + 1024;
+  static_assert(kScaleOff % 16 == 0 && kWSmem <= 232448, "shared memory");
   // SPLIT, once the item's products are done: its rows of O, fp32, padded against
   // bank conflicts, and their (reference max, sum) over the K and V rings
   static constexpr int kPartRow = D + 4;
@@ -104,6 +124,15 @@ struct Item {
   __device__ int nt() const { return max(nt0, nt1); }
 };
 static_assert(sizeof(Item) == kItemBytes, "ring entry");
+
+// int8: the scales of a key tile, relative to their largest.
+struct TileScales {
+  uint16_t k[8], v[8];  // f16, of each 16 keys
+  float k_ref;          // below 0: there is no such tile, nor any after it
+  float v_log2, v_inv;  // log2 of V's reference, and 1 / 2^v_log2
+  float pad;
+};
+static_assert(sizeof(TileScales) == kScaleBytes, "ring entry");
 
 // Walks the items of one CTA in order (whole warps only): 32 sequences at a
 // time, lane i knows the row tiles of sequence base + i.
@@ -212,12 +241,13 @@ __device__ __forceinline__ uint64_t add_pair(uint64_t a, uint64_t b) {
 // The items of this CTA (SPLIT: of its cluster) that have a page out of range in one
 // of their key tiles, once all their rows are written: each row anew over the keys
 // whose pages are in range, a warp a row and a key at a time.  An error path, slow.
-template <int D, bool KV8>
+template <int D, bool KV8, bool SC>
 __device__ __forceinline__ void redo_bad_items(const PrefillParams& p, int kpo, int csize) {
   constexpr int E = D / 32;  // a lane's dims
   const int lane = threadIdx.x & 31, warps = blockDim.x >> 5, ps = p.pool.page_size, G = p.group;
   const int worker = (int)(blockIdx.x % csize) * warps + (threadIdx.x >> 5), workers = csize * warps;
   auto element = [&](const void* pool, int64_t at) {
+    if (SC) return (float)static_cast<const signed char*>(pool)[at];
     if (KV8) {
       const uint32_t f = e4m3x2_lo_to_f16x2(static_cast<const unsigned char*>(pool)[at]);
       return __half2float(__ushort_as_half((unsigned short)(f & 0xFFFFu)));
@@ -256,16 +286,21 @@ __device__ __forceinline__ void redo_bad_items(const PrefillParams& p, int kpo, 
         if (!in_range(j)) continue;
         const int64_t page = ld_input(bt + (j >> p.pool.page_shift));
         const int64_t at = ((page * ps + (j & (ps - 1))) * p.pool.num_kv_heads + x.hk) * D + lane * E;
-        float s = 0.f;
+        float s = 0.f, ks = 1.f, vs = 1.f;
+        if constexpr (SC) {
+          const int64_t c = ((page * ps + (j & (ps - 1))) >> p.scale_shift) * p.pool.num_kv_heads + x.hk;
+          ks = clamp_scale(__uint_as_float(ld_input(reinterpret_cast<const uint32_t*>(p.key_scales) + c)));
+          vs = clamp_scale(__uint_as_float(ld_input(reinterpret_cast<const uint32_t*>(p.value_scales) + c)));
+        }
 #pragma unroll
-        for (int e = 0; e < E; ++e) s = fmaf(q[e], element(p.pool.key_pool, at + e), s);
+        for (int e = 0; e < E; ++e) s = fmaf(q[e], element(p.pool.key_pool, at + e) * ks, s);
 #pragma unroll
         for (int i = 16; i > 0; i >>= 1) s += __shfl_xor_sync(0xffffffffu, s, i);
         const float mn = fmaxf(m, s), a = fast_exp2(m - mn), w = fast_exp2(s - mn);
         m = mn;
         l = fmaf(l, a, w);
 #pragma unroll
-        for (int e = 0; e < E; ++e) o[e] = fmaf(o[e], a, w * element(p.pool.value_pool, at + e));
+        for (int e = 0; e < E; ++e) o[e] = fmaf(o[e], a, w * (element(p.pool.value_pool, at + e) * vs));
       }
       const float inv = l > 0.f ? p.v_scale / l : 0.f;
 #pragma unroll
@@ -276,12 +311,14 @@ __device__ __forceinline__ void redo_bad_items(const PrefillParams& p, int kpo, 
 
 // SPLIT: csize CTAs of a cluster share an item, and there are clusters for all
 // items (a CTA has one item at most); else csize is 1.
-template <int D, bool KV8, bool SPLIT>
-__global__ void __launch_bounds__(WCfg<D, KV8>::kThreads, 1)
+template <int D, bool KV8, bool SPLIT, bool SC = false>
+__global__ void __launch_bounds__(WCfg<D, KV8, SC>::kThreads, 1)
     prefill_window_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_constant__ CUtensorMap tmap_v,
                           const __grid_constant__ PrefillParams p, int csize_arg) {
   const int csize = SPLIT ? csize_arg : 1;
-  using C = WCfg<D, KV8>;
+  using C = WCfg<D, KV8, SC>;
+  static_assert(!SC || KV8, "int8 codes land as e4m3 ones do");
+  constexpr bool kItemWarp = !KV8 || SC;  // warp 10 derives the items, else the TMA warp
   extern __shared__ unsigned char smem_raw[];
   unsigned char* smem = reinterpret_cast<unsigned char*>(
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
@@ -300,6 +337,7 @@ __global__ void __launch_bounds__(WCfg<D, KV8>::kThreads, 1)
   volatile Item* item_ring = reinterpret_cast<volatile Item*>(smem + C::kItemOff);
   int4* meta = reinterpret_cast<int4*>(smem + C::kMetaOff);     // [8 tiles] {KV head, valid, hid0, hid1}
 
+  volatile TileScales* scale_ring = reinterpret_cast<volatile TileScales*>(smem + C::kScaleOff);
   volatile int* bad_page = reinterpret_cast<volatile int*>(smem + C::kBadOff);
 
   if (tid == 0) {
@@ -313,17 +351,21 @@ __global__ void __launch_bounds__(WCfg<D, KV8>::kThreads, 1)
     for (int s = 0; s < kNSK; ++s) {
       mbar_init(bar(W_KFULL + s), 1);
       mbar_init(bar(W_KEMPTY + s), 1);
-      mbar_init(bar(W_KREADY + s), 1);
+      mbar_init(bar(W_KREADY + s), SC ? kI8Warps : 1);
     }
     for (int s = 0; s < kNSV; ++s) {
       mbar_init(bar(W_VFULL + s), 1);
       mbar_init(bar(W_VEMPTY + s), 1);
-      mbar_init(bar(W_VREADY + s), 1);
+      mbar_init(bar(W_VREADY + s), SC ? kI8Warps : 1);
     }
     mbar_init(bar(W_VLAND), 1);
+    for (int s = 0; SC && s < kScaleTiles; ++s) {
+      mbar_init(bar(W_CFULL + s), 1);
+      mbar_init(bar(W_CEMPTY + s), 4 * kQT + kI8Warps);
+    }
     for (int s = 0; s < kItems; ++s) {
       mbar_init(bar(W_IFULL + s), 1);
-      mbar_init(bar(W_IEMPTY + s), 4 * kQT + 2 + (KV8 ? 2 : 0));  // each warp with a role
+      mbar_init(bar(W_IEMPTY + s), 4 * kQT + 2 + (KV8 && !SC ? 2 : 0));  // each warp that reads items
     }
     fence_mbar_init();
   }
@@ -363,7 +405,7 @@ __global__ void __launch_bounds__(WCfg<D, KV8>::kThreads, 1)
     return alive && x->n >= 0;
   };
   // Derive the next item and hand it out as entry i (whole warp); false at the end.
-  auto publish_next = [&](Walker& wk, int i) {
+  auto publish_next = [&](Walker& wk, int i, Item* item = nullptr) {
     Item x = {};
     const bool got = (!SPLIT || i == 0) && wk.next(p, kpo, csize, &x);
     if (!got) x.n = -1;
@@ -375,6 +417,7 @@ __global__ void __launch_bounds__(WCfg<D, KV8>::kThreads, 1)
       mbar_arrive(bar(W_IFULL + i % kItems));
     }
     __syncwarp();
+    if (item != nullptr) *item = x;
     return got;
   };
   if (warp >= 4 * kQT) {
@@ -415,9 +458,9 @@ __global__ void __launch_bounds__(WCfg<D, KV8>::kThreads, 1)
       return __shfl_sync(0xffffffffu, t, 0) != 0;
     };
     Walker wk;
-    if (KV8) wk.start(p, csize);
+    if (!kItemWarp) wk.start(p, csize);
     int pub = 0, seen = 0;      // items handed out, items taken for their K tiles
-    bool all_out = !KV8;        // the last entry says that there are no more
+    bool all_out = kItemWarp;   // the last entry says that there are no more
     int j = 0, raw = -1;
     bool more = false, end = false;  // `it` has a K tile j left to issue; no item is left
     int kt = 0, vt = 0;  // tiles issued so far, over all items
@@ -432,7 +475,7 @@ __global__ void __launch_bounds__(WCfg<D, KV8>::kThreads, 1)
         ++pub;
         progressed = true;
       }
-      if (!more && !end && (KV8 ? seen < pub : phase_done(W_IFULL + seen % kItems, (uint32_t)((seen / kItems) & 1)))) {
+      if (!more && !end && (!kItemWarp ? seen < pub : phase_done(W_IFULL + seen % kItems, (uint32_t)((seen / kItems) & 1)))) {
         end = !read_item(seen, &it);
         ++seen;
         more = !end && it.nt() > 0;
@@ -526,7 +569,156 @@ __global__ void __launch_bounds__(WCfg<D, KV8>::kThreads, 1)
     }
   }
 
-  if (KV8 && (warp == kCvtWarp || warp == kCvtWarp + 1)) {
+  if constexpr (SC) {
+    if (warp == kCvtWarp) {
+      // ======================= items and scales, int8 pools =======================
+      Walker wk;
+      wk.start(p, csize);
+      const int per = 1 << p.scale_shift;                   // tokens of a scale: 16 or more
+      const int lanes = per < kBN ? kBN / per : 1;          // scales of a tile
+      int kt = 0;
+      auto hand_out = [&](const TileScales& t) {            // lane 0's
+        const int s = kt % kScaleTiles;
+        if (kt >= kScaleTiles && alive)
+          alive = mbar_wait(bar(W_CEMPTY + s), (uint32_t)((kt / kScaleTiles - 1) & 1), p.err);
+        volatile TileScales* e = scale_ring + s;
+#pragma unroll
+        for (int i = 0; i < kScaleBytes / 4; ++i)
+          reinterpret_cast<volatile uint32_t*>(e)[i] = reinterpret_cast<const uint32_t*>(&t)[i];
+        mbar_arrive(bar(W_CFULL + s));
+      };
+      // an item ahead of the scales: the others take the next item before they begin one
+      Item nx = {};
+      bool more = publish_next(wk, 0, &nx);
+      for (int i = 0; more && alive; ++i) {
+        const Item x = nx;
+        if (i + 1 >= kItems)
+          alive = __all_sync(0xffffffffu, mbar_wait(bar(W_IEMPTY + (i + 1) % kItems),
+                                                    (uint32_t)(((i + 1) / kItems - 1) & 1), p.err));
+        more = publish_next(wk, i + 1, &nx);
+        const int32_t* bt = p.block_table + (int64_t)x.b * p.max_blocks;
+        auto page_of = [&](int j) {  // of this lane's scale of tile j
+          const int l = x.base + j * kBN + lane * per, key = l < x.head_keys ? l : l + x.gap;
+          return lane < lanes && key < x.L ? ld_input(bt + (key >> pshift)) : -1;
+        };
+        int page = x.nt() > 0 ? page_of(0) : -1;
+        for (int j = 0; j < x.nt(); ++j, ++kt) {
+          const int l = x.base + j * kBN + lane * per, key = l < x.head_keys ? l : l + x.gap;
+          float ks = 0.f, vs = 0.f;
+          if (page >= 0 && page < p.pool.num_pages) {
+            const int64_t slot = ((int64_t)page << pshift) + (key & (ps - 1));
+            const int64_t c = (slot >> p.scale_shift) * p.pool.num_kv_heads + x.hk;
+            ks = clamp_scale(__uint_as_float(ld_input(reinterpret_cast<const uint32_t*>(p.key_scales) + c)));
+            vs = clamp_scale(__uint_as_float(ld_input(reinterpret_cast<const uint32_t*>(p.value_scales) + c)));
+          }
+          if (j + 1 < x.nt()) page = page_of(j + 1);
+          float kr = ks, vr = vs;
+#pragma unroll
+          for (int o = 4; o > 0; o >>= 1) {  // eight lanes at most have one
+            kr = fmaxf(kr, __shfl_xor_sync(0xffffffffu, kr, o));
+            vr = fmaxf(vr, __shfl_xor_sync(0xffffffffu, vr, o));
+          }
+          kr = fmaxf(kr, kScaleMin);
+          vr = fmaxf(vr, kScaleMin);
+          const unsigned mine = (uint32_t)__half_as_ushort(__float2half_rn(ks / kr)) |
+                                ((uint32_t)__half_as_ushort(__float2half_rn(vs / vr)) << 16);
+          TileScales t;
+#pragma unroll
+          for (int k = 0; k < 8; ++k) {
+            const unsigned w = __shfl_sync(0xffffffffu, mine, (k * 16) >> p.scale_shift);
+            t.k[k] = (uint16_t)(w & 0xFFFFu);
+            t.v[k] = (uint16_t)(w >> 16);
+          }
+          t.k_ref = kr;
+          t.v_log2 = __log2f(vr);
+          t.v_inv = fast_exp2(-t.v_log2);  // of the very power that P carries
+          t.pad = 0.f;
+          if (lane == 0) hand_out(t);
+          alive = __shfl_sync(0xffffffffu, alive ? 1 : 0, 0) != 0;
+          if (!alive) break;
+        }
+      }
+      TileScales t = {};
+      t.k_ref = -1.f;
+      if (lane == 0) hand_out(t);
+    }
+    if (warp >= 16 - kI8Warps) {
+      // ======================= int8 -> f16 converters (warps 12 .. 15) =======================
+      // Tiles in the order that the products ask for them: K(0), then K(t + 1), V(t).
+      const int part = warp - (16 - kI8Warps);
+      auto convert = [&](unsigned char* slot, const volatile uint16_t* ratios) {
+        constexpr int kChunks = D / 16, kKeysPerLoad = 32 / kChunks, kLoads = 8 / kKeysPerLoad;
+        const int q4 = lane >> 3, j8 = lane & 7;
+        const int m = D == 128 ? (j8 & 3) + 4 * (j8 >> 2) : lane % kChunks;
+        const int r0 = D == 128 ? 2 * (q4 >> 1) + ((j8 >> 2) ^ (q4 & 1)) : lane / kChunks;
+        const unsigned char* codes = slot + kBN * D;
+        uint4 raw[4][kLoads];  // this warp's quarter of the tile: four 8-key blocks
+#pragma unroll
+        for (int kb = 0; kb < 4; ++kb)
+#pragma unroll
+          for (int x = 0; x < kLoads; ++x)
+            raw[kb][x] = *reinterpret_cast<const uint4*>(codes + ((part * 4 + kb) * 8 + r0 + x * kKeysPerLoad) * D + m * 16);
+        const uint32_t two[2] = {(uint32_t)ratios[part * 2] * 0x10001u, (uint32_t)ratios[part * 2 + 1] * 0x10001u};
+        named_barrier(2, kI8Warps * 32);  // the f16 tile lies over the codes: all are read
+#pragma unroll
+        for (int kb = 0; kb < 4; ++kb) {
+          const __half2 f = *reinterpret_cast<const __half2*>(&two[kb >> 1]);
+          auto both = [&](uint32_t c) {
+            const __half2 v = __hmul2(*reinterpret_cast<const __half2*>(&c), f);
+            return *reinterpret_cast<const uint32_t*>(&v);
+          };
+#pragma unroll
+          for (int x = 0; x < kLoads; ++x) {
+            const int kr = r0 + x * kKeysPerLoad;
+            const uint4 w = raw[kb][x];
+            unsigned char* blk = slot + (part * 4 + kb) * C::kRowBlock + kr * 128;
+            const int c0 = 2 * m, c1 = 2 * m + 1;  // 8-dim chunks over D
+            *reinterpret_cast<uint4*>(blk + (c0 >> 3) * 1024 + (((c0 & 7) ^ kr) << 4)) =
+                make_uint4(both(i8x2_to_f16x2<0, 1>(w.x)), both(i8x2_to_f16x2<2, 3>(w.x)),
+                           both(i8x2_to_f16x2<0, 1>(w.y)), both(i8x2_to_f16x2<2, 3>(w.y)));
+            *reinterpret_cast<uint4*>(blk + (c1 >> 3) * 1024 + (((c1 & 7) ^ kr) << 4)) =
+                make_uint4(both(i8x2_to_f16x2<0, 1>(w.z)), both(i8x2_to_f16x2<2, 3>(w.z)),
+                           both(i8x2_to_f16x2<0, 1>(w.w)), both(i8x2_to_f16x2<2, 3>(w.w)));
+          }
+        }
+      };
+      auto tile = [&](int t, bool isv) {
+        const int n = isv ? kNSV : kNSK, sl = t % n;
+        if (alive)
+          alive = mbar_wait(bar((isv ? W_VFULL : W_KFULL) + sl), (uint32_t)((t / n) & 1), p.err);
+        convert(smem + (isv ? C::kVOff : C::kKOff) + sl * C::kKVTile,
+                isv ? scale_ring[t % kScaleTiles].v : scale_ring[t % kScaleTiles].k);
+        fence_proxy_async_smem();  // the f16 tile before the tensor core reads it
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar((isv ? W_VREADY : W_KREADY) + sl));
+      };
+      auto there = [&](int t) {  // the tile exists (its scales are handed out)
+        const int s = t % kScaleTiles;
+        if (alive) alive = mbar_wait(bar(W_CFULL + s), (uint32_t)((t / kScaleTiles) & 1), p.err);
+        return alive && scale_ring[s].k_ref >= 0.f;
+      };
+      // (named barriers inside: the four warps go on or stop together)
+      auto agreed = [&](bool x) {
+        int any;
+        asm volatile("{\n .reg .pred p, q;\n setp.ne.s32 p, %1, 0;\n bar.red.and.pred q, 3, %2, p;\n selp.s32 %0, 1, 0, q;\n}\n"
+                     : "=r"(any)
+                     : "r"(x ? 1 : 0), "r"(kI8Warps * 32)
+                     : "memory");
+        return any != 0;
+      };
+      bool have = agreed(there(0));
+      if (have) tile(0, false);
+      for (int t = 0; have; ++t) {
+        have = agreed(there(t + 1));
+        if (have) tile(t + 1, false);
+        tile(t, true);
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar(W_CEMPTY + t % kScaleTiles));
+      }
+    }
+  }
+
+  if (KV8 && !SC && (warp == kCvtWarp || warp == kCvtWarp + 1)) {
     // ======================= e4m3 -> f16 converters (K: warp 10, V: warp 11) =======================
     const bool isv = warp == kCvtWarp + 1;
     const int nslots = isv ? kNSV : kNSK;
@@ -704,6 +896,7 @@ __global__ void __launch_bounds__(WCfg<D, KV8>::kThreads, 1)
       publish_q();
     }
     uint32_t sn = 0, on = 0;  // S tiles and finished O's awaited so far
+    int cn = 0;               // SC: tiles whose scales are taken
     while (have) {
       it = nx;
       const int ntt = tiles_of(it);
@@ -721,7 +914,19 @@ __global__ void __launch_bounds__(WCfg<D, KV8>::kThreads, 1)
       const int pos_max = it.first + (min(it.row0 + (t + 1) * kBM, rows) - 1) / G;
       const int wlo_max = max(0, max(0, pos_max) - p.window + 1) - it.gap;
       float m_ref = -INFINITY, l = 0.f;
+      float f = sl2, lv = 0.f, iv = 1.f;  // SC: the tile's factor of S, log2 of V's reference and its inverse
+      auto take_scales = [&]() {
+        const int s = cn % kScaleTiles;
+        if (alive) alive = mbar_wait(bar(W_CFULL + s), (uint32_t)((cn / kScaleTiles) & 1), p.err);
+        f = sl2 * scale_ring[s].k_ref;
+        lv = scale_ring[s].v_log2;
+        iv = scale_ring[s].v_inv;
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar(W_CEMPTY + s));
+        ++cn;
+      };
       for (int j = 0; j < ntt; ++j) {
+        if constexpr (SC) take_scales();
         if (alive) alive = mbar_wait(bar(W_SFULL + t), sn & 1u, p.err);
         ++sn;
         tc_fence_after();
@@ -753,7 +958,7 @@ __global__ void __launch_bounds__(WCfg<D, KV8>::kThreads, 1)
           mx[i] = fmaxf(mx[i], __uint_as_float(v[i][31]));
         }
         float tmax = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
-        tmax *= sl2;
+        tmax = SC ? fmaf(tmax, f, lv) : tmax * sl2;
         // reference max: moved only when the row max grows by more than 2^8
         float alpha = 1.f;
         bool rescale = false;
@@ -767,7 +972,7 @@ __global__ void __launch_bounds__(WCfg<D, KV8>::kThreads, 1)
         // P = exp2(x - m) as bf16 (f16) pairs, written over the S columns: V's type, the one that the product takes
         // beside it; l sums the fp32 ones.  Against 64 bits an output is off by 0.0023 of its norm so (codes:
         // 0.0017), by 0.0017 with its own rounding alone
-        const uint64_t mul = pair(sl2, sl2), sub = pair(-mbase, -mbase);
+        const uint64_t mul = pair(f, f), sub = pair(lv - mbase, lv - mbase);
         uint64_t rs[4] = {0ull, 0ull, 0ull, 0ull};
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
@@ -785,7 +990,7 @@ __global__ void __launch_bounds__(WCfg<D, KV8>::kThreads, 1)
           tmem_st32(s_col + h * 32, w);
         }
         const float2 sum = unpair(add_pair(add_pair(rs[0], rs[1]), add_pair(rs[2], rs[3])));
-        l += sum.x + sum.y;
+        l = SC ? fmaf(sum.x + sum.y, iv, l) : l + (sum.x + sum.y);
         // O is rescaled in place only when some row of the warp moved its
         // reference max.  PV_t(j-1) is complete: S_t(j) was issued after it.
         if (__any_sync(0xffffffffu, rescale)) {
@@ -803,6 +1008,8 @@ __global__ void __launch_bounds__(WCfg<D, KV8>::kThreads, 1)
         tc_fence_before();
         mbar_arrive(bar(W_PFULL + t));
       }
+      if constexpr (SC)
+        for (int j = ntt; j < it.nt(); ++j) take_scales();  // tiles of the other query tile alone
       if (next_q) {
         if (ntt == 0) copy_q(nx);
         publish_q();
@@ -944,7 +1151,7 @@ __global__ void __launch_bounds__(WCfg<D, KV8>::kThreads, 1)
     for (int c = 0; c < csize; ++c) redo |= ld_cluster(map_rank(smem_u32(smem + C::kBadOff), c)) != 0u;
     cluster_sync();  // no CTA leaves while another reads its memory; every row of the item is written
   }
-  if (__builtin_expect(redo, 0)) redo_bad_items<D, KV8>(p, kpo, csize);
+  if (__builtin_expect(redo, 0)) redo_bad_items<D, KV8, SC>(p, kpo, csize);
 }
 
 // CTAs of an item: one where the items fill the SMs; else as many (a power of two
@@ -959,18 +1166,18 @@ int window_split(int num_sms, int64_t items, int64_t max_keys) {
   return c;
 }
 
-template <int D, bool KV8, bool SPLIT>
+template <int D, bool KV8, bool SPLIT, bool SC>
 cudaError_t launch_items(const PrefillParams& p, const CUtensorMap& tk, const CUtensorMap& tv, unsigned grid, int csize,
                          cudaStream_t s) {
-  using C = WCfg<D, KV8>;
-  auto kern = prefill_window_kernel<D, KV8, SPLIT>;
+  using C = WCfg<D, KV8, SC>;
+  auto kern = prefill_window_kernel<D, KV8, SPLIT, SC>;
   const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kWSmem);
   if (e != cudaSuccess) return e;
   if (!SPLIT) return launch_pdl(kern, dim3(grid), dim3(C::kThreads), (size_t)C::kWSmem, s, tk, tv, p, 1);
   return launch_pdl_cluster(kern, dim3(grid), dim3(C::kThreads), (size_t)C::kWSmem, csize, s, tk, tv, p, csize);
 }
 
-template <int D, bool KV8>
+template <int D, bool KV8, bool SC = false>
 cudaError_t launch_window(const PrefillParams& p, int num_sms, cudaStream_t s) {
   CUtensorMap tk, tv;
   if (!encode_prefill_tmaps<D, KV8>(p, &tk, &tv)) return cudaErrorInvalidValue;
@@ -982,8 +1189,8 @@ cudaError_t launch_window(const PrefillParams& p, int num_sms, cudaStream_t s) {
   const int64_t keys = std::min<int64_t>((int64_t)p.max_blocks * p.pool.page_size,
                                          (int64_t)p.window + p.num_sinks + kQT * kBM / p.group);
   const int csize = window_split(num_sms, items, keys);
-  if (csize > 1) return launch_items<D, KV8, true>(p, tk, tv, (unsigned)(items * csize), csize, s);
-  return launch_items<D, KV8, false>(p, tk, tv, (unsigned)(items < num_sms ? items : num_sms), 1, s);
+  if (csize > 1) return launch_items<D, KV8, true, SC>(p, tk, tv, (unsigned)(items * csize), csize, s);
+  return launch_items<D, KV8, false, SC>(p, tk, tv, (unsigned)(items < num_sms ? items : num_sms), 1, s);
 }
 
 }  // namespace
@@ -991,6 +1198,8 @@ cudaError_t launch_window(const PrefillParams& p, int num_sms, cudaStream_t s) {
 cudaError_t launch_prefill_window(const PrefillParams& p, int num_sms, cudaStream_t s) {
   if (p.max_q_len <= 0 || p.batch <= 0) return cudaSuccess;
   if (p.pool.page_size < 8 || p.pool.page_shift < 0) return cudaErrorInvalidValue;
+  if (p.key_scales != nullptr)
+    return p.pool.head_dim == 128 ? launch_window<128, true, true>(p, num_sms, s) : launch_window<64, true, true>(p, num_sms, s);
   if (p.kv8) return p.pool.head_dim == 128 ? launch_window<128, true>(p, num_sms, s) : launch_window<64, true>(p, num_sms, s);
   return p.pool.head_dim == 128 ? launch_window<128, false>(p, num_sms, s) : launch_window<64, false>(p, num_sms, s);
 }

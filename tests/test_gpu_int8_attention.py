@@ -1,0 +1,199 @@
+"""Attention over int8 pools with a scale for each block of tokens and KV head,
+against the oracle on the values that the codes stand for."""
+import numpy as np
+import pytest
+import torch
+
+from serving_slot_mapping_gb300 import build as build_mod
+from serving_slot_mapping_gb300 import capi
+
+from _int8 import Case
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _lib(cuda_device):
+    build_mod.build()
+    capi.lib()
+    capi.device_error()  # clear
+
+
+def decode(lens, **k):
+    lens = np.asarray(lens)
+    return Case(np.ones_like(lens), lens - 1, **k)
+
+
+RAGGED = [1, 15, 16, 17, 0, 33, 64, 129, 500, 31]
+
+
+@pytest.mark.parametrize("hq,hkv", [(1, 1), (8, 8), (8, 2), (12, 3), (16, 4), (32, 8), (16, 1), (32, 1), (64, 2), (128, 4)])
+@pytest.mark.parametrize("d", [64, 128])
+def test_decode_head_layouts(cuda_device, hq, hkv, d):
+    decode(RAGGED, hq=hq, hkv=hkv, d=d, seed=hq + d).check(capi, cuda_device)
+
+
+@pytest.mark.parametrize("ps,blk", [(16, 16), (32, 16), (32, 32), (64, 16), (128, 64), (256, 256), (1024, 32)])
+def test_decode_pages_and_blocks(cuda_device, ps, blk):
+    decode(RAGGED + [1500], ps=ps, blk=blk, hkv=4, seed=ps + blk).check(capi, cuda_device)
+
+
+@pytest.mark.parametrize("lens", [[1], [16], [4096], [0, 0, 0], [1] * 40, list(range(1, 400, 7)), [5000, 3, 700]])
+def test_decode_batches(cuda_device, lens):
+    decode(lens, hq=32, hkv=8, d=128, seed=len(lens)).check(capi, cuda_device)
+
+
+def test_decode_many_short_sequences(cuda_device):
+    decode(np.random.default_rng(3).integers(0, 60, size=600), hq=16, hkv=2, d=64).check(capi, cuda_device)
+
+
+@pytest.mark.parametrize("scale", [0.0, -0.2, 1.0])
+def test_decode_scale(cuda_device, scale):
+    decode(RAGGED, scale=scale).check(capi, cuda_device)
+
+
+@pytest.mark.parametrize("spread", [0.0, 3.0, 7.0])
+def test_decode_scales_far_apart(cuda_device, spread):
+    """Blocks whose scales differ by many powers of two, in K and in V."""
+    decode([300, 40, 1000], spread=spread, seed=5, scale=0.02).check(capi, cuda_device)
+
+
+def test_decode_first_block_with_tiny_values(cuda_device):
+    """Most of the weight on a block whose V is almost 0 (a first token): the others'
+    weights keep their precision and the row's sum its size."""
+    c = decode([200], hq=4, hkv=1, d=64, seed=9)
+    p = c.table[0, 0]
+    c.vs[p] *= 2.0 ** -20
+    c.kp[p, 0] = torch.sign(c.q[0, :1].float()).mul(127).to(torch.int8)
+    c.ks[p] = 0.1
+    c.check(capi, cuda_device)
+
+
+@pytest.mark.parametrize("value", [0.0, -3.0, float("nan"), 2.0 ** -60, 2.0 ** 60, float("inf")])
+def test_decode_scales_are_clamped(cuda_device, value):
+    c = decode([40, 70], hq=4, hkv=2, seed=2)
+    c.vs[c.table[1, 1]] = value
+    if not value > 1:
+        c.ks[c.table[0, 1]] = value
+    c.check(capi, cuda_device)
+
+
+@pytest.mark.parametrize("bad", [[(0, 0)], [(0, 3)], [(1, 1), (1, 2)], [(0, 0), (1, 0)]])
+@pytest.mark.parametrize("hkv", [2, 8])
+def test_decode_keys_of_bad_pages_take_no_part(cuda_device, bad, hkv):
+    c = decode([100, 75, 16], hq=16, hkv=hkv, d=128 if hkv == 8 else 64, bad=bad)
+    c.check(capi, cuda_device, error=(1, None))
+
+
+def test_decode_of_nothing_but_a_bad_page_gives_zeros(cuda_device):
+    c = decode([16, 20], bad=[(0, 0)])
+    out = c.run(capi, cuda_device)
+    torch.cuda.synchronize()
+    assert capi.device_error()[0] == 1
+    assert (out[0] == 0).all() and torch.isfinite(out).all()
+
+
+PREFILLS = [([5], [0]), ([1, 1, 2], [0, 300, 7]), ([300, 17, 130], [0, 1000, 128]), ([64, 1, 0, 33], [0, 0, 5, 63]),
+            ([257], [1]), ([700, 40], [300, 2000])]
+
+
+@pytest.mark.parametrize("new,cached", PREFILLS)
+@pytest.mark.parametrize("d", [64, 128])
+def test_prefill_batches(cuda_device, new, cached, d):
+    Case(new, cached, hq=8, hkv=2, d=d, seed=sum(new)).check(capi, cuda_device)
+
+
+@pytest.mark.parametrize("hq,hkv", [(1, 1), (4, 4), (12, 3), (32, 8), (16, 1), (32, 1)])
+def test_prefill_head_layouts(cuda_device, hq, hkv):
+    Case([70, 9], [50, 0], hq=hq, hkv=hkv, d=128, seed=hq).check(capi, cuda_device)
+
+
+@pytest.mark.parametrize("ps,blk", [(16, 16), (32, 16), (32, 32), (64, 64), (128, 16), (256, 256), (512, 128)])
+def test_prefill_pages_and_blocks(cuda_device, ps, blk):
+    Case([150, 3], [600, 129], ps=ps, blk=blk, seed=ps).check(capi, cuda_device)
+
+
+def test_prefill_many_items(cuda_device):
+    """More items than SMs: the persistent loop, its rings and both sizes of tiles."""
+    rng = np.random.default_rng(1)
+    Case(rng.integers(0, 300, size=40), rng.integers(0, 200, size=40), hq=16, hkv=4, d=64, seed=4).check(capi, cuda_device)
+
+
+@pytest.mark.parametrize("scale", [0.0, -0.2, 0.5])
+def test_prefill_scale(cuda_device, scale):
+    Case([100], [60], scale=scale).check(capi, cuda_device)
+
+
+@pytest.mark.parametrize("spread", [3.0, 7.0])
+def test_prefill_scales_far_apart(cuda_device, spread):
+    Case([130, 20], [300, 40], spread=spread, seed=5, scale=0.02).check(capi, cuda_device)
+
+
+def test_prefill_rows_without_a_key_are_zeros(cuda_device):
+    c = Case([20, 5], [-8, 3], seed=6)
+    out = c.check(capi, cuda_device)
+    assert (out[:8] == 0).all()
+
+
+@pytest.mark.parametrize("new,cached,bad", [([40], [100], [(0, 1)]), ([300], [700], [(0, 0), (0, 20)])])
+def test_prefill_keys_of_bad_pages_take_no_part(cuda_device, new, cached, bad):
+    """Compared with a sequence that never had those pages' keys, row by row (rows that
+    lie before the page see none of it)."""
+    c = Case(new, cached, bad=bad, seed=8)
+    out = c.run(capi, cuda_device)
+    torch.cuda.synchronize()
+    assert capi.device_error()[0] == 1
+    gone = {m for _, m in bad}
+    keep = [m for m in range(-(-int(c.lens[0]) // c.ps)) if m not in gone]
+    c.seen[0, :len(keep)] = c.seen[0, keep]
+    c.lens = c.lens - c.ps * len(gone)
+    c.bad = []
+    c.compare(out)
+
+
+def test_replays_on_other_inputs_and_two_calls_at_once(cuda_device):
+    """A captured decode and prefill replayed on other lengths, tables, codes and scales;
+    two calls in flight with workspaces of their own give the same bits."""
+    a = decode([100, 7, 300], hq=32, hkv=8, d=128, seed=1)
+    b = decode([250, 300, 1], hq=32, hkv=8, d=128, seed=2)
+    width = max(a.table.shape[1], b.table.shape[1])
+    pages = max(a.kp.shape[0], b.kp.shape[0])
+    def padded(c):
+        grow = lambda t, n, v: torch.cat([t, torch.full((n - t.shape[0],) + t.shape[1:], v, dtype=t.dtype)]) if t is not None else None
+        t = c.tensors("cpu")
+        table = torch.full((3, width), -7, dtype=torch.int32)
+        table[:, :t[5].shape[1]] = t[5]
+        return [x.to(cuda_device) for x in (grow(t[0], pages, 1), grow(t[1], pages, 1), grow(t[2], pages, 1.0),
+                                            grow(t[3], pages, 1.0), t[4], table, t[6])]
+    ta, tb = padded(a), padded(b)
+    eager = [capi.paged_attention_decode_int8(*t, a.scale, max_seq_len=300) for t in (ta, tb)]
+    live = [t.clone() for t in ta]
+    ws, out = capi.decode_workspace(3, 32, live[0]), torch.empty_like(eager[0])
+    call = lambda: capi.paged_attention_decode_int8(*live, a.scale, max_seq_len=300, out=out, workspace=ws)
+    call()
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        call()
+    for t, want in ((tb, eager[1]), (ta, eager[0]), (tb, eager[1])):
+        for x, y in zip(live, t):
+            x.copy_(y)
+        g.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(out, want)
+    s1, s2 = torch.cuda.Stream(), torch.cuda.Stream()
+    torch.cuda.synchronize()
+    outs = []
+    for _ in range(5):
+        outs.append((capi.paged_attention_decode_int8(*ta, a.scale, max_seq_len=300, stream=s1),
+                     capi.paged_attention_decode_int8(*tb, a.scale, max_seq_len=300, stream=s2)))
+    torch.cuda.synchronize()
+    for x, y in outs:
+        assert torch.equal(x, eager[0]) and torch.equal(y, eager[1])
+    assert capi.device_error() == (0, 0)
+
+
+@pytest.mark.parametrize("new,cached", [([150], [3000]), ([40] * 30, [900] * 30), ([2000, 3, 700], [0, 2500, 100])])
+def test_prefill_long_items(cuda_device, new, cached):
+    """Items of many key tiles, alone on a CTA, shared by a cluster, and several in turn."""
+    Case(new, cached, hq=16, hkv=4, d=64, ps=32, blk=32, seed=7).check(capi, cuda_device)
