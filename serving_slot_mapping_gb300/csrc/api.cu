@@ -1118,6 +1118,11 @@ pa_status check_evict(const float* mass, int64_t mass_stride, const int32_t* seq
   return PA_OK;
 }
 
+// Whether every row of both masses starts on 16 bytes.
+int32_t mass_vec(const float* mass, int64_t stride, const float* new_mass, int64_t new_stride, int32_t batch) {
+  return aligned(mass, 16) && aligned(new_mass, 16) && (batch == 1 || (stride % 4 == 0 && new_stride % 4 == 0)) ? 1 : 0;
+}
+
 // Whether an output meets one of the inputs of n entries of 4 bytes each.
 struct Span {
   const void* at;
@@ -1166,6 +1171,7 @@ pa_status paged_kv_evict_rows(const float* mass, int64_t mass_stride, const int3
   p.batch = batch;
   p.width = width;
   p.max_len = width;
+  p.vec = mass_vec(mass, mass_stride, new_mass, new_mass_stride, batch);
   p.budget = budget;
   p.num_sinks = num_sinks;
   p.num_recent = num_recent;
@@ -1210,6 +1216,7 @@ pa_status paged_kv_evict_pages(const float* mass, int64_t mass_stride, const int
   p.batch = batch;
   p.width = width;
   p.max_len = max_len;
+  p.vec = mass_vec(mass, mass_stride, new_mass, new_mass_stride, batch);
   p.budget = budget;
   p.num_sinks = num_sinks;
   p.num_recent = num_recent;

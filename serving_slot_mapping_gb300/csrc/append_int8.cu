@@ -57,8 +57,9 @@ __device__ __forceinline__ float max_abs8(float a, uint4 v) {
   return a;
 }
 
-// Tokens [blockIdx.x * per_cta, + per_cta): the runs that begin there.  blockIdx.y:
-// a share of the (head, tensor) pairs.
+// Tokens [blockIdx.x * per_cta, + per_cta), at most 32: the runs that begin there.
+// blockIdx.y: a share of the (run, tensor, head) tasks.  Every warp finds the runs by
+// itself, from the slots of these tokens and of the 32 before them, a lane each.
 template <int D>
 __global__ void __launch_bounds__(kAppendWarps * 32) append_int8_kernel(const __grid_constant__ AppendInt8Params p,
                                                                         int per_cta) {
@@ -69,86 +70,105 @@ __global__ void __launch_bounds__(kAppendWarps * 32) append_int8_kernel(const __
   const int sub = lane / kLanes, col = lane % kLanes;
   const int64_t first = (int64_t)blockIdx.x * per_cta;
   const int pairs = 2 * p.num_kv_heads;
+  const unsigned kAll = 0xffffffffu;
   griddep_wait();
-  auto slot_at = [&](int64_t t) -> int64_t { return t < p.num_tokens ? ld_input(p.slot_mapping + t) : -1; };
-  auto block_of = [&](int64_t s) -> int64_t { return s < 0 || s >= p.num_slots ? -1 : s >> p.scale_shift; };
-  for (int i = 0; i < per_cta; ++i) {
-    const int64_t t0 = first + i;
-    if (t0 >= p.num_tokens) return;
-    const int64_t s0 = slot_at(t0), blk = block_of(s0);
-    if (s0 >= p.num_slots && blockIdx.y == 0 && threadIdx.x == 0) record_error(p.err, ERR_SLOT, s0);
-    if (blk < 0) continue;
-    // the first token of a run: the last token with a slot before it, among 32, is of
-    // another block
-    {
-      const int64_t before = t0 - 1 - lane >= 0 ? block_of(slot_at(t0 - 1 - lane)) : -1;
-      const unsigned there = __ballot_sync(0xffffffffu, before >= 0);
-      if (there != 0u && __shfl_sync(0xffffffffu, before, __ffs(there) - 1) == blk) continue;
-    }
-    // its span (the run's tokens, and padding), and whether it holds the block's first slot
-    int64_t n = 1;
-    bool fresh = s0 == (blk << p.scale_shift);
-    for (;;) {
-      const int64_t s = slot_at(t0 + n + lane), x = block_of(s);
-      const unsigned same = __ballot_sync(0xffffffffu, x == blk), other = __ballot_sync(0xffffffffu, x >= 0 && x != blk);
-      const unsigned mine = same & (other == 0u ? 0xffffffffu : (1u << (__ffs(other) - 1)) - 1u);
+  auto slot_at = [&](int64_t t) {  // -1: no token, or one without a place
+    const int64_t s = t >= 0 && t < p.num_tokens ? ld_input(p.slot_mapping + t) : -1;
+    return s < 0 || s >= p.num_slots ? -1 : (int)s;
+  };
+  auto block_of = [&](int s) { return s >> p.scale_shift; };  // -1: none
+  const int slot = slot_at(first + lane), blk = block_of(slot);
+  const int blk0 = block_of(slot_at(first - 32 + lane));
+  if (blockIdx.y == 0 && warp == 0 && lane < per_cta && first + lane < p.num_tokens) {
+    const int64_t s = ld_input(p.slot_mapping + first + lane);
+    if (s >= p.num_slots) record_error(p.err, ERR_SLOT, s);
+  }
+  // the first token of a run: the last token with a slot before it, among 32, is of
+  // another block
+  const unsigned there = __ballot_sync(kAll, blk >= 0), there0 = __ballot_sync(kAll, blk0 >= 0);
+  const unsigned lower = there & ((1u << lane) - 1u);
+  const int last = lower != 0u ? 31 - __clz(lower) : 31 - __clz(there0 | 1u);
+  const int pb = __shfl_sync(kAll, blk, last), pb0 = __shfl_sync(kAll, blk0, last);
+  const int before = lower != 0u ? pb : (there0 != 0u && last >= lane ? pb0 : -1);
+  const unsigned leaders = __ballot_sync(kAll, lane < per_cta && blk >= 0 && before != blk);
+  const int tasks = __popc(leaders) * pairs;
+  for (int task = blockIdx.y * kAppendWarps + warp; task < tasks; task += gridDim.y * kAppendWarps) {
+    const int pair = task % pairs;
+    unsigned m = leaders;
+    for (int i = task / pairs; i > 0; --i) m &= m - 1u;
+    const int l = __ffs(m) - 1;
+    const int64_t t0 = first + l;
+    const int b = __shfl_sync(kAll, blk, l);
+    const int head_slot = b << p.scale_shift;
+    // the span (the run's tokens, and padding), and whether it holds the block's first slot
+    auto members = [&](int x, unsigned from, bool* ends) {
+      const unsigned same = __ballot_sync(kAll, x == b) & from, other = __ballot_sync(kAll, x >= 0 && x != b) & from;
+      *ends = other != 0u;
+      return same & (other == 0u ? kAll : (1u << (__ffs(other) - 1)) - 1u);
+    };
+    bool ends;
+    unsigned mine = members(blk, kAll << l, &ends);
+    bool fresh = __any_sync(kAll, ((mine >> lane) & 1u) && slot == head_slot);
+    int64_t n = 32 - __clz(mine) - l;
+    while (!ends) {
+      const int s = slot_at(t0 + n + lane);
+      mine = members(block_of(s), kAll, &ends);
       if (mine == 0u) break;  // (32 padding tokens end a run)
-      fresh |= __any_sync(0xffffffffu, ((mine >> lane) & 1u) && s == (blk << p.scale_shift));
+      fresh |= __any_sync(kAll, ((mine >> lane) & 1u) && s == head_slot) != 0;
       n += 32 - __clz(mine);
-      if (other != 0u) break;
     }
-    for (int pair = blockIdx.y * kAppendWarps + warp; pair < pairs; pair += gridDim.y * kAppendWarps) {
-      const bool isv = pair >= p.num_kv_heads;
-      const int h = isv ? pair - p.num_kv_heads : pair;
-      const __nv_bfloat16* src = static_cast<const __nv_bfloat16*>(isv ? p.value : p.key) + h * D + col * 8;
-      const int64_t stride = isv ? p.value_stride : p.key_stride;
-      signed char* pool = static_cast<signed char*>(isv ? p.value_pool : p.key_pool) + h * D;
-      float* scale = (isv ? p.value_scales : p.key_scales) + blk * p.num_kv_heads + h;
-      const int64_t pitch = (int64_t)p.num_kv_heads * D;
-      auto row = [&](int64_t r) {
-        return ld_stream(reinterpret_cast<const uint4*>(src + (t0 + r) * stride));
-      };
-      // the slot of span row r; -1: a padding token
-      auto slot_of = [&](int64_t r) -> int64_t {
-        const int64_t s = r < n ? slot_at(t0 + r) : -1;
-        return block_of(s) == blk ? s : -1;
-      };
-      const float old = fresh ? 0.f : clamp_scale(__uint_as_float(ld_input(reinterpret_cast<const uint32_t*>(scale))));
-      uint4 v[kPasses];
-      int64_t at[kPasses];
-      float a = 0.f;
+    const bool isv = pair >= p.num_kv_heads;
+    const int h = isv ? pair - p.num_kv_heads : pair;
+    const int64_t stride = isv ? p.value_stride : p.key_stride;
+    const __nv_bfloat16* src = static_cast<const __nv_bfloat16*>(isv ? p.value : p.key) + t0 * stride + h * D + col * 8;
+    signed char* pool = static_cast<signed char*>(isv ? p.value_pool : p.key_pool) + h * D + col * 8;
+    float* scale = (isv ? p.value_scales : p.key_scales) + (int64_t)b * p.num_kv_heads + h;
+    const int64_t pitch = (int64_t)p.num_kv_heads * D;
+    auto row = [&](int64_t r) { return ld_stream(reinterpret_cast<const uint4*>(src + r * stride)); };
+    uint4 v[kPasses];
 #pragma unroll
-      for (int x = 0; x < kPasses; ++x) {
-        const int64_t r = x * kRows + sub;
-        v[x] = r < n ? row(r) : make_uint4(0u, 0u, 0u, 0u);
-        at[x] = slot_of(r);
+    for (int x = 0; x < kPasses; ++x) {
+      const int r = x * kRows + sub;
+      v[x] = r < n ? row(r) : make_uint4(0u, 0u, 0u, 0u);
+    }
+    const float old = fresh ? 0.f : clamp_scale(__uint_as_float(ld_input(reinterpret_cast<const uint32_t*>(scale))));
+    // the slot of span row r; -1: a padding token
+    auto mine_of = [&](int64_t r) {
+      const int s = r < n ? slot_at(t0 + r) : -1;
+      return block_of(s) == b ? s : -1;
+    };
+    int at[kPasses];
+    float a = 0.f;
+#pragma unroll
+    for (int x = 0; x < kPasses; ++x) {
+      const int r = x * kRows + sub, s = __shfl_sync(kAll, slot, (l + r) & 31);
+      at[x] = l + r < 32 ? (r < n && block_of(s) == b ? s : -1) : mine_of(r);
+    }
+#pragma unroll
+    for (int x = 0; x < kPasses; ++x)
+      if (at[x] >= 0) a = max_abs8(a, v[x]);
+    for (int64_t r = 16 + sub; r < n; r += kRows)
+      if (mine_of(r) >= 0) a = max_abs8(a, row(r));
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) a = fmaxf(a, __shfl_xor_sync(kAll, a, o));
+    const float s = fmaxf(old, clamp_scale(__fdiv_rn(a, 127.f)));
+    if (!fresh && s > old) {
+      const float ratio = __fdiv_rn(old, s);
+      const int rows = 1 << p.scale_shift;
+      for (int r = sub; r < rows; r += kRows) {
+        uint2* c = reinterpret_cast<uint2*>(pool + (int64_t)(head_slot + r) * pitch);
+        const uint2 w = ld_input(c);
+        *c = make_uint2(rescale4(w.x, ratio), rescale4(w.y, ratio));
       }
+    }
+    __syncwarp();  // the rows below land over the re-encoded ones
+    if (lane == 0) *scale = s;
 #pragma unroll
-      for (int x = 0; x < kPasses; ++x)
-        if (at[x] >= 0) a = max_abs8(a, v[x]);
-      for (int64_t r = 16 + sub; r < n; r += kRows)
-        if (slot_of(r) >= 0) a = max_abs8(a, row(r));
-#pragma unroll
-      for (int o = 16; o > 0; o >>= 1) a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, o));
-      const float s = fmaxf(old, clamp_scale(__fdiv_rn(a, 127.f)));
-      if (!fresh && s > old) {
-        const float ratio = __fdiv_rn(old, s);
-        const int rows = 1 << p.scale_shift;
-        for (int r = sub; r < rows; r += kRows) {
-          uint2* c = reinterpret_cast<uint2*>(pool + ((blk << p.scale_shift) + r) * pitch + col * 8);
-          const uint2 w = ld_input(c);
-          *c = make_uint2(rescale4(w.x, ratio), rescale4(w.y, ratio));
-        }
-      }
-      __syncwarp();  // the rows below land over the re-encoded ones
-      if (lane == 0) *scale = s;
-#pragma unroll
-      for (int x = 0; x < kPasses; ++x)
-        if (at[x] >= 0) *reinterpret_cast<uint2*>(pool + at[x] * pitch + col * 8) = codes8(v[x], s);
-      for (int64_t r = 16 + sub; r < n; r += kRows) {
-        const int64_t to = slot_of(r);
-        if (to >= 0) *reinterpret_cast<uint2*>(pool + to * pitch + col * 8) = codes8(row(r), s);
-      }
+    for (int x = 0; x < kPasses; ++x)
+      if (at[x] >= 0) *reinterpret_cast<uint2*>(pool + (int64_t)at[x] * pitch) = codes8(v[x], s);
+    for (int64_t r = 16 + sub; r < n; r += kRows) {
+      const int to = mine_of(r);
+      if (to >= 0) *reinterpret_cast<uint2*>(pool + (int64_t)to * pitch) = codes8(row(r), s);
     }
   }
 }

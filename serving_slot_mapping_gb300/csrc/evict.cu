@@ -28,6 +28,8 @@ namespace {
 constexpr int kEvictThreads = 512;
 constexpr int kEvictWarps = kEvictThreads / 32;
 constexpr int kCacheUnits = kMaxEvictPages / 8 + 32;  // keys in shared memory: 160 KB
+constexpr int kBins = 4 * kEvictThreads;              // digits of 11, 11 and 10 bits
+constexpr int kAhead = 4;                             // vectors of a thread in flight
 
 // A float as an integer of the same order; NaN lowest, -0 as 0.
 __device__ __forceinline__ uint32_t order_key(float x) {
@@ -38,15 +40,21 @@ __device__ __forceinline__ uint32_t order_key(float x) {
 __device__ __forceinline__ float ld_float(const float* p) {
   return __uint_as_float(ld_input(reinterpret_cast<const uint32_t*>(p)));
 }
+__device__ __forceinline__ float4 ld_float4(const float* p) {
+  const uint4 v = ld_input(reinterpret_cast<const uint4*>(p));
+  return make_float4(__uint_as_float(v.x), __uint_as_float(v.y), __uint_as_float(v.z), __uint_as_float(v.w));
+}
 
 struct EvictShared {
-  uint32_t hist[256];
-  uint32_t sums[256];          // of the cluster
+  uint32_t hist[kBins];
+  uint32_t warp_sum[kEvictWarps];
   uint32_t above, ties;        // this CTA's units above the threshold (or kept anyway), and at it
   uint32_t digit, left;        // the threshold's digit, units still to be taken at it
   uint32_t warp_above[kEvictWarps], warp_ties[kEvictWarps];
   int32_t count;
 };
+
+__device__ __forceinline__ float plus(float a, float b) { return __fadd_rn(a, b); }
 
 // The weight of a page, for the warp's pages: rows [u * ps, + ps) below L.  M: rows a lane.
 template <int M>
@@ -58,16 +66,29 @@ __device__ __forceinline__ float page_weight(const float* mass, int64_t row, int
   for (int h = M / 2; h > 0; h >>= 1)
 #pragma unroll
     for (int k = 0; k < M / 2; ++k)
-      if (k < h) v[k] += v[k + h];
+      if (k < h) v[k] = plus(v[k], v[k + h]);
   float x = v[0];
-  for (int o = step; o > 0; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
+  for (int o = step; o > 0; o >>= 1) x = plus(x, __shfl_xor_sync(0xffffffffu, x, o));
   return x;
+}
+
+// The same from vectors of four rows, pages of 4 to 128 rows: lanes o / 4 apart add
+// rows o apart, then the vector's own.
+__device__ __forceinline__ float page_weight4(float4 v, int ps) {
+  for (int o = ps / 8; o > 0; o >>= 1) {
+    v.x = plus(v.x, __shfl_xor_sync(0xffffffffu, v.x, o));
+    v.y = plus(v.y, __shfl_xor_sync(0xffffffffu, v.y, o));
+    v.z = plus(v.z, __shfl_xor_sync(0xffffffffu, v.z, o));
+    v.w = plus(v.w, __shfl_xor_sync(0xffffffffu, v.w, o));
+  }
+  return plus(plus(v.x, v.z), plus(v.y, v.w));
 }
 
 template <bool PAGES>
 __global__ void __launch_bounds__(kEvictThreads) evict_kernel(const __grid_constant__ EvictParams p, int csize) {
-  extern __shared__ uint32_t cache[];
-  __shared__ EvictShared sh;
+  extern __shared__ uint4 cache4[];
+  uint32_t* cache = reinterpret_cast<uint32_t*>(cache4);
+  __shared__ __align__(16) EvictShared sh;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int b = blockIdx.x / csize, rank = blockIdx.x - b * csize;
   griddep_wait();
@@ -83,103 +104,150 @@ __global__ void __launch_bounds__(kEvictThreads) evict_kernel(const __grid_const
   const uint32_t want = over ? (uint32_t)(p.budget - front - (units - back)) : 0u;  // of [front, back)
   const int per = ((units + csize - 1) / csize + 31) / 32 * 32;
   const int lo = min(units, rank * per), hi = min(units, lo + per);
-  auto key_of = [&](int u) { return order_key(ld_float(mass + u)); };  // rows
   const int cached = min(hi - lo, kCacheUnits);
-  if (over) {
+  const bool select = over && want > 0u;
+  // ---- the keys of this stretch ----
+  if (select) {
     if constexpr (PAGES) {
-      const int lanes = min(ps, 32), pages = 32 / lanes, m = ps > 32 ? ps / 32 : 1;
-      for (int u0 = lo + warp * pages; u0 < hi; u0 += kEvictWarps * pages) {
-        const int u = u0 + lane / lanes;
-        const int64_t row = (int64_t)u * ps + lane % lanes;
-        const int end = u < hi ? L : 0;
-        float x;
-        switch (m) {
-          case 1: x = page_weight<1>(mass, row, end, lanes / 2); break;
-          case 2: x = page_weight<2>(mass, row, end, 16); break;
-          case 4: x = page_weight<4>(mass, row, end, 16); break;
-          case 8: x = page_weight<8>(mass, row, end, 16); break;
-          case 16: x = page_weight<16>(mass, row, end, 16); break;
-          default: x = page_weight<32>(mass, row, end, 16); break;
+      if (p.vec && ps >= 4 && ps <= 128) {
+        const int pages = 128 / ps, lanes = ps / 4;  // of a warp's vectors
+        const int step = kEvictWarps * pages;
+        for (int u0 = lo + warp * pages; u0 < hi; u0 += step * kAhead) {
+          float4 v[kAhead];
+#pragma unroll
+          for (int k = 0; k < kAhead; ++k) {
+            const int u = u0 + k * step + lane / lanes;
+            const int64_t row = (int64_t)u * ps + lane % lanes * 4;
+            v[k] = make_float4(0.f, 0.f, 0.f, 0.f);
+            if (u < hi && row + 3 < L) {
+              v[k] = ld_float4(mass + row);
+            } else if (u < hi) {
+              if (row < L) v[k].x = ld_float(mass + row);
+              if (row + 1 < L) v[k].y = ld_float(mass + row + 1);
+              if (row + 2 < L) v[k].z = ld_float(mass + row + 2);
+            }
+          }
+#pragma unroll
+          for (int k = 0; k < kAhead; ++k) {
+            const int u = u0 + k * step + lane / lanes;
+            const float x = page_weight4(v[k], ps);
+            if (u < hi && lane % lanes == 0) cache[u - lo] = order_key(x);
+          }
         }
-        if (u < hi && lane % lanes == 0) cache[u - lo] = order_key(x);
+      } else {
+        const int lanes = min(ps, 32), pages = 32 / lanes, m = ps > 32 ? ps / 32 : 1;
+        for (int u0 = lo + warp * pages; u0 < hi; u0 += kEvictWarps * pages) {
+          const int u = u0 + lane / lanes;
+          const int64_t row = (int64_t)u * ps + lane % lanes;
+          const int end = u < hi ? L : 0;
+          float x;
+          switch (m) {
+            case 1: x = page_weight<1>(mass, row, end, lanes / 2); break;
+            case 2: x = page_weight<2>(mass, row, end, 16); break;
+            case 4: x = page_weight<4>(mass, row, end, 16); break;
+            case 8: x = page_weight<8>(mass, row, end, 16); break;
+            case 16: x = page_weight<16>(mass, row, end, 16); break;
+            default: x = page_weight<32>(mass, row, end, 16); break;
+          }
+          if (u < hi && lane % lanes == 0) cache[u - lo] = order_key(x);
+        }
       }
     } else {
-      for (int i = tid; i < cached; i += kEvictThreads) cache[i] = key_of(lo + i);
+      const int vecs = p.vec ? cached / 4 : 0;  // lo is a multiple of 32
+      for (int i0 = tid; i0 < vecs; i0 += kAhead * kEvictThreads) {
+        float4 v[kAhead];
+#pragma unroll
+        for (int k = 0; k < kAhead; ++k)
+          if (i0 + k * kEvictThreads < vecs) v[k] = ld_float4(mass + lo + 4 * (i0 + k * kEvictThreads));
+#pragma unroll
+        for (int k = 0; k < kAhead; ++k)
+          if (i0 + k * kEvictThreads < vecs)
+            cache4[i0 + k * kEvictThreads] =
+                make_uint4(order_key(v[k].x), order_key(v[k].y), order_key(v[k].z), order_key(v[k].w));
+      }
+      for (int i = 4 * vecs + tid; i < cached; i += kEvictThreads) cache[i] = order_key(ld_float(mass + lo + i));
     }
   }
-  auto key = [&](int u) { return PAGES || u - lo < kCacheUnits ? cache[u - lo] : key_of(u); };
+  auto key = [&](int u) { return PAGES || u - lo < kCacheUnits ? cache[u - lo] : order_key(ld_float(mass + u)); };
   // ---- the threshold: the want-th largest key of [front, back) ----
   uint32_t prefix = 0u, left = want;  // digits so far; units still to be found below them
-  const bool select = over && want > 0u;
   if (select) {
     const int a = max(lo, front), e = min(hi, back);
-    for (int shift = 24; shift >= 0; shift -= 8) {
-      if (tid < 256) sh.hist[tid] = 0u;
+    for (int pass = 0; pass < 3; ++pass) {
+      const int shift = pass == 0 ? 21 : (pass == 1 ? 10 : 0);
+      const uint32_t digits = pass == 2 ? 1023u : 2047u;
+      reinterpret_cast<uint4*>(sh.hist)[tid] = make_uint4(0u, 0u, 0u, 0u);
       __syncthreads();
       for (int u = a + tid; u < e; u += kEvictThreads) {
         const uint32_t k = key(u);
-        if (shift == 24 || (k >> (shift + 8)) == (prefix >> (shift + 8))) atomicAdd(&sh.hist[(k >> shift) & 255u], 1u);
+        if (pass == 0 || (k >> (pass == 1 ? 21 : 10)) == (prefix >> (pass == 1 ? 21 : 10)))
+          atomicAdd(&sh.hist[(k >> shift) & digits], 1u);
       }
       if (csize > 1) cluster_sync(); else __syncthreads();
-      if (tid < 256) {
-        uint32_t n = 0u;
-        if (csize > 1)
-          for (int c = 0; c < csize; ++c) n += ld_cluster(map_rank(smem_u32(&sh.hist[tid]), c));
-        else
-          n = sh.hist[tid];
-        sh.sums[tid] = n;
+      // thread i: digits 4 (511 - i) .. + 3 of all CTAs, the highest digits first
+      const int g = kEvictThreads - 1 - tid;
+      uint4 n = reinterpret_cast<const uint4*>(sh.hist)[g];
+      if (csize > 1) {
+        n = make_uint4(0u, 0u, 0u, 0u);
+        for (int c = 0; c < csize; ++c) {
+          const float4 x = ld_cluster4(map_rank(smem_u32(&sh.hist[4 * g]), c));
+          n.x += __float_as_uint(x.x);
+          n.y += __float_as_uint(x.y);
+          n.z += __float_as_uint(x.z);
+          n.w += __float_as_uint(x.w);
+        }
+      }
+      const uint32_t mine = n.x + n.y + n.z + n.w;
+      uint32_t incl = mine;
+      for (int o = 1; o < 32; o <<= 1) {
+        const uint32_t t = __shfl_up_sync(0xffffffffu, incl, o);
+        if (lane >= o) incl += t;
+      }
+      if (lane == 31) sh.warp_sum[warp] = incl;
+      __syncthreads();
+      for (int w = 0; w < warp; ++w) incl += sh.warp_sum[w];
+      uint32_t before = incl - mine;
+      if (incl >= left && before < left) {
+        int d = 4 * g + 3;
+        const uint32_t four[4] = {n.w, n.z, n.y, n.x};
+#pragma unroll
+        for (int k = 0; k < 3; ++k)
+          if (d == 4 * g + 3 - k && before + four[k] < left) {
+            before += four[k];
+            --d;
+          }
+        sh.digit = (uint32_t)d;
+        sh.left = left - before;
       }
       if (csize > 1) cluster_sync(); else __syncthreads();  // every histogram is read
-      if (warp == 0) {  // lane i: digits 255 - 8 i down to 248 - 8 i
-        uint32_t n = 0u;
-        for (int k = 0; k < 8; ++k) n += sh.sums[255 - 8 * lane - k];
-        uint32_t incl = n;
-        for (int o = 1; o < 32; o <<= 1) {
-          const uint32_t t = __shfl_up_sync(0xffffffffu, incl, o);
-          if (lane >= o) incl += t;
-        }
-        if (incl >= left && incl - n < left) {
-          uint32_t before = incl - n;
-          int d = 255 - 8 * lane;
-          while (before + sh.sums[d] < left) before += sh.sums[d--];
-          sh.digit = (uint32_t)d;
-          sh.left = left - before;
-        }
-      }
-      __syncthreads();
       prefix |= sh.digit << shift;
       left = sh.left;
     }
   }
   // ---- this stretch's units above the threshold and at it ----
-  auto classify = [&](int u, bool* above, bool* tie) {
-    *above = *tie = false;
-    if (u >= hi) return;
-    if (u < front || u >= back) {
-      *above = true;
-    } else if (select) {
-      const uint32_t k = key(u);
-      *above = k > prefix;
-      *tie = k == prefix;
-    }
-  };
   // a warp walks a stretch of its own, 32 units at a time
   const int wper = (((hi - lo) + kEvictWarps - 1) / kEvictWarps + 31) / 32 * 32;
   const int wlo = min(hi, lo + warp * wper), whi = min(hi, wlo + wper);
+  auto classify = [&](int u, uint32_t k, bool* above, bool* tie) {
+    const bool may = select && u >= front && u < back;
+    *above = u < whi && (may ? k > prefix : u < front || u >= back);
+    *tie = u < whi && may && k == prefix;
+  };
   __syncthreads();
   uint32_t n_above = 0u, n_ties = 0u;
   for (int u0 = wlo; u0 < whi; u0 += 32) {
     bool ab, ti;
-    classify(u0 + lane, &ab, &ti);
-    ab &= u0 + lane < whi;
-    ti &= u0 + lane < whi;
-    n_above += __popc(__ballot_sync(0xffffffffu, ab));
-    n_ties += __popc(__ballot_sync(0xffffffffu, ti));
+    classify(u0 + lane, select && u0 + lane < whi ? key(u0 + lane) : 0u, &ab, &ti);
+    n_above += ab ? 1u : 0u;
+    n_ties += ti ? 1u : 0u;
   }
+  n_above = __reduce_add_sync(0xffffffffu, n_above);
+  n_ties = __reduce_add_sync(0xffffffffu, n_ties);
   if (lane == 0) {
     sh.warp_above[warp] = n_above;
     sh.warp_ties[warp] = n_ties;
   }
+  if (tid == 0) sh.count = 0;
   __syncthreads();
   if (tid == 0) {
     uint32_t x = 0u, y = 0u;
@@ -189,6 +257,13 @@ __global__ void __launch_bounds__(kEvictThreads) evict_kernel(const __grid_const
     }
     sh.above = x;
     sh.ties = y;
+  }
+  // where this sequence's list begins
+  if constexpr (!PAGES) {
+    int n = 0;
+    for (int i = tid; i < b; i += kEvictThreads) n += ld_seq_len(p.seq_lens, i, p.max_len, nullptr) > p.budget ? 1 : 0;
+    n = __reduce_add_sync(0xffffffffu, n);
+    if (lane == 0 && n != 0) atomicAdd(&sh.count, n);
   }
   if (csize > 1) cluster_sync(); else __syncthreads();
   uint32_t above = 0u, ties = 0u, all_above = 0u;
@@ -206,55 +281,95 @@ __global__ void __launch_bounds__(kEvictThreads) evict_kernel(const __grid_const
     ties += sh.warp_ties[w];
   }
   const uint32_t kept_total = select ? all_above + left : all_above;
-  // ---- where this sequence's list begins ----
-  int64_t list = 0;
-  if constexpr (!PAGES) {
-    if (tid == 0) sh.count = 0;
-    __syncthreads();
-    const int share = p.budget - p.num_sinks;
-    int n = 0;
-    for (int i = tid; i < b; i += kEvictThreads) n += ld_seq_len(p.seq_lens, i, p.max_len, nullptr) > p.budget ? 1 : 0;
-    n = __reduce_add_sync(0xffffffffu, n);
-    if (lane == 0 && n != 0) atomicAdd(&sh.count, n);
-    __syncthreads();
-    list = (int64_t)sh.count * share;
-    if (rank == 0 && tid == 0) {
-      if (b == 0) p.keep_indptr[0] = 0;
-      p.keep_indptr[b + 1] = (int32_t)(list + (over ? share : 0));
-      p.base[b] = over ? p.num_sinks : L;
-    }
+  const int share = PAGES ? 0 : p.budget - p.num_sinks;
+  const int64_t list = (int64_t)sh.count * share;
+  if (!PAGES && rank == 0 && tid == 0) {
+    if (b == 0) p.keep_indptr[0] = 0;
+    p.keep_indptr[b + 1] = (int32_t)(list + (over ? share : 0));
+    p.base[b] = over ? p.num_sinks : L;
   }
   // ---- ranks, and the moves ----
-  for (int u0 = wlo; u0 < whi; u0 += 32) {
-    const int u = u0 + lane;
+  // The rank of unit u0 + lane among those kept, 0xFFFFFFFF if it goes; `before`: the
+  // kept ones in front of it.
+  auto rank_of = [&](int u, uint32_t k, uint32_t* before) {
     bool ab, ti;
-    classify(u, &ab, &ti);
-    ab &= u < whi;
-    ti &= u < whi;
+    classify(u, k, &ab, &ti);
     const unsigned ma = __ballot_sync(0xffffffffu, ab), mt = __ballot_sync(0xffffffffu, ti);
     const unsigned below = (1u << lane) - 1u;
     const uint32_t tr = ties + __popc(mt & below);
-    const bool kept = ab || (ti && tr < left);
-    const uint32_t at = above + __popc(ma & below) + min(tr, select ? left : 0u);
-    if constexpr (PAGES) {
-      if (u < whi) {
-        const int page = ld_input(p.block_table + (int64_t)b * p.max_blocks + u);
-        p.new_block_table[(int64_t)b * p.max_blocks + (kept ? at : kept_total + ((uint32_t)u - at))] = page;
-      }
-      for (unsigned m = __ballot_sync(0xffffffffu, kept); m != 0u; m &= m - 1u) {
-        const int src = __ffs(m) - 1;
-        const int64_t to = (int64_t)__shfl_sync(0xffffffffu, at, src) * ps, from = (int64_t)(u0 + src) * ps;
-        for (int r = lane; r < ps && from + r < L; r += 32) new_mass[to + r] = ld_float(mass + from + r);
-      }
-    } else if (kept) {
-      new_mass[at] = ld_float(mass + u);
-      if (over && (int)at >= p.num_sinks) p.keep[list + (int)at - p.num_sinks] = u;
-    }
+    *before = above + __popc(ma & below) + min(tr, select ? left : 0u);
     above += __popc(ma);
     ties += __popc(mt);
+    return ab || (ti && tr < left) ? *before : 0xFFFFFFFFu;
+  };
+  if constexpr (PAGES) {
+    const int64_t table = (int64_t)b * p.max_blocks;
+    for (int u0 = wlo; u0 < whi; u0 += 32) {
+      const int u = u0 + lane;
+      uint32_t before;
+      const uint32_t r = rank_of(u, select && u < whi ? key(u) : 0u, &before);
+      if (u < whi) {
+        p.new_block_table[table + (r != 0xFFFFFFFFu ? r : kept_total + ((uint32_t)u - before))] =
+            ld_input(p.block_table + table + u);
+        cache[u - lo] = r;  // its key is done with: each warp reads its own stretch alone
+      }
+    }
+    __syncthreads();
+    // the rows of the stretch that stay, four at a time where pages and rows allow
+    const int64_t row0 = (int64_t)lo * ps, row1 = min((int64_t)L, (int64_t)hi * ps);
+    const int shift = 31 - __clz(ps);
+    if (p.vec && ps >= 4) {
+      for (int64_t i0 = row0 / 4 + tid; 4 * i0 + 3 < row1; i0 += kAhead * kEvictThreads) {
+        float4 v[kAhead];
+        int64_t to[kAhead];
+#pragma unroll
+        for (int k = 0; k < kAhead; ++k) {
+          const int64_t row = 4 * (i0 + k * kEvictThreads);
+          to[k] = -1;
+          if (row + 3 < row1) {
+            const uint32_t r = cache[(int)(row >> shift) - lo];
+            if (r != 0xFFFFFFFFu) {
+              to[k] = (int64_t)r * ps + (row & (ps - 1));
+              v[k] = ld_float4(mass + row);
+            }
+          }
+        }
+#pragma unroll
+        for (int k = 0; k < kAhead; ++k)
+          if (to[k] >= 0) *reinterpret_cast<float4*>(new_mass + to[k]) = v[k];
+      }
+    }
+    const int64_t rest = p.vec && ps >= 4 ? row1 / 4 * 4 : row0;  // (lo * ps is a multiple of 32)
+    for (int64_t row = max(rest, row0) + tid; row < row1; row += kEvictThreads) {
+      const uint32_t r = cache[(int)(row >> shift) - lo];
+      if (r != 0xFFFFFFFFu) new_mass[(int64_t)r * ps + (row & (ps - 1))] = ld_float(mass + row);
+    }
+  } else {
+    for (int u0 = wlo; u0 < whi; u0 += 32 * kAhead) {
+      float v[kAhead];
+#pragma unroll
+      for (int k = 0; k < kAhead; ++k) v[k] = u0 + 32 * k + lane < whi ? ld_float(mass + u0 + 32 * k + lane) : 0.f;
+#pragma unroll
+      for (int k = 0; k < kAhead; ++k) {
+        uint32_t before;
+        const uint32_t r = rank_of(u0 + 32 * k + lane, order_key(v[k]), &before);
+        if (r != 0xFFFFFFFFu) {
+          new_mass[r] = v[k];
+          if (over && (int)r >= p.num_sinks) p.keep[list + (int)r - p.num_sinks] = u0 + 32 * k + lane;
+        }
+      }
+    }
   }
   const int new_len = PAGES ? L - ps * (units - (int)kept_total) : (int)kept_total;
-  for (int i = new_len + rank * kEvictThreads + tid; i < p.width; i += csize * kEvictThreads) new_mass[i] = 0.f;
+  int zero = new_len;
+  if (p.vec) {  // whole vectors of zeros behind the next multiple of 4
+    const int z4 = (new_len + 3) / 4;
+    for (int i = z4 + rank * kEvictThreads + tid; 4 * i + 3 < p.width; i += csize * kEvictThreads)
+      reinterpret_cast<float4*>(new_mass)[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (rank == 0 && tid < 4 && new_len + tid < min(4 * z4, p.width)) new_mass[new_len + tid] = 0.f;
+    zero = max(new_len, p.width / 4 * 4);
+  }
+  for (int i = zero + rank * kEvictThreads + tid; i < p.width; i += csize * kEvictThreads) new_mass[i] = 0.f;
   if constexpr (PAGES) {
     for (int i = units + rank * kEvictThreads + tid; i < p.max_blocks; i += csize * kEvictThreads)
       p.new_block_table[(int64_t)b * p.max_blocks + i] = ld_input(p.block_table + (int64_t)b * p.max_blocks + i);
@@ -269,15 +384,16 @@ cudaError_t launch_evict(const EvictParams& p, bool pages, int num_sms, cudaStre
   if (p.batch <= 0) return cudaSuccess;
   const int64_t units = pages ? std::min<int64_t>(p.max_blocks, (p.max_len + p.page_size - 1) / p.page_size) : p.max_len;
   if (pages && units > kMaxEvictPages) return cudaErrorInvalidValue;  // their weights have no place
-  // CTAs of a sequence: as many as find an SM, with 4096 units each or more; enough
+  // CTAs of a sequence: as many as find an SM, with 4096 rows each or more; enough
   // that their stretches fit in shared memory, where 8 can
+  const int64_t rows = pages ? units * p.page_size : units;
   int csize = 1;
-  while (csize < 8 && ((int64_t)p.batch * csize * 2 <= num_sms && units >= 4096 * 2 * (int64_t)csize)) csize *= 2;
+  while (csize < 8 && ((int64_t)p.batch * csize * 2 <= num_sms && rows >= 4096 * 2 * (int64_t)csize)) csize *= 2;
   while (csize < 8 && units > (int64_t)csize * (kCacheUnits - 32)) csize *= 2;
   const int64_t stretch = (units + csize - 1) / csize + 32;
-  const int smem = (int)(stretch < kCacheUnits ? stretch : kCacheUnits) * 4;
+  const int smem = (int)(stretch < kCacheUnits ? stretch : kCacheUnits) * 4 + 16;
   auto kern = pages ? evict_kernel<true> : evict_kernel<false>;
-  const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kCacheUnits * 4);
+  const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kCacheUnits * 4 + 16);
   if (e != cudaSuccess) return e;
   return launch_pdl_cluster(kern, dim3((unsigned)(p.batch * csize)), dim3(kEvictThreads), (size_t)smem, csize, s, p, csize);
 }

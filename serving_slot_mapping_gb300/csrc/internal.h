@@ -76,6 +76,7 @@ struct EvictParams {
   int32_t* new_block_table;
   int32_t* new_seq_lens;
   int32_t max_blocks, page_size;
+  int32_t vec;              // rows of both masses start on 16 bytes
   unsigned long long* err;
 };
 cudaError_t launch_evict(const EvictParams& p, bool pages, int num_sms, cudaStream_t s);
