@@ -30,13 +30,13 @@
 // up; slots of loaded pages that no row of the sequence sees (between the sinks
 // and the sequence's first window key, or at and past L_b) are zeroed in V.
 // int8 pools (SC; paged_attention_prefill_int8, a window that reaches every key): the
-// codes land like e4m3 ones.  A tile's 16-key blocks each have a scale; with R the
+// codes land as they are, in stages of their own.  A tile's 16-key blocks each have a scale; with R the
 // largest of the tile, for K and for V:
 // * warp 10 looks the scales up ahead and hands out, per tile, the f16 ratios s / R
 //   of the 8 blocks and R_k, log2 R_v, 1 / R_v (a ring of four tiles);
-// * four converter warps take a whole tile of codes into registers, meet, and write
-//   f16(code * ratio) over it (code exact, ratio and product rounded: 2^-11 of a
-//   value at most, beside 2^-8 of its own rounding to 8 bits);
+// * four converter warps take the tiles in the order that the products ask for them,
+//   K(0), then K(t + 1), V(t), and write f16(code * ratio) (code exact, ratio and
+//   product rounded: 2^-10 of a value at most, beside 2^-8 of its own rounding to 8 bits);
 // * R_k goes into the factor of S that the softmax has anyway, log2 R_v into the
 //   reference max (y = x + log2 R_v; P = 2^(y - m) stays in f16's range whatever the
 //   scales are), and l sums P / R_v.  No work is added for an element of S.
@@ -79,7 +79,7 @@ struct WCfg : PCfg<D, KV8> {
   // (2 x 192 + 120) = 3 x 168.
   // int8: a fourth one, 128 registers a thread at launch.
   static constexpr int kThreads = SC ? 512 : 384;
-  static constexpr int kSoftmaxRegs = KV8 ? 192 : 200, kOtherRegs = SC ? 64 : (KV8 ? 120 : 104);
+  static constexpr int kSoftmaxRegs = SC ? 144 : (KV8 ? 192 : 200), kOtherRegs = SC ? 112 : (KV8 ? 120 : 104);
   static_assert(SC ? 2 * kSoftmaxRegs + 2 * kOtherRegs <= 4 * 128 : 2 * kSoftmaxRegs + kOtherRegs <= 3 * 168,
                 "more registers than the launch has");
   // 8 tiles in flight: {KV head, valid, hid0, hid1} after the first slots of their boxes
@@ -89,6 +89,16 @@ struct WCfg : PCfg<D, KV8> {
   static constexpr int kTmemOff = kWBarOff + kWBars * 8;  // the word that tcgen05.alloc writes, behind every barrier
   static_assert(kTmemOff >= kWBarOff + 8 * W_COUNT, "the TMEM base lies on a barrier");
   static constexpr int kBadOff = kTmemOff + 8;  // a page out of range was met
+  // int8: K and V rings of two f16 tiles each, then two stages of codes (16 KB for 128
+  // dims), in the space of the others' three and two tiles.  Codes that land in the slot
+  // of their f16 tile (as e4m3 ones do) can be loaded only once the products on that
+  // slot's last tile are done, and load and conversion then lie in a row: 1426 us for 19
+  // chunks of 512 after 4096 tokens, 32 / 8 heads; with stages of their own 
+  static constexpr int kNK = SC ? 2 : kNSK;
+  static constexpr int kVRing = SC ? Base::kKOff + 2 * Base::kKVTile : Base::kVOff;
+  static constexpr int kCodeOff = Base::kKOff + (2 + kNSV) * Base::kKVTile;
+  static constexpr int kCodeTile = kBN * D;
+  static_assert(!SC || kCodeOff + 2 * kCodeTile <= Base::kPageOff, "the stages of codes");
   static constexpr int kScaleOff = kTmemOff + 16;
   static constexpr int kWSmem = kScaleOff + (SC ? kScaleTiles * kScaleBytes : 0) + 1024;
   static_assert(kScaleOff % 16 == 0 && kWSmem <= 232448, "shared memory");
@@ -318,6 +328,7 @@ __global__ void __launch_bounds__(WCfg<D, KV8, SC>::kThreads, 1)
   const int csize = SPLIT ? csize_arg : 1;
   using C = WCfg<D, KV8, SC>;
   static_assert(!SC || KV8, "int8 codes land as e4m3 ones do");
+  constexpr int NK = C::kNK;
   constexpr bool kItemWarp = !KV8 || SC;  // warp 10 derives the items, else the TMA warp
   extern __shared__ unsigned char smem_raw[];
   unsigned char* smem = reinterpret_cast<unsigned char*>(
@@ -329,7 +340,7 @@ __global__ void __launch_bounds__(WCfg<D, KV8, SC>::kThreads, 1)
   const int ops = kBN / kpo;
   unsigned char* q_s = smem + C::kQOff;
   const uint32_t k_base = smem_u32(smem + C::kKOff);
-  const uint32_t v_base = smem_u32(smem + C::kVOff);
+  const uint32_t v_base = smem_u32(smem + C::kVRing);
   const uint32_t bars = smem_u32(smem + C::kWBarOff);
   auto bar = [&](int i) { return bars + 8u * i; };
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + C::kTmemOff);
@@ -354,7 +365,7 @@ __global__ void __launch_bounds__(WCfg<D, KV8, SC>::kThreads, 1)
       mbar_init(bar(W_KREADY + s), SC ? kI8Warps : 1);
     }
     for (int s = 0; s < kNSV; ++s) {
-      mbar_init(bar(W_VFULL + s), 1);
+      mbar_init(bar(W_VFULL + s), SC ? kI8Warps : 1);  // (int8: the stage of codes is free)
       mbar_init(bar(W_VEMPTY + s), 1);
       mbar_init(bar(W_VREADY + s), SC ? kI8Warps : 1);
     }
@@ -446,8 +457,8 @@ __global__ void __launch_bounds__(WCfg<D, KV8, SC>::kThreads, 1)
       if (lane == 0) mbar_arrive_expect_tx(full, (uint32_t)cnt * box_bytes);
       __syncwarp();
       if (ok) {
-        if (KV8)  // codes in the ring slot's upper half, [keys][D B]
-          tma_load_3d(dst + (uint32_t)(kBN * D + lane * kpo * D), map, 0, slot, hk, full);
+        if (KV8)  // codes [keys][D B] in the ring slot's upper half (int8: in a stage of their own)
+          tma_load_3d(dst + (uint32_t)((SC ? 0 : kBN * D) + lane * kpo * D), map, 0, slot, hk, full);
         else
           tma_load_5d(dst + (uint32_t)(lane * (kpo / 8)) * C::kRowBlock, map, 0, 0, 0, slot >> 3, hk, full);
       }
@@ -486,7 +497,13 @@ __global__ void __launch_bounds__(WCfg<D, KV8, SC>::kThreads, 1)
         }
         progressed = true;
       }
-      if (more && (kt < kNSK || phase_done(W_KEMPTY + kt % kNSK, (uint32_t)((kt / kNSK - 1) & 1)))) {
+      // int8: stage (kt + vt) % 2 of the codes, in the converters' order
+      const int stage = (kt + vt) & 1;
+      const bool stage_free = SC && (kt + vt < 2 || phase_done(W_VFULL + stage, (uint32_t)(((kt + vt) / 2 - 1) & 1)));
+      const uint32_t code_dst = smem_u32(smem + C::kCodeOff) + stage * C::kCodeTile;
+      const bool v_turn = SC && stage_free && vt < kt && (kt - vt == 2 || (end && !more));
+      if (more && (SC ? stage_free && kt - vt < 2
+                      : (kt < kNSK || phase_done(W_KEMPTY + kt % kNSK, (uint32_t)((kt / kNSK - 1) & 1))))) {
         const int key = box_key(j);
         int slot = -1;
         if (box_used(key)) {
@@ -503,13 +520,22 @@ __global__ void __launch_bounds__(WCfg<D, KV8, SC>::kThreads, 1)
           const int end = it.seq_start <= it.head_keys ? it.seq_start : max(it.head_keys, it.seq_start - it.gap);
           meta[kt & 7] = make_int4(it.hk, min(it.L - it.gap - l0, kBN), max(0, p.num_sinks - l0), min(end - l0, kBN));
         }
-        issue(&tmap_k, k_base + (kt % kNSK) * C::kKVTile, it.hk, slot, bar(W_KFULL + kt % kNSK));
+        if constexpr (SC)
+          issue(&tmap_k, code_dst, it.hk, slot, bar(W_KFULL + stage));
+        else
+          issue(&tmap_k, k_base + (kt % kNSK) * C::kKVTile, it.hk, slot, bar(W_KFULL + kt % kNSK));
         ++kt;
         more = ++j < it.nt();
         if (more) raw = fetch(j);
         progressed = true;
       }
-      if (vt < kt && (vt < kNSV || phase_done(W_VEMPTY + vt % kNSV, (uint32_t)((vt / kNSV - 1) & 1)))) {
+      if constexpr (SC) {
+        if (v_turn) {
+          issue(&tmap_v, code_dst, meta[vt & 7].x, slot_ring[(vt & 7) * 32 + lane], bar(W_KFULL + stage));
+          ++vt;
+          progressed = true;
+        }
+      } else if (vt < kt && (vt < kNSV || phase_done(W_VEMPTY + vt % kNSV, (uint32_t)((vt / kNSV - 1) & 1)))) {
         const int4 m = meta[vt & 7];
         // rows that may hold anything meet P = 0 and must be zeros (e4m3: the converter writes them)
         const bool clear = !KV8 && (m.y < kBN || m.z < m.w);
@@ -644,50 +670,54 @@ __global__ void __launch_bounds__(WCfg<D, KV8, SC>::kThreads, 1)
     }
     if (warp >= 16 - kI8Warps) {
       // ======================= int8 -> f16 converters (warps 12 .. 15) =======================
-      // Tiles in the order that the products ask for them: K(0), then K(t + 1), V(t).
       const int part = warp - (16 - kI8Warps);
-      auto convert = [&](unsigned char* slot, const volatile uint16_t* ratios) {
-        constexpr int kChunks = D / 16, kKeysPerLoad = 32 / kChunks, kLoads = 8 / kKeysPerLoad;
-        const int q4 = lane >> 3, j8 = lane & 7;
-        const int m = D == 128 ? (j8 & 3) + 4 * (j8 >> 2) : lane % kChunks;
-        const int r0 = D == 128 ? 2 * (q4 >> 1) + ((j8 >> 2) ^ (q4 & 1)) : lane / kChunks;
-        const unsigned char* codes = slot + kBN * D;
-        uint4 raw[4][kLoads];  // this warp's quarter of the tile: four 8-key blocks
+      int ct = 0;  // tiles of codes taken
+      constexpr int kChunks = D / 16, kKeysPerLoad = 32 / kChunks, kLoads = 8 / kKeysPerLoad;
+      const int q4 = lane >> 3, j8 = lane & 7;  // (bank-conflict-free as in convert_tile_e4m3)
+      const int m = D == 128 ? (j8 & 3) + 4 * (j8 >> 2) : lane % kChunks;
+      const int r0 = D == 128 ? 2 * (q4 >> 1) + ((j8 >> 2) ^ (q4 & 1)) : lane / kChunks;
+      auto tile = [&](int t, bool isv) {
+        const int n = isv ? kNSV : NK, sl = t % n, stage = ct & 1;
+        if (alive) alive = mbar_wait(bar(W_KFULL + stage), (uint32_t)((ct >> 1) & 1), p.err);
+        ++ct;
+        if (t >= n && alive)  // the products on the slot's last tile are done
+          alive = mbar_wait(bar((isv ? W_VEMPTY : W_KEMPTY) + sl), (uint32_t)((t / n - 1) & 1), p.err);
+        const volatile uint16_t* ratios = (isv ? scale_ring[t % kScaleTiles].v : scale_ring[t % kScaleTiles].k) + part * 2;
+        // this warp's quarter of the tile: four 8-key blocks, two (of one scale) at a time
+        const unsigned char* codes = smem + C::kCodeOff + stage * C::kCodeTile + (part * 32 + r0) * D + m * 16;
+        unsigned char* slot = smem + (isv ? C::kVRing : C::kKOff) + sl * C::kKVTile + part * 4 * C::kRowBlock;
+#pragma unroll 1
+        for (int k2 = 0; k2 < 2; ++k2) {
+          uint4 raw[2][kLoads];
 #pragma unroll
-        for (int kb = 0; kb < 4; ++kb)
+          for (int kb = 0; kb < 2; ++kb)
 #pragma unroll
-          for (int x = 0; x < kLoads; ++x)
-            raw[kb][x] = *reinterpret_cast<const uint4*>(codes + ((part * 4 + kb) * 8 + r0 + x * kKeysPerLoad) * D + m * 16);
-        const uint32_t two[2] = {(uint32_t)ratios[part * 2] * 0x10001u, (uint32_t)ratios[part * 2 + 1] * 0x10001u};
-        named_barrier(2, kI8Warps * 32);  // the f16 tile lies over the codes: all are read
-#pragma unroll
-        for (int kb = 0; kb < 4; ++kb) {
-          const __half2 f = *reinterpret_cast<const __half2*>(&two[kb >> 1]);
+            for (int x = 0; x < kLoads; ++x)
+              raw[kb][x] = *reinterpret_cast<const uint4*>(codes + ((2 * k2 + kb) * 8 + x * kKeysPerLoad) * D);
+          const uint32_t two = (uint32_t)ratios[k2] * 0x10001u;
+          const __half2 f = *reinterpret_cast<const __half2*>(&two);
           auto both = [&](uint32_t c) {
             const __half2 v = __hmul2(*reinterpret_cast<const __half2*>(&c), f);
             return *reinterpret_cast<const uint32_t*>(&v);
           };
 #pragma unroll
-          for (int x = 0; x < kLoads; ++x) {
-            const int kr = r0 + x * kKeysPerLoad;
-            const uint4 w = raw[kb][x];
-            unsigned char* blk = slot + (part * 4 + kb) * C::kRowBlock + kr * 128;
-            const int c0 = 2 * m, c1 = 2 * m + 1;  // 8-dim chunks over D
-            *reinterpret_cast<uint4*>(blk + (c0 >> 3) * 1024 + (((c0 & 7) ^ kr) << 4)) =
-                make_uint4(both(i8x2_to_f16x2<0, 1>(w.x)), both(i8x2_to_f16x2<2, 3>(w.x)),
-                           both(i8x2_to_f16x2<0, 1>(w.y)), both(i8x2_to_f16x2<2, 3>(w.y)));
-            *reinterpret_cast<uint4*>(blk + (c1 >> 3) * 1024 + (((c1 & 7) ^ kr) << 4)) =
-                make_uint4(both(i8x2_to_f16x2<0, 1>(w.z)), both(i8x2_to_f16x2<2, 3>(w.z)),
-                           both(i8x2_to_f16x2<0, 1>(w.w)), both(i8x2_to_f16x2<2, 3>(w.w)));
-          }
+          for (int kb = 0; kb < 2; ++kb)
+#pragma unroll
+            for (int x = 0; x < kLoads; ++x) {
+              const int kr = r0 + x * kKeysPerLoad;
+              const uint4 w = raw[kb][x];
+              unsigned char* blk = slot + (2 * k2 + kb) * C::kRowBlock + kr * 128;
+              const int c0 = 2 * m, c1 = 2 * m + 1;  // 8-dim chunks over D
+              *reinterpret_cast<uint4*>(blk + (c0 >> 3) * 1024 + (((c0 & 7) ^ kr) << 4)) =
+                  make_uint4(both(i8x2_to_f16x2<0, 1>(w.x)), both(i8x2_to_f16x2<2, 3>(w.x)),
+                             both(i8x2_to_f16x2<0, 1>(w.y)), both(i8x2_to_f16x2<2, 3>(w.y)));
+              *reinterpret_cast<uint4*>(blk + (c1 >> 3) * 1024 + (((c1 & 7) ^ kr) << 4)) =
+                  make_uint4(both(i8x2_to_f16x2<0, 1>(w.z)), both(i8x2_to_f16x2<2, 3>(w.z)),
+                             both(i8x2_to_f16x2<0, 1>(w.w)), both(i8x2_to_f16x2<2, 3>(w.w)));
+            }
         }
-      };
-      auto tile = [&](int t, bool isv) {
-        const int n = isv ? kNSV : kNSK, sl = t % n;
-        if (alive)
-          alive = mbar_wait(bar((isv ? W_VFULL : W_KFULL) + sl), (uint32_t)((t / n) & 1), p.err);
-        convert(smem + (isv ? C::kVOff : C::kKOff) + sl * C::kKVTile,
-                isv ? scale_ring[t % kScaleTiles].v : scale_ring[t % kScaleTiles].k);
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar(W_VFULL + stage));  // the codes are read
         fence_proxy_async_smem();  // the f16 tile before the tensor core reads it
         __syncwarp();
         if (lane == 0) mbar_arrive(bar((isv ? W_VREADY : W_KREADY) + sl));
@@ -697,23 +727,23 @@ __global__ void __launch_bounds__(WCfg<D, KV8, SC>::kThreads, 1)
         if (alive) alive = mbar_wait(bar(W_CFULL + s), (uint32_t)((t / kScaleTiles) & 1), p.err);
         return alive && scale_ring[s].k_ref >= 0.f;
       };
-      // (named barriers inside: the four warps go on or stop together)
-      auto agreed = [&](bool x) {
-        int any;
-        asm volatile("{\n .reg .pred p, q;\n setp.ne.s32 p, %1, 0;\n bar.red.and.pred q, 3, %2, p;\n selp.s32 %0, 1, 0, q;\n}\n"
-                     : "=r"(any)
-                     : "r"(x ? 1 : 0), "r"(kI8Warps * 32)
-                     : "memory");
-        return any != 0;
-      };
-      bool have = agreed(there(0));
-      if (have) tile(0, false);
-      for (int t = 0; have; ++t) {
-        have = agreed(there(t + 1));
-        if (have) tile(t + 1, false);
-        tile(t, true);
-        __syncwarp();
-        if (lane == 0) mbar_arrive(bar(W_CEMPTY + t % kScaleTiles));
+      int kt = 0, vt = 0;
+      bool ended = false;
+      for (;;) {  // (one call: see kHeld below)
+        bool isv = kt - vt == 2 || ended;
+        if (!isv && !__all_sync(0xffffffffu, there(kt))) {
+          ended = true;
+          isv = true;
+        }
+        if (isv && vt == kt) break;
+        tile(isv ? vt : kt, isv);
+        if (isv) {
+          __syncwarp();
+          if (lane == 0) mbar_arrive(bar(W_CEMPTY + vt % kScaleTiles));
+          ++vt;
+        } else {
+          ++kt;
+        }
       }
     }
   }
@@ -764,9 +794,9 @@ __global__ void __launch_bounds__(WCfg<D, KV8, SC>::kThreads, 1)
         // S_t of key tile j of an item whose tiles start at k0: wait for K where
         // this is the first S of the tile, free its stage where it is the last
         auto issue_s = [&](const Item& x, int k0, int t, int j) {
-          const int kt = k0 + j, sk = kt % kNSK;
+          const int kt = k0 + j, sk = kt % NK;
           if (t == 0 || j >= x.nt0) {
-            if (alive) alive = mbar_wait(bar(kKWait + sk), (uint32_t)((kt / kNSK) & 1), p.err);
+            if (alive) alive = mbar_wait(bar(kKWait + sk), (uint32_t)((kt / NK) & 1), p.err);
           }
           tc_fence_after();
           const uint64_t qd = q_desc + (uint64_t)((t * C::kQBytes) >> 4);
@@ -935,29 +965,38 @@ __global__ void __launch_bounds__(WCfg<D, KV8, SC>::kThreads, 1)
         const int l0 = it.base + j * kBN;
         // some row does not see some key of the tile
         const bool masked = l0 + kBN - 1 > lim_min || (l0 < wlo_max && l0 + kBN > p.num_sinks);
-        // the row of S, and its max
-        uint32_t v[4][32];
+        constexpr int kHeld = SC ? 1 : 4;
+        uint32_t v[kHeld][32];
+        auto load = [&](int first) {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) tmem_ld32(s_col + i * 32, v[i]);
-        tmem_wait_ld();
-        if (masked) {
+          for (int i = 0; i < kHeld; ++i) tmem_ld32(s_col + (first + i) * 32, v[i]);
+          tmem_wait_ld();
+          if (masked) {
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const int c0 = l0 + 32 * i;
-            const uint32_t see = bits_to(lim - c0) & (~bits_to(wlo - 1 - c0) | bits_to(p.num_sinks - 1 - c0));
+            for (int i = 0; i < kHeld; ++i) {
+              const int c0 = l0 + 32 * (first + i);
+              const uint32_t see = bits_to(lim - c0) & (~bits_to(wlo - 1 - c0) | bits_to(p.num_sinks - 1 - c0));
 #pragma unroll
-            for (int e = 0; e < 32; ++e) v[i][e] = ((see >> e) & 1u) ? v[i][e] : 0xFF800000u;
+              for (int e = 0; e < 32; ++e) v[i][e] = ((see >> e) & 1u) ? v[i][e] : 0xFF800000u;
+            }
           }
-        }
-        float mx[4];
+        };
+        float tmax = -INFINITY;
+#pragma unroll 1
+        for (int first = 0; first < 4; first += kHeld) {
+          load(first);
+          float mx[kHeld];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          mx[i] = __uint_as_float(v[i][0]);
+          for (int i = 0; i < kHeld; ++i) {
+            float& x = mx[i];
+            x = __uint_as_float(v[i][0]);
 #pragma unroll
-          for (int e = 1; e < 31; e += 2) mx[i] = max3(mx[i], __uint_as_float(v[i][e]), __uint_as_float(v[i][e + 1]));
-          mx[i] = fmaxf(mx[i], __uint_as_float(v[i][31]));
+            for (int e = 1; e < 31; e += 2) x = max3(x, __uint_as_float(v[i][e]), __uint_as_float(v[i][e + 1]));
+            x = fmaxf(x, __uint_as_float(v[i][31]));
+          }
+#pragma unroll
+          for (int i = 0; i < kHeld; ++i) tmax = fmaxf(tmax, mx[i]);
         }
-        float tmax = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
         tmax = SC ? fmaf(tmax, f, lv) : tmax * sl2;
         // reference max: moved only when the row max grows by more than 2^8
         float alpha = 1.f;
@@ -974,6 +1013,24 @@ __global__ void __launch_bounds__(WCfg<D, KV8, SC>::kThreads, 1)
         // 0.0017), by 0.0017 with its own rounding alone
         const uint64_t mul = pair(f, f), sub = pair(lv - mbase, lv - mbase);
         uint64_t rs[4] = {0ull, 0ull, 0ull, 0ull};
+        if constexpr (SC) {
+#pragma unroll 1
+          for (int first = 0; first < 4; first += kHeld) {
+            load(first);
+#pragma unroll
+            for (int cb = 0; cb < kHeld; ++cb) {
+              uint32_t w[16];
+#pragma unroll
+              for (int e = 0; e < 32; e += 2) {
+                const float2 x = unpair(fma_pair(pair(__uint_as_float(v[cb][e]), __uint_as_float(v[cb][e + 1])), mul, sub));
+                const float p0 = fast_exp2(x.x), p1 = fast_exp2(x.y);
+                rs[(e >> 1) & 3] = add_pair(rs[(e >> 1) & 3], pair(p0, p1));
+                w[e >> 1] = pack_f16(p0, p1);
+              }
+              tmem_st16(s_col + (first + cb) * 16, w);
+            }
+          }
+        } else {
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
           uint32_t w[32];
@@ -982,12 +1039,13 @@ __global__ void __launch_bounds__(WCfg<D, KV8, SC>::kThreads, 1)
 #pragma unroll
             for (int e = 0; e < 32; e += 2) {
               const float2 x = unpair(fma_pair(
-                  pair(__uint_as_float(v[2 * h + cb][e]), __uint_as_float(v[2 * h + cb][e + 1])), mul, sub));
+                  pair(__uint_as_float(v[(2 * h + cb) % kHeld][e]), __uint_as_float(v[(2 * h + cb) % kHeld][e + 1])), mul, sub));
               const float p0 = fast_exp2(x.x), p1 = fast_exp2(x.y);
               rs[(e >> 1) & 3] = add_pair(rs[(e >> 1) & 3], pair(p0, p1));
               w[cb * 16 + (e >> 1)] = KV8 ? pack_f16(p0, p1) : pack_bf16(p0, p1);
             }
           tmem_st32(s_col + h * 32, w);
+        }
         }
         const float2 sum = unpair(add_pair(add_pair(rs[0], rs[1]), add_pair(rs[2], rs[3])));
         l = SC ? fmaf(sum.x + sum.y, iv, l) : l + (sum.x + sum.y);
@@ -1047,18 +1105,21 @@ __global__ void __launch_bounds__(WCfg<D, KV8, SC>::kThreads, 1)
       long long dst[4];
 #pragma unroll
       for (int k = 0; k < 4; ++k) dst[k] = __shfl_sync(0xffffffffu, off, (lane & ~3) + k);
-      uint32_t oall[D / 32][32];
+      constexpr int kOut = SC ? 1 : D / 32;  // 32 columns each, held at once
+#pragma unroll 1
+      for (int first = 0; first < D / 32; first += kOut) {
+      uint32_t oall[kOut][32];
 #pragma unroll
-      for (int cb = 0; cb < D / 32; ++cb)
+      for (int cb = 0; cb < kOut; ++cb)
         if (ntt > 0) {
-          tmem_ld32(o_col + cb * 32, oall[cb]);
+          tmem_ld32(o_col + (first + cb) * 32, oall[cb]);
         } else {
 #pragma unroll
           for (int e = 0; e < 32; ++e) oall[cb][e] = 0u;
         }
       if (ntt > 0) tmem_wait_ld();
 #pragma unroll
-      for (int cb = 0; cb < D / 32; ++cb) {
+      for (int cb = 0; cb < kOut; ++cb) {
         const uint32_t (&o)[32] = oall[cb];
         uint32_t w[4][4];  // unit u: columns 8u .. 8u + 7
 #pragma unroll
@@ -1082,8 +1143,9 @@ __global__ void __launch_bounds__(WCfg<D, KV8, SC>::kThreads, 1)
 #pragma unroll
         for (int k = 0; k < 4; ++k)  // row k of the quad, this lane's unit of it
           if (dst[k] >= 0)
-            *reinterpret_cast<uint4*>(outp + dst[k] + cb * 32 + (lane & 3) * 8) =
+            *reinterpret_cast<uint4*>(outp + dst[k] + (first + cb) * 32 + (lane & 3) * 8) =
                 make_uint4(w[k][0], w[k][1], w[k][2], w[k][3]);
+      }
       }
       tc_fence_before();  // O is read before this thread's next P lets PV write it again
     }
