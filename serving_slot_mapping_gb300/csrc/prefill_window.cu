@@ -185,6 +185,11 @@ struct Walker {
     it->b = base + i;
     it->hk = (int)(w - gt * Hkv);
     w += gridDim.x / csize;
+    fill(p, kpo, csize, tile, it);
+    return true;
+  }
+  // The rest of item `it` = (b, hk, row tile).
+  static __device__ void fill(const PrefillParams& p, int kpo, int csize, int tile, Item* it) {
     const int ps = p.pool.page_size;
     it->n = seq_rows(p, it->b, &it->qs);
     it->L = ld_seq_len(p.seq_lens, it->b, p.max_blocks * ps, nullptr);
@@ -211,7 +216,80 @@ struct Walker {
       it->nt1 = min(max(it->nt1 - j0, 0), per);
       it->base = j0 * kBN;
     }
-    return true;
+  }
+};
+
+// The same items with the ones of most keys first, dealt out to the CTAs forwards and
+// backwards in turn (ranks c, 2N - 1 - c, 2N + c, ...), so that the sums of keys come
+// out even: without a window an item has from one key tile to all of its sequence's.
+// Items are ranked by level = key tiles up to their last row's own key, then by sequence;
+// count(b, level), the row tiles of sequence b at a level or above, is a closed form, so
+// a rank is found by stepping the level down, a lane a sequence.  No window.
+struct SortedWalker {
+  int level, round;
+  int64_t above, upto;  // row tiles of levels > level, >= level
+
+  // Row tiles of sequence b with at least `level` key tiles (none past the batch).
+  __device__ int count(const PrefillParams& p, int b, int level_) const {
+    if (b >= p.batch) return 0;
+    int qs;
+    const int n = seq_rows(p, b, &qs);
+    const int T = row_tiles((int64_t)min(n, p.max_q_len) * p.group);
+    if (level_ <= 0 || T == 0) return T;
+    const int L = ld_seq_len(p.seq_lens, b, p.max_blocks * p.pool.page_size, nullptr);
+    const int64_t key = (int64_t)(level_ - 1) * kBN;  // a row at this position or behind it
+    if (L - 1 < key) return 0;
+    const int64_t x = key - (L - n);
+    return T - (int)min(x <= 0 ? (int64_t)0 : x * p.group / (kQT * kBM), (int64_t)T - 1);
+  }
+  __device__ int64_t total(const PrefillParams& p, int level_) const {
+    int sum = 0;  // at most 2^31 tokens of 32 heads make 2^28 row tiles
+#pragma unroll 4
+    for (int b = threadIdx.x & 31; b < p.batch; b += 32) sum += count(p, b, level_);
+    return __reduce_add_sync(0xffffffffu, sum);
+  }
+  __device__ void start(const PrefillParams& p, int) {
+    int top = 0;
+#pragma unroll 4
+    for (int b = threadIdx.x & 31; b < p.batch; b += 32)
+      top = max(top, ld_seq_len(p.seq_lens, b, p.max_blocks * p.pool.page_size, nullptr) / kBN + 1);
+    level = __reduce_max_sync(0xffffffffu, top);
+    round = 0;
+    above = 0;
+    upto = total(p, level);
+  }
+  __device__ bool next(const PrefillParams& p, int kpo, int csize, Item* it) {
+    const int N = gridDim.x / csize, c = blockIdx.x / csize, Hkv = p.pool.num_kv_heads;
+    const int64_t rank = (int64_t)round * N + ((round & 1) ? N - 1 - c : c);
+    ++round;
+    const int64_t g = rank / Hkv;
+    while (upto <= g) {
+      if (level == 0) return false;
+      above = upto;
+      upto = total(p, --level);
+    }
+    int rel = (int)(g - above);  // among the row tiles of this level
+    it->hk = (int)(rank - g * Hkv);
+    for (int base = 0;; base += 32) {
+      const int b = base + (threadIdx.x & 31), more = count(p, b, level + 1), mine = count(p, b, level) - more;
+      int incl = mine;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int t = __shfl_up_sync(0xffffffffu, incl, o);
+        if ((threadIdx.x & 31) >= o) incl += t;
+      }
+      const int all = __shfl_sync(0xffffffffu, incl, 31);
+      if (rel < all) {
+        const int i = __popc(__ballot_sync(0xffffffffu, incl <= rel));
+        it->b = base + i;
+        const int before = __shfl_sync(0xffffffffu, incl - mine, i);
+        // the tiles of sequence b at this level: [T - count(level), T - count(level + 1))
+        const int first = __shfl_sync(0xffffffffu, count(p, b, 0) - more - mine, i);
+        Walker::fill(p, kpo, csize, first + rel - before, it);
+        return true;
+      }
+      rel -= all;
+    }
   }
 };
 
@@ -264,7 +342,7 @@ __device__ __forceinline__ void redo_bad_items(const PrefillParams& p, int kpo, 
     }
     return __bfloat162float(static_cast<const __nv_bfloat16*>(pool)[at]);
   };
-  Walker wk;
+  std::conditional_t<SC, SortedWalker, Walker> wk;  // this CTA's items
   wk.start(p, csize);
   Item x;
   while (wk.next(p, kpo, csize, &x)) {
@@ -416,7 +494,7 @@ __global__ void __launch_bounds__(WCfg<D, KV8, SC>::kThreads, 1)
     return alive && x->n >= 0;
   };
   // Derive the next item and hand it out as entry i (whole warp); false at the end.
-  auto publish_next = [&](Walker& wk, int i, Item* item = nullptr) {
+  auto publish_next = [&](auto& wk, int i, Item* item = nullptr) {
     Item x = {};
     const bool got = (!SPLIT || i == 0) && wk.next(p, kpo, csize, &x);
     if (!got) x.n = -1;
@@ -598,7 +676,7 @@ __global__ void __launch_bounds__(WCfg<D, KV8, SC>::kThreads, 1)
   if constexpr (SC) {
     if (warp == kCvtWarp) {
       // ======================= items and scales, int8 pools =======================
-      Walker wk;
+      SortedWalker wk;
       wk.start(p, csize);
       const int per = 1 << p.scale_shift;                   // tokens of a scale: 16 or more
       const int lanes = per < kBN ? kBN / per : 1;          // scales of a tile
@@ -965,15 +1043,19 @@ __global__ void __launch_bounds__(WCfg<D, KV8, SC>::kThreads, 1)
         const int l0 = it.base + j * kBN;
         // some row does not see some key of the tile
         const bool masked = l0 + kBN - 1 > lim_min || (l0 < wlo_max && l0 + kBN > p.num_sinks);
-        constexpr int kHeld = SC ? 1 : 4;
-        uint32_t v[kHeld][32];
-        auto load = [&](int first) {
+        // The row of S, and its max.  Held whole where the code allows; int8 (SC) reads it
+        // again for P, 32 columns at a time in loops: with the converters' and the scales'
+        // code beside it, the unrolled form had warps wait for instructions (4.2 per issue)
+        // and took 1258 us where the loops take 740 (19 chunks of 512 after 4096 tokens,
+        // 32 / 8 heads of 128).
+        constexpr int kHeld = SC ? 1 : 4, kExpHeld = 1;
+        auto load = [&](auto& v, int first, int n) {
 #pragma unroll
-          for (int i = 0; i < kHeld; ++i) tmem_ld32(s_col + (first + i) * 32, v[i]);
+          for (int i = 0; i < n; ++i) tmem_ld32(s_col + (first + i) * 32, v[i]);
           tmem_wait_ld();
           if (masked) {
 #pragma unroll
-            for (int i = 0; i < kHeld; ++i) {
+            for (int i = 0; i < n; ++i) {
               const int c0 = l0 + 32 * (first + i);
               const uint32_t see = bits_to(lim - c0) & (~bits_to(wlo - 1 - c0) | bits_to(p.num_sinks - 1 - c0));
 #pragma unroll
@@ -982,9 +1064,10 @@ __global__ void __launch_bounds__(WCfg<D, KV8, SC>::kThreads, 1)
           }
         };
         float tmax = -INFINITY;
+        uint32_t v[kHeld][32];
 #pragma unroll 1
         for (int first = 0; first < 4; first += kHeld) {
-          load(first);
+          load(v, first, kHeld);
           float mx[kHeld];
 #pragma unroll
           for (int i = 0; i < kHeld; ++i) {
@@ -1013,39 +1096,35 @@ __global__ void __launch_bounds__(WCfg<D, KV8, SC>::kThreads, 1)
         // 0.0017), by 0.0017 with its own rounding alone
         const uint64_t mul = pair(f, f), sub = pair(lv - mbase, lv - mbase);
         uint64_t rs[4] = {0ull, 0ull, 0ull, 0ull};
+        auto exp32 = [&](const uint32_t (&x32)[32], uint32_t* w) {  // 32 columns -> 16 words of P
+#pragma unroll
+          for (int e = 0; e < 32; e += 2) {
+            const float2 x = unpair(fma_pair(pair(__uint_as_float(x32[e]), __uint_as_float(x32[e + 1])), mul, sub));
+            const float p0 = fast_exp2(x.x), p1 = fast_exp2(x.y);
+            rs[(e >> 1) & 3] = add_pair(rs[(e >> 1) & 3], pair(p0, p1));
+            w[e >> 1] = KV8 ? pack_f16(p0, p1) : pack_bf16(p0, p1);
+          }
+        };
         if constexpr (SC) {
 #pragma unroll 1
-          for (int first = 0; first < 4; first += kHeld) {
-            load(first);
+          for (int first = 0; first < 4; first += kExpHeld) {
+            uint32_t x[kExpHeld][32];
+            load(x, first, kExpHeld);
 #pragma unroll
-            for (int cb = 0; cb < kHeld; ++cb) {
+            for (int cb = 0; cb < kExpHeld; ++cb) {
               uint32_t w[16];
-#pragma unroll
-              for (int e = 0; e < 32; e += 2) {
-                const float2 x = unpair(fma_pair(pair(__uint_as_float(v[cb][e]), __uint_as_float(v[cb][e + 1])), mul, sub));
-                const float p0 = fast_exp2(x.x), p1 = fast_exp2(x.y);
-                rs[(e >> 1) & 3] = add_pair(rs[(e >> 1) & 3], pair(p0, p1));
-                w[e >> 1] = pack_f16(p0, p1);
-              }
+              exp32(x[cb], w);
               tmem_st16(s_col + (first + cb) * 16, w);
             }
           }
         } else {
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          uint32_t w[32];
+          for (int h = 0; h < 2; ++h) {
+            uint32_t w[32];
 #pragma unroll
-          for (int cb = 0; cb < 2; ++cb)
-#pragma unroll
-            for (int e = 0; e < 32; e += 2) {
-              const float2 x = unpair(fma_pair(
-                  pair(__uint_as_float(v[(2 * h + cb) % kHeld][e]), __uint_as_float(v[(2 * h + cb) % kHeld][e + 1])), mul, sub));
-              const float p0 = fast_exp2(x.x), p1 = fast_exp2(x.y);
-              rs[(e >> 1) & 3] = add_pair(rs[(e >> 1) & 3], pair(p0, p1));
-              w[cb * 16 + (e >> 1)] = KV8 ? pack_f16(p0, p1) : pack_bf16(p0, p1);
-            }
-          tmem_st32(s_col + h * 32, w);
-        }
+            for (int cb = 0; cb < 2; ++cb) exp32(v[(2 * h + cb) % kHeld], w + 16 * cb);
+            tmem_st32(s_col + h * 32, w);
+          }
         }
         const float2 sum = unpair(add_pair(add_pair(rs[0], rs[1]), add_pair(rs[2], rs[3])));
         l = SC ? fmaf(sum.x + sum.y, iv, l) : l + (sum.x + sum.y);

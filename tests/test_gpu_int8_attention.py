@@ -135,7 +135,8 @@ def test_prefill_rows_without_a_key_are_zeros(cuda_device):
     assert (out[:8] == 0).all()
 
 
-@pytest.mark.parametrize("new,cached,bad", [([40], [100], [(0, 1)]), ([300], [700], [(0, 0), (0, 20)])])
+@pytest.mark.parametrize("new,cached,bad", [([40], [100], [(0, 1)]), ([300], [700], [(0, 0), (0, 20)]),
+                                            ([300, 2000, 40, 900], [500, 0, 60, 400], [(0, 3)])])
 def test_prefill_keys_of_bad_pages_take_no_part(cuda_device, new, cached, bad):
     """Compared with a sequence that never had those pages' keys, row by row (rows that
     lie before the page see none of it)."""
@@ -146,7 +147,7 @@ def test_prefill_keys_of_bad_pages_take_no_part(cuda_device, new, cached, bad):
     gone = {m for _, m in bad}
     keep = [m for m in range(-(-int(c.lens[0]) // c.ps)) if m not in gone]
     c.seen[0, :len(keep)] = c.seen[0, keep]
-    c.lens = c.lens - c.ps * len(gone)
+    c.lens[0] -= c.ps * len(gone)
     c.bad = []
     c.compare(out)
 
@@ -197,3 +198,9 @@ def test_replays_on_other_inputs_and_two_calls_at_once(cuda_device):
 def test_prefill_long_items(cuda_device, new, cached):
     """Items of many key tiles, alone on a CTA, shared by a cluster, and several in turn."""
     Case(new, cached, hq=16, hkv=4, d=64, ps=32, blk=32, seed=7).check(capi, cuda_device)
+
+
+def test_prefill_many_sequences(cuda_device):
+    """More sequences than a warp ranks at once, most of them short, some empty."""
+    rng = np.random.default_rng(5)
+    Case(rng.integers(0, 40, size=300), rng.integers(0, 300, size=300), hq=8, hkv=2, d=64, seed=3).check(capi, cuda_device)
