@@ -299,13 +299,15 @@ __device__ __noinline__ void merge_segment(const DecodeParams& p, int b, int hkb
 
 // Compile-time shape of one configuration: HB heads per box, RT row tiles,
 // WC the weighted cut and publisher warp for 16-row groups.
-template <int D, int HB, int RT, bool KV8 = false, bool WC = false>
+template <int D, int HB, int RT, bool KV8 = false, bool WC = false, bool SC = false>
 struct Cfg {
   static constexpr int kConsumers = 8;
   // 16-key blocks a consumer warp takes per stage: two for 32-row groups, so
   // each of those warps (latency-bound, one per row tile) carries twice the
   // keys through one softmax step and has independent MMA chains to overlap
-  static constexpr int BPW = RT;
+  // (int8: for 16-row groups too; making f16 of its codes takes twice the instructions of
+  // e4m3, and one chain a warp left the warps waiting for themselves)
+  static constexpr int BPW = SC ? 2 : RT;
   static constexpr int NBS = kConsumers * BPW / (HB * RT);  // blocks per stage
   static constexpr int NW = NBS / BPW;                      // consumer warps per (head, row tile)
   static constexpr int kKvProducers = 2;                  // KV producer warps, alternating stages
@@ -347,13 +349,13 @@ struct Layout {
   int stages, qslot, bar_off, mrg_off, prefix_off, scale_off, total;
 };
 
-// Scales of a stage: [K, V][block of the stage][head of the box] fp32, 8 a tensor; then
-// a word with a bit for each block whose page is out of range.
-constexpr int kStageScales = 80;
+// Scales of a stage: [K, V][block of the stage][head of the box] fp32, 16 a tensor at
+// most; then a word with a bit for each block whose page is out of range.
+constexpr int kStageScales = 144;
 
 template <int D, int HB, int RT, bool KV8 = false, bool WC = false, bool SC = false>
 __host__ __device__ inline Layout make_layout(int G, int B, int budget) {
-  using C = Cfg<D, HB, RT, KV8, WC>;
+  using C = Cfg<D, HB, RT, KV8, WC, SC>;
   Layout L;
   L.qslot = ((HB * G * D * 2) + 127) / 128 * 128;
   const int merge = C::NW > 1 ? HB * G * (D + 2) * 4 : 0;  // one slot: the chained merge below
@@ -372,13 +374,14 @@ __host__ __device__ inline Layout make_layout(int G, int B, int budget) {
 }
 
 template <int D, int HB, int RT, bool KV8, bool FUSED, bool WC = false, int EXT = 0>
-__global__ void __launch_bounds__(Cfg<D, HB, RT, KV8, WC>::kThreads, 1)
+__global__ void __launch_bounds__(Cfg<D, HB, RT, KV8, WC, (EXT & kExtScales) != 0>::kThreads, 1)
     decode_split_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_constant__ CUtensorMap tmap_v,
                         DecodeParams p) {
-  using C = Cfg<D, HB, RT, KV8, WC>;
-  constexpr int NBS = C::NBS, BPW = C::BPW, NW = C::NW;
   constexpr bool SC = (EXT & kExtScales) != 0, MASS = (EXT & kExtMass) != 0;
-  static_assert(!SC || (KV8 && !FUSED && NBS * HB == 8), "int8 codes come as e4m3 ones do, 8 scales a stage and tensor");
+  using C = Cfg<D, HB, RT, KV8, WC, SC>;
+  constexpr int NBS = C::NBS, BPW = C::BPW, NW = C::NW;
+  static_assert(!SC || (KV8 && !FUSED && NBS * HB <= 16 && 2 * NBS <= 32),
+                "int8 codes come as e4m3 ones do, 16 scales a stage and tensor at most, a lane a block and tensor");
   extern __shared__ unsigned char smem_raw[];
   unsigned char* smem = reinterpret_cast<unsigned char*>(
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
@@ -693,7 +696,7 @@ __global__ void __launch_bounds__(Cfg<D, HB, RT, KV8, WC>::kThreads, 1)
     const int slabs_per_op = R == 16 ? C::kSlabs : 1;
     const int boxes_per_block = (16 / R) * (C::kSlabs / slabs_per_op);
     constexpr int kOpsPerLane = 2;  // at most 2 tensors x 8 blocks x 4 boxes = 64 ops a stage
-    static_assert(2 * NBS * 2 * (D / 64) <= 32 * kOpsPerLane, "ops per stage");
+    static_assert(SC || 2 * NBS * 2 * (D / 64) <= 32 * kOpsPerLane, "ops per stage");
     // op -> (block jj, first row q*R of the box) and its shared-memory offset in
     // the stage; tensor TT = K or V, slab sl
     struct OpGeom {
@@ -786,7 +789,7 @@ __global__ void __launch_bounds__(Cfg<D, HB, RT, KV8, WC>::kThreads, 1)
         // of 16 slots or more: one box a block), so it brings that block's scales
         const OpGeom g = nbs == NBS ? full_geom[0] : geom(nbs, lane);
         if (g.on && (cur.k + g.jj) * 16 < cur.L) {
-          const uint32_t sdst = smem_u32(smem + lay.scale_off) + slot * kStageScales + g.TT * 32 + g.jj * HB * 4;
+          const uint32_t sdst = smem_u32(smem + lay.scale_off) + slot * kStageScales + g.TT * 64 + g.jj * HB * 4;
           if (row[0] >= 0)
             cp_async_floats<HB>(sdst, (g.TT ? p.value_scales : p.key_scales) +
                                           (int64_t)(row[0] >> p.scale_shift) * Hkv + cur.hk * HB);
@@ -794,7 +797,7 @@ __global__ void __launch_bounds__(Cfg<D, HB, RT, KV8, WC>::kThreads, 1)
         const unsigned bad =
             __ballot_sync(0xffffffffu, g.on && g.TT == 0 && (cur.k + g.jj) * 16 < cur.L && row[0] < 0);
         if (lane == 0)  // lanes 0 .. nbs - 1 have the blocks of K
-          *reinterpret_cast<volatile uint32_t*>(smem + lay.scale_off + slot * kStageScales + 64) = bad;
+          *reinterpret_cast<volatile uint32_t*>(smem + lay.scale_off + slot * kStageScales + 128) = bad;
         cp_async_arrive(full_bar(slot));
       }
       if (lane == 0) mbar_arrive_expect_tx(full_bar(slot), (uint32_t)(issued * R * C::kRowBytes * HB * slabs_per_op));
@@ -914,8 +917,8 @@ __global__ void __launch_bounds__(Cfg<D, HB, RT, KV8, WC>::kThreads, 1)
           if (jb >= nbs) continue;
           if constexpr (SC) {
             const float* sc = reinterpret_cast<const float*>(smem + lay.scale_off + slot * kStageScales);
-            const float ks = sc[jb * HB + h], vs = sc[8 + jb * HB + h];
-            if ((reinterpret_cast<const uint32_t*>(sc)[16] >> jb) & 1u) valid[bb] = 0;  // a page out of range
+            const float ks = sc[jb * HB + h], vs = sc[16 + jb * HB + h];
+            if ((reinterpret_cast<const uint32_t*>(sc)[32] >> jb) & 1u) valid[bb] = 0;  // a page out of range
             kf[bb] = sl2 * clamp_scale(ks);
             lv[bb] = __log2f(clamp_scale(vs));
             iv[bb] = fast_exp2(-lv[bb]);  // of the very power that p' carries
@@ -981,32 +984,31 @@ __global__ void __launch_bounds__(Cfg<D, HB, RT, KV8, WC>::kThreads, 1)
             }
           }
         }
-        float score[MASS ? 2 * BPW : 1][4];
 #pragma unroll
-        for (int t = 0; t < 2 * BPW; ++t)
+        for (int t = 0; t < 2 * BPW; ++t) {
+          if constexpr (MASS) {
+            // the scores themselves, for key_mass_kernel (whole 16-key blocks: rows of the
+            // scratch are padded to them)
+            if (jw * BPW + (t >> 1) < nbs) {
+              float x[4];
+#pragma unroll
+              for (int e = 0; e < 4; ++e) {
+                const int key = (t & 1) * 8 + (lane & 3) * 2 + (e & 1);
+                x[e] = key < valid[t >> 1] ? s[t][e] * (SC ? kf[t >> 1] : sl2) : -INFINITY;
+              }
+              const int64_t key = (int64_t)(first_k + done + jw * BPW + (t >> 1)) * 16 + (t & 1) * 8 + (lane & 3) * 2;
+              float* to = p.scores + ((int64_t)cc.b * Hq + (int64_t)hk * G) * p.score_stride + key;
+              if (rA < G) *reinterpret_cast<float2*>(to + rA * p.score_stride) = make_float2(x[0], x[1]);
+              if (rB < G) *reinterpret_cast<float2*>(to + rB * p.score_stride) = make_float2(x[2], x[3]);
+            }
+          }
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
             const int key = (t & 1) * 8 + (lane & 3) * 2 + (e & 1);
-            if constexpr (MASS) {
-              // the score itself, kept for key_mass_kernel
-              const float x = key < valid[t >> 1] ? s[t][e] * (SC ? kf[t >> 1] : sl2) : -INFINITY;
-              score[t][e] = x;
-              if constexpr (!SC) s[t][e] = x;
-            }
             if constexpr (SC)
               s[t][e] = key < valid[t >> 1] ? fmaf(s[t][e], kf[t >> 1], lv[t >> 1]) : -INFINITY;
-            else if constexpr (!MASS)
+            else
               s[t][e] = key < valid[t >> 1] ? s[t][e] * sl2 : -INFINITY;
-          }
-        if constexpr (MASS) {
-          // whole 16-key blocks (rows of the scratch are padded to them)
-#pragma unroll
-          for (int t = 0; t < 2 * BPW; ++t) {
-            if (jw * BPW + (t >> 1) >= nbs) continue;
-            const int64_t key = (int64_t)(first_k + done + jw * BPW + (t >> 1)) * 16 + (t & 1) * 8 + (lane & 3) * 2;
-            float* x = p.scores + ((int64_t)cc.b * Hq + (int64_t)hk * G) * p.score_stride + key;
-            if (rA < G) *reinterpret_cast<float2*>(x + rA * p.score_stride) = make_float2(score[t][0], score[t][1]);
-            if (rB < G) *reinterpret_cast<float2*>(x + rB * p.score_stride) = make_float2(score[t][2], score[t][3]);
           }
         }
         float mx0 = -INFINITY, mx1 = -INFINITY;
@@ -1342,7 +1344,7 @@ namespace {
 
 template <int D, int HB, int RT, bool KV8, bool FUSED, bool WC = false, int EXT = 0>
 cudaError_t launch_split(const DecodeParams& p, const CUtensorMap& tk, const CUtensorMap& tv, cudaStream_t s) {
-  using C = Cfg<D, HB, RT, KV8, WC>;
+  using C = Cfg<D, HB, RT, KV8, WC, (EXT & kExtScales) != 0>;
   const Layout lay = make_layout<D, HB, RT, KV8, WC, (EXT & kExtScales) != 0>(p.group, p.batch, p.smem_budget);
   if (lay.stages < 2) return cudaErrorInvalidConfiguration;
   auto kern = decode_split_kernel<D, HB, RT, KV8, FUSED, WC, EXT>;
