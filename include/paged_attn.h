@@ -623,7 +623,7 @@ pa_status paged_attention_prefill_int8(const pa_kv_pool* pool, const pa_kv_scale
  *
  * Summed over the layers or steps that share a block table, it says which keys
  * the queries still look at (paged_kv_evict_rows, paged_kv_evict_pages).  The sum
- * is fp32, heads in ascending order, the same on every run.  The pages have no
+ * is fp32, in an order of its own that is the same on every run.  The pages have no
  * counterpart of this call.
  *
  * pool, scales  bf16, e4m3 (scales NULL) or int8 pools, with the limits of their

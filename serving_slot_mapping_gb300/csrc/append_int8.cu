@@ -8,7 +8,7 @@
 //      = max(clamp(s), n)     else; where s' > s the block's other rows, whose codes
 //                             stand for c s, become rint(c (s / s'))
 //   c  = rint(x / s'), at most 127 in magnitude (NaN: 0)
-// all in fp32, one division and one rounding (to nearest even) a row element.
+// all in fp32, a division's quotient and one rounding (to nearest even) a row element.
 //
 // A run is the consecutive tokens whose slots lie in one block, padding tokens between
 // them aside (31 at most in a row); a warp takes a run for one head and tensor: up to 16
@@ -27,15 +27,41 @@ namespace {
 
 constexpr int kAppendWarps = 4;
 
-// bf16 pair -> two codes' bytes (low 16 bits).
-__device__ __forceinline__ uint32_t codes2(uint32_t w, float s) {
-  const int a = min(max(__float2int_rn(__fdiv_rn(__uint_as_float(w << 16), s)), -127), 127);
-  const int b = min(max(__float2int_rn(__fdiv_rn(__uint_as_float(w & 0xFFFF0000u), s)), -127), 127);
-  return (uint32_t)(a & 0xFF) | ((uint32_t)(b & 0xFF) << 8);
+// The rounded quotient of x by the block's scale, in the low byte: RN(x / s) by the
+// reciprocal y = RN(1 / s) and one correction of the product with its remainder
+// (Markstein's division), then rounding to an integer by adding 1.5 2^23, whose low bits
+// the integer is in.  The same as the division's code for every 24-bit scale and every
+// bf16 value up to 127.5 scales (compared on the GPU, all of them).  Not for NaN.
+__device__ __forceinline__ uint32_t code_of(float x, float s, float y) {
+  const float q = __fmul_rn(x, y);
+  return __float_as_uint(__fadd_rn(__fmaf_rn(__fmaf_rn(-s, q, x), y, q), 12582912.f));
+}
+// The same for any x, by the division: infinities saturate, NaN becomes 0.
+__device__ __forceinline__ uint32_t code_of_any(float x, float s) {
+  return (uint32_t)min(max(__float2int_rn(__fdiv_rn(x, s)), -127), 127);
 }
 
-__device__ __forceinline__ uint2 codes8(uint4 v, float s) {
-  return make_uint2(codes2(v.x, s) | (codes2(v.y, s) << 16), codes2(v.z, s) | (codes2(v.w, s) << 16));
+// Eight bf16 elements -> eight codes.  `plain`: they are finite.
+__device__ __forceinline__ uint2 codes8(uint4 v, float s, float y, bool plain) {
+  const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+  uint32_t c[8];
+  if (plain) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      c[2 * i] = code_of(__uint_as_float(w[i] << 16), s, y);
+      c[2 * i + 1] = code_of(__uint_as_float(w[i] & 0xFFFF0000u), s, y);
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      c[2 * i] = code_of_any(__uint_as_float(w[i] << 16), s);
+      c[2 * i + 1] = code_of_any(__uint_as_float(w[i] & 0xFFFF0000u), s);
+    }
+  }
+  auto four = [&](int i) {
+    return __byte_perm(__byte_perm(c[i], c[i + 1], 0x0040), __byte_perm(c[i + 2], c[i + 3], 0x0040), 0x5410);
+  };
+  return make_uint2(four(0), four(4));
 }
 
 // Four codes times r, rounded.
@@ -49,7 +75,17 @@ __device__ __forceinline__ uint32_t rescale4(uint32_t w, float r) {
   return o;
 }
 
-__device__ __forceinline__ float max_abs8(float a, uint4 v) {
+// The larger magnitudes, element by element (first in the low half); NaN wins in `any`
+// and loses in `number`.
+__device__ __forceinline__ void max_abs8(__nv_bfloat162* any, uint4 v) {
+  const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const uint32_t m = w[i] & 0x7FFF7FFFu;
+    *any = __hmax2_nan(*any, *reinterpret_cast<const __nv_bfloat162*>(&m));
+  }
+}
+__device__ __forceinline__ float max_number8(float a, uint4 v) {
   const uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
   for (int i = 0; i < 4; ++i)
@@ -138,20 +174,33 @@ __global__ void __launch_bounds__(kAppendWarps * 32) append_int8_kernel(const __
       return block_of(s) == b ? s : -1;
     };
     int at[kPasses];
-    float a = 0.f;
 #pragma unroll
     for (int x = 0; x < kPasses; ++x) {
       const int r = x * kRows + sub, s = __shfl_sync(kAll, slot, (l + r) & 31);
       at[x] = l + r < 32 ? (r < n && block_of(s) == b ? s : -1) : mine_of(r);
     }
+    __nv_bfloat162 any = __float2bfloat162_rn(0.f);
 #pragma unroll
     for (int x = 0; x < kPasses; ++x)
-      if (at[x] >= 0) a = max_abs8(a, v[x]);
+      if (at[x] >= 0) max_abs8(&any, v[x]);
     for (int64_t r = 16 + sub; r < n; r += kRows)
-      if (mine_of(r) >= 0) a = max_abs8(a, row(r));
+      if (mine_of(r) >= 0) max_abs8(&any, row(r));
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) a = fmaxf(a, __shfl_xor_sync(kAll, a, o));
+    for (int o = 16; o > 0; o >>= 1) any = __hmax2_nan(any, __shfl_xor_sync(kAll, any, o));
+    float a = __bfloat162float(__hmax_nan(any.x, any.y));
+    const bool plain = a <= 3.3e38f;  // neither infinities nor NaN
+    if (a != a) {                     // the largest of the numbers
+      a = 0.f;
+#pragma unroll 1
+      for (int64_t r = sub; r < n; r += kRows)
+        if (mine_of(r) >= 0) a = max_number8(a, row(r));
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) a = fmaxf(a, __shfl_xor_sync(kAll, a, o));
+    }
     const float s = fmaxf(old, clamp_scale(__fdiv_rn(a, 127.f)));
+    // a finite value past 127.5 scales needs saturating too: above the largest scale
+    const bool fast = plain && a <= 127.5f * kScaleMax;
+    const float y = __frcp_rn(s);
     if (!fresh && s > old) {
       const float ratio = __fdiv_rn(old, s);
       const int rows = 1 << p.scale_shift;
@@ -165,10 +214,10 @@ __global__ void __launch_bounds__(kAppendWarps * 32) append_int8_kernel(const __
     if (lane == 0) *scale = s;
 #pragma unroll
     for (int x = 0; x < kPasses; ++x)
-      if (at[x] >= 0) *reinterpret_cast<uint2*>(pool + (int64_t)at[x] * pitch) = codes8(v[x], s);
+      if (at[x] >= 0) *reinterpret_cast<uint2*>(pool + (int64_t)at[x] * pitch) = codes8(v[x], s, y, fast);
     for (int64_t r = 16 + sub; r < n; r += kRows) {
       const int to = mine_of(r);
-      if (to >= 0) *reinterpret_cast<uint2*>(pool + (int64_t)to * pitch) = codes8(row(r), s);
+      if (to >= 0) *reinterpret_cast<uint2*>(pool + (int64_t)to * pitch) = codes8(row(r), s, y, fast);
     }
   }
 }

@@ -4,8 +4,10 @@
 // A weight needs its row's whole sum, which is known when the decode ends: the
 // decode kernel (decode_split.cuh, kExtMass) leaves the scaled scores x [B, Hq, keys]
 // and each row's lse = log2 sum_j 2^x, and key_mass_kernel computes
-//   mass_out[b, j] = decay mass_in[b, j] + sum_h 2^(x[b, h, j] - lse[b, h]),
-// heads in ascending order, so the sums are the same on every run.
+//   mass_out[b, j] = decay mass_in[b, j] + sum_h 2^(x[b, h, j] - lse[b, h]).
+// A block takes 128 keys of a sequence, four a lane; its warps share the heads, each
+// with all its loads in flight (up to 32 heads in one round trip), and their sums are
+// added in the order of the warps: the same on every run.
 //
 // 4 Hq bytes a key read (mostly from L2, where the decode has just put them) beside
 // 4 to 8 of mass.
@@ -17,45 +19,62 @@ namespace pa {
 
 namespace {
 
-constexpr int kMassThreads = 128;
-constexpr int kMaxMassHeads = 1024;  // lse staged this many heads at a time
+constexpr int kMassWarps = 8;
+constexpr int kMassKeys = 128;   // of a block
+constexpr int kMassAhead = 4;    // heads of a warp in flight
 
-__global__ void __launch_bounds__(kMassThreads) key_mass_kernel(const __grid_constant__ KeyMassParams p) {
-  __shared__ float lse[kMaxMassHeads];
+__global__ void __launch_bounds__(kMassWarps * 32) key_mass_kernel(const __grid_constant__ KeyMassParams p) {
+  __shared__ float4 part[kMassWarps][32];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   griddep_wait();
   const int b = blockIdx.y, L = ld_seq_len(p.seq_lens, b, p.max_len, nullptr);
-  const int j = (blockIdx.x * kMassThreads + threadIdx.x) * 2;
-  if (blockIdx.x * kMassThreads * 2 >= L) return;
-  float a0 = 0.f, a1 = 0.f;
-  for (int h0 = 0; h0 < p.num_q_heads; h0 += kMaxMassHeads) {
-    const int heads = min(kMaxMassHeads, p.num_q_heads - h0);
-    if (h0 > 0) __syncthreads();
-    for (int h = threadIdx.x; h < heads; h += kMassThreads)
-      lse[h] = __uint_as_float(ld_input(reinterpret_cast<const uint32_t*>(p.lse) + (int64_t)b * p.num_q_heads + h0 + h));
-    __syncthreads();
-    if (j < L) {
-      const float* x = p.scores + ((int64_t)b * p.num_q_heads + h0) * p.score_stride + j;
-#pragma unroll 8
-      for (int h = 0; h < heads; ++h) {
-        const uint2 v = ld_input(reinterpret_cast<const uint2*>(x + h * p.score_stride));
-        a0 += fast_exp2(__uint_as_float(v.x) - lse[h]);
-        a1 += fast_exp2(__uint_as_float(v.y) - lse[h]);
+  const int j0 = blockIdx.x * kMassKeys, j = j0 + 4 * lane;
+  if (j0 >= L) return;
+  const int Hq = p.num_q_heads;
+  float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
+  if (j < L) {  // (rows of the scores are padded to 16 keys)
+    const float* x = p.scores + (int64_t)b * Hq * p.score_stride + j;
+    const uint32_t* lse = reinterpret_cast<const uint32_t*>(p.lse) + (int64_t)b * Hq;
+    for (int h0 = warp; h0 < Hq; h0 += kMassWarps * kMassAhead) {
+      uint4 v[kMassAhead];
+      float m[kMassAhead];
+#pragma unroll
+      for (int k = 0; k < kMassAhead; ++k) {
+        const int h = h0 + k * kMassWarps;
+        if (h < Hq) {
+          v[k] = ld_input(reinterpret_cast<const uint4*>(x + h * p.score_stride));
+          m[k] = __uint_as_float(ld_input(lse + h));
+        }
+      }
+#pragma unroll
+      for (int k = 0; k < kMassAhead; ++k) {
+        if (h0 + k * kMassWarps >= Hq) break;
+        a.x += fast_exp2(__uint_as_float(v[k].x) - m[k]);
+        a.y += fast_exp2(__uint_as_float(v[k].y) - m[k]);
+        a.z += fast_exp2(__uint_as_float(v[k].z) - m[k]);
+        a.w += fast_exp2(__uint_as_float(v[k].w) - m[k]);
       }
     }
   }
-  float* out = p.mass_out + b * p.mass_stride;
-  const uint32_t* in = reinterpret_cast<const uint32_t*>(p.mass_in) + b * p.mass_stride;
-  if (j < L) out[j] = p.mass_in != nullptr ? fmaf(p.decay, __uint_as_float(ld_input(in + j)), a0) : a0;
-  if (j + 1 < L) out[j + 1] = p.mass_in != nullptr ? fmaf(p.decay, __uint_as_float(ld_input(in + j + 1)), a1) : a1;
+  part[warp][lane] = a;
+  __syncthreads();
+  const int key = j0 + threadIdx.x;
+  if (threadIdx.x >= kMassKeys || key >= L) return;
+  float sum = 0.f;
+#pragma unroll
+  for (int w = 0; w < kMassWarps; ++w) sum += reinterpret_cast<const float*>(part[w])[threadIdx.x];
+  const int64_t at = b * p.mass_stride + key;
+  p.mass_out[at] =
+      p.mass_in != nullptr ? fmaf(p.decay, __uint_as_float(ld_input(reinterpret_cast<const uint32_t*>(p.mass_in) + at)), sum)
+                           : sum;
 }
 
 }  // namespace
 
 cudaError_t launch_key_mass(const KeyMassParams& p, cudaStream_t s) {
   if (p.max_keys <= 0) return cudaSuccess;
-  const int per = kMassThreads * 2;
-  return launch_pdl(key_mass_kernel, dim3((unsigned)((p.max_keys + per - 1) / per), (unsigned)p.batch),
-                    dim3(kMassThreads), 0, s, p);
+  return launch_pdl(key_mass_kernel, dim3((unsigned)((p.max_keys + kMassKeys - 1) / kMassKeys), (unsigned)p.batch),
+                    dim3(kMassWarps * 32), 0, s, p);
 }
 
 cudaError_t launch_decode_scores(const DecodeParams& p, cudaStream_t s) {

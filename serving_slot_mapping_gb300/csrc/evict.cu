@@ -30,6 +30,7 @@ constexpr int kEvictWarps = kEvictThreads / 32;
 constexpr int kCacheUnits = kMaxEvictPages / 8 + 32;  // keys in shared memory: 160 KB
 constexpr int kBins = 4 * kEvictThreads;              // digits of 11, 11 and 10 bits
 constexpr int kAhead = 4;                             // vectors of a thread in flight
+constexpr int kRowsAhead = 8;                         // masses of a lane in flight as they move
 
 // A float as an integer of the same order; NaN lowest, -0 as 0.
 __device__ __forceinline__ uint32_t order_key(float x) {
@@ -345,12 +346,12 @@ __global__ void __launch_bounds__(kEvictThreads) evict_kernel(const __grid_const
       if (r != 0xFFFFFFFFu) new_mass[(int64_t)r * ps + (row & (ps - 1))] = ld_float(mass + row);
     }
   } else {
-    for (int u0 = wlo; u0 < whi; u0 += 32 * kAhead) {
-      float v[kAhead];
+    for (int u0 = wlo; u0 < whi; u0 += 32 * kRowsAhead) {
+      float v[kRowsAhead];
 #pragma unroll
-      for (int k = 0; k < kAhead; ++k) v[k] = u0 + 32 * k + lane < whi ? ld_float(mass + u0 + 32 * k + lane) : 0.f;
+      for (int k = 0; k < kRowsAhead; ++k) v[k] = u0 + 32 * k + lane < whi ? ld_float(mass + u0 + 32 * k + lane) : 0.f;
 #pragma unroll
-      for (int k = 0; k < kAhead; ++k) {
+      for (int k = 0; k < kRowsAhead; ++k) {
         uint32_t before;
         const uint32_t r = rank_of(u0 + 32 * k + lane, order_key(v[k]), &before);
         if (r != 0xFFFFFFFFu) {
