@@ -16,7 +16,8 @@ def key_weights(key_pool, q, block_table, seq_lens, scale):
     out = []
     for b, L in enumerate(np.asarray(seq_lens).tolist()):
         total = np.zeros(L)
-        K = np.array([key_pool[block_table[b, j // ps], j % ps] for j in range(L)], dtype=np.float64).reshape(L, hkv, d)
+        j = np.arange(L)
+        K = np.asarray(key_pool[np.asarray(block_table)[b, j // ps], j % ps], dtype=np.float64)
         for h in range(hq):
             if L == 0:
                 continue

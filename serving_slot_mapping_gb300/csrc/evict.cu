@@ -47,7 +47,7 @@ __device__ __forceinline__ float4 ld_float4(const float* p) {
 }
 
 struct EvictShared {
-  uint32_t hist[kBins];
+  uint32_t hist[3][kBins];     // of each digit: one barrier of the cluster a digit
   uint32_t warp_sum[kEvictWarps];
   uint32_t above, ties;        // this CTA's units above the threshold (or kept anyway), and at it
   uint32_t digit, left;        // the threshold's digit, units still to be taken at it
@@ -109,6 +109,8 @@ __global__ void __launch_bounds__(kEvictThreads) evict_kernel(const __grid_const
   const bool select = over && want > 0u;
   // ---- the keys of this stretch ----
   if (select) {
+#pragma unroll
+    for (int d = 0; d < 3; ++d) reinterpret_cast<uint4*>(sh.hist[d])[tid] = make_uint4(0u, 0u, 0u, 0u);
     if constexpr (PAGES) {
       if (p.vec && ps >= 4 && ps <= 128) {
         const int pages = 128 / ps, lanes = ps / 4;  // of a warp's vectors
@@ -169,7 +171,22 @@ __global__ void __launch_bounds__(kEvictThreads) evict_kernel(const __grid_const
       for (int i = 4 * vecs + tid; i < cached; i += kEvictThreads) cache[i] = order_key(ld_float(mass + lo + i));
     }
   }
+  // f(key) for the units of [a, e), four a thread and step, in any order
+  auto each = [&](int a, int e, auto f) {
+    const int vecs = (cached + 3) / 4;
+#pragma unroll 4
+    for (int i = tid; i < vecs; i += kEvictThreads) {
+      const uint4 k = cache4[i];
+      const int u = lo + 4 * i;
+      if (u >= a && u < e) f(k.x);
+      if (u + 1 >= a && u + 1 < e) f(k.y);
+      if (u + 2 >= a && u + 2 < e) f(k.z);
+      if (u + 3 >= a && u + 3 < e) f(k.w);
+    }
+    for (int u = max(a, lo + cached) + tid; u < e; u += kEvictThreads) f(order_key(ld_float(mass + u)));
+  };
   auto key = [&](int u) { return PAGES || u - lo < kCacheUnits ? cache[u - lo] : order_key(ld_float(mass + u)); };
+  __syncthreads();
   // ---- the threshold: the want-th largest key of [front, back) ----
   uint32_t prefix = 0u, left = want;  // digits so far; units still to be found below them
   if (select) {
@@ -177,21 +194,19 @@ __global__ void __launch_bounds__(kEvictThreads) evict_kernel(const __grid_const
     for (int pass = 0; pass < 3; ++pass) {
       const int shift = pass == 0 ? 21 : (pass == 1 ? 10 : 0);
       const uint32_t digits = pass == 2 ? 1023u : 2047u;
-      reinterpret_cast<uint4*>(sh.hist)[tid] = make_uint4(0u, 0u, 0u, 0u);
-      __syncthreads();
-      for (int u = a + tid; u < e; u += kEvictThreads) {
-        const uint32_t k = key(u);
-        if (pass == 0 || (k >> (pass == 1 ? 21 : 10)) == (prefix >> (pass == 1 ? 21 : 10)))
-          atomicAdd(&sh.hist[(k >> shift) & digits], 1u);
-      }
+      uint32_t* hist = sh.hist[pass];
+      const int top = pass == 0 ? 31 : (pass == 1 ? 21 : 10);  // where the digits found so far end
+      each(a, e, [&](uint32_t k) {
+        if (pass == 0 || (k >> top) == (prefix >> top)) atomicAdd(&hist[(k >> shift) & digits], 1u);
+      });
       if (csize > 1) cluster_sync(); else __syncthreads();
       // thread i: digits 4 (511 - i) .. + 3 of all CTAs, the highest digits first
       const int g = kEvictThreads - 1 - tid;
-      uint4 n = reinterpret_cast<const uint4*>(sh.hist)[g];
+      uint4 n = reinterpret_cast<const uint4*>(hist)[g];
       if (csize > 1) {
         n = make_uint4(0u, 0u, 0u, 0u);
         for (int c = 0; c < csize; ++c) {
-          const float4 x = ld_cluster4(map_rank(smem_u32(&sh.hist[4 * g]), c));
+          const float4 x = ld_cluster4(map_rank(smem_u32(hist + 4 * g), c));
           n.x += __float_as_uint(x.x);
           n.y += __float_as_uint(x.y);
           n.z += __float_as_uint(x.z);
@@ -220,7 +235,7 @@ __global__ void __launch_bounds__(kEvictThreads) evict_kernel(const __grid_const
         sh.digit = (uint32_t)d;
         sh.left = left - before;
       }
-      if (csize > 1) cluster_sync(); else __syncthreads();  // every histogram is read
+      __syncthreads();
       prefix |= sh.digit << shift;
       left = sh.left;
     }
@@ -236,6 +251,7 @@ __global__ void __launch_bounds__(kEvictThreads) evict_kernel(const __grid_const
   };
   __syncthreads();
   uint32_t n_above = 0u, n_ties = 0u;
+#pragma unroll 4
   for (int u0 = wlo; u0 < whi; u0 += 32) {
     bool ab, ti;
     classify(u0 + lane, select && u0 + lane < whi ? key(u0 + lane) : 0u, &ab, &ti);

@@ -124,8 +124,8 @@ class Case:
             G = q.shape[1] // K.shape[2]
             e = np.zeros(q.shape[:2])
             for b in range(len(self.lens)):   # largest of sum_d |q_d K_d| over the sequence's keys
-                slots = [(self.seen[b, j // self.ps], j % self.ps) for j in range(int(self.lens[b]))]
-                k = np.abs(np.array([K[p, o] for p, o in slots])) if slots else np.zeros((1,) + K.shape[2:])
+                j = np.arange(int(self.lens[b]))
+                k = np.abs(K[self.seen[b, j // self.ps], j % self.ps]) if len(j) else np.zeros((1,) + K.shape[2:])
                 for h in range(q.shape[1]):
                     rows = np.abs(q[self.qsl[b]:self.qsl[b + 1], h])
                     e[self.qsl[b]:self.qsl[b + 1], h] = (rows @ k[:, h // G].T).max(axis=1, initial=0.0)
