@@ -71,7 +71,8 @@ def evict_pages(mass, seq_lens, page_size, budget, num_sinks, num_recent):
         front, back = -(-num_sinks // page_size), max(0, L - max(1, num_recent)) // page_size
         stay = sorted(list(range(front)) + _heaviest(weights, front, back, budget - front - (n - back))
                       + list(range(back, n)))
-        out.append((stay, [i for i in range(n) if i not in set(stay)]))
+        gone = set(range(n)) - set(stay)
+        out.append((stay, sorted(gone)))
     return out
 
 
