@@ -631,7 +631,7 @@ pa_status paged_attention_prefill_int8(const pa_kv_pool* pool, const pa_kv_scale
  *               the tensor-core kernels do not take.
  * mass_in       device f32 [batch, mass_stride] rows, mass_out itself, or NULL: 0.
  *               Rows that overlap mass_out otherwise are refused (PA_ERR_SHAPE).
- * decay         finite; 1 adds, 0 forgets, between them old weights fade.
+ * decay         finite; 1 adds, between 1 and 0 old weights fade, 0: mass_in is not read.
  * mass_out      device f32, rows mass_stride >= max_seq_len apart.
  * max_seq_len   a longer sequence is cut to it and recorded (code 3).
  * workspace     paged_attention_decode_mass_workspace_size(...) bytes, 16-byte

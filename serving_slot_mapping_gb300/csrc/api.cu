@@ -1092,7 +1092,7 @@ pa_status paged_attention_decode_mass(const pa_kv_pool* pool, const pa_kv_scales
   m.lse = p.lse;
   m.score_stride = p.score_stride;
   m.seq_lens = seq_lens;
-  m.mass_in = mass_in;
+  m.mass_in = decay == 0.f ? nullptr : mass_in;  // nothing of it is left, whatever it holds
   m.mass_out = mass_out;
   m.mass_stride = mass_stride;
   m.decay = decay;

@@ -293,6 +293,22 @@ struct SortedWalker {
   }
 };
 
+// int8: sorted up to 256 sequences, whose ranks a warp finds in eight steps.  8 chunks of
+// 512-2048 after 0-8192 tokens: 1898 us in plain order, 1040 sorted; 256 of 24 after 200:
+// 134 sorted; 2048 of 16 after 100: 2704 us sorted (64 steps an item).
+struct AnyWalker {
+  bool sorted;
+  SortedWalker s;
+  Walker w;
+  __device__ void start(const PrefillParams& p, int csize) {
+    sorted = p.batch <= 256;
+    if (sorted) s.start(p, csize); else w.start(p, csize);
+  }
+  __device__ bool next(const PrefillParams& p, int kpo, int csize, Item* it) {
+    return sorted ? s.next(p, kpo, csize, it) : w.next(p, kpo, csize, it);
+  }
+};
+
 // Bits 0 .. k of a word (none for k < 0).
 __device__ __forceinline__ uint32_t bits_to(int k) {
   return k < 0 ? 0u : (k >= 31 ? 0xFFFFFFFFu : 0xFFFFFFFFu >> (31 - k));
@@ -342,7 +358,7 @@ __device__ __forceinline__ void redo_bad_items(const PrefillParams& p, int kpo, 
     }
     return __bfloat162float(static_cast<const __nv_bfloat16*>(pool)[at]);
   };
-  std::conditional_t<SC, SortedWalker, Walker> wk;  // this CTA's items
+  std::conditional_t<SC, AnyWalker, Walker> wk;  // this CTA's items
   wk.start(p, csize);
   Item x;
   while (wk.next(p, kpo, csize, &x)) {
@@ -676,7 +692,7 @@ __global__ void __launch_bounds__(WCfg<D, KV8, SC>::kThreads, 1)
   if constexpr (SC) {
     if (warp == kCvtWarp) {
       // ======================= items and scales, int8 pools =======================
-      SortedWalker wk;
+      AnyWalker wk;
       wk.start(p, csize);
       const int per = 1 << p.scale_shift;                   // tokens of a scale: 16 or more
       const int lanes = per < kBN ? kBN / per : 1;          // scales of a tile

@@ -204,3 +204,55 @@ def test_prefill_many_sequences(cuda_device):
     """More sequences than a warp ranks at once, most of them short, some empty."""
     rng = np.random.default_rng(5)
     Case(rng.integers(0, 40, size=300), rng.integers(0, 300, size=300), hq=8, hkv=2, d=64, seed=3).check(capi, cuda_device)
+
+
+def test_prefill_first_block_with_tiny_values(cuda_device):
+    """Most of the weight on a block whose V is almost 0, in a tile of its own."""
+    c = Case([70], [200], hq=4, hkv=1, d=64, ps=128, blk=128, seed=9)
+    p = c.table[0, 0]
+    c.vs[p] *= 2.0 ** -20
+    c.ks[p] *= 3.0
+    c.check(capi, cuda_device)
+
+
+@pytest.mark.parametrize("value", [0.0, float("nan"), 2.0 ** -60, 2.0 ** 60])
+def test_prefill_scales_are_clamped(cuda_device, value):
+    c = Case([30], [60], hq=4, hkv=2, seed=2)
+    c.vs[c.table[0, 1]] = value
+    if not value > 1:
+        c.ks[c.table[0, 3]] = value
+    c.check(capi, cuda_device)
+
+
+def test_prefill_replayed_on_other_inputs(cuda_device):
+    """Captured once, replayed on other lengths, chunks, tables, codes and scales: the bits
+    of an eager call (sequences shared by clusters, whose parts depend on the launch alone)."""
+    cases = [Case(n, c, hq=8, hkv=2, d=128, seed=i) for i, (n, c) in
+             enumerate([([40, 0, 100], [300, 5, 0]), ([1, 130, 9], [0, 200, 333]), ([50, 50, 40], [0, 0, 0])])]
+    pages, width = max(c.kp.shape[0] for c in cases), max(c.table.shape[1] for c in cases)
+    live = None
+    for k, c in enumerate(cases):
+        t = c.tensors("cpu")
+        grow = lambda x, v: torch.cat([x, torch.full((pages - x.shape[0],) + x.shape[1:], v, dtype=x.dtype)])
+        table = torch.full((3, width), -7, dtype=torch.int32)
+        table[:, :t[5].shape[1]] = t[5]
+        q = torch.zeros(150, 8, 128, dtype=torch.bfloat16)
+        q[:t[4].shape[0]] = t[4]
+        now = [x.to(cuda_device) for x in (grow(t[0], 1), grow(t[1], 1), grow(t[2], 1.0), grow(t[3], 1.0), q, t[7], table, t[6])]
+        want = capi.paged_attention_prefill_int8(*now, c.scale, 130, max_seq_len=340, out=torch.zeros_like(now[4]))
+        if live is None:
+            live, out = [x.clone() for x in now], torch.zeros_like(now[4])
+            torch.cuda.synchronize()
+            g = torch.cuda.CUDAGraph()
+            with torch.cuda.graph(g):
+                capi.paged_attention_prefill_int8(*live, c.scale, 130, max_seq_len=340, out=out)
+        for x, y in zip(live, now):
+            x.copy_(y)
+        out.zero_()
+        g.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(out, want)
+        n = int(c.n.sum())
+        assert (out[n:] == 0).all()          # rows behind the last sequence
+        c.compare(out[:n])
+    assert capi.device_error() == (0, 0)

@@ -85,6 +85,8 @@ def test_mass_of_steps_before(cuda_device):
     before = torch.rand(3, 400, device=cuda_device)
     for decay in (1.0, 0.5, 0.0, -1.0):
         check_mass(c, cuda_device, before=before.cpu().numpy(), decay=decay, mass_in=before[:, :301], stride=400)
+    nan = torch.full((3, 400), float("nan"), device=cuda_device)
+    check_mass(c, cuda_device, before=np.zeros((3, 400)), decay=0.0, mass_in=nan[:, :301], stride=400)
     # in place, twice
     m = torch.zeros(3, 300, device=cuda_device)
     kp, vp, ks, vs, q, bt, L, _ = c.tensors(cuda_device)
@@ -199,6 +201,8 @@ def test_evict_pages(cuda_device, ps, odd):
     lens = [0, 1, ps, ps + 1, 5 * ps, 5 * ps + 1, 9 * ps - 1 if ps > 1 else 9, 9 * ps + 3 if ps > 3 else 9]
     check_pages(cuda_device, masses(8, width, ps, odd=odd), lens, ps, 5, 1, 2, extra=3)
     check_pages(cuda_device, masses(8, width, ps + 1), lens, ps, 2, 0, 0)
+    # rows that start on 16 bytes: vectors
+    check_pages(cuda_device, masses(8, 9 * ps + 8 - ps % 4, ps + 2, odd=odd), lens, ps, 4, 1, 1, extra=1)
 
 
 @pytest.mark.parametrize("B,pages,ps", [(1, 30000, 4), (2, 9000, 16), (40, 300, 16), (1, 100000, 1)])
@@ -246,4 +250,14 @@ def test_evict_replayed_on_other_inputs(cuda_device):
             assert torch.equal(got[:n], want[:n])
         for got, want in zip(pages, capi.paged_kv_evict_pages(m, bt, L, 16, 7, 4, 20)):
             assert torch.equal(got, want)
+    assert capi.device_error() == (0, 0)
+
+
+def test_evict_of_nothing(cuda_device):
+    """No column, or nothing over the budget."""
+    L = torch.zeros(2, dtype=torch.int32, device=cuda_device)
+    ptr, keep, base, new = capi.paged_kv_evict_rows(torch.empty(2, 0, device=cuda_device), L, 5, 1, 1)
+    assert ptr.tolist() == [0, 0, 0] and base.tolist() == [0, 0] and new.shape == (2, 0) and keep.numel() == 0
+    check_rows(cuda_device, masses(2, 8, 1), [8, 3], 8, 0, 0)
+    check_pages(cuda_device, masses(2, 8, 1), [8, 3], 4, 2, 0, 0)
     assert capi.device_error() == (0, 0)
