@@ -1009,6 +1009,20 @@ pa_status ext_decode_params(const pa_kv_pool* pool, const pa_kv_scales* scales, 
   return PA_OK;
 }
 
+// A decode over an int8 pool (with p.scores: and its scores): short parts on clusters,
+// long or uneven ones by the cut that they share.
+cudaError_t launch_int8_decode(pa::DecodeParams& p, int32_t max_seq_len, cudaStream_t s) {
+  const int csize = (int64_t)p.batch * p.pool.num_kv_heads > INT32_MAX / 8  // grid x, 8 CTAs each at most
+                        ? 0
+                        : pa::decode_int8_cluster(num_sms(), p.batch, p.pool.num_kv_heads, p.group, max_seq_len);
+  if (csize > 0) {
+    p.window = INT32_MAX;
+    p.num_sinks = 0;
+    return pa::launch_decode_window(p, num_sms(), csize, s);
+  }
+  return p.scores != nullptr ? pa::launch_decode_scores(p, s) : pa::launch_decode_int8(p, s);
+}
+
 // Bytes of the scores and sums behind a decode's own workspace.
 int64_t score_stride(int32_t max_seq_len) { return align_up((size_t)max_seq_len, 16); }
 size_t lse_bytes(int32_t batch, int32_t num_q_heads) { return align_up((size_t)batch * num_q_heads * 4, 256); }
@@ -1028,7 +1042,7 @@ pa_status paged_attention_decode_int8(const pa_kv_pool* pool, const pa_kv_scales
   st = ext_decode_params(pool, scales, q, out, batch, num_q_heads, dense_table(block_table, max_blocks_per_seq, seq_lens),
                          max_seq_len, scale, workspace, workspace_bytes, &p);
   if (st != PA_OK) return st;
-  return launched(pa::launch_decode_int8(p, static_cast<cudaStream_t>(stream)));
+  return launched(launch_int8_decode(p, max_seq_len, static_cast<cudaStream_t>(stream)));
 }
 
 pa_status paged_attention_prefill_int8(const pa_kv_pool* pool, const pa_kv_scales* scales, const void* q, void* out,
@@ -1085,7 +1099,7 @@ pa_status paged_attention_decode_mass(const pa_kv_pool* pool, const pa_kv_scales
   p.score_stride = score_stride(max_seq_len);
   p.max_keys = max_seq_len;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  st = launched(pa::launch_decode_scores(p, s));
+  st = launched(codes8 ? launch_int8_decode(p, max_seq_len, s) : pa::launch_decode_scores(p, s));
   if (st != PA_OK) return st;
   pa::KeyMassParams m{};
   m.scores = p.scores;

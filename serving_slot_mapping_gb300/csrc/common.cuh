@@ -215,6 +215,9 @@ __device__ __forceinline__ float fast_exp2(float x) {
   return y;
 }
 
+// log2 of a row's sum of 2^x, from its (m, l); +inf without a key (its weights are 0).
+__device__ __forceinline__ float row_lse(float m, float l) { return l > 0.f ? m + log2f(l) : __int_as_float(0x7F800000); }
+
 // Swizzled byte offset of 16-byte chunk `chunk` of row `row` in a tile whose
 // rows are `row_bytes` long (row_bytes a multiple of 128): the chunk index is
 // XOR-ed with (row % 8) so that 8 rows read at one logical chunk hit 8

@@ -88,8 +88,6 @@ namespace pa {
 
 namespace {
 
-constexpr int kExtScales = 1, kExtMass = 2;  // bits of EXT
-
 // keys of sequence b (either page-table form), with / without recording bad input
 __device__ __forceinline__ int nblk_of(const DecodeParams& p, int b, int max_len) {
   return (seq_keys(p.seq_lens, p.kv_indptr, p.kv_last_page_len, p.kv_len, b, p.pool.page_size, max_len, p.err) + 15) >> 4;
@@ -152,9 +150,6 @@ __device__ __forceinline__ unsigned long long ld_acquire_gpu(const unsigned long
   asm volatile("ld.acquire.gpu.global.u64 %0, [%1];\n" : "=l"(v) : "l"(ptr) : "memory");
   return v;
 }
-
-// log2 of a row's sum of 2^x, from its (m, l); +inf without a key (its weights are 0).
-__device__ __forceinline__ float row_lse(float m, float l) { return l > 0.f ? m + log2f(l) : INFINITY; }
 
 // One warp merges query row (head h of the box, row g) of segment `seg`, cut
 // into parts by CTAs c0 .. c0 + nparts - 1 (a CTA that owns no unit, only

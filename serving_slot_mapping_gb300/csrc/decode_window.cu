@@ -1,5 +1,8 @@
 // paged_attention_decode_window: decode over a sliding window and the first
-// tokens of each sequence, split over the CTAs of a thread-block cluster.
+// tokens of each sequence, split over the CTAs of a thread-block cluster.  Also
+// paged_attention_decode_int8 and paged_attention_decode_mass over int8 pools where the
+// parts are short (decode_int8_cluster), with a window that hides nothing (EXT: its
+// scales and scores are those of decode_split.cuh).
 //
 //   out[b, h] = softmax_j(scale * q[b,h] . K_b[j, h/G]) V_b[j, h/G],
 //   j < L_b with j >= L_b - window or j < num_sinks
@@ -81,7 +84,7 @@ bool deep_rings(int num_sms, int64_t ctas) { return ctas <= 4 * (int64_t)num_sms
 
 // RT: warps per team, each with NT tiles of 8 query heads of the group; DEEP: see
 // deep_rings.
-template <int D, bool KV8, int RT, int NT, bool DEEP>
+template <int D, bool KV8, int RT, int NT, bool DEEP, bool SC = false>
 struct DCfg {
   static constexpr int kConsumers = kTeams * RT;           // warps
   static constexpr int kThreads = 32 * (kConsumers + 1);   // + the producer warp
@@ -102,7 +105,8 @@ struct DCfg {
   static constexpr int kPartMl = kTeams * kHeads * kRow * 4;
   static constexpr int kParts = kPartMl + (kTeams + 1) * kHeads * 8;
   static constexpr int kBarOff = kRing > kParts ? kRing : (kParts + 127) / 128 * 128;
-  static constexpr int kSmem = kBarOff + 2 * kTeams * kStages * 8 + 1024;
+  static constexpr int kScaleOff = kBarOff + 2 * kTeams * kStages * 8;  // SC: [team][stage] {K's scale, V's}
+  static constexpr int kSmem = kScaleOff + (SC ? kTeams * kStages * 8 : 0) + 1024;
   static_assert(kTeams * kStages <= 32 * (kTeams + 1), "one thread sets up each stage's barriers");
 };
 
@@ -118,13 +122,14 @@ __device__ __forceinline__ uint32_t transpose8(uint32_t x) {
 // a key at a time: team 0's partial rows and (m, l), the other teams' empty.  An
 // error path, slow, which works out its blocks anew so that the loop before it holds
 // no register for it.
-template <int D, bool KV8, int HEADS, int ROW>
+template <int D, bool KV8, int HEADS, int ROW, int EXT>
 __device__ __forceinline__ void skip_bad_pages(const DecodeParams& p, int csize, float* part, float2* part_ml) {
   constexpr int E = D / 32;  // a lane's dims
   const int lane = threadIdx.x & 31, ps = p.pool.page_size, G = p.group;
   const int seg = blockIdx.x / csize, rank = blockIdx.x - seg * csize;
   const int b = seg / p.pool.num_kv_heads, hk = seg - b * p.pool.num_kv_heads;
-  const int L = ld_seq_len(p.seq_lens, b, p.max_blocks * ps, nullptr);
+  constexpr bool SC = (EXT & kExtScales) != 0, MASS = (EXT & kExtMass) != 0;
+  const int L = ld_seq_len(p.seq_lens, b, MASS ? min(p.max_blocks * ps, p.max_keys) : p.max_blocks * ps, nullptr);
   const WinSpan win = win_span(p, L);
   const int nblk = ((L + 15) >> 4) - win.gap, per = (nblk + csize - 1) / csize;
   const int k0 = rank * per, k1 = min(nblk, k0 + per);
@@ -133,6 +138,7 @@ __device__ __forceinline__ void skip_bad_pages(const DecodeParams& p, int csize,
   for (int i = threadIdx.x; i < kTeams * HEADS; i += blockDim.x) part_ml[i] = make_float2(-INFINITY, 0.f);
   __syncthreads();
   auto element = [&](const void* pool, int64_t at) {
+    if (SC) return (float)static_cast<const signed char*>(pool)[at];
     if (KV8) {
       const uint32_t f = e4m3x2_lo_to_f16x2(static_cast<const unsigned char*>(pool)[at]);
       return __half2float(__ushort_as_half((unsigned short)(f & 0xFFFFu)));
@@ -150,18 +156,28 @@ __device__ __forceinline__ void skip_bad_pages(const DecodeParams& p, int csize,
       const int j = win_block(win, i >> 4) * 16 + (i & 15);
       if (j >= L || (j >= p.num_sinks && j < win.start)) continue;
       const int page = ld_input(bt + (j >> p.pool.page_shift));
-      if (page < 0 || page >= p.pool.num_pages) continue;
-      const int64_t at = (((int64_t)page * ps + (j & (ps - 1))) * p.pool.num_kv_heads + hk) * D + lane * E;
-      float s = 0.f;
+      if (page < 0 || page >= p.pool.num_pages) {
+        if (MASS && lane == 0)
+          p.scores[((int64_t)b * p.num_q_heads + (int64_t)hk * G + head) * p.score_stride + j] = -INFINITY;
+        continue;
+      }
+      const int64_t slot = (int64_t)page * ps + (j & (ps - 1));
+      const int64_t at = (slot * p.pool.num_kv_heads + hk) * D + lane * E;
+      float s = 0.f, ks = 1.f, vs = 1.f;
+      if (SC) {
+        const int64_t c = (slot >> p.scale_shift) * p.pool.num_kv_heads + hk;
+        ks = clamp_scale(__uint_as_float(ld_input(reinterpret_cast<const uint32_t*>(p.key_scales) + c)));
+        vs = clamp_scale(__uint_as_float(ld_input(reinterpret_cast<const uint32_t*>(p.value_scales) + c)));
+      }
 #pragma unroll
-      for (int e = 0; e < E; ++e) s = fmaf(qv[e], element(p.pool.key_pool, at + e), s);
+      for (int e = 0; e < E; ++e) s = fmaf(qv[e], element(p.pool.key_pool, at + e) * ks, s);
 #pragma unroll
       for (int x = 16; x > 0; x >>= 1) s += __shfl_xor_sync(0xffffffffu, s, x);
       const float mn = fmaxf(m, s), a = fast_exp2(m - mn), w = fast_exp2(s - mn);
       m = mn;
       l = fmaf(l, a, w);
 #pragma unroll
-      for (int e = 0; e < E; ++e) o[e] = fmaf(o[e], a, w * element(p.pool.value_pool, at + e));
+      for (int e = 0; e < E; ++e) o[e] = fmaf(o[e], a, w * (element(p.pool.value_pool, at + e) * vs));
     }
 #pragma unroll
     for (int e = 0; e < E; ++e) part[head * ROW + lane * E + e] = o[e];
@@ -169,11 +185,13 @@ __device__ __forceinline__ void skip_bad_pages(const DecodeParams& p, int csize,
   }
 }
 
-template <int D, bool KV8, int RT, int NT, bool DEEP>
+template <int D, bool KV8, int RT, int NT, bool DEEP, int EXT = 0>
 __global__ void __launch_bounds__(DCfg<D, KV8, RT, NT, DEEP>::kThreads, DCfg<D, KV8, RT, NT, DEEP>::kPerSm)
     decode_window_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_constant__ CUtensorMap tmap_v,
                           const __grid_constant__ DecodeParams p, int csize) {
-  using C = DCfg<D, KV8, RT, NT, DEEP>;
+  constexpr bool SC = (EXT & kExtScales) != 0, MASS = (EXT & kExtMass) != 0;
+  using C = DCfg<D, KV8, RT, NT, DEEP, SC>;
+  static_assert(!SC || KV8, "int8 codes land as e4m3 ones do");
   constexpr int S = C::kStages;
   extern __shared__ unsigned char smem_raw[];
   unsigned char* smem = reinterpret_cast<unsigned char*>(
@@ -189,7 +207,7 @@ __global__ void __launch_bounds__(DCfg<D, KV8, RT, NT, DEEP>::kThreads, DCfg<D, 
   __shared__ volatile int bad_page;  // one out of range was met
   if (tid == 0) bad_page = 0;
   if (tid < kTeams * S) {
-    mbar_init(bars + 8u * tid, 2);  // full: the lanes that issue K and V
+    mbar_init(bars + 8u * tid, SC ? 4 : 2);  // full: the lanes that issue K and V (and their scales)
     mbar_init(bars + 8u * (kTeams * S + tid), RT);  // empty: the team's warps
     fence_mbar_init();
   }
@@ -199,7 +217,8 @@ __global__ void __launch_bounds__(DCfg<D, KV8, RT, NT, DEEP>::kThreads, DCfg<D, 
   // a call among decodes alone and nothing behind an append (32 sequences, append and
   // decode 26.3 us either way).
   griddep_wait();
-  const int L = ld_seq_len(p.seq_lens, b, p.max_blocks * ps, tid == 0 && rank == 0 && hk == 0 ? p.err : nullptr);
+  const int L = ld_seq_len(p.seq_lens, b, MASS ? min(p.max_blocks * ps, p.max_keys) : p.max_blocks * ps,
+                           tid == 0 && rank == 0 && hk == 0 ? p.err : nullptr);
   const WinSpan win = win_span(p, L);
   const int nblk = ((L + 15) >> 4) - win.gap;  // the sequence's blocks with a visible key
   const int per = (nblk + csize - 1) / csize;
@@ -261,6 +280,12 @@ __global__ void __launch_bounds__(DCfg<D, KV8, RT, NT, DEEP>::kThreads, DCfg<D, 
           ++boxes;
         }
         if (alive) alive = mbar_wait(empty_bar(team, slot), phase, p.err);
+        if constexpr (SC) {
+          if (rows[0] >= 0)
+            cp_async_floats<1>(smem_u32(smem + C::kScaleOff) + (uint32_t)((team * S + slot) * 8 + T * 4),
+                               (T ? p.value_scales : p.key_scales) + (int64_t)(rows[0] >> p.scale_shift) * Hkv + hk);
+          cp_async_arrive(bar);
+        }
         mbar_arrive_expect_tx(bar, (uint32_t)(boxes * C::kSlabs * R * C::kRowBytes));
         const uint32_t dst = ring + (uint32_t)(slot * C::kBlockBytes);
 #pragma unroll
@@ -351,6 +376,15 @@ __global__ void __launch_bounds__(DCfg<D, KV8, RT, NT, DEEP>::kThreads, DCfg<D, 
     const int valid = L - key0;  // >= 1
     const int hid0 = max(0, p.num_sinks - key0), hid1 = min(16, win.start - key0);  // rows between sinks and window
     const bool edge = valid < 16 || hid0 < hid1;
+    // int8: S's factor, log2 of V's scale (in the exponent: y = x + log2 v, see
+    // decode_split.cuh) and the inverse of the very power that the weights carry
+    float bmul = mul, lv = 0.f, iv = 1.f;
+    if constexpr (SC) {
+      const float2 sc = *reinterpret_cast<const float2*>(smem + C::kScaleOff + (team * S + slot) * 8);
+      bmul = mul * clamp_scale(sc.x);
+      lv = __log2f(clamp_scale(sc.y));
+      iv = fast_exp2(-lv);
+    }
     if (edge) {
       // hidden rows may hold anything (NaN would survive P = 0): zero them in V
       // (by the team's first warp; the second waits); a row's chunks stay in the
@@ -382,7 +416,14 @@ __global__ void __launch_bounds__(DCfg<D, KV8, RT, NT, DEEP>::kThreads, DCfg<D, 
       float s0[4] = {0.f, 0.f, 0.f, 0.f}, s1[4] = {0.f, 0.f, 0.f, 0.f};  // two halves of the dims, for latency
 #pragma unroll
       for (int x = 0; x < kFrags; ++x) {
-        if (KV8) {
+        if (SC) {
+          const uint32_t a[4] = {i8x2_to_f16x2<0, 1>(f[x][0]), i8x2_to_f16x2<0, 1>(f[x][1]), i8x2_to_f16x2<2, 3>(f[x][0]),
+                                 i8x2_to_f16x2<2, 3>(f[x][1])};
+          const uint32_t a2[4] = {i8x2_to_f16x2<0, 1>(f[x][2]), i8x2_to_f16x2<0, 1>(f[x][3]), i8x2_to_f16x2<2, 3>(f[x][2]),
+                                  i8x2_to_f16x2<2, 3>(f[x][3])};
+          mma_f16_16816(s0, a, qf[n][2 * x][0], qf[n][2 * x][1]);
+          mma_f16_16816(s1, a2, qf[n][2 * x + 1][0], qf[n][2 * x + 1][1]);
+        } else if (KV8) {
           const uint32_t a[4] = {e4m3x2_lo_to_f16x2(f[x][0]), e4m3x2_lo_to_f16x2(f[x][1]), e4m3x2_hi_to_f16x2(f[x][0]),
                                  e4m3x2_hi_to_f16x2(f[x][1])};
           const uint32_t a2[4] = {e4m3x2_lo_to_f16x2(f[x][2]), e4m3x2_lo_to_f16x2(f[x][3]),
@@ -406,6 +447,25 @@ __global__ void __launch_bounds__(DCfg<D, KV8, RT, NT, DEEP>::kThreads, DCfg<D, 
         }
       }
     }
+    if constexpr (MASS) {
+      // the scores, for key_mass_kernel: eight keys of a head a sector
+#pragma unroll
+      for (int n = 0; n < NT; ++n)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          const int head = (rt * NT + n) * 8 + 2 * c4 + e;
+          if (head >= G) continue;
+          float* to = p.scores + ((int64_t)b * Hq + (int64_t)hk * G + head) * p.score_stride + key0 + r8;
+          to[0] = s[n][e] * bmul;
+          to[8] = s[n][2 + e] * bmul;
+        }
+    }
+    if constexpr (SC) {  // y, rounded before the max is taken off: exact there however large the scores are
+#pragma unroll
+      for (int n = 0; n < NT; ++n)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) s[n][e] = fmaf(s[n][e], bmul, lv);
+    }
     float mn[NT][2];
     bool moved = false;
 #pragma unroll
@@ -416,7 +476,7 @@ __global__ void __launch_bounds__(DCfg<D, KV8, RT, NT, DEEP>::kThreads, DCfg<D, 
         mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 4));
         mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 8));
         mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 16));
-        mn[n][e] = fmaxf(m[n][e], mx * mul);  // finite: a block has a visible key
+        mn[n][e] = fmaxf(m[n][e], SC ? mx : mx * mul);  // finite: a block has a visible key
         moved |= mn[n][e] != m[n][e];
       }
     if (__any_sync(0xffffffffu, moved)) {
@@ -444,16 +504,26 @@ __global__ void __launch_bounds__(DCfg<D, KV8, RT, NT, DEEP>::kThreads, DCfg<D, 
     for (int n = 0; n < NT; ++n) {
       float w[4];
 #pragma unroll
-      for (int e = 0; e < 4; ++e) w[e] = fast_exp2(fmaf(s[n][e], mul, -mn[n][e & 1]));
-      l[n][0] += w[0] + w[2];
-      l[n][1] += w[1] + w[3];
+      for (int e = 0; e < 4; ++e) w[e] = fast_exp2(SC ? s[n][e] - mn[n][e & 1] : fmaf(s[n][e], mul, -mn[n][e & 1]));
+      l[n][0] = SC ? fmaf(w[0] + w[2], iv, l[n][0]) : l[n][0] + (w[0] + w[2]);
+      l[n][1] = SC ? fmaf(w[1] + w[3], iv, l[n][1]) : l[n][1] + (w[1] + w[3]);
       pb[n][0] = transpose8(KV8 ? pack_f16(w[0], w[1]) : pack_bf16(w[0], w[1]));
       pb[n][1] = transpose8(KV8 ? pack_f16(w[2], w[3]) : pack_bf16(w[2], w[3]));
     }
 #pragma unroll
     for (int x = 0; x < kFrags; ++x) {
       ldmatrix_x4_trans(vbase + voff[x % kOffs] + (x / kOffs) * C::kSlabBytes, f[x][0], f[x][1], f[x][2], f[x][3]);
-      if (KV8) {
+      if (SC) {
+        const uint32_t a[4] = {i8x2_to_f16x2<0, 2>(f[x][0]), i8x2_to_f16x2<1, 3>(f[x][0]), i8x2_to_f16x2<0, 2>(f[x][1]),
+                               i8x2_to_f16x2<1, 3>(f[x][1])};
+        const uint32_t a2[4] = {i8x2_to_f16x2<0, 2>(f[x][2]), i8x2_to_f16x2<1, 3>(f[x][2]), i8x2_to_f16x2<0, 2>(f[x][3]),
+                                i8x2_to_f16x2<1, 3>(f[x][3])};
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
+          mma_f16_16816(o[n][2 * x], a, pb[n][0], pb[n][1]);
+          mma_f16_16816(o[n][2 * x + 1], a2, pb[n][0], pb[n][1]);
+        }
+      } else if (KV8) {
         // codes of keys 2c, 2c + 1 and dims 2j, 2j + 1 (j = lane / 4), regrouped by dim:
         // the even dims of the chunk are the tile's rows 0 - 7, the odd ones 8 - 15
 #pragma unroll
@@ -511,12 +581,13 @@ __global__ void __launch_bounds__(DCfg<D, KV8, RT, NT, DEEP>::kThreads, DCfg<D, 
   }
   __syncthreads();
   if (__builtin_expect(bad_page != 0, 0)) {
-    skip_bad_pages<D, KV8, C::kHeads, C::kRow>(p, csize, part, part_ml);
+    skip_bad_pages<D, KV8, C::kHeads, C::kRow, EXT>(p, csize, part, part_ml);
     __syncthreads();
   }
   const int items = G * (D / 4);  // float4s of the output
   __nv_bfloat16* out = static_cast<__nv_bfloat16*>(p.out) + ((int64_t)b * Hq + (int64_t)hk * G) * D;
-  auto store = [&](int x, float4 acc, float den) {
+  auto store = [&](int x, float4 acc, float M, float den) {
+    if (MASS && x % (D / 4) == 0) p.lse[(int64_t)b * Hq + (int64_t)hk * G + x / (D / 4)] = row_lse(M, den);
     const float inv = den > 0.f ? p.v_scale / den : 0.f;  // v_scale: 1 for bf16 pools
     uint2 packed;
     packed.x = pack_bf16(acc.x * inv, acc.y * inv);
@@ -539,7 +610,7 @@ __global__ void __launch_bounds__(DCfg<D, KV8, RT, NT, DEEP>::kThreads, DCfg<D, 
       acc.x += f * v.x; acc.y += f * v.y; acc.z += f * v.z; acc.w += f * v.w;
     }
     if (csize == 1) {
-      store(x, acc, den);
+      store(x, acc, M, den);
     } else {  // the CTA's partial over team 0's place; (M, den) after the teams' (m, l)
       *reinterpret_cast<float4*>(part + row * C::kRow + 4 * c) = acc;
       if (c == 0) part_ml[kTeams * C::kHeads + row] = make_float2(M, den);
@@ -571,32 +642,43 @@ __global__ void __launch_bounds__(DCfg<D, KV8, RT, NT, DEEP>::kThreads, DCfg<D, 
         den += f * ml[r].y;
         acc.x += f * v[r].x; acc.y += f * v[r].y; acc.z += f * v[r].z; acc.w += f * v[r].w;
       }
-      store(x, acc, den);
+      store(x, acc, M, den);
     }
     cluster_sync();  // no CTA leaves while another reads its memory
   }
 }
 
-template <int D, bool KV8, int RT, int NT, bool DEEP>
+template <int D, bool KV8, int RT, int NT, bool DEEP, int EXT>
 cudaError_t launch_window(const DecodeParams& p, const CUtensorMap& tk, const CUtensorMap& tv, int csize,
                            cudaStream_t s) {
-  using C = DCfg<D, KV8, RT, NT, DEEP>;
-  auto kern = decode_window_kernel<D, KV8, RT, NT, DEEP>;
+  using C = DCfg<D, KV8, RT, NT, DEEP, (EXT & kExtScales) != 0>;
+  auto kern = decode_window_kernel<D, KV8, RT, NT, DEEP, EXT>;
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
   if (e != cudaSuccess) return e;
   const unsigned grid = (unsigned)((int64_t)p.batch * p.pool.num_kv_heads * csize);
   return launch_pdl_cluster(kern, dim3(grid), dim3(C::kThreads), (size_t)C::kSmem, csize, s, tk, tv, p, csize);
 }
 
-template <int D, bool KV8>
+template <int D, bool KV8, int EXT = 0>
 cudaError_t launch_group(const DecodeParams& p, const CUtensorMap& tk, const CUtensorMap& tv, int num_sms, int csize,
                          cudaStream_t s) {
   if (p.group <= 8)
     return deep_rings(num_sms, (int64_t)p.batch * p.pool.num_kv_heads * csize)
-               ? launch_window<D, KV8, 1, 1, true>(p, tk, tv, csize, s)
-               : launch_window<D, KV8, 1, 1, false>(p, tk, tv, csize, s);
-  return p.group <= 16 ? launch_window<D, KV8, 1, 2, false>(p, tk, tv, csize, s)
-                       : launch_window<D, KV8, 2, 2, false>(p, tk, tv, csize, s);
+               ? launch_window<D, KV8, 1, 1, true, EXT>(p, tk, tv, csize, s)
+               : launch_window<D, KV8, 1, 1, false, EXT>(p, tk, tv, csize, s);
+  return p.group <= 16 ? launch_window<D, KV8, 1, 2, false, EXT>(p, tk, tv, csize, s)
+                       : launch_window<D, KV8, 2, 2, false, EXT>(p, tk, tv, csize, s);
+}
+
+// int8 pools, without a window; scores kept where wanted.
+cudaError_t launch_int8(const DecodeParams& p, const CUtensorMap& tk, const CUtensorMap& tv, int num_sms, int csize,
+                        cudaStream_t s) {
+  const bool d128 = p.pool.head_dim == 128;
+  if (p.scores != nullptr)
+    return d128 ? launch_group<128, true, kExtScales | kExtMass>(p, tk, tv, num_sms, csize, s)
+                : launch_group<64, true, kExtScales | kExtMass>(p, tk, tv, num_sms, csize, s);
+  return d128 ? launch_group<128, true, kExtScales>(p, tk, tv, num_sms, csize, s)
+              : launch_group<64, true, kExtScales>(p, tk, tv, num_sms, csize, s);
 }
 
 }  // namespace
@@ -617,6 +699,18 @@ int decode_window_cluster(int num_sms, int32_t batch, int32_t num_kv_heads, int3
   return c;
 }
 
+// Where a CTA gets 1024 keys at most: a cluster's start and merge cost less than those of
+// the cut that all CTAs share (8 sequences of 512-4096 keys, 8 KV heads of 128: 20.3
+// against 30.6 us; 64 of 10-1000, 3 heads of 64: 15.7 against 36.7), while of longer parts,
+// of uneven lengths, the longest sets the time (32 sequences of 512-4096: 63.5 against
+// 49.8; one of 16,384: 34.4 against 29.3).  2048 where the segments are so many that the
+// SMs even them out (2048 of 1000-2000 keys: 145.8 against 151.9; of 4096: not).
+int decode_int8_cluster(int num_sms, int32_t batch, int32_t num_kv_heads, int32_t group, int64_t max_keys) {
+  const int c = decode_window_cluster(num_sms, batch, num_kv_heads, group, max_keys);
+  const int64_t limit = (int64_t)batch * num_kv_heads >= 4 * (int64_t)num_sms ? 2048 : 1024;
+  return (max_keys + c - 1) / c <= limit ? c : 0;
+}
+
 cudaError_t launch_decode_window(const DecodeParams& p, int num_sms, int csize, cudaStream_t s) {
   const int D = p.pool.head_dim;
   const int R = p.pool.page_size < 16 ? p.pool.page_size : 16;
@@ -626,6 +720,7 @@ cudaError_t launch_decode_window(const DecodeParams& p, int num_sms, int csize, 
     if (!encode_pool_tmap_u8(&tk, p.pool.key_pool, rows, p.pool.num_kv_heads, D, R, 1, true) ||
         !encode_pool_tmap_u8(&tv, p.pool.value_pool, rows, p.pool.num_kv_heads, D, R, 1, true))
       return cudaErrorInvalidValue;
+    if (p.key_scales != nullptr) return launch_int8(p, tk, tv, num_sms, csize, s);
     return D == 128 ? launch_group<128, true>(p, tk, tv, num_sms, csize, s) : launch_group<64, true>(p, tk, tv, num_sms, csize, s);
   }
   const int slabs = R == 16 ? D / 64 : 1;

@@ -10,6 +10,10 @@ namespace pa {
 // Codes of the device error word beside those of common.cuh and tma.cuh.
 enum : unsigned long long { ERR_POSITION = 6, ERR_KEEP = 7 };
 
+// Bits of EXT, the decode kernels' template parameter for int8 codes with block scales
+// and for kept scores.
+constexpr int kExtScales = 1, kExtMass = 2;
+
 // Geometry of one layer's pool, as the kernels see it.
 struct PoolGeom {
   const void* key_pool;
@@ -272,6 +276,9 @@ cudaError_t launch_decode_cascade_bf16(const DecodeParams& p, cudaStream_t s, cu
 // max_keys visible keys.
 int decode_window_cluster(int num_sms, int32_t batch, int32_t num_kv_heads, int32_t group, int64_t max_keys);
 cudaError_t launch_decode_window(const DecodeParams& p, int num_sms, int csize, cudaStream_t s);
+// int8 pools: the cluster size with which that kernel (its window wide open) takes a
+// decode of sequences of at most max_keys keys, 0: the split kernel's.
+int decode_int8_cluster(int num_sms, int32_t batch, int32_t num_kv_heads, int32_t group, int64_t max_keys);
 // Dynamic shared memory the bf16 decode split kernel needs.
 // (size_t)-1 when no stage ring of >= 2 stages fits the budget.
 size_t decode_smem_bytes(int head_dim, int group, int batch, int heads_per_box, int budget, bool kv8, bool scales);

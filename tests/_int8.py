@@ -27,14 +27,17 @@ class Case:
     score_error = 0.0
 
     def __init__(self, new, cached, hq=8, hkv=2, d=64, ps=16, blk=16, seed=0, scale=None, spread=0.5, dtype="int8",
-                 bad=(), k_scale=0.02, v_scale=0.03):
+                 bad=(), k_scale=0.02, v_scale=0.03, room=0):
         rng = np.random.default_rng(seed)
         self.ps, self.blk, self.d, self.dtype = ps, blk, d, dtype
         self.n = np.asarray(new, dtype=np.int64)
         self.lens = np.maximum(np.asarray(cached, dtype=np.int64) + self.n, 0).astype(np.int32)
         B = len(self.lens)
         self.qsl = np.concatenate([[0], np.cumsum(self.n)]).astype(np.int32)
-        mb = max(1, int((self.lens.max(initial=0) + ps - 1) // ps)) + 1
+        # room: more columns than the sequences need, and a bound on their lengths as wide: a
+        # decode then takes the kernel for long contexts
+        mb = max(1, int((self.lens.max(initial=0) + ps - 1) // ps)) + 1 + room
+        self.max_len = mb * ps if room else max(1, int(self.lens.max(initial=0)))
         pages = [int(-(-int(L) // ps)) for L in self.lens]
         P = sum(pages) + 4
         ids = iter(rng.permutation(P))
@@ -142,7 +145,7 @@ class Case:
 
     def run(self, capi, device, **k):
         kp, vp, ks, vs, q, bt, L, qsl = self.args = self.tensors(device)
-        k.setdefault("max_seq_len", max(1, int(self.lens.max(initial=0))))
+        k.setdefault("max_seq_len", self.max_len)
         k.setdefault("out", torch.full_like(q, float("nan")))
         if self.is_decode:
             return capi.paged_attention_decode_int8(kp, vp, ks, vs, q, bt, L, self.scale, **k)

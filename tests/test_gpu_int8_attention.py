@@ -19,49 +19,58 @@ def _lib(cuda_device):
     capi.device_error()  # clear
 
 
-def decode(lens, **k):
+def decode(room, lens, **k):
     lens = np.asarray(lens)
-    return Case(np.ones_like(lens), lens - 1, **k)
+    return Case(np.ones_like(lens), lens - 1, room=room // (k.get("ps", 16) // 16), **k)
 
 
+# both kernels: short parts on clusters; the cut that all CTAs share
+both = pytest.mark.parametrize("room", [0, 2400], ids=["clusters", "cut"])
 RAGGED = [1, 15, 16, 17, 0, 33, 64, 129, 500, 31]
 
 
+@both
 @pytest.mark.parametrize("hq,hkv", [(1, 1), (8, 8), (8, 2), (12, 3), (16, 4), (32, 8), (16, 1), (32, 1), (64, 2), (128, 4)])
 @pytest.mark.parametrize("d", [64, 128])
-def test_decode_head_layouts(cuda_device, hq, hkv, d):
-    decode(RAGGED, hq=hq, hkv=hkv, d=d, seed=hq + d).check(capi, cuda_device)
+def test_decode_head_layouts(cuda_device, room, hq, hkv, d):
+    decode(room, RAGGED, hq=hq, hkv=hkv, d=d, seed=hq + d).check(capi, cuda_device)
 
 
+@both
 @pytest.mark.parametrize("ps,blk", [(16, 16), (32, 16), (32, 32), (64, 16), (128, 64), (256, 256), (1024, 32)])
-def test_decode_pages_and_blocks(cuda_device, ps, blk):
-    decode(RAGGED + [1500], ps=ps, blk=blk, hkv=4, seed=ps + blk).check(capi, cuda_device)
+def test_decode_pages_and_blocks(cuda_device, room, ps, blk):
+    decode(room, RAGGED + [1500], ps=ps, blk=blk, hkv=4, seed=ps + blk).check(capi, cuda_device)
 
 
+@both
 @pytest.mark.parametrize("lens", [[1], [16], [4096], [0, 0, 0], [1] * 40, list(range(1, 400, 7)), [5000, 3, 700]])
-def test_decode_batches(cuda_device, lens):
-    decode(lens, hq=32, hkv=8, d=128, seed=len(lens)).check(capi, cuda_device)
+def test_decode_batches(cuda_device, room, lens):
+    decode(room, lens, hq=32, hkv=8, d=128, seed=len(lens)).check(capi, cuda_device)
 
 
-def test_decode_many_short_sequences(cuda_device):
-    decode(np.random.default_rng(3).integers(0, 60, size=600), hq=16, hkv=2, d=64).check(capi, cuda_device)
+@both
+def test_decode_many_short_sequences(cuda_device, room):
+    decode(room, np.random.default_rng(3).integers(0, 60, size=600), hq=16, hkv=2, d=64).check(capi, cuda_device)
 
 
+@both
 @pytest.mark.parametrize("scale", [0.0, -0.2, 1.0])
-def test_decode_scale(cuda_device, scale):
-    decode(RAGGED, scale=scale).check(capi, cuda_device)
+def test_decode_scale(cuda_device, room, scale):
+    decode(room, RAGGED, scale=scale).check(capi, cuda_device)
 
 
+@both
 @pytest.mark.parametrize("spread", [0.0, 3.0, 7.0])
-def test_decode_scales_far_apart(cuda_device, spread):
+def test_decode_scales_far_apart(cuda_device, room, spread):
     """Blocks whose scales differ by many powers of two, in K and in V."""
-    decode([300, 40, 1000], spread=spread, seed=5, scale=0.02).check(capi, cuda_device)
+    decode(room, [300, 40, 1000], spread=spread, seed=5, scale=0.02).check(capi, cuda_device)
 
 
-def test_decode_first_block_with_tiny_values(cuda_device):
+@both
+def test_decode_first_block_with_tiny_values(cuda_device, room):
     """Most of the weight on a block whose V is almost 0 (a first token): the others'
     weights keep their precision and the row's sum its size."""
-    c = decode([200], hq=4, hkv=1, d=64, seed=9)
+    c = decode(room, [200], hq=4, hkv=1, d=64, seed=9)
     p = c.table[0, 0]
     c.vs[p] *= 2.0 ** -20
     c.kp[p, 0] = torch.sign(c.q[0, :1].float()).mul(127).to(torch.int8)
@@ -69,24 +78,27 @@ def test_decode_first_block_with_tiny_values(cuda_device):
     c.check(capi, cuda_device)
 
 
+@both
 @pytest.mark.parametrize("value", [0.0, -3.0, float("nan"), 2.0 ** -60, 2.0 ** 60, float("inf")])
-def test_decode_scales_are_clamped(cuda_device, value):
-    c = decode([40, 70], hq=4, hkv=2, seed=2)
+def test_decode_scales_are_clamped(cuda_device, room, value):
+    c = decode(room, [40, 70], hq=4, hkv=2, seed=2)
     c.vs[c.table[1, 1]] = value
     if not value > 1:
         c.ks[c.table[0, 1]] = value
     c.check(capi, cuda_device)
 
 
+@both
 @pytest.mark.parametrize("bad", [[(0, 0)], [(0, 3)], [(1, 1), (1, 2)], [(0, 0), (1, 0)]])
 @pytest.mark.parametrize("hkv", [2, 8])
-def test_decode_keys_of_bad_pages_take_no_part(cuda_device, bad, hkv):
-    c = decode([100, 75, 16], hq=16, hkv=hkv, d=128 if hkv == 8 else 64, bad=bad)
+def test_decode_keys_of_bad_pages_take_no_part(cuda_device, room, bad, hkv):
+    c = decode(room, [100, 75, 16], hq=16, hkv=hkv, d=128 if hkv == 8 else 64, bad=bad)
     c.check(capi, cuda_device, error=(1, None))
 
 
-def test_decode_of_nothing_but_a_bad_page_gives_zeros(cuda_device):
-    c = decode([16, 20], bad=[(0, 0)])
+@both
+def test_decode_of_nothing_but_a_bad_page_gives_zeros(cuda_device, room):
+    c = decode(room, [16, 20], bad=[(0, 0)])
     out = c.run(capi, cuda_device)
     torch.cuda.synchronize()
     assert capi.device_error()[0] == 1
@@ -152,12 +164,13 @@ def test_prefill_keys_of_bad_pages_take_no_part(cuda_device, new, cached, bad):
     c.compare(out)
 
 
-def test_replays_on_other_inputs_and_two_calls_at_once(cuda_device):
+@pytest.mark.parametrize("msl", [300, 40000], ids=["clusters", "cut"])
+def test_replays_on_other_inputs_and_two_calls_at_once(cuda_device, msl):
     """A captured decode and prefill replayed on other lengths, tables, codes and scales;
     two calls in flight with workspaces of their own give the same bits."""
-    a = decode([100, 7, 300], hq=32, hkv=8, d=128, seed=1)
-    b = decode([250, 300, 1], hq=32, hkv=8, d=128, seed=2)
-    width = max(a.table.shape[1], b.table.shape[1])
+    a = decode(0, [100, 7, 300], hq=32, hkv=8, d=128, seed=1)
+    b = decode(0, [250, 300, 1], hq=32, hkv=8, d=128, seed=2)
+    width = max(a.table.shape[1], b.table.shape[1], msl // 16)
     pages = max(a.kp.shape[0], b.kp.shape[0])
     def padded(c):
         grow = lambda t, n, v: torch.cat([t, torch.full((n - t.shape[0],) + t.shape[1:], v, dtype=t.dtype)]) if t is not None else None
@@ -167,10 +180,10 @@ def test_replays_on_other_inputs_and_two_calls_at_once(cuda_device):
         return [x.to(cuda_device) for x in (grow(t[0], pages, 1), grow(t[1], pages, 1), grow(t[2], pages, 1.0),
                                             grow(t[3], pages, 1.0), t[4], table, t[6])]
     ta, tb = padded(a), padded(b)
-    eager = [capi.paged_attention_decode_int8(*t, a.scale, max_seq_len=300) for t in (ta, tb)]
+    eager = [capi.paged_attention_decode_int8(*t, a.scale, max_seq_len=msl) for t in (ta, tb)]
     live = [t.clone() for t in ta]
     ws, out = capi.decode_workspace(3, 32, live[0]), torch.empty_like(eager[0])
-    call = lambda: capi.paged_attention_decode_int8(*live, a.scale, max_seq_len=300, out=out, workspace=ws)
+    call = lambda: capi.paged_attention_decode_int8(*live, a.scale, max_seq_len=msl, out=out, workspace=ws)
     call()
     torch.cuda.synchronize()
     g = torch.cuda.CUDAGraph()
@@ -186,8 +199,8 @@ def test_replays_on_other_inputs_and_two_calls_at_once(cuda_device):
     torch.cuda.synchronize()
     outs = []
     for _ in range(5):
-        outs.append((capi.paged_attention_decode_int8(*ta, a.scale, max_seq_len=300, stream=s1),
-                     capi.paged_attention_decode_int8(*tb, a.scale, max_seq_len=300, stream=s2)))
+        outs.append((capi.paged_attention_decode_int8(*ta, a.scale, max_seq_len=msl, stream=s1),
+                     capi.paged_attention_decode_int8(*tb, a.scale, max_seq_len=msl, stream=s2)))
     torch.cuda.synchronize()
     for x, y in outs:
         assert torch.equal(x, eager[0]) and torch.equal(y, eager[1])

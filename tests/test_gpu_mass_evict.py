@@ -30,7 +30,7 @@ RAGGED = [1, 15, 16, 17, 0, 33, 64, 129, 500, 31]
 
 def run_mass(c, device, mass_in=None, decay=1.0, stride=None, **k):
     kp, vp, ks, vs, q, bt, L, _ = c.tensors(device)
-    msl = max(1, int(c.lens.max(initial=0)))
+    msl = c.max_len
     B = len(c.lens)
     store = torch.full((B, stride or msl + 3), -7.0, device=device)
     m = store[:, :msl + 1] if stride else store
@@ -67,6 +67,8 @@ def check_mass(c, device, before=None, decay=1.0, **k):
 @pytest.mark.parametrize("hq,hkv,d", [(1, 1, 64), (8, 2, 64), (32, 8, 128), (12, 3, 128), (32, 1, 128), (16, 16, 64), (64, 2, 64)])
 def test_mass_head_layouts(cuda_device, dtype, hq, hkv, d):
     check_mass(decode(RAGGED, hq=hq, hkv=hkv, d=d, dtype=dtype, seed=hq), cuda_device)
+    if dtype == "int8":   # the kernel for long contexts too
+        check_mass(decode(RAGGED, hq=hq, hkv=hkv, d=d, dtype=dtype, seed=hq, room=2400), cuda_device)
 
 
 @pytest.mark.parametrize("dtype,ps,blk", [("bf16", 8, 8), ("bf16", 64, 64), ("e4m3", 8, 8), ("e4m3", 32, 32), ("int8", 64, 32)])
@@ -78,6 +80,8 @@ def test_mass_page_sizes(cuda_device, dtype, ps, blk):
 @pytest.mark.parametrize("dtype", ["bf16", "int8"])
 def test_mass_batches(cuda_device, lens, dtype):
     check_mass(decode(lens, hq=32, hkv=8, d=128, dtype=dtype, seed=len(lens)), cuda_device)
+    if dtype == "int8":
+        check_mass(decode(lens, hq=32, hkv=8, d=128, dtype=dtype, seed=len(lens), room=2400), cuda_device)
 
 
 def test_mass_of_steps_before(cuda_device):
@@ -99,9 +103,10 @@ def test_mass_of_steps_before(cuda_device):
 
 def test_mass_is_that_of_the_plain_decode(cuda_device):
     """The attention beside it is bit for bit that of the plain call."""
-    c = decode([300, 41, 900], hq=32, hkv=8, d=128, dtype="int8")
-    out, _ = check_mass(c, cuda_device)
-    assert torch.equal(out, c.run(capi, cuda_device))
+    for room in (0, 2400):
+        c = decode([300, 41, 900], hq=32, hkv=8, d=128, dtype="int8", room=room)
+        out, _ = check_mass(c, cuda_device)
+        assert torch.equal(out, c.run(capi, cuda_device))
 
 
 def test_a_sequence_past_max_seq_len_is_cut_to_it(cuda_device):
@@ -116,11 +121,12 @@ def test_a_sequence_past_max_seq_len_is_cut_to_it(cuda_device):
 
 
 def test_mass_skips_keys_of_bad_pages_int8(cuda_device):
-    c = decode([100, 75], bad=[(0, 2)])
-    out, m = run_mass(c, cuda_device)
-    assert capi.device_error()[0] == 1
-    c.compare(out)
-    assert (m[0, 32:48] == 0).all() and abs(float(m[0, :100].sum()) - 8) < 1e-3
+    for room in (0, 2400):
+        c = decode([100, 75], bad=[(0, 2)], room=room)
+        out, m = run_mass(c, cuda_device)
+        assert capi.device_error()[0] == 1
+        c.compare(out)
+        assert (m[0, 32:48] == 0).all() and abs(float(m[0, :100].sum()) - 8) < 1e-3
 
 
 # ---- eviction --------------------------------------------------------------------
