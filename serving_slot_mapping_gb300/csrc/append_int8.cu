@@ -11,15 +11,20 @@
 // all in fp32, a division's quotient and one rounding (to nearest even) a row element.
 //
 // A run is the consecutive tokens whose slots lie in one block, padding tokens between
-// them aside (31 at most in a row); a warp takes a run for one head and tensor: up to 16
-// rows stay in registers between their maximum and their codes, so they are read once.  A re-encoded block is rewritten whole before
-// the run's own rows (__syncwarp orders the two), so the warp need not know which
-// rows are its own.
+// them aside (31 at most in a row).  A team takes a run for one head and tensor: one warp,
+// two where a block has 32 tokens, four from 64 on.  16 rows a warp stay in registers
+// between their maximum and their codes, so they are read once.  (Blocks of 64, 10,304
+// tokens, 8 heads of 128: 24.1 us, with one warp a run 36.4.)  A re-encoded block is rewritten
+// whole before the run's own rows, so the team need not know which rows are its own.
+// Six CTAs of an SM (80 registers a thread) hide each other's chains of slots, rows,
+// maximum and codes: 15.3 us for 10,304 tokens in blocks of 16 (9.3 of bytes); five 18.0,
+// eight, which spill, 15.4.
 #include <algorithm>
 
 #include "common.cuh"
 #include "inputs.cuh"
 #include "internal.h"
+#include "tma.cuh"
 
 namespace pa {
 
@@ -93,11 +98,12 @@ __device__ __forceinline__ float max_number8(float a, uint4 v) {
   return a;
 }
 
-// Tokens [blockIdx.x * per_cta, + per_cta), at most 32: the runs that begin there.
+// Tokens [blockIdx.x * per_cta, + per_cta), at most 32: the runs that begin there.  W:
+// warps of a team.
 // blockIdx.y: a share of the (run, tensor, head) tasks.  Every warp finds the runs by
 // itself, from the slots of these tokens and of the 32 before them, a lane each.
-template <int D>
-__global__ void __launch_bounds__(kAppendWarps * 32) append_int8_kernel(const __grid_constant__ AppendInt8Params p,
+template <int D, int W>
+__global__ void __launch_bounds__(kAppendWarps * 32, 6) append_int8_kernel(const __grid_constant__ AppendInt8Params p,
                                                                         int per_cta) {
   constexpr int kLanes = D / 8;            // lanes of a row
   constexpr int kRows = 32 / kLanes;       // rows of a pass
@@ -107,6 +113,27 @@ __global__ void __launch_bounds__(kAppendWarps * 32) append_int8_kernel(const __
   const int64_t first = (int64_t)blockIdx.x * per_cta;
   const int pairs = 2 * p.num_kv_heads;
   const unsigned kAll = 0xffffffffu;
+  constexpr int kTeams = kAppendWarps / W;
+  __shared__ float most[kAppendWarps];
+  const int team = warp / W, w0 = warp % W * 16;  // w0: this warp's first row of the span
+  auto team_sync = [&]() {
+    if constexpr (W == 1) __syncwarp();
+    else named_barrier(1 + team, W * 32);
+  };
+  // the largest of the team's values (NaN wins), for every warp of it
+  auto team_max = [&](float a) {
+    if constexpr (W == 1) return a;
+    if (lane == 0) most[warp] = a;
+    team_sync();
+    a = most[team * W];
+#pragma unroll
+    for (int i = 1; i < W; ++i) {
+      const float x = most[team * W + i];
+      a = a != a || x != x ? a + x : fmaxf(a, x);
+    }
+    team_sync();  // read before the next one is written
+    return a;
+  };
   griddep_wait();
   auto slot_at = [&](int64_t t) {  // -1: no token, or one without a place
     const int64_t s = t >= 0 && t < p.num_tokens ? ld_input(p.slot_mapping + t) : -1;
@@ -128,7 +155,7 @@ __global__ void __launch_bounds__(kAppendWarps * 32) append_int8_kernel(const __
   const int before = lower != 0u ? pb : (there0 != 0u && last >= lane ? pb0 : -1);
   const unsigned leaders = __ballot_sync(kAll, lane < per_cta && blk >= 0 && before != blk);
   const int tasks = __popc(leaders) * pairs;
-  for (int task = blockIdx.y * kAppendWarps + warp; task < tasks; task += gridDim.y * kAppendWarps) {
+  for (int task = blockIdx.y * kTeams + team; task < tasks; task += gridDim.y * kTeams) {
     const int pair = task % pairs;
     unsigned m = leaders;
     for (int i = task / pairs; i > 0; --i) m &= m - 1u;
@@ -164,7 +191,7 @@ __global__ void __launch_bounds__(kAppendWarps * 32) append_int8_kernel(const __
     uint4 v[kPasses];
 #pragma unroll
     for (int x = 0; x < kPasses; ++x) {
-      const int r = x * kRows + sub;
+      const int r = w0 + x * kRows + sub;
       v[x] = r < n ? row(r) : make_uint4(0u, 0u, 0u, 0u);
     }
     const float old = fresh ? 0.f : clamp_scale(__uint_as_float(ld_input(reinterpret_cast<const uint32_t*>(scale))));
@@ -176,26 +203,32 @@ __global__ void __launch_bounds__(kAppendWarps * 32) append_int8_kernel(const __
     int at[kPasses];
 #pragma unroll
     for (int x = 0; x < kPasses; ++x) {
-      const int r = x * kRows + sub, s = __shfl_sync(kAll, slot, (l + r) & 31);
+      const int r = w0 + x * kRows + sub, s = __shfl_sync(kAll, slot, (l + r) & 31);
       at[x] = l + r < 32 ? (r < n && block_of(s) == b ? s : -1) : mine_of(r);
     }
+    // f(row, slot) for this warp's rows of the span from `first` on that are the run's
+    auto each = [&](int64_t from, auto f) {
+      for (int64_t c = from + w0; c < n; c += 16 * W)
+        for (int64_t r = c + sub; r < min(n, c + 16); r += kRows) {
+          const int to = mine_of(r);
+          if (to >= 0) f(r, to);
+        }
+    };
     __nv_bfloat162 any = __float2bfloat162_rn(0.f);
 #pragma unroll
     for (int x = 0; x < kPasses; ++x)
       if (at[x] >= 0) max_abs8(&any, v[x]);
-    for (int64_t r = 16 + sub; r < n; r += kRows)
-      if (mine_of(r) >= 0) max_abs8(&any, row(r));
+    each(16 * W, [&](int64_t r, int) { max_abs8(&any, row(r)); });
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) any = __hmax2_nan(any, __shfl_xor_sync(kAll, any, o));
-    float a = __bfloat162float(__hmax_nan(any.x, any.y));
+    float a = team_max(__bfloat162float(__hmax_nan(any.x, any.y)));
     const bool plain = a <= 3.3e38f;  // neither infinities nor NaN
     if (a != a) {                     // the largest of the numbers
       a = 0.f;
-#pragma unroll 1
-      for (int64_t r = sub; r < n; r += kRows)
-        if (mine_of(r) >= 0) a = max_number8(a, row(r));
+      each(0, [&](int64_t r, int) { a = max_number8(a, row(r)); });
 #pragma unroll
       for (int o = 16; o > 0; o >>= 1) a = fmaxf(a, __shfl_xor_sync(kAll, a, o));
+      a = team_max(a);
     }
     const float s = fmaxf(old, clamp_scale(__fdiv_rn(a, 127.f)));
     // a finite value past 127.5 scales needs saturating too: above the largest scale
@@ -204,35 +237,42 @@ __global__ void __launch_bounds__(kAppendWarps * 32) append_int8_kernel(const __
     if (!fresh && s > old) {
       const float ratio = __fdiv_rn(old, s);
       const int rows = 1 << p.scale_shift;
-      for (int r = sub; r < rows; r += kRows) {
-        uint2* c = reinterpret_cast<uint2*>(pool + (int64_t)(head_slot + r) * pitch);
-        const uint2 w = ld_input(c);
-        *c = make_uint2(rescale4(w.x, ratio), rescale4(w.y, ratio));
-      }
+      for (int c = w0; c < rows; c += 16 * W)
+        for (int r = c + sub; r < c + 16; r += kRows) {  // (a block has 16 tokens or a multiple)
+          uint2* to = reinterpret_cast<uint2*>(pool + (int64_t)(head_slot + r) * pitch);
+          const uint2 w = ld_input(to);
+          *to = make_uint2(rescale4(w.x, ratio), rescale4(w.y, ratio));
+        }
     }
-    __syncwarp();  // the rows below land over the re-encoded ones
-    if (lane == 0) *scale = s;
+    team_sync();  // the rows below land over the re-encoded ones
+    if (lane == 0 && w0 == 0) *scale = s;
 #pragma unroll
     for (int x = 0; x < kPasses; ++x)
       if (at[x] >= 0) *reinterpret_cast<uint2*>(pool + (int64_t)at[x] * pitch) = codes8(v[x], s, y, fast);
-    for (int64_t r = 16 + sub; r < n; r += kRows) {
-      const int to = mine_of(r);
-      if (to >= 0) *reinterpret_cast<uint2*>(pool + (int64_t)to * pitch) = codes8(row(r), s, y, fast);
-    }
+    each(16 * W, [&](int64_t r, int to) {
+      *reinterpret_cast<uint2*>(pool + (int64_t)to * pitch) = codes8(row(r), s, y, fast);
+    });
   }
+}
+
+template <int W>
+cudaError_t launch_teams(const AppendInt8Params& p, int num_sms, cudaStream_t s) {
+  constexpr int kTeams = kAppendWarps / W;
+  const int shares = (2 * p.num_kv_heads + kTeams - 1) / kTeams;
+  // one token a CTA while that fills the SMs four times at most (a decode step: every
+  // token is a run), else 16
+  const int per_cta = p.num_tokens * shares <= 4 * (int64_t)num_sms ? 1 : 16;
+  const int64_t ctas = (p.num_tokens + per_cta - 1) / per_cta;
+  auto kern = p.head_dim == 128 ? append_int8_kernel<128, W> : append_int8_kernel<64, W>;
+  return launch_pdl(kern, dim3((unsigned)ctas, (unsigned)std::min(shares, 65535)), dim3(kAppendWarps * 32), 0, s, p, per_cta);
 }
 
 }  // namespace
 
 cudaError_t launch_append_int8(const AppendInt8Params& p, int num_sms, cudaStream_t s) {
   if (p.num_tokens <= 0) return cudaSuccess;
-  const int shares = (2 * p.num_kv_heads + kAppendWarps - 1) / kAppendWarps;
-  // one token a CTA while that fills the SMs four times at most (a decode step: every
-  // token is a run), else 16
-  const int per_cta = p.num_tokens * shares <= 4 * (int64_t)num_sms ? 1 : 16;
-  const int64_t ctas = (p.num_tokens + per_cta - 1) / per_cta;
-  auto kern = p.head_dim == 128 ? append_int8_kernel<128> : append_int8_kernel<64>;
-  return launch_pdl(kern, dim3((unsigned)ctas, (unsigned)std::min(shares, 65535)), dim3(kAppendWarps * 32), 0, s, p, per_cta);
+  if (p.scale_shift == 4) return launch_teams<1>(p, num_sms, s);
+  return p.scale_shift == 5 ? launch_teams<2>(p, num_sms, s) : launch_teams<4>(p, num_sms, s);
 }
 
 }  // namespace pa
