@@ -9,11 +9,17 @@
 // A cluster of CTAs shares a sequence, each a stretch of its units, whose keys (floats
 // as ordered integers) stay in shared memory where they fit.  The threshold comes from
 // four histograms of 8 bits each (a radix select; integer counts, so the result is the
-// same on every run), added up over the cluster through distributed shared memory; then
-// each CTA knows how many units before its stretch are kept, and one pass ranks and
-// moves its own.
+// same on every run), added up over the cluster through distributed shared memory; a
+// digit that takes all of its keys ends the search.  Then each CTA knows how many units
+// before its stretch are kept, and one pass ranks and moves its own.  What a digit costs
+// is what each CTA reads of the others' counts: digits of 11 bits, 8 KB a CTA, took 4.2
+// us a digit on 8 CTAs and 8 us on 16, these 2.7 on 16 (one sequence of 131,072 rows:
+// 25, 32 and 17 us in all).
 // Bytes: the masses once read and once written (and the re-reads of units that do not
-// fit in shared memory).
+// fit in shared memory).  256 sequences of up to 8192 rows by pages of 16 take 23 us
+// (55 MB; 8 us at the rate of a copy): one wave of CTAs, as long as its longest
+// sequences.  One long sequence is latency on its few CTAs: the loads, each digit's
+// counts and barriers, the moves.
 #include <algorithm>
 
 #include "cluster.cuh"
@@ -28,9 +34,10 @@ namespace {
 constexpr int kEvictThreads = 512;
 constexpr int kEvictWarps = kEvictThreads / 32;
 constexpr int kCacheUnits = kMaxEvictPages / 8 + 32;  // keys in shared memory: 160 KB
-constexpr int kBins = 4 * kEvictThreads;              // digits of 11, 11 and 10 bits
+constexpr int kDigits = 4, kBins = 256;               // of 8 bits each
 constexpr int kAhead = 4;                             // vectors of a thread in flight
-constexpr int kRowsAhead = 8;                         // masses of a lane in flight as they move
+constexpr int kMaxCtas = 16;                          // of a cluster (more than 8 are opted in to)
+constexpr int kRowsAhead = 16;                        // masses of a lane in flight as they move
 
 // A float as an integer of the same order; NaN lowest, -0 as 0.
 __device__ __forceinline__ uint32_t order_key(float x) {
@@ -47,10 +54,9 @@ __device__ __forceinline__ float4 ld_float4(const float* p) {
 }
 
 struct EvictShared {
-  uint32_t hist[3][kBins];     // of each digit: one barrier of the cluster a digit
-  uint32_t warp_sum[kEvictWarps];
+  uint32_t hist[kDigits][kBins];   // this CTA's, of each digit: one barrier of the cluster a digit
+  uint32_t total[kDigits][kBins];  // the cluster's
   uint32_t above, ties;        // this CTA's units above the threshold (or kept anyway), and at it
-  uint32_t digit, left;        // the threshold's digit, units still to be taken at it
   uint32_t warp_above[kEvictWarps], warp_ties[kEvictWarps];
   int32_t count;
 };
@@ -109,8 +115,8 @@ __global__ void __launch_bounds__(kEvictThreads) evict_kernel(const __grid_const
   const bool select = over && want > 0u;
   // ---- the keys of this stretch ----
   if (select) {
-#pragma unroll
-    for (int d = 0; d < 3; ++d) reinterpret_cast<uint4*>(sh.hist[d])[tid] = make_uint4(0u, 0u, 0u, 0u);
+    static_assert(2 * kDigits * kBins == 4 * kEvictThreads, "a vector a thread");
+    reinterpret_cast<uint4*>(sh.hist[0])[tid] = make_uint4(0u, 0u, 0u, 0u);  // and the totals behind
     if constexpr (PAGES) {
       if (p.vec && ps >= 4 && ps <= 128) {
         const int pages = 128 / ps, lanes = ps / 4;  // of a warp's vectors
@@ -191,53 +197,56 @@ __global__ void __launch_bounds__(kEvictThreads) evict_kernel(const __grid_const
   uint32_t prefix = 0u, left = want;  // digits so far; units still to be found below them
   if (select) {
     const int a = max(lo, front), e = min(hi, back);
-    for (int pass = 0; pass < 3; ++pass) {
-      const int shift = pass == 0 ? 21 : (pass == 1 ? 10 : 0);
-      const uint32_t digits = pass == 2 ? 1023u : 2047u;
+    for (int pass = 0; pass < kDigits; ++pass) {
+      const int shift = 24 - 8 * pass;
       uint32_t* hist = sh.hist[pass];
-      const int top = pass == 0 ? 31 : (pass == 1 ? 21 : 10);  // where the digits found so far end
       each(a, e, [&](uint32_t k) {
-        if (pass == 0 || (k >> top) == (prefix >> top)) atomicAdd(&hist[(k >> shift) & digits], 1u);
+        if (((uint64_t)(k ^ prefix) >> (shift + 8)) == 0) atomicAdd(&hist[(k >> shift) & 255u], 1u);
       });
-      if (csize > 1) cluster_sync(); else __syncthreads();
-      // thread i: digits 4 (511 - i) .. + 3 of all CTAs, the highest digits first
-      const int g = kEvictThreads - 1 - tid;
-      uint4 n = reinterpret_cast<const uint4*>(hist)[g];
       if (csize > 1) {
-        n = make_uint4(0u, 0u, 0u, 0u);
-        for (int c = 0; c < csize; ++c) {
-          const float4 x = ld_cluster4(map_rank(smem_u32(hist + 4 * g), c));
-          n.x += __float_as_uint(x.x);
-          n.y += __float_as_uint(x.y);
-          n.z += __float_as_uint(x.z);
-          n.w += __float_as_uint(x.w);
+        cluster_sync();
+        // 64 threads to a CTA's histogram
+        for (int c = tid >> 6; c < csize; c += kEvictThreads / 64) {
+          const int g = 4 * (tid & 63);
+          const float4 x = ld_cluster4(map_rank(smem_u32(hist + g), c));
+          uint32_t* t = sh.total[pass] + g;
+          if (__float_as_uint(x.x) != 0u) atomicAdd(t, __float_as_uint(x.x));
+          if (__float_as_uint(x.y) != 0u) atomicAdd(t + 1, __float_as_uint(x.y));
+          if (__float_as_uint(x.z) != 0u) atomicAdd(t + 2, __float_as_uint(x.z));
+          if (__float_as_uint(x.w) != 0u) atomicAdd(t + 3, __float_as_uint(x.w));
         }
+        hist = sh.total[pass];
       }
-      const uint32_t mine = n.x + n.y + n.z + n.w;
+      __syncthreads();
+      // each warp by itself: lane i has digits 8 (31 - i) .. + 7, the highest first
+      const int g = 31 - lane;
+      const uint4 n0 = reinterpret_cast<const uint4*>(hist)[2 * g], n1 = reinterpret_cast<const uint4*>(hist)[2 * g + 1];
+      const uint32_t n[8] = {n1.w, n1.z, n1.y, n1.x, n0.w, n0.z, n0.y, n0.x};
+      const uint32_t mine = n[0] + n[1] + n[2] + n[3] + n[4] + n[5] + n[6] + n[7];
       uint32_t incl = mine;
+#pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
         const uint32_t t = __shfl_up_sync(0xffffffffu, incl, o);
         if (lane >= o) incl += t;
       }
-      if (lane == 31) sh.warp_sum[warp] = incl;
-      __syncthreads();
-      for (int w = 0; w < warp; ++w) incl += sh.warp_sum[w];
-      uint32_t before = incl - mine;
-      if (incl >= left && before < left) {
-        int d = 4 * g + 3;
-        const uint32_t four[4] = {n.w, n.z, n.y, n.x};
+      uint32_t before = incl - mine, d = 8u * (uint32_t)g + 7u, here = n[0];
 #pragma unroll
-        for (int k = 0; k < 3; ++k)
-          if (d == 4 * g + 3 - k && before + four[k] < left) {
-            before += four[k];
-            --d;
-          }
-        sh.digit = (uint32_t)d;
-        sh.left = left - before;
+      for (int k = 0; k < 7; ++k)
+        if (d == 8u * (uint32_t)g + 7u - k && before + n[k] < left) {
+          before += n[k];
+          here = n[k + 1];
+          --d;
+        }
+      // the first lane whose digits reach `left` (the last one, where none would)
+      const unsigned reach = __ballot_sync(0xffffffffu, incl >= left);
+      const int at = reach != 0u ? __ffs(reach) - 1 : 31;
+      prefix |= __shfl_sync(0xffffffffu, d, at) << shift;
+      left -= __shfl_sync(0xffffffffu, before, at);
+      if (__shfl_sync(0xffffffffu, here, at) == left && prefix != 0u) {
+        --prefix;  // every key that begins with these digits stays: no more of them are needed
+        left = 0u;
+        break;
       }
-      __syncthreads();
-      prefix |= sh.digit << shift;
-      left = sh.left;
     }
   }
   // ---- this stretch's units above the threshold and at it ----
@@ -251,12 +260,26 @@ __global__ void __launch_bounds__(kEvictThreads) evict_kernel(const __grid_const
   };
   __syncthreads();
   uint32_t n_above = 0u, n_ties = 0u;
-#pragma unroll 4
-  for (int u0 = wlo; u0 < whi; u0 += 32) {
+  auto count = [&](int u, uint32_t k) {
     bool ab, ti;
-    classify(u0 + lane, select && u0 + lane < whi ? key(u0 + lane) : 0u, &ab, &ti);
+    classify(u, k, &ab, &ti);
     n_above += ab ? 1u : 0u;
     n_ties += ti ? 1u : 0u;
+  };
+  if (!select) {  // all of them, or those at the ends
+    for (int u = wlo + lane; u < whi; u += 32) count(u, 0u);
+  } else if (whi - lo <= cached) {  // four units a lane and step
+#pragma unroll 2
+    for (int i = (wlo - lo + 3) / 4 + lane; 4 * i < whi - lo; i += 32) {  // wlo: a multiple of 32 past lo, or hi
+      const uint4 k = cache4[i];
+      const int u = lo + 4 * i;
+      count(u, k.x);
+      count(u + 1, k.y);
+      count(u + 2, k.z);
+      count(u + 3, k.w);
+    }
+  } else {
+    for (int u = wlo + lane; u < whi; u += 32) count(u, key(u));
   }
   n_above = __reduce_add_sync(0xffffffffu, n_above);
   n_ties = __reduce_add_sync(0xffffffffu, n_ties);
@@ -284,14 +307,15 @@ __global__ void __launch_bounds__(kEvictThreads) evict_kernel(const __grid_const
   }
   if (csize > 1) cluster_sync(); else __syncthreads();
   uint32_t above = 0u, ties = 0u, all_above = 0u;
-  for (int c = 0; c < csize; ++c) {
-    const uint32_t x = csize > 1 ? ld_cluster(map_rank(smem_u32(&sh.above), c)) : sh.above;
-    const uint32_t y = csize > 1 ? ld_cluster(map_rank(smem_u32(&sh.ties), c)) : sh.ties;
-    if (c < rank) {
-      above += x;
-      ties += y;
-    }
-    all_above += x;
+  if (csize > 1) {
+    // lane c reads the counts of CTA c (above and ties lie side by side)
+    const float2 v = lane < csize ? ld_cluster2(map_rank(smem_u32(&sh.above), lane)) : make_float2(0.f, 0.f);
+    const uint32_t x = lane < csize ? __float_as_uint(v.x) : 0u, y = lane < csize ? __float_as_uint(v.y) : 0u;
+    all_above = __reduce_add_sync(0xffffffffu, x);
+    above = __reduce_add_sync(0xffffffffu, lane < rank ? x : 0u);
+    ties = __reduce_add_sync(0xffffffffu, lane < rank ? y : 0u);
+  } else {
+    all_above = sh.above;
   }
   for (int w = 0; w < warp; ++w) {
     above += sh.warp_above[w];
@@ -402,15 +426,18 @@ cudaError_t launch_evict(const EvictParams& p, bool pages, int num_sms, cudaStre
   const int64_t units = pages ? std::min<int64_t>(p.max_blocks, (p.max_len + p.page_size - 1) / p.page_size) : p.max_len;
   if (pages && units > kMaxEvictPages) return cudaErrorInvalidValue;  // their weights have no place
   // CTAs of a sequence: as many as find an SM, with 4096 rows each or more; enough
-  // that their stretches fit in shared memory, where 8 can
+  // that their stretches fit in shared memory, where 16 can.  One sequence of 131,072
+  // rows: 21 us on 8 CTAs, 16 on 16; of 8192 rows, where one CTA would do: 11.4 us on
+  // two, 9.8 on one; of 32,768: 11.9 us on eight, 13.9 on four.
   const int64_t rows = pages ? units * p.page_size : units;
   int csize = 1;
-  while (csize < 8 && ((int64_t)p.batch * csize * 2 <= num_sms && rows >= 4096 * 2 * (int64_t)csize)) csize *= 2;
-  while (csize < 8 && units > (int64_t)csize * (kCacheUnits - 32)) csize *= 2;
+  while (csize < kMaxCtas && ((int64_t)p.batch * csize * 2 <= num_sms && rows >= 4096 * 2 * (int64_t)csize)) csize *= 2;
+  while (csize < kMaxCtas && units > (int64_t)csize * (kCacheUnits - 32)) csize *= 2;
   const int64_t stretch = (units + csize - 1) / csize + 32;
   const int smem = (int)(stretch < kCacheUnits ? stretch : kCacheUnits) * 4 + 16;
   auto kern = pages ? evict_kernel<true> : evict_kernel<false>;
-  const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kCacheUnits * 4 + 16);
+  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kCacheUnits * 4 + 16);
+  if (e == cudaSuccess && csize > 8) e = cudaFuncSetAttribute(kern, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
   if (e != cudaSuccess) return e;
   return launch_pdl_cluster(kern, dim3((unsigned)(p.batch * csize)), dim3(kEvictThreads), (size_t)smem, csize, s, p, csize);
 }

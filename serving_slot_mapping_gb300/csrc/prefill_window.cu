@@ -40,7 +40,8 @@
 // * R_k goes into the factor of S that the softmax has anyway, log2 R_v into the
 //   reference max (y = x + log2 R_v; P = 2^(y - m) stays in f16's range whatever the
 //   scales are), and l sums P / R_v.  No work is added for an element of S.
-// Sixteen warps for that: 2 x 192 + 2 x 64 registers a thread.
+// Sixteen warps for that: 2 x 144 + 2 x 112 registers a thread, and the softmax in loops
+// of 32 columns: written out, it and the conversion did not fit in the instruction cache.
 // A block_table entry out of range is noted by the TMA warp; a CTA that met one
 // computes the rows of its items with such a page again at its end, without their
 // keys (redo_bad_items).  The loop knows nothing of them: masks told to the softmax by
@@ -93,7 +94,7 @@ struct WCfg : PCfg<D, KV8> {
   // dims), in the space of the others' three and two tiles.  Codes that land in the slot
   // of their f16 tile (as e4m3 ones do) can be loaded only once the products on that
   // slot's last tile are done, and load and conversion then lie in a row: 1426 us for 19
-  // chunks of 512 after 4096 tokens, 32 / 8 heads; with stages of their own 
+  // chunks of 512 after 4096 tokens, 32 / 8 heads; with stages of their own 1370.
   static constexpr int kNK = SC ? 2 : kNSK;
   static constexpr int kVRing = SC ? Base::kKOff + 2 * Base::kKVTile : Base::kVOff;
   static constexpr int kCodeOff = Base::kKOff + (2 + kNSV) * Base::kKVTile;
