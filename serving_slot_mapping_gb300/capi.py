@@ -864,7 +864,7 @@ def _mass_rows(t, name, B, width):
         raise ValueError(f"{name} must be float32 [{B}, {width} or more]")
     if t.shape[1] > 1 and t.stride(1) != 1:
         raise ValueError(f"the rows of {name} must be contiguous")
-    return t.stride(0) if B > 1 else max(t.shape[1], 1)
+    return t.stride(0) if B > 1 else max(width, 1)
 
 
 def paged_attention_decode_mass(key_pool, value_pool, q, block_table, seq_lens, scale, mass_out, mass_in=None, decay=1.0,

@@ -1125,7 +1125,7 @@ pa_status check_evict(const float* mass, int64_t mass_stride, const int32_t* seq
                       int64_t new_mass_stride, int32_t protect) {
   if (batch < 0 || width < 0 || budget < 0 || num_sinks < 0 || num_recent < 0) return PA_ERR_SHAPE;
   if (mass_stride < width || new_mass_stride < width || protect > budget) return PA_ERR_SHAPE;
-  if (batch > INT32_MAX / 8 || mass_stride > INT32_MAX || new_mass_stride > INT32_MAX) return PA_ERR_RANGE;
+  if (batch > INT32_MAX / 16 || mass_stride > INT32_MAX || new_mass_stride > INT32_MAX) return PA_ERR_RANGE;
   if (batch == 0) return PA_OK;
   if (seq_lens == nullptr || (width > 0 && (mass == nullptr || new_mass == nullptr))) return PA_ERR_NULL;
   if (!aligned(mass, 4) || !aligned(new_mass, 4) || !aligned(seq_lens, 4)) return PA_ERR_ALIGN;

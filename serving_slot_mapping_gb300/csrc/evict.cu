@@ -16,7 +16,7 @@
 // us a digit on 8 CTAs and 8 us on 16, these 2.7 on 16 (one sequence of 131,072 rows:
 // 25, 32 and 17 us in all).
 // Bytes: the masses once read and once written (and the re-reads of units that do not
-// fit in shared memory).  256 sequences of up to 8192 rows by pages of 16 take 23 us
+// fit in shared memory).  256 sequences of 1k to 32k rows by pages of 16 take 23 us
 // (55 MB; 8 us at the rate of a copy): one wave of CTAs, as long as its longest
 // sequences.  One long sequence is latency on its few CTAs: the loads, each digit's
 // counts and barriers, the moves.

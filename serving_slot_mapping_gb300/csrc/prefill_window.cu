@@ -1065,7 +1065,7 @@ __global__ void __launch_bounds__(WCfg<D, KV8, SC>::kThreads, 1)
         // code beside it, the unrolled form had warps wait for instructions (4.2 per issue)
         // and took 1258 us where the loops take 740 (19 chunks of 512 after 4096 tokens,
         // 32 / 8 heads of 128).
-        constexpr int kHeld = SC ? 1 : 4, kExpHeld = 1;
+        constexpr int kHeld = SC ? 1 : 4;
         auto load = [&](auto& v, int first, int n) {
 #pragma unroll
           for (int i = 0; i < n; ++i) tmem_ld32(s_col + (first + i) * 32, v[i]);
@@ -1124,15 +1124,11 @@ __global__ void __launch_bounds__(WCfg<D, KV8, SC>::kThreads, 1)
         };
         if constexpr (SC) {
 #pragma unroll 1
-          for (int first = 0; first < 4; first += kExpHeld) {
-            uint32_t x[kExpHeld][32];
-            load(x, first, kExpHeld);
-#pragma unroll
-            for (int cb = 0; cb < kExpHeld; ++cb) {
-              uint32_t w[16];
-              exp32(x[cb], w);
-              tmem_st16(s_col + (first + cb) * 16, w);
-            }
+          for (int cb = 0; cb < 4; ++cb) {
+            uint32_t x[1][32], w[16];
+            load(x, cb, 1);
+            exp32(x[0], w);
+            tmem_st16(s_col + cb * 16, w);
           }
         } else {
 #pragma unroll
@@ -1204,44 +1200,44 @@ __global__ void __launch_bounds__(WCfg<D, KV8, SC>::kThreads, 1)
       constexpr int kOut = SC ? 1 : D / 32;  // 32 columns each, held at once
 #pragma unroll 1
       for (int first = 0; first < D / 32; first += kOut) {
-      uint32_t oall[kOut][32];
+        uint32_t oall[kOut][32];
 #pragma unroll
-      for (int cb = 0; cb < kOut; ++cb)
-        if (ntt > 0) {
-          tmem_ld32(o_col + (first + cb) * 32, oall[cb]);
-        } else {
+        for (int cb = 0; cb < kOut; ++cb)
+          if (ntt > 0) {
+            tmem_ld32(o_col + (first + cb) * 32, oall[cb]);
+          } else {
 #pragma unroll
-          for (int e = 0; e < 32; ++e) oall[cb][e] = 0u;
-        }
-      if (ntt > 0) tmem_wait_ld();
+            for (int e = 0; e < 32; ++e) oall[cb][e] = 0u;
+          }
+        if (ntt > 0) tmem_wait_ld();
 #pragma unroll
-      for (int cb = 0; cb < kOut; ++cb) {
-        const uint32_t (&o)[32] = oall[cb];
-        uint32_t w[4][4];  // unit u: columns 8u .. 8u + 7
+        for (int cb = 0; cb < kOut; ++cb) {
+          const uint32_t (&o)[32] = oall[cb];
+          uint32_t w[4][4];  // unit u: columns 8u .. 8u + 7
 #pragma unroll
-        for (int u = 0; u < 4; ++u)
+          for (int u = 0; u < 4; ++u)
 #pragma unroll
-          for (int i = 0; i < 4; ++i)
-            w[u][i] = pack_bf16(__uint_as_float(o[8 * u + 2 * i]) * inv, __uint_as_float(o[8 * u + 2 * i + 1]) * inv);
+            for (int i = 0; i < 4; ++i)
+              w[u][i] = pack_bf16(__uint_as_float(o[8 * u + 2 * i]) * inv, __uint_as_float(o[8 * u + 2 * i + 1]) * inv);
 #pragma unroll
-        for (int s = 1; s < 4; s <<= 1) {
-          const bool odd = (lane & s) != 0;
+          for (int s = 1; s < 4; s <<= 1) {
+            const bool odd = (lane & s) != 0;
 #pragma unroll
-          for (int u = 0; u < 4; ++u) {
-            if (u & s) continue;
+            for (int u = 0; u < 4; ++u) {
+              if (u & s) continue;
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              const uint32_t got = __shfl_xor_sync(0xffffffffu, odd ? w[u][i] : w[u | s][i], s);
-              if (odd) w[u][i] = got; else w[u | s][i] = got;
+              for (int i = 0; i < 4; ++i) {
+                const uint32_t got = __shfl_xor_sync(0xffffffffu, odd ? w[u][i] : w[u | s][i], s);
+                if (odd) w[u][i] = got; else w[u | s][i] = got;
+              }
             }
           }
-        }
 #pragma unroll
-        for (int k = 0; k < 4; ++k)  // row k of the quad, this lane's unit of it
-          if (dst[k] >= 0)
-            *reinterpret_cast<uint4*>(outp + dst[k] + (first + cb) * 32 + (lane & 3) * 8) =
-                make_uint4(w[k][0], w[k][1], w[k][2], w[k][3]);
-      }
+          for (int k = 0; k < 4; ++k)  // row k of the quad, this lane's unit of it
+            if (dst[k] >= 0)
+              *reinterpret_cast<uint4*>(outp + dst[k] + (first + cb) * 32 + (lane & 3) * 8) =
+                  make_uint4(w[k][0], w[k][1], w[k][2], w[k][3]);
+        }
       }
       tc_fence_before();  // O is read before this thread's next P lets PV write it again
     }

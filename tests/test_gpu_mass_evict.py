@@ -101,6 +101,17 @@ def test_mass_of_steps_before(cuda_device):
     assert torch.equal(m, 2 * once)
 
 
+def test_mass_rows_of_one_sequence_and_two_widths(cuda_device):
+    """One sequence has no row stride: the masses before may lie in a wider tensor."""
+    c = decode([40], dtype="bf16")
+    kp, vp, ks, vs, q, bt, L, _ = c.tensors(cuda_device)
+    before = torch.rand(1, 53, device=cuda_device)
+    got, once = torch.zeros(1, 41, device=cuda_device), torch.zeros(1, 53, device=cuda_device)
+    capi.paged_attention_decode_mass(kp, vp, q, bt, L, c.scale, got, mass_in=before, max_seq_len=40)
+    capi.paged_attention_decode_mass(kp, vp, q, bt, L, c.scale, once, mass_in=before, max_seq_len=40)
+    assert torch.equal(got[:, :40], once[:, :40]) and float(got[0, 40]) == 0
+
+
 def test_mass_is_that_of_the_plain_decode(cuda_device):
     """The attention beside it is bit for bit that of the plain call."""
     for room in (0, 2400):
