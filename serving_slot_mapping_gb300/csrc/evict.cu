@@ -8,15 +8,16 @@
 //
 // A cluster of CTAs shares a sequence, each a stretch of its units, whose keys (floats
 // as ordered integers) stay in shared memory where they fit.  The threshold comes from
-// four histograms of 8 bits each (a radix select; integer counts, so the result is the
-// same on every run), added up over the cluster through distributed shared memory; a
-// digit that takes all of its keys ends the search.  Then each CTA knows how many units
+// histograms of its digits (a radix select; integer counts, so the result is the same on
+// every run), added up over the cluster through distributed shared memory; a digit that
+// takes all of its keys ends the search.  Then each CTA knows how many units
 // before its stretch are kept, and one pass ranks and moves its own.  What a digit costs
-// is what each CTA reads of the others' counts: digits of 11 bits, 8 KB a CTA, took 4.2
-// us a digit on 8 CTAs and 8 us on 16, these 2.7 on 16 (one sequence of 131,072 rows:
-// 25, 32 and 17 us in all).
+// in a cluster is what each CTA reads of the others' counts: digits of 11 bits, 8 KB a
+// CTA, took 4.2 us a digit on 8 CTAs and 8 us on 16, 8 bits 2.7 on 16 (one sequence of
+// 131,072 rows: 25, 32 and 17 us in all).  Alone, a CTA takes 11 (32 sequences of
+// 512-4096 rows: 8.5 us, with 8 bits 9.4).
 // Bytes: the masses once read and once written (and the re-reads of units that do not
-// fit in shared memory).  256 sequences of 1k to 32k rows by pages of 16 take 23 us
+// fit in shared memory).  256 sequences of 1k to 32k rows by pages of 16 take 22 us
 // (55 MB; 8 us at the rate of a copy): one wave of CTAs, as long as its longest
 // sequences.  One long sequence is latency on its few CTAs: the loads, each digit's
 // counts and barriers, the moves.
@@ -34,7 +35,6 @@ namespace {
 constexpr int kEvictThreads = 512;
 constexpr int kEvictWarps = kEvictThreads / 32;
 constexpr int kCacheUnits = kMaxEvictPages / 8 + 32;  // keys in shared memory: 160 KB
-constexpr int kDigits = 4, kBins = 256;               // of 8 bits each
 constexpr int kAhead = 4;                             // vectors of a thread in flight
 constexpr int kMaxCtas = 16;                          // of a cluster (more than 8 are opted in to)
 constexpr int kRowsAhead = 16;                        // masses of a lane in flight as they move
@@ -53,10 +53,15 @@ __device__ __forceinline__ float4 ld_float4(const float* p) {
   return make_float4(__uint_as_float(v.x), __uint_as_float(v.y), __uint_as_float(v.z), __uint_as_float(v.w));
 }
 
+template <bool CL>
 struct EvictShared {
-  uint32_t hist[kDigits][kBins];   // this CTA's, of each digit: one barrier of the cluster a digit
-  uint32_t total[kDigits][kBins];  // the cluster's
+  // CL: this CTA's counts of four digits of 8 bits (one barrier of the cluster a digit)
+  // and behind them the cluster's; one CTA: of digits of 11, 11 and 10 bits
+  static constexpr int kBins = CL ? 256 : 2048, kHists = CL ? 8 : 3;
+  uint32_t hist[kHists][kBins];
   uint32_t above, ties;        // this CTA's units above the threshold (or kept anyway), and at it
+  uint32_t digit, left, here;  // the threshold's digit, units still to be taken at it, and all units at it
+  uint32_t warp_sum[kEvictWarps];
   uint32_t warp_above[kEvictWarps], warp_ties[kEvictWarps];
   int32_t count;
 };
@@ -91,12 +96,42 @@ __device__ __forceinline__ float page_weight4(float4 v, int ps) {
   return plus(plus(v.x, v.z), plus(v.y, v.w));
 }
 
-template <bool PAGES>
+// The warp's inclusive sums.
+__device__ __forceinline__ uint32_t warp_sums(uint32_t x, int lane) {
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const uint32_t t = __shfl_up_sync(0xffffffffu, x, o);
+    if (lane >= o) x += t;
+  }
+  return x;
+}
+
+// Which of the digits highest, highest - 1, .. the left-th key has: n their counts,
+// *before the keys of higher digits (and of all above the one found), *here its count.
+template <int N>
+__device__ __forceinline__ uint32_t find_digit(const uint32_t (&n)[N], uint32_t highest, uint32_t left, uint32_t* before,
+                                               uint32_t* here) {
+  uint32_t d = highest;
+  *here = n[0];
+#pragma unroll
+  for (int k = 0; k + 1 < N; ++k)
+    if (d == highest - k && *before + n[k] < left) {
+      *before += n[k];
+      *here = n[k + 1];
+      --d;
+    }
+  return d;
+}
+
+// CL: a cluster of csize CTAs a sequence; else one CTA.
+template <bool PAGES, bool CL>
 __global__ void __launch_bounds__(kEvictThreads) evict_kernel(const __grid_constant__ EvictParams p, int csize) {
+  using Shared = EvictShared<CL>;
   extern __shared__ uint4 cache4[];
   uint32_t* cache = reinterpret_cast<uint32_t*>(cache4);
-  __shared__ __align__(16) EvictShared sh;
+  __shared__ __align__(16) Shared sh;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  if constexpr (!CL) csize = 1;
   const int b = blockIdx.x / csize, rank = blockIdx.x - b * csize;
   griddep_wait();
   const int L = ld_seq_len(p.seq_lens, b, p.max_len, rank == 0 && tid == 0 ? p.err : nullptr);
@@ -115,8 +150,8 @@ __global__ void __launch_bounds__(kEvictThreads) evict_kernel(const __grid_const
   const bool select = over && want > 0u;
   // ---- the keys of this stretch ----
   if (select) {
-    static_assert(2 * kDigits * kBins == 4 * kEvictThreads, "a vector a thread");
-    reinterpret_cast<uint4*>(sh.hist[0])[tid] = make_uint4(0u, 0u, 0u, 0u);  // and the totals behind
+    for (int i = tid; i < Shared::kHists * Shared::kBins / 4; i += kEvictThreads)
+      reinterpret_cast<uint4*>(sh.hist[0])[i] = make_uint4(0u, 0u, 0u, 0u);
     if constexpr (PAGES) {
       if (p.vec && ps >= 4 && ps <= 128) {
         const int pages = 128 / ps, lanes = ps / 4;  // of a warp's vectors
@@ -197,52 +232,62 @@ __global__ void __launch_bounds__(kEvictThreads) evict_kernel(const __grid_const
   uint32_t prefix = 0u, left = want;  // digits so far; units still to be found below them
   if (select) {
     const int a = max(lo, front), e = min(hi, back);
-    for (int pass = 0; pass < kDigits; ++pass) {
-      const int shift = 24 - 8 * pass;
+    for (int pass = 0; pass < (CL ? 4 : 3); ++pass) {
+      // the digit's lowest bit, and the one above its highest
+      const int shift = CL ? 24 - 8 * pass : max(0, 21 - 11 * pass), top = CL ? shift + 8 : (pass == 0 ? 32 : 32 - 11 * pass);
       uint32_t* hist = sh.hist[pass];
       each(a, e, [&](uint32_t k) {
-        if (((uint64_t)(k ^ prefix) >> (shift + 8)) == 0) atomicAdd(&hist[(k >> shift) & 255u], 1u);
+        if (((uint64_t)(k ^ prefix) >> top) == 0) atomicAdd(&hist[(k >> shift) & ((1u << (top - shift)) - 1u)], 1u);
       });
-      if (csize > 1) {
+      uint32_t here;
+      if constexpr (CL) {
         cluster_sync();
         // 64 threads to a CTA's histogram
+        uint32_t* total = sh.hist[4 + pass];
+        const int g = 31 - lane;
         for (int c = tid >> 6; c < csize; c += kEvictThreads / 64) {
-          const int g = 4 * (tid & 63);
-          const float4 x = ld_cluster4(map_rank(smem_u32(hist + g), c));
-          uint32_t* t = sh.total[pass] + g;
-          if (__float_as_uint(x.x) != 0u) atomicAdd(t, __float_as_uint(x.x));
-          if (__float_as_uint(x.y) != 0u) atomicAdd(t + 1, __float_as_uint(x.y));
-          if (__float_as_uint(x.z) != 0u) atomicAdd(t + 2, __float_as_uint(x.z));
-          if (__float_as_uint(x.w) != 0u) atomicAdd(t + 3, __float_as_uint(x.w));
+          const int at = 4 * (tid & 63);
+          const float4 x = ld_cluster4(map_rank(smem_u32(hist + at), c));
+          if (__float_as_uint(x.x) != 0u) atomicAdd(total + at, __float_as_uint(x.x));
+          if (__float_as_uint(x.y) != 0u) atomicAdd(total + at + 1, __float_as_uint(x.y));
+          if (__float_as_uint(x.z) != 0u) atomicAdd(total + at + 2, __float_as_uint(x.z));
+          if (__float_as_uint(x.w) != 0u) atomicAdd(total + at + 3, __float_as_uint(x.w));
         }
-        hist = sh.total[pass];
-      }
-      __syncthreads();
-      // each warp by itself: lane i has digits 8 (31 - i) .. + 7, the highest first
-      const int g = 31 - lane;
-      const uint4 n0 = reinterpret_cast<const uint4*>(hist)[2 * g], n1 = reinterpret_cast<const uint4*>(hist)[2 * g + 1];
-      const uint32_t n[8] = {n1.w, n1.z, n1.y, n1.x, n0.w, n0.z, n0.y, n0.x};
-      const uint32_t mine = n[0] + n[1] + n[2] + n[3] + n[4] + n[5] + n[6] + n[7];
-      uint32_t incl = mine;
-#pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const uint32_t t = __shfl_up_sync(0xffffffffu, incl, o);
-        if (lane >= o) incl += t;
-      }
-      uint32_t before = incl - mine, d = 8u * (uint32_t)g + 7u, here = n[0];
-#pragma unroll
-      for (int k = 0; k < 7; ++k)
-        if (d == 8u * (uint32_t)g + 7u - k && before + n[k] < left) {
-          before += n[k];
-          here = n[k + 1];
-          --d;
+        __syncthreads();
+        // each warp by itself: lane i has digits 8 (31 - i) .. + 7, the highest first
+        const uint4 n0 = reinterpret_cast<const uint4*>(total)[2 * g], n1 = reinterpret_cast<const uint4*>(total)[2 * g + 1];
+        const uint32_t n[8] = {n1.w, n1.z, n1.y, n1.x, n0.w, n0.z, n0.y, n0.x};
+        const uint32_t mine = n[0] + n[1] + n[2] + n[3] + n[4] + n[5] + n[6] + n[7];
+        const uint32_t incl = warp_sums(mine, lane);
+        uint32_t before = incl - mine, d = find_digit(n, 8u * (uint32_t)g + 7u, left, &before, &here);
+        // the first lane whose digits reach `left`
+        const int at = __ffs(__ballot_sync(0xffffffffu, incl >= left)) - 1;
+        prefix |= __shfl_sync(0xffffffffu, d, at) << shift;
+        left -= __shfl_sync(0xffffffffu, before, at);
+        here = __shfl_sync(0xffffffffu, here, at);
+      } else {
+        __syncthreads();
+        // thread i: digits 4 (511 - i) .. + 3, the highest first
+        const int g = kEvictThreads - 1 - tid;
+        const uint4 v = reinterpret_cast<const uint4*>(hist)[g];
+        const uint32_t n[4] = {v.w, v.z, v.y, v.x};
+        const uint32_t mine = v.x + v.y + v.z + v.w;
+        uint32_t incl = warp_sums(mine, lane);
+        if (lane == 31) sh.warp_sum[warp] = incl;
+        __syncthreads();
+        for (int w = 0; w < warp; ++w) incl += sh.warp_sum[w];
+        uint32_t before = incl - mine;
+        if (incl >= left && before < left) {  // one thread
+          sh.digit = find_digit(n, 4u * (uint32_t)g + 3u, left, &before, &here);
+          sh.left = left - before;
+          sh.here = here;
         }
-      // the first lane whose digits reach `left` (the last one, where none would)
-      const unsigned reach = __ballot_sync(0xffffffffu, incl >= left);
-      const int at = reach != 0u ? __ffs(reach) - 1 : 31;
-      prefix |= __shfl_sync(0xffffffffu, d, at) << shift;
-      left -= __shfl_sync(0xffffffffu, before, at);
-      if (__shfl_sync(0xffffffffu, here, at) == left && prefix != 0u) {
+        __syncthreads();
+        prefix |= sh.digit << shift;
+        left = sh.left;
+        here = sh.here;
+      }
+      if (here == left && prefix != 0u) {
         --prefix;  // every key that begins with these digits stays: no more of them are needed
         left = 0u;
         break;
@@ -305,9 +350,9 @@ __global__ void __launch_bounds__(kEvictThreads) evict_kernel(const __grid_const
     n = __reduce_add_sync(0xffffffffu, n);
     if (lane == 0 && n != 0) atomicAdd(&sh.count, n);
   }
-  if (csize > 1) cluster_sync(); else __syncthreads();
+  if constexpr (CL) cluster_sync(); else __syncthreads();
   uint32_t above = 0u, ties = 0u, all_above = 0u;
-  if (csize > 1) {
+  if constexpr (CL) {
     // lane c reads the counts of CTA c (above and ties lie side by side)
     const float2 v = lane < csize ? ld_cluster2(map_rank(smem_u32(&sh.above), lane)) : make_float2(0.f, 0.f);
     const uint32_t x = lane < csize ? __float_as_uint(v.x) : 0u, y = lane < csize ? __float_as_uint(v.y) : 0u;
@@ -416,7 +461,7 @@ __global__ void __launch_bounds__(kEvictThreads) evict_kernel(const __grid_const
       p.new_block_table[(int64_t)b * p.max_blocks + i] = ld_input(p.block_table + (int64_t)b * p.max_blocks + i);
     if (rank == 0 && tid == 0) p.new_seq_lens[b] = new_len;
   }
-  if (csize > 1) cluster_sync();  // no CTA leaves while another reads its counts
+  if constexpr (CL) cluster_sync();  // no CTA leaves while another reads its counts
 }
 
 }  // namespace
@@ -435,7 +480,8 @@ cudaError_t launch_evict(const EvictParams& p, bool pages, int num_sms, cudaStre
   while (csize < kMaxCtas && units > (int64_t)csize * (kCacheUnits - 32)) csize *= 2;
   const int64_t stretch = (units + csize - 1) / csize + 32;
   const int smem = (int)(stretch < kCacheUnits ? stretch : kCacheUnits) * 4 + 16;
-  auto kern = pages ? evict_kernel<true> : evict_kernel<false>;
+  auto kern = csize > 1 ? (pages ? evict_kernel<true, true> : evict_kernel<false, true>)
+                        : (pages ? evict_kernel<true, false> : evict_kernel<false, false>);
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kCacheUnits * 4 + 16);
   if (e == cudaSuccess && csize > 8) e = cudaFuncSetAttribute(kern, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
   if (e != cudaSuccess) return e;
