@@ -219,10 +219,17 @@ __global__ void __launch_bounds__(kEvictThreads) evict_kernel(const __grid_const
     for (int i = tid; i < vecs; i += kEvictThreads) {
       const uint4 k = cache4[i];
       const int u = lo + 4 * i;
-      if (u >= a && u < e) f(k.x);
-      if (u + 1 >= a && u + 1 < e) f(k.y);
-      if (u + 2 >= a && u + 2 < e) f(k.z);
-      if (u + 3 >= a && u + 3 < e) f(k.w);
+      if (u >= a && u + 3 < e) {
+        f(k.x);
+        f(k.y);
+        f(k.z);
+        f(k.w);
+      } else {
+        if (u >= a && u < e) f(k.x);
+        if (u + 1 >= a && u + 1 < e) f(k.y);
+        if (u + 2 >= a && u + 2 < e) f(k.z);
+        if (u + 3 >= a && u + 3 < e) f(k.w);
+      }
     }
     for (int u = max(a, lo + cached) + tid; u < e; u += kEvictThreads) f(order_key(ld_float(mass + u)));
   };
@@ -298,6 +305,7 @@ __global__ void __launch_bounds__(kEvictThreads) evict_kernel(const __grid_const
   // a warp walks a stretch of its own, 32 units at a time
   const int wper = (((hi - lo) + kEvictWarps - 1) / kEvictWarps + 31) / 32 * 32;
   const int wlo = min(hi, lo + warp * wper), whi = min(hi, wlo + wper);
+  const bool inside = select && wlo >= front && whi <= back;  // the key alone says whether a unit stays
   auto classify = [&](int u, uint32_t k, bool* above, bool* tie) {
     const bool may = select && u >= front && u < back;
     *above = u < whi && (may ? k > prefix : u < front || u >= back);
@@ -318,10 +326,15 @@ __global__ void __launch_bounds__(kEvictThreads) evict_kernel(const __grid_const
     for (int i = (wlo - lo + 3) / 4 + lane; 4 * i < whi - lo; i += 32) {  // wlo: a multiple of 32 past lo, or hi
       const uint4 k = cache4[i];
       const int u = lo + 4 * i;
-      count(u, k.x);
-      count(u + 1, k.y);
-      count(u + 2, k.z);
-      count(u + 3, k.w);
+      if (inside && u + 3 < whi) {
+        n_above += (k.x > prefix ? 1u : 0u) + (k.y > prefix ? 1u : 0u) + (k.z > prefix ? 1u : 0u) + (k.w > prefix ? 1u : 0u);
+        n_ties += (k.x == prefix ? 1u : 0u) + (k.y == prefix ? 1u : 0u) + (k.z == prefix ? 1u : 0u) + (k.w == prefix ? 1u : 0u);
+      } else {
+        count(u, k.x);
+        count(u + 1, k.y);
+        count(u + 2, k.z);
+        count(u + 3, k.w);
+      }
     }
   } else {
     for (int u = wlo + lane; u < whi; u += 32) count(u, key(u));
@@ -435,6 +448,21 @@ __global__ void __launch_bounds__(kEvictThreads) evict_kernel(const __grid_const
       float v[kRowsAhead];
 #pragma unroll
       for (int k = 0; k < kRowsAhead; ++k) v[k] = u0 + 32 * k + lane < whi ? ld_float(mass + u0 + 32 * k + lane) : 0.f;
+      if (inside && left == 0u) {  // and no tie does
+#pragma unroll
+        for (int k = 0; k < kRowsAhead; ++k) {
+          const int u = u0 + 32 * k + lane;
+          const bool stays = u < whi && order_key(v[k]) > prefix;
+          const unsigned m = __ballot_sync(0xffffffffu, stays);
+          const uint32_t r = above + __popc(m & ((1u << lane) - 1u));
+          above += __popc(m);
+          if (stays) {
+            new_mass[r] = v[k];
+            p.keep[list + (int)r - p.num_sinks] = u;
+          }
+        }
+        continue;
+      }
 #pragma unroll
       for (int k = 0; k < kRowsAhead; ++k) {
         uint32_t before;
