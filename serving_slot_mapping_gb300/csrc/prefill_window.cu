@@ -1082,8 +1082,13 @@ __global__ void __launch_bounds__(WCfg<D, KV8, SC>::kThreads, 1)
         };
         float tmax = -INFINITY;
         uint32_t v[kHeld][32];
+        const bool by_load = SC && !masked;  // the loads find the max: less code in the loop, and fewer registers
+        if (by_load) {
 #pragma unroll 1
-        for (int first = 0; first < 4; first += kHeld) {
+          for (int cb = 0; cb < 4; ++cb) tmax = fmaxf(tmax, tmem_max32(s_col + cb * 32));
+        }
+#pragma unroll 1
+        for (int first = by_load ? 4 : 0; first < 4; first += kHeld) {
           load(v, first, kHeld);
           float mx[kHeld];
 #pragma unroll
