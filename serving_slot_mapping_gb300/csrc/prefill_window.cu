@@ -767,7 +767,7 @@ __global__ void __launch_bounds__(WCfg<D, KV8, SC>::kThreads, 1)
       // ======================= int8 -> f16 converters (warps 12 .. 15) =======================
       const int part = warp - (16 - kI8Warps);
       int ct = 0;  // tiles of codes taken
-      constexpr int kChunks = D / 16, kKeysPerLoad = 32 / kChunks, kLoads = 8 / kKeysPerLoad;
+      constexpr int kChunks = D / 16, kKeysPerLoad = 32 / kChunks, kLoads = 8 / kKeysPerLoad, kAtOnce = 2 / kLoads;
       const int q4 = lane >> 3, j8 = lane & 7;  // (bank-conflict-free as in convert_tile_e4m3)
       const int m = D == 128 ? (j8 & 3) + 4 * (j8 >> 2) : lane % kChunks;
       const int r0 = D == 128 ? 2 * (q4 >> 1) + ((j8 >> 2) ^ (q4 & 1)) : lane / kChunks;
@@ -778,30 +778,31 @@ __global__ void __launch_bounds__(WCfg<D, KV8, SC>::kThreads, 1)
         if (t >= n && alive)  // the products on the slot's last tile are done
           alive = mbar_wait(bar((isv ? W_VEMPTY : W_KEMPTY) + sl), (uint32_t)((t / n - 1) & 1), p.err);
         const volatile uint16_t* ratios = (isv ? scale_ring[t % kScaleTiles].v : scale_ring[t % kScaleTiles].k) + part * 2;
-        // this warp's quarter of the tile: four 8-key blocks, two (of one scale) at a time
+        // this warp's quarter of the tile: four 8-key blocks, two loads of a lane at a time (four
+        // were more code than the instruction cache has room for: 762 us where these take 702)
         const unsigned char* codes = smem + C::kCodeOff + stage * C::kCodeTile + (part * 32 + r0) * D + m * 16;
         unsigned char* slot = smem + (isv ? C::kVRing : C::kKOff) + sl * C::kKVTile + part * 4 * C::kRowBlock;
 #pragma unroll 1
-        for (int k2 = 0; k2 < 2; ++k2) {
-          uint4 raw[2][kLoads];
+        for (int k0 = 0; k0 < 4; k0 += kAtOnce) {
+          uint4 raw[kAtOnce][kLoads];
 #pragma unroll
-          for (int kb = 0; kb < 2; ++kb)
+          for (int kb = 0; kb < kAtOnce; ++kb)
 #pragma unroll
             for (int x = 0; x < kLoads; ++x)
-              raw[kb][x] = *reinterpret_cast<const uint4*>(codes + ((2 * k2 + kb) * 8 + x * kKeysPerLoad) * D);
-          const uint32_t two = (uint32_t)ratios[k2] * 0x10001u;
+              raw[kb][x] = *reinterpret_cast<const uint4*>(codes + ((k0 + kb) * 8 + x * kKeysPerLoad) * D);
+          const uint32_t two = (uint32_t)ratios[k0 >> 1] * 0x10001u;
           const __half2 f = *reinterpret_cast<const __half2*>(&two);
           auto both = [&](uint32_t c) {
             const __half2 v = __hmul2(*reinterpret_cast<const __half2*>(&c), f);
             return *reinterpret_cast<const uint32_t*>(&v);
           };
 #pragma unroll
-          for (int kb = 0; kb < 2; ++kb)
+          for (int kb = 0; kb < kAtOnce; ++kb)
 #pragma unroll
             for (int x = 0; x < kLoads; ++x) {
               const int kr = r0 + x * kKeysPerLoad;
               const uint4 w = raw[kb][x];
-              unsigned char* blk = slot + (2 * k2 + kb) * C::kRowBlock + kr * 128;
+              unsigned char* blk = slot + (k0 + kb) * C::kRowBlock + kr * 128;
               const int c0 = 2 * m, c1 = 2 * m + 1;  // 8-dim chunks over D
               *reinterpret_cast<uint4*>(blk + (c0 >> 3) * 1024 + (((c0 & 7) ^ kr) << 4)) =
                   make_uint4(both(i8x2_to_f16x2<0, 1>(w.x)), both(i8x2_to_f16x2<2, 3>(w.x)),
