@@ -1083,7 +1083,10 @@ __global__ void __launch_bounds__(WCfg<D, KV8, SC>::kThreads, 1)
         };
         float tmax = -INFINITY;
         uint32_t v[kHeld][32];
-        const bool by_load = SC && !masked;  // the loads find the max: less code in the loop, and fewer registers
+        // The loads find the max where nothing is masked: less code again (heads of 64: 661 -> 592
+        // us).  Max and P in one pass, done again where the reference moves, needs P held in
+        // registers and the loop written out: 1239 us for 770.
+        const bool by_load = SC && !masked;
         if (by_load) {
 #pragma unroll 1
           for (int cb = 0; cb < 4; ++cb) tmax = fmaxf(tmax, tmem_max32(s_col + cb * 32));
