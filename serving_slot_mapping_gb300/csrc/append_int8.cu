@@ -35,8 +35,9 @@ constexpr int kAppendWarps = 4;
 // The rounded quotient of x by the block's scale, in the low byte: RN(x / s) by the
 // reciprocal y = RN(1 / s) and one correction of the product with its remainder
 // (Markstein's division), then rounding to an integer by adding 1.5 2^23, whose low bits
-// the integer is in.  The same as the division's code for every 24-bit scale and every
-// bf16 value up to 127.5 scales (compared on the GPU, all of them).  Not for NaN.
+// the integer is in.  The same as the division's code for bf16 values of less than 127.5
+// scales (the tests compare every quotient of a new block, and a sample of the scales of
+// blocks in use); 127.5 itself is a tie that would become 128.  Not for NaN.
 __device__ __forceinline__ uint32_t code_of(float x, float s, float y) {
   const float q = __fmul_rn(x, y);
   return __float_as_uint(__fadd_rn(__fmaf_rn(__fmaf_rn(-s, q, x), y, q), 12582912.f));
@@ -231,8 +232,8 @@ __global__ void __launch_bounds__(kAppendWarps * 32, 6) append_int8_kernel(const
       a = team_max(a);
     }
     const float s = fmaxf(old, clamp_scale(__fdiv_rn(a, 127.f)));
-    // a finite value past 127.5 scales needs saturating too: above the largest scale
-    const bool fast = plain && a <= 127.5f * kScaleMax;
+    // values of 127.5 scales and more, which the largest scale leaves, need saturating too
+    const bool fast = plain && a < 127.5f * kScaleMax;
     const float y = __frcp_rn(s);
     if (!fresh && s > old) {
       const float ratio = __fdiv_rn(old, s);
