@@ -594,9 +594,9 @@ pa_status paged_kv_append_int8(const pa_kv_pool* pool, const pa_kv_scales* scale
  * paged_attention_decode / paged_attention_prefill over an int8 pool: the
  * attention of the values that the codes stand for.  Products are f16 with fp32
  * sums: the codes are exact, the queries are rounded to f16 (exact for bf16 values
- * of magnitude 2^-14 .. 65504, their largest), the softmax weights too; the prefill
- * also rounds each code times its scale, relative to the largest scale of its tile
- * of 128 keys, to f16.  The keys of a page that is out of range take no part.
+ * of magnitude 2^-14 .. 65504, their largest), and so is each softmax weight times
+ * its V scale, relative to the largest such product among the keys that the row sees.
+ * The keys of a page that is out of range take no part.
  * out is 8-byte aligned (decode), q and out are 16-byte aligned (prefill).  Every
  * other argument, limit, the workspace (dtype PA_DTYPE_INT8) and the results are
  * those of the plain calls.

@@ -30,16 +30,21 @@
 // up; slots of loaded pages that no row of the sequence sees (between the sinks
 // and the sequence's first window key, or at and past L_b) are zeroed in V.
 // int8 pools (SC; paged_attention_prefill_int8, a window that reaches every key): the
-// codes land as they are, in stages of their own.  A tile's 16-key blocks each have a scale; with R the
-// largest of the tile, for K and for V:
-// * warp 10 looks the scales up ahead and hands out, per tile, the f16 ratios s / R
-//   of the 8 blocks and R_k, log2 R_v, 1 / R_v (a ring of four tiles);
+// codes land as they are, in stages of their own, and become f16 exactly.  A tile's 16-key
+// blocks each have a scale for K and one for V, k and v, which reach a row only through
+// the columns that it sees:
+// * warp 10 looks the scales up ahead and hands out, per tile, {scale * k, log2 v, 1 / v}
+//   of its 8 blocks (a ring of four tiles);
 // * four converter warps take the tiles in the order that the products ask for them,
-//   K(0), then K(t + 1), V(t), and write f16(code * ratio) (code exact, ratio and
-//   product rounded: 2^-10 of a value at most, beside 2^-8 of its own rounding to 8 bits);
-// * R_k goes into the factor of S that the softmax has anyway, log2 R_v into the
-//   reference max (y = x + log2 R_v; P = 2^(y - m) stays in f16's range whatever the
-//   scales are), and l sums P / R_v.  No work is added for an element of S.
+//   K(0), then K(t + 1), V(t);
+// * k goes into the factor of S that the softmax has anyway, log2 v into the exponent, as
+//   in decode_split.cuh: y = x + log2 v, the reference max m follows y, P = 2^(y - m)
+//   stays in f16's range whatever the scales of the visible blocks are, and l sums P / v.
+//   y is rounded before m is taken off it, so that the largest P is 1 however large the
+//   scores are: an addition for two elements of S, beside the fused multiply-add (8 chunks
+//   of 512-2048 after 0-8192 tokens, 32 / 8 heads of 128: 933 us, without it 919).
+//   (Scales multiplied into the codes, relative to their tile's largest, took 948 us there,
+//   and cost a row its keys' last bits for the sake of blocks that it does not see.)
 // Sixteen warps for that: 2 x 144 + 2 x 112 registers a thread, and the softmax in loops
 // of 32 columns: written out, it and the conversion did not fit in the instruction cache.
 // A block_table entry out of range is noted by the TMA warp; a CTA that met one
@@ -61,7 +66,7 @@ constexpr int kItems = 4;        // items whose geometry is in shared memory
 constexpr int kItemBytes = 52;
 constexpr int kWBars = 40;
 constexpr int kScaleTiles = 4;   // int8: tiles whose scales are in shared memory
-constexpr int kScaleBytes = 48;
+constexpr int kScaleBytes = 128;
 constexpr int kI8Warps = 4;      // int8: converter warps 12 .. 15; warp 10 hands out items and scales
 
 enum { W_QFULL = 0, W_KFULL = W_QFULL + kQT, W_KEMPTY = W_KFULL + kNSK, W_VFULL = W_KEMPTY + kNSK,
@@ -84,7 +89,9 @@ struct WCfg : PCfg<D, KV8> {
   static_assert(SC ? 2 * kSoftmaxRegs + 2 * kOtherRegs <= 4 * 128 : 2 * kSoftmaxRegs + kOtherRegs <= 3 * 168,
                 "more registers than the launch has");
   // 8 tiles in flight: {KV head, valid, hid0, hid1} after the first slots of their boxes
-  static constexpr int kMetaOff = Base::kPageOff + 8 * 32 * 4;
+  // (int8: pages of 16 slots or more, so 8 boxes at most)
+  static constexpr int kBoxes = SC ? 8 : 32;
+  static constexpr int kMetaOff = Base::kPageOff + 8 * kBoxes * 4;
   static constexpr int kItemOff = kMetaOff + 8 * 16;
   static constexpr int kWBarOff = kItemOff + kItems * kItemBytes;
   static constexpr int kTmemOff = kWBarOff + kWBars * 8;  // the word that tcgen05.alloc writes, behind every barrier
@@ -136,12 +143,9 @@ struct Item {
 };
 static_assert(sizeof(Item) == kItemBytes, "ring entry");
 
-// int8: the scales of a key tile, relative to their largest.
+// int8: the scales of a key tile, for each 16 keys.
 struct TileScales {
-  uint16_t k[8], v[8];  // f16, of each 16 keys
-  float k_ref;          // below 0: there is no such tile, nor any after it
-  float v_log2, v_inv;  // log2 of V's reference, and 1 / 2^v_log2
-  float pad;
+  float4 of[8];  // factor of S (the first one below 0: no such tile, nor any after it), log2 v, 1 / 2^(log2 v), 0
 };
 static_assert(sizeof(TileScales) == kScaleBytes, "ring entry");
 
@@ -439,11 +443,11 @@ __global__ void __launch_bounds__(WCfg<D, KV8, SC>::kThreads, 1)
   const uint32_t bars = smem_u32(smem + C::kWBarOff);
   auto bar = [&](int i) { return bars + 8u * i; };
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + C::kTmemOff);
-  int* slot_ring = reinterpret_cast<int*>(smem + C::kPageOff);  // [8 tiles][32 lanes] first slot of each box, -1: none
+  int* slot_ring = reinterpret_cast<int*>(smem + C::kPageOff);  // [8 tiles][kBoxes] first slot of each box, -1: none
   volatile Item* item_ring = reinterpret_cast<volatile Item*>(smem + C::kItemOff);
   int4* meta = reinterpret_cast<int4*>(smem + C::kMetaOff);     // [8 tiles] {KV head, valid, hid0, hid1}
 
-  volatile TileScales* scale_ring = reinterpret_cast<volatile TileScales*>(smem + C::kScaleOff);
+  TileScales* scale_ring = reinterpret_cast<TileScales*>(smem + C::kScaleOff);
   volatile int* bad_page = reinterpret_cast<volatile int*>(smem + C::kBadOff);
 
   if (tid == 0) {
@@ -609,7 +613,7 @@ __global__ void __launch_bounds__(WCfg<D, KV8, SC>::kThreads, 1)
             slot = (int)(((int64_t)raw << pshift) + (key & (ps - 1)));
           }
         }
-        slot_ring[(kt & 7) * 32 + lane] = slot;
+        if (lane < C::kBoxes) slot_ring[(kt & 7) * C::kBoxes + lane] = slot;
         if (lane == 0) {
           const int l0 = it.base + j * kBN;  // rows of the tile: valid ones, and those no row of the sequence sees
           const int end = it.seq_start <= it.head_keys ? it.seq_start : max(it.head_keys, it.seq_start - it.gap);
@@ -626,7 +630,8 @@ __global__ void __launch_bounds__(WCfg<D, KV8, SC>::kThreads, 1)
       }
       if constexpr (SC) {
         if (v_turn) {
-          issue(&tmap_v, code_dst, meta[vt & 7].x, slot_ring[(vt & 7) * 32 + lane], bar(W_KFULL + stage));
+          issue(&tmap_v, code_dst, meta[vt & 7].x, lane < C::kBoxes ? slot_ring[(vt & 7) * C::kBoxes + lane] : -1,
+                bar(W_KFULL + stage));
           ++vt;
           progressed = true;
         }
@@ -636,7 +641,7 @@ __global__ void __launch_bounds__(WCfg<D, KV8, SC>::kThreads, 1)
         const bool clear = !KV8 && (m.y < kBN || m.z < m.w);
         if (!clear || land_slot < 0) {
           const int s = vt % kNSV;
-          issue(&tmap_v, v_base + s * C::kKVTile, m.x, slot_ring[(vt & 7) * 32 + lane],
+          issue(&tmap_v, v_base + s * C::kKVTile, m.x, slot_ring[(vt & 7) * C::kBoxes + lane],
                 bar(clear ? (int)W_VLAND : W_VFULL + s));
           if (clear) {
             land_slot = s;
@@ -698,15 +703,14 @@ __global__ void __launch_bounds__(WCfg<D, KV8, SC>::kThreads, 1)
       const int per = 1 << p.scale_shift;                   // tokens of a scale: 16 or more
       const int lanes = per < kBN ? kBN / per : 1;          // scales of a tile
       int kt = 0;
-      auto hand_out = [&](const TileScales& t) {            // lane 0's
+      auto hand_out = [&](float4 mine) {                    // lanes 0 .. 7: of a block each
         const int s = kt % kScaleTiles;
-        if (kt >= kScaleTiles && alive)
+        if (kt >= kScaleTiles && alive)  // each lane writes, so each waits
           alive = mbar_wait(bar(W_CEMPTY + s), (uint32_t)((kt / kScaleTiles - 1) & 1), p.err);
-        volatile TileScales* e = scale_ring + s;
-#pragma unroll
-        for (int i = 0; i < kScaleBytes / 4; ++i)
-          reinterpret_cast<volatile uint32_t*>(e)[i] = reinterpret_cast<const uint32_t*>(&t)[i];
-        mbar_arrive(bar(W_CFULL + s));
+        alive = __all_sync(0xffffffffu, alive);
+        if (lane < 8) scale_ring[s].of[lane] = mine;
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar(W_CFULL + s));
       };
       // an item ahead of the scales: the others take the next item before they begin one
       Item nx = {};
@@ -725,7 +729,7 @@ __global__ void __launch_bounds__(WCfg<D, KV8, SC>::kThreads, 1)
         int page = x.nt() > 0 ? page_of(0) : -1;
         for (int j = 0; j < x.nt(); ++j, ++kt) {
           const int l = x.base + j * kBN + lane * per, key = l < x.head_keys ? l : l + x.gap;
-          float ks = 0.f, vs = 0.f;
+          float ks = kScaleMin, vs = kScaleMin;  // (no key, or a page out of range: any value)
           if (page >= 0 && page < p.pool.num_pages) {
             const int64_t slot = ((int64_t)page << pshift) + (key & (ps - 1));
             const int64_t c = (slot >> p.scale_shift) * p.pool.num_kv_heads + x.hk;
@@ -733,35 +737,15 @@ __global__ void __launch_bounds__(WCfg<D, KV8, SC>::kThreads, 1)
             vs = clamp_scale(__uint_as_float(ld_input(reinterpret_cast<const uint32_t*>(p.value_scales) + c)));
           }
           if (j + 1 < x.nt()) page = page_of(j + 1);
-          float kr = ks, vr = vs;
-#pragma unroll
-          for (int o = 4; o > 0; o >>= 1) {  // eight lanes at most have one
-            kr = fmaxf(kr, __shfl_xor_sync(0xffffffffu, kr, o));
-            vr = fmaxf(vr, __shfl_xor_sync(0xffffffffu, vr, o));
-          }
-          kr = fmaxf(kr, kScaleMin);
-          vr = fmaxf(vr, kScaleMin);
-          const unsigned mine = (uint32_t)__half_as_ushort(__float2half_rn(ks / kr)) |
-                                ((uint32_t)__half_as_ushort(__float2half_rn(vs / vr)) << 16);
-          TileScales t;
-#pragma unroll
-          for (int k = 0; k < 8; ++k) {
-            const unsigned w = __shfl_sync(0xffffffffu, mine, (k * 16) >> p.scale_shift);
-            t.k[k] = (uint16_t)(w & 0xFFFFu);
-            t.v[k] = (uint16_t)(w >> 16);
-          }
-          t.k_ref = kr;
-          t.v_log2 = __log2f(vr);
-          t.v_inv = fast_exp2(-t.v_log2);  // of the very power that P carries
-          t.pad = 0.f;
-          if (lane == 0) hand_out(t);
-          alive = __shfl_sync(0xffffffffu, alive ? 1 : 0, 0) != 0;
+          const int from = ((lane & 7) * 16) >> p.scale_shift;  // the lane with the scales of block `lane`
+          const float v_log2 = __log2f(__shfl_sync(0xffffffffu, vs, from));
+          // (a factor of 0 would make NaN of a masked column)
+          hand_out(make_float4(fmaxf(sl2 * __shfl_sync(0xffffffffu, ks, from), 0x1p-126f), v_log2,
+                               fast_exp2(-v_log2), 0.f));  // the inverse of the very power that P carries
           if (!alive) break;
         }
       }
-      TileScales t = {};
-      t.k_ref = -1.f;
-      if (lane == 0) hand_out(t);
+      hand_out(make_float4(-1.f, 0.f, 0.f, 0.f));
     }
     if (warp >= 16 - kI8Warps) {
       // ======================= int8 -> f16 converters (warps 12 .. 15) =======================
@@ -777,7 +761,6 @@ __global__ void __launch_bounds__(WCfg<D, KV8, SC>::kThreads, 1)
         ++ct;
         if (t >= n && alive)  // the products on the slot's last tile are done
           alive = mbar_wait(bar((isv ? W_VEMPTY : W_KEMPTY) + sl), (uint32_t)((t / n - 1) & 1), p.err);
-        const volatile uint16_t* ratios = (isv ? scale_ring[t % kScaleTiles].v : scale_ring[t % kScaleTiles].k) + part * 2;
         // this warp's quarter of the tile: four 8-key blocks, two loads of a lane at a time (four
         // were more code than the instruction cache has room for: 762 us where these take 702)
         const unsigned char* codes = smem + C::kCodeOff + stage * C::kCodeTile + (part * 32 + r0) * D + m * 16;
@@ -790,12 +773,6 @@ __global__ void __launch_bounds__(WCfg<D, KV8, SC>::kThreads, 1)
 #pragma unroll
             for (int x = 0; x < kLoads; ++x)
               raw[kb][x] = *reinterpret_cast<const uint4*>(codes + ((k0 + kb) * 8 + x * kKeysPerLoad) * D);
-          const uint32_t two = (uint32_t)ratios[k0 >> 1] * 0x10001u;
-          const __half2 f = *reinterpret_cast<const __half2*>(&two);
-          auto both = [&](uint32_t c) {
-            const __half2 v = __hmul2(*reinterpret_cast<const __half2*>(&c), f);
-            return *reinterpret_cast<const uint32_t*>(&v);
-          };
 #pragma unroll
           for (int kb = 0; kb < kAtOnce; ++kb)
 #pragma unroll
@@ -805,11 +782,11 @@ __global__ void __launch_bounds__(WCfg<D, KV8, SC>::kThreads, 1)
               unsigned char* blk = slot + (k0 + kb) * C::kRowBlock + kr * 128;
               const int c0 = 2 * m, c1 = 2 * m + 1;  // 8-dim chunks over D
               *reinterpret_cast<uint4*>(blk + (c0 >> 3) * 1024 + (((c0 & 7) ^ kr) << 4)) =
-                  make_uint4(both(i8x2_to_f16x2<0, 1>(w.x)), both(i8x2_to_f16x2<2, 3>(w.x)),
-                             both(i8x2_to_f16x2<0, 1>(w.y)), both(i8x2_to_f16x2<2, 3>(w.y)));
+                  make_uint4(i8x2_to_f16x2<0, 1>(w.x), i8x2_to_f16x2<2, 3>(w.x), i8x2_to_f16x2<0, 1>(w.y),
+                             i8x2_to_f16x2<2, 3>(w.y));
               *reinterpret_cast<uint4*>(blk + (c1 >> 3) * 1024 + (((c1 & 7) ^ kr) << 4)) =
-                  make_uint4(both(i8x2_to_f16x2<0, 1>(w.z)), both(i8x2_to_f16x2<2, 3>(w.z)),
-                             both(i8x2_to_f16x2<0, 1>(w.w)), both(i8x2_to_f16x2<2, 3>(w.w)));
+                  make_uint4(i8x2_to_f16x2<0, 1>(w.z), i8x2_to_f16x2<2, 3>(w.z), i8x2_to_f16x2<0, 1>(w.w),
+                             i8x2_to_f16x2<2, 3>(w.w));
             }
         }
         __syncwarp();
@@ -821,7 +798,7 @@ __global__ void __launch_bounds__(WCfg<D, KV8, SC>::kThreads, 1)
       auto there = [&](int t) {  // the tile exists (its scales are handed out)
         const int s = t % kScaleTiles;
         if (alive) alive = mbar_wait(bar(W_CFULL + s), (uint32_t)((t / kScaleTiles) & 1), p.err);
-        return alive && scale_ring[s].k_ref >= 0.f;
+        return alive && scale_ring[s].of[0].x >= 0.f;
       };
       int kt = 0, vt = 0;
       bool ended = false;
@@ -832,14 +809,9 @@ __global__ void __launch_bounds__(WCfg<D, KV8, SC>::kThreads, 1)
           isv = true;
         }
         if (isv && vt == kt) break;
+        if (!isv && lane == 0) mbar_arrive(bar(W_CEMPTY + kt % kScaleTiles));  // that it exists is all that is read
         tile(isv ? vt : kt, isv);
-        if (isv) {
-          __syncwarp();
-          if (lane == 0) mbar_arrive(bar(W_CEMPTY + vt % kScaleTiles));
-          ++vt;
-        } else {
-          ++kt;
-        }
+        if (isv) ++vt; else ++kt;
       }
     }
   }
@@ -1040,15 +1012,15 @@ __global__ void __launch_bounds__(WCfg<D, KV8, SC>::kThreads, 1)
       const int pos_max = it.first + (min(it.row0 + (t + 1) * kBM, rows) - 1) / G;
       const int wlo_max = max(0, max(0, pos_max) - p.window + 1) - it.gap;
       float m_ref = -INFINITY, l = 0.f;
-      float f = sl2, lv = 0.f, iv = 1.f;  // SC: the tile's factor of S, log2 of V's reference and its inverse
+      const float4* of = nullptr;  // SC: the tile's scales, of each 16 columns
       auto take_scales = [&]() {
         const int s = cn % kScaleTiles;
         if (alive) alive = mbar_wait(bar(W_CFULL + s), (uint32_t)((cn / kScaleTiles) & 1), p.err);
-        f = sl2 * scale_ring[s].k_ref;
-        lv = scale_ring[s].v_log2;
-        iv = scale_ring[s].v_inv;
+        of = scale_ring[s].of;
+      };
+      auto leave_scales = [&]() {
         __syncwarp();
-        if (lane == 0) mbar_arrive(bar(W_CEMPTY + s));
+        if (lane == 0) mbar_arrive(bar(W_CEMPTY + cn % kScaleTiles));
         ++cn;
       };
       for (int j = 0; j < ntt; ++j) {
@@ -1089,28 +1061,45 @@ __global__ void __launch_bounds__(WCfg<D, KV8, SC>::kThreads, 1)
         const bool by_load = SC && !masked;
         if (by_load) {
 #pragma unroll 1
-          for (int cb = 0; cb < 4; ++cb) tmax = fmaxf(tmax, tmem_max32(s_col + cb * 32));
+          for (int cb = 0; cb < 4; ++cb) {
+            const float2 c0 = *reinterpret_cast<const float2*>(of + 2 * cb), c1 = *reinterpret_cast<const float2*>(of + 2 * cb + 1);
+            const float2 x = tmem_max16x2(s_col + cb * 32);
+            tmax = max3(tmax, fmaf(x.x, c0.x, c0.y), fmaf(x.y, c1.x, c1.y));
+          }
         }
 #pragma unroll 1
         for (int first = by_load ? 4 : 0; first < 4; first += kHeld) {
           load(v, first, kHeld);
-          float mx[kHeld];
+          if constexpr (SC) {
 #pragma unroll
-          for (int i = 0; i < kHeld; ++i) {
-            float& x = mx[i];
-            x = __uint_as_float(v[i][0]);
+            for (int h = 0; h < 2; ++h) {
+              const uint32_t* c = v[0] + 16 * h;
+              float x = __uint_as_float(c[0]);
 #pragma unroll
-            for (int e = 1; e < 31; e += 2) x = max3(x, __uint_as_float(v[i][e]), __uint_as_float(v[i][e + 1]));
-            x = fmaxf(x, __uint_as_float(v[i][31]));
+              for (int e = 1; e < 15; e += 2) x = max3(x, __uint_as_float(c[e]), __uint_as_float(c[e + 1]));
+              x = fmaxf(x, __uint_as_float(c[15]));
+              tmax = fmaxf(tmax, fmaf(x, of[2 * first + h].x, of[2 * first + h].y));
+            }
+          } else {
+            float mx[kHeld];
+#pragma unroll
+            for (int i = 0; i < kHeld; ++i) {
+              float& x = mx[i];
+              x = __uint_as_float(v[i][0]);
+#pragma unroll
+              for (int e = 1; e < 31; e += 2) x = max3(x, __uint_as_float(v[i][e]), __uint_as_float(v[i][e + 1]));
+              x = fmaxf(x, __uint_as_float(v[i][31]));
+            }
+#pragma unroll
+            for (int i = 0; i < kHeld; ++i) tmax = fmaxf(tmax, mx[i]);
           }
-#pragma unroll
-          for (int i = 0; i < kHeld; ++i) tmax = fmaxf(tmax, mx[i]);
         }
-        tmax = SC ? fmaf(tmax, f, lv) : tmax * sl2;
+        if constexpr (!SC) tmax *= sl2;
         // reference max: moved only when the row max grows by more than 2^8
         float alpha = 1.f;
         bool rescale = false;
-        if (tmax > m_ref + kRescaleThreshold) {
+        // (int8: by the difference, which is exact: a sum rounded up would let P past f16's range)
+        if (SC ? tmax - m_ref > kRescaleThreshold : tmax > m_ref + kRescaleThreshold) {
           alpha = m_ref == -INFINITY ? 0.f : fast_exp2(m_ref - tmax);
           m_ref = tmax;
           l *= alpha;
@@ -1120,36 +1109,49 @@ __global__ void __launch_bounds__(WCfg<D, KV8, SC>::kThreads, 1)
         // P = exp2(x - m) as bf16 (f16) pairs, written over the S columns: V's type, the one that the product takes
         // beside it; l sums the fp32 ones.  Against 64 bits an output is off by 0.0023 of its norm so (codes:
         // 0.0017), by 0.0017 with its own rounding alone
-        const uint64_t mul = pair(f, f), sub = pair(lv - mbase, lv - mbase);
+        const uint64_t sub = pair(-mbase, -mbase);
         uint64_t rs[4] = {0ull, 0ull, 0ull, 0ull};
-        auto exp32 = [&](const uint32_t (&x32)[32], uint32_t* w) {  // 32 columns -> 16 words of P
-#pragma unroll
-          for (int e = 0; e < 32; e += 2) {
-            const float2 x = unpair(fma_pair(pair(__uint_as_float(x32[e]), __uint_as_float(x32[e + 1])), mul, sub));
-            const float p0 = fast_exp2(x.x), p1 = fast_exp2(x.y);
-            rs[(e >> 1) & 3] = add_pair(rs[(e >> 1) & 3], pair(p0, p1));
-            w[e >> 1] = KV8 ? pack_f16(p0, p1) : pack_bf16(p0, p1);
-          }
-        };
         if constexpr (SC) {
 #pragma unroll 1
           for (int cb = 0; cb < 4; ++cb) {
             uint32_t x[1][32], w[16];
+            const float4 c2[2] = {of[2 * cb], of[2 * cb + 1]};  // read ahead of the columns: 1002 -> 933 us
             load(x, cb, 1);
-            exp32(x[0], w);
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+              const float4 c = c2[h];
+              const uint64_t mul = pair(c.x, c.x), add = pair(c.y, c.y), inv = pair(c.z, c.z);
+#pragma unroll
+              for (int e = 16 * h; e < 16 * h + 16; e += 2) {
+                const uint64_t y = fma_pair(pair(__uint_as_float(x[0][e]), __uint_as_float(x[0][e + 1])), mul, add);
+                const float2 d = unpair(add_pair(y, sub));
+                const float p0 = fast_exp2(d.x), p1 = fast_exp2(d.y);
+                rs[(e >> 1) & 3] = fma_pair(pair(p0, p1), inv, rs[(e >> 1) & 3]);
+                w[e >> 1] = pack_f16(p0, p1);
+              }
+            }
             tmem_st16(s_col + cb * 16, w);
           }
         } else {
+          const uint64_t mul = pair(sl2, sl2);
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
             uint32_t w[32];
 #pragma unroll
-            for (int cb = 0; cb < 2; ++cb) exp32(v[(2 * h + cb) % kHeld], w + 16 * cb);
+            for (int cb = 0; cb < 2; ++cb)
+#pragma unroll
+              for (int e = 0; e < 32; e += 2) {
+                const uint32_t (&c)[32] = v[(2 * h + cb) % kHeld];
+                const float2 x = unpair(fma_pair(pair(__uint_as_float(c[e]), __uint_as_float(c[e + 1])), mul, sub));
+                const float p0 = fast_exp2(x.x), p1 = fast_exp2(x.y);
+                rs[(e >> 1) & 3] = add_pair(rs[(e >> 1) & 3], pair(p0, p1));
+                w[cb * 16 + (e >> 1)] = KV8 ? pack_f16(p0, p1) : pack_bf16(p0, p1);
+              }
             tmem_st32(s_col + h * 32, w);
           }
         }
         const float2 sum = unpair(add_pair(add_pair(rs[0], rs[1]), add_pair(rs[2], rs[3])));
-        l = SC ? fmaf(sum.x + sum.y, iv, l) : l + (sum.x + sum.y);
+        l += sum.x + sum.y;
         // O is rescaled in place only when some row of the warp moved its
         // reference max.  PV_t(j-1) is complete: S_t(j) was issued after it.
         if (__any_sync(0xffffffffu, rescale)) {
@@ -1166,9 +1168,13 @@ __global__ void __launch_bounds__(WCfg<D, KV8, SC>::kThreads, 1)
         tmem_wait_st();
         tc_fence_before();
         mbar_arrive(bar(W_PFULL + t));
+        if constexpr (SC) leave_scales();
       }
       if constexpr (SC)
-        for (int j = ntt; j < it.nt(); ++j) take_scales();  // tiles of the other query tile alone
+        for (int j = ntt; j < it.nt(); ++j) {  // tiles of the other query tile alone
+          take_scales();
+          leave_scales();
+        }
       if (next_q) {
         if (ntt == 0) copy_q(nx);
         publish_q();

@@ -86,17 +86,18 @@ __device__ __forceinline__ void tmem_ld32(uint32_t taddr, uint32_t (&v)[32]) {
       : "r"(taddr));
 }
 
-// The largest of 32 consecutive fp32 columns of this thread's TMEM lane (NaN aside), found
-// as they are loaded; the columns themselves are dropped.
-__device__ __forceinline__ float tmem_max32(uint32_t taddr) {
-  float x;
+// The largest of each 16 of 32 consecutive fp32 columns of this thread's TMEM lane (NaN aside),
+// found as they are loaded; the columns themselves are dropped.
+__device__ __forceinline__ float2 tmem_max16x2(uint32_t taddr) {
+  float2 x;
   asm volatile(
       "{\n.reg .b32 d<32>;\n"
-      "tcgen05.ld.red.sync.aligned.32x32b.x32.max.f32 {d0,d1,d2,d3,d4,d5,d6,d7,d8,d9,d10,d11,d12,d13,d14,d15,"
-      "d16,d17,d18,d19,d20,d21,d22,d23,d24,d25,d26,d27,d28,d29,d30,d31}, %0, [%1];\n"
+      "tcgen05.ld.red.sync.aligned.32x32b.x16.max.f32 {d0,d1,d2,d3,d4,d5,d6,d7,d8,d9,d10,d11,d12,d13,d14,d15}, %0, [%2];\n"
+      "tcgen05.ld.red.sync.aligned.32x32b.x16.max.f32 {d16,d17,d18,d19,d20,d21,d22,d23,d24,d25,d26,d27,d28,d29,d30,"
+      "d31}, %1, [%3];\n"
       "tcgen05.wait::ld.sync.aligned;\n}\n"
-      : "=f"(x)
-      : "r"(taddr)
+      : "=&f"(x.x), "=&f"(x.y)
+      : "r"(taddr), "r"(taddr + 16)
       : "memory");
   return x;
 }
