@@ -620,6 +620,8 @@ pa_status paged_attention_prefill_int8(const pa_kv_pool* pool, const pa_kv_scale
  *
  *   mass_out[b, j] = decay * mass_in[b, j] + sum_h softmax_j(scale * q[b,h] . K_b[j, h/G]),
  *   j in [0, seq_lens[b]); entries at and past seq_lens[b] are left as they were.
+ *   The keys of a page that is out of range take no part, whatever the pool's type: their
+ *   weight is 0.
  *
  * Summed over the layers or steps that share a block table, it says which keys
  * the queries still look at (paged_kv_evict_rows, paged_kv_evict_pages).  The sum

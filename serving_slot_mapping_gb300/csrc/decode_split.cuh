@@ -59,7 +59,9 @@
 //   into a scratch [B, Hq, keys], and every finished row its log2 of the sum of
 //   2^x; key_mass_kernel (decode_mass.cu) makes weights of them.  4 Hq bytes a key
 //   written and read, 6 % of a bf16 GQA key's bytes, against half of them for
-//   multiplying q and K again.
+//   multiplying q and K again.  The keys of a page out of range take no part, whatever
+//   the pool: nothing was loaded for them, and what a stage holds in their places would
+//   stay in the masses of every key of the sequence.
 // * Keys at or past L_b are masked in S and their V rows are zeroed in shared
 //   memory, so stale or NaN-poisoned slots never reach the output.
 // * At a segment (sequence x head box) end, warps that shared a head merge in
@@ -348,7 +350,9 @@ struct Layout {
 // most; then a word with a bit for each block whose page is out of range.
 constexpr int kStageScales = 144;
 
-template <int D, int HB, int RT, bool KV8 = false, bool WC = false, bool SC = false>
+// MASS without scales: a word a stage, with two bits for each block, one for each 8 keys
+// whose page is out of range.  They take a part of the slack that `fixed` has.
+template <int D, int HB, int RT, bool KV8 = false, bool WC = false, bool SC = false, bool MASS = false>
 __host__ __device__ inline Layout make_layout(int G, int B, int budget) {
   using C = Cfg<D, HB, RT, KV8, WC, SC>;
   Layout L;
@@ -363,8 +367,13 @@ __host__ __device__ inline Layout make_layout(int G, int B, int budget) {
   L.bar_off = s * C::kStageBytes + 2 * L.qslot;
   L.mrg_off = L.bar_off + (2 * s + C::kBars) * 8 + 128;  // + the pending-merge list
   L.prefix_off = L.mrg_off + merge;
-  L.scale_off = (L.prefix_off + prefix + 127) / 128 * 128;
+  L.scale_off = (L.prefix_off + prefix + 127) / 128 * 128;  // (prefix_off + prefix: multiples of 8)
   L.total = SC ? L.scale_off + kMaxStages * kStageScales + 1024 : L.prefix_off + prefix + 1024;
+  if (MASS && !SC) {
+    static_assert(kMaxStages * 4 <= 128, "the words fit in the slack");
+    L.scale_off = L.prefix_off + prefix;
+    L.total += kMaxStages * 4;
+  }
   return L;
 }
 
@@ -385,7 +394,7 @@ __global__ void __launch_bounds__(Cfg<D, HB, RT, KV8, WC, (EXT & kExtScales) != 
   const int Hkv = p.pool.num_kv_heads;
   const int Hg = Hkv / HB;  // head boxes per sequence
   const int Hq = p.num_q_heads;
-  const Layout lay = make_layout<D, HB, RT, KV8, WC, SC>(G, B, p.smem_budget);
+  const Layout lay = make_layout<D, HB, RT, KV8, WC, SC, MASS>(G, B, p.smem_budget);
   const int S = lay.stages;
   unsigned char* ring = smem;
   unsigned char* qring = smem + S * C::kStageBytes;
@@ -795,6 +804,17 @@ __global__ void __launch_bounds__(Cfg<D, HB, RT, KV8, WC, (EXT & kExtScales) != 
           *reinterpret_cast<volatile uint32_t*>(smem + lay.scale_off + slot * kStageScales + 128) = bad;
         cp_async_arrive(full_bar(slot));
       }
+      if constexpr (MASS && !SC) {
+        unsigned gone = 0u;
+#pragma unroll
+        for (int x = 0; x < kOpsPerLane; ++x) {
+          const OpGeom g = nbs == NBS ? full_geom[x] : geom(nbs, lane + 32 * x);
+          if (g.on && g.TT == 0 && (cur.k + g.jj) * 16 + g.q * R < cur.L && row[x] < 0)
+            gone |= (R == 16 ? 3u : 1u << g.q) << (2 * g.jj);
+        }
+        gone = __reduce_or_sync(0xffffffffu, gone);
+        if (lane == 0) *reinterpret_cast<volatile uint32_t*>(smem + lay.scale_off + 4 * slot) = gone;
+      }
       if (lane == 0) mbar_arrive_expect_tx(full_bar(slot), (uint32_t)(issued * R * C::kRowBytes * HB * slabs_per_op));
       __syncwarp();
 #pragma unroll
@@ -918,6 +938,21 @@ __global__ void __launch_bounds__(Cfg<D, HB, RT, KV8, WC, (EXT & kExtScales) != 
             lv[bb] = __log2f(clamp_scale(vs));
             iv[bb] = fast_exp2(-lv[bb]);  // of the very power that p' carries
           }
+          unsigned gone = 0u;  // bit i: keys 8 i .. + 7 have no page
+          if constexpr (MASS && !SC) {
+            gone = (*reinterpret_cast<const volatile uint32_t*>(smem + lay.scale_off + 4 * slot) >> (2 * jb)) & 3u;
+            if (gone != 0u) {  // as the rows past L_b below
+              constexpr int kCh = C::kRowBytes / 16;
+              for (int e = lane; e < 16 * C::kSlabs * kCh; e += 32) {
+                const int row = e / (C::kSlabs * kCh), rem = e % (C::kSlabs * kCh);
+                if ((gone >> (row >> 3)) & 1u)
+                  *reinterpret_cast<uint4*>(vt + (rem / kCh) * C::kBoxBytes + row * C::kRowBytes + (rem % kCh) * 16) =
+                      make_uint4(0, 0, 0, 0);
+              }
+              __syncwarp();
+              touched = true;
+            }
+          }
           if (valid[bb] < 16) {
             // rows past L_b may hold stale or poisoned data (NaN would survive
             // P = 0): zero them in V; K is masked below.  A row's chunks stay in
@@ -948,6 +983,8 @@ __global__ void __launch_bounds__(Cfg<D, HB, RT, KV8, WC, (EXT & kExtScales) != 
             __syncwarp();
             touched = true;
           }
+          // (beside each other: one register less where they are short)
+          if constexpr (MASS && !SC) valid[bb] = min(valid[bb], 16) | (int)(gone << 8);
           const uint32_t kbase = smem_u32(kt);
           if (KV8) {
             // e4m3 K as 16-bit pairs: matrix m = keys (m & 1) * 8 .. + 7 of
@@ -981,6 +1018,8 @@ __global__ void __launch_bounds__(Cfg<D, HB, RT, KV8, WC, (EXT & kExtScales) != 
         }
 #pragma unroll
         for (int t = 0; t < 2 * BPW; ++t) {
+          int seen = valid[t >> 1];
+          if constexpr (MASS && !SC) seen = (seen >> (8 + (t & 1))) & 1 ? 0 : seen & 31;
           if constexpr (MASS) {
             // the scores themselves, for key_mass_kernel (whole 16-key blocks: rows of the
             // scratch are padded to them)
@@ -989,7 +1028,7 @@ __global__ void __launch_bounds__(Cfg<D, HB, RT, KV8, WC, (EXT & kExtScales) != 
 #pragma unroll
               for (int e = 0; e < 4; ++e) {
                 const int key = (t & 1) * 8 + (lane & 3) * 2 + (e & 1);
-                x[e] = key < valid[t >> 1] ? s[t][e] * (SC ? kf[t >> 1] : sl2) : -INFINITY;
+                x[e] = key < seen ? s[t][e] * (SC ? kf[t >> 1] : sl2) : -INFINITY;
               }
               const int64_t key = (int64_t)(first_k + done + jw * BPW + (t >> 1)) * 16 + (t & 1) * 8 + (lane & 3) * 2;
               float* to = p.scores + ((int64_t)cc.b * Hq + (int64_t)hk * G) * p.score_stride + key;
@@ -1001,9 +1040,9 @@ __global__ void __launch_bounds__(Cfg<D, HB, RT, KV8, WC, (EXT & kExtScales) != 
           for (int e = 0; e < 4; ++e) {
             const int key = (t & 1) * 8 + (lane & 3) * 2 + (e & 1);
             if constexpr (SC)
-              s[t][e] = key < valid[t >> 1] ? fmaf(s[t][e], kf[t >> 1], lv[t >> 1]) : -INFINITY;
+              s[t][e] = key < seen ? fmaf(s[t][e], kf[t >> 1], lv[t >> 1]) : -INFINITY;
             else
-              s[t][e] = key < valid[t >> 1] ? s[t][e] * sl2 : -INFINITY;
+              s[t][e] = key < seen ? s[t][e] * sl2 : -INFINITY;
           }
         }
         float mx0 = -INFINITY, mx1 = -INFINITY;
@@ -1017,7 +1056,7 @@ __global__ void __launch_bounds__(Cfg<D, HB, RT, KV8, WC, (EXT & kExtScales) != 
         mx1 = fmaxf(mx1, __shfl_xor_sync(0xffffffffu, mx1, 1));
         mx1 = fmaxf(mx1, __shfl_xor_sync(0xffffffffu, mx1, 2));
         float mn0 = fmaxf(m0, mx0), mn1 = fmaxf(m1, mx1);
-        if constexpr (SC) {  // no key yet (a page out of range): any finite reference
+        if constexpr (EXT != 0) {  // no key yet (a page out of range): any finite reference
           mn0 = mn0 == -INFINITY ? -1e30f : mn0;
           mn1 = mn1 == -INFINITY ? -1e30f : mn1;
         }
@@ -1340,7 +1379,8 @@ namespace {
 template <int D, int HB, int RT, bool KV8, bool FUSED, bool WC = false, int EXT = 0>
 cudaError_t launch_split(const DecodeParams& p, const CUtensorMap& tk, const CUtensorMap& tv, cudaStream_t s) {
   using C = Cfg<D, HB, RT, KV8, WC, (EXT & kExtScales) != 0>;
-  const Layout lay = make_layout<D, HB, RT, KV8, WC, (EXT & kExtScales) != 0>(p.group, p.batch, p.smem_budget);
+  const Layout lay =
+      make_layout<D, HB, RT, KV8, WC, (EXT & kExtScales) != 0, (EXT & kExtMass) != 0>(p.group, p.batch, p.smem_budget);
   if (lay.stages < 2) return cudaErrorInvalidConfiguration;
   auto kern = decode_split_kernel<D, HB, RT, KV8, FUSED, WC, EXT>;
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, lay.total);
