@@ -492,28 +492,56 @@ __global__ void __launch_bounds__(kEvictThreads) evict_kernel(const __grid_const
   if constexpr (CL) cluster_sync();  // no CTA leaves while another reads its counts
 }
 
+// Whether a cluster of kMaxCtas CTAs, more than the 8 that every GPU takes, finds its SMs
+// beside one another (on a part of a GPU it may not).
+template <typename Kernel>
+bool most_fit(Kernel kern, size_t smem) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(kMaxCtas);
+  cfg.blockDim = dim3(kEvictThreads);
+  cfg.dynamicSmemBytes = smem;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = kMaxCtas;
+  attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  int n = 0;
+  const bool ok = cudaOccupancyMaxActiveClusters(&n, kern, &cfg) == cudaSuccess;
+  if (!ok) (void)cudaGetLastError();
+  return ok && n > 0;
+}
+
 }  // namespace
+
+// CTAs of a sequence, `most` at most: as many as find an SM, with 4096 rows each or more;
+// enough that their stretches fit in shared memory, where `most` can.  One sequence of
+// 131,072 rows: 21 us on 8 CTAs, 16 on 16; of 8192 rows, where one CTA would do: 11.4 us on
+// two, 9.8 on one; of 32,768: 11.9 us on eight, 13.9 on four.
+int evict_cluster(int num_sms, int32_t batch, int64_t units, int64_t rows, int most) {
+  int c = 1;
+  while (c < most && ((int64_t)batch * c * 2 <= num_sms && rows >= 4096 * 2 * (int64_t)c)) c *= 2;
+  while (c < most && units > (int64_t)c * (kCacheUnits - 32)) c *= 2;
+  return c;
+}
 
 cudaError_t launch_evict(const EvictParams& p, bool pages, int num_sms, cudaStream_t s) {
   if (p.batch <= 0) return cudaSuccess;
   const int64_t units = pages ? std::min<int64_t>(p.max_blocks, (p.max_len + p.page_size - 1) / p.page_size) : p.max_len;
   if (pages && units > kMaxEvictPages) return cudaErrorInvalidValue;  // their weights have no place
-  // CTAs of a sequence: as many as find an SM, with 4096 rows each or more; enough
-  // that their stretches fit in shared memory, where 16 can.  One sequence of 131,072
-  // rows: 21 us on 8 CTAs, 16 on 16; of 8192 rows, where one CTA would do: 11.4 us on
-  // two, 9.8 on one; of 32,768: 11.9 us on eight, 13.9 on four.
   const int64_t rows = pages ? units * p.page_size : units;
-  int csize = 1;
-  while (csize < kMaxCtas && ((int64_t)p.batch * csize * 2 <= num_sms && rows >= 4096 * 2 * (int64_t)csize)) csize *= 2;
-  while (csize < kMaxCtas && units > (int64_t)csize * (kCacheUnits - 32)) csize *= 2;
-  const int64_t stretch = (units + csize - 1) / csize + 32;
-  const int smem = (int)(stretch < kCacheUnits ? stretch : kCacheUnits) * 4 + 16;
+  int csize = evict_cluster(num_sms, p.batch, units, rows, kMaxCtas);
   auto kern = csize > 1 ? (pages ? evict_kernel<true, true> : evict_kernel<false, true>)
                         : (pages ? evict_kernel<true, false> : evict_kernel<false, false>);
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kCacheUnits * 4 + 16);
   if (e == cudaSuccess && csize > 8) e = cudaFuncSetAttribute(kern, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
   if (e != cudaSuccess) return e;
-  return launch_pdl_cluster(kern, dim3((unsigned)(p.batch * csize)), dim3(kEvictThreads), (size_t)smem, csize, s, p, csize);
+  auto smem_of = [&](int c) {
+    const int64_t stretch = (units + c - 1) / c + 32;
+    return (size_t)(stretch < kCacheUnits ? stretch : kCacheUnits) * 4 + 16;
+  };
+  if (csize > 8 && !most_fit(kern, smem_of(csize))) csize = evict_cluster(num_sms, p.batch, units, rows, 8);
+  return launch_pdl_cluster(kern, dim3((unsigned)(p.batch * csize)), dim3(kEvictThreads), smem_of(csize), csize, s, p, csize);
 }
 
 }  // namespace pa

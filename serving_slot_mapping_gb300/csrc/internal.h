@@ -84,6 +84,8 @@ struct EvictParams {
   unsigned long long* err;
 };
 cudaError_t launch_evict(const EvictParams& p, bool pages, int num_sms, cudaStream_t s);
+// CTAs that share a sequence of `units` rows or pages (`rows` rows), a power of two, `most` at most.
+int evict_cluster(int num_sms, int32_t batch, int64_t units, int64_t rows, int most);
 
 // ---- norm, rotation and append (norm_rope.cu) --------------------------------
 struct NormRopeParams {
