@@ -669,7 +669,7 @@ pa_status paged_attention_decode_mass(const pa_kv_pool* pool, const pa_kv_scales
  *
  * mass, new_mass  device f32 [batch, width], rows mass_stride / new_mass_stride >=
  *               width apart; a sequence longer than width is cut to it and
- *               recorded (code 3).
+ *               recorded (code 3).  width is at most 2^31 - 65536 (PA_ERR_RANGE).
  * budget        >= num_sinks + num_recent (PA_ERR_SHAPE).
  * keep_indptr   device int32 [batch + 1], written.   base  device int32 [batch], written.
  * keep          device int32 [num_keep], num_keep >= batch * (budget - num_sinks) (0
@@ -700,7 +700,7 @@ pa_status paged_kv_evict_rows(const float* mass, int64_t mass_stride, const int3
  * budget        in pages, at least ceil(num_sinks / page_size) + 1 +
  *               (max(num_recent, 1) + page_size - 2) / page_size (PA_ERR_SHAPE): the most
  *               pages that the rows kept in any case lie in.
- * At most 327,424 pages a sequence (PA_ERR_RANGE).
+ * At most 327,424 pages a sequence and 2^31 - 65536 columns of the table (PA_ERR_RANGE).
  */
 pa_status paged_kv_evict_pages(const float* mass, int64_t mass_stride, const int32_t* block_table,
                                int32_t max_blocks_per_seq, const int32_t* seq_lens, int32_t batch,

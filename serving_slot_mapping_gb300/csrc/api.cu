@@ -1119,6 +1119,10 @@ pa_status paged_attention_decode_mass(const pa_kv_pool* pool, const pa_kv_scales
 
 namespace {
 
+// Rows, and columns of a block table, that the eviction's kernels count in 32 bits, with
+// what their last steps go past the end: 16 CTAs x 512 threads x vectors of 4.
+constexpr int32_t kMaxEvictWidth = INT32_MAX - 65535;
+
 // What the two forms of eviction share; the caller has set its own arrays.
 pa_status check_evict(const float* mass, int64_t mass_stride, const int32_t* seq_lens, int32_t batch, int32_t width,
                       int32_t budget, int32_t num_sinks, int32_t num_recent, const float* new_mass,
@@ -1126,6 +1130,7 @@ pa_status check_evict(const float* mass, int64_t mass_stride, const int32_t* seq
   if (batch < 0 || width < 0 || budget < 0 || num_sinks < 0 || num_recent < 0) return PA_ERR_SHAPE;
   if (mass_stride < width || new_mass_stride < width || protect > budget) return PA_ERR_SHAPE;
   if (batch > INT32_MAX / 16 || mass_stride > INT32_MAX || new_mass_stride > INT32_MAX) return PA_ERR_RANGE;
+  if (width > kMaxEvictWidth) return PA_ERR_RANGE;
   if (batch == 0) return PA_OK;
   if (seq_lens == nullptr || (width > 0 && (mass == nullptr || new_mass == nullptr))) return PA_ERR_NULL;
   if (!aligned(mass, 4) || !aligned(new_mass, 4) || !aligned(seq_lens, 4)) return PA_ERR_ALIGN;
@@ -1204,7 +1209,7 @@ pa_status paged_kv_evict_pages(const float* mass, int64_t mass_stride, const int
                                int64_t new_mass_stride, void* stream) {
   if (page_size <= 0 || max_blocks_per_seq <= 0) return PA_ERR_SHAPE;
   if (!is_pow2(page_size) || page_size > 1024) return PA_ERR_UNSUPPORTED;
-  if ((int64_t)max_blocks_per_seq * page_size > INT32_MAX) return PA_ERR_RANGE;
+  if ((int64_t)max_blocks_per_seq * page_size > INT32_MAX || max_blocks_per_seq > kMaxEvictWidth) return PA_ERR_RANGE;
   // pages that hold sinks, and the most that the last max(num_recent, 1) rows lie in
   const int64_t recent = std::max(num_recent, 1);
   const int64_t protect = ((int64_t)std::max(num_sinks, 0) + page_size - 1) / page_size + (recent + page_size - 2) / page_size + 1;
