@@ -635,7 +635,9 @@ pa_status paged_attention_prefill_int8(const pa_kv_pool* pool, const pa_kv_scale
  *               Rows that overlap mass_out otherwise are refused (PA_ERR_SHAPE).
  * decay         finite; 1 adds, between 1 and 0 old weights fade, 0: mass_in is not read.
  * mass_out      device f32, rows mass_stride >= max_seq_len apart.
- * max_seq_len   a longer sequence is cut to it and recorded (code 3).
+ * max_seq_len   at most 2^31 - 1024 (PA_ERR_RANGE); a longer sequence is cut to it and
+ *               recorded (code 3).  The workspace has 4 bytes for each query head and
+ *               key up to it: pass the longest length rather than what the table holds.
  * workspace     paged_attention_decode_mass_workspace_size(...) bytes, 16-byte
  *               aligned, contents need no initialisation.
  * out is 8-byte aligned.  Every other argument is as for paged_attention_decode.

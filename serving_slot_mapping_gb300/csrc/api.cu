@@ -1076,6 +1076,7 @@ pa_status paged_attention_decode_mass(const pa_kv_pool* pool, const pa_kv_scales
   if (st != PA_OK) return st;
   if (core_path(pool)) return PA_ERR_UNSUPPORTED;  // the scores are those of the tensor-core kernel
   if (batch > 65535) return PA_ERR_RANGE;          // grid y
+  if (max_seq_len > INT32_MAX - 1023) return PA_ERR_RANGE;  // keys and those of a last block are counted in 32 bits
   if (!std::isfinite(decay)) return PA_ERR_RANGE;
   if (mass_stride < max_seq_len) return PA_ERR_SHAPE;
   if (mass_stride > INT32_MAX) return PA_ERR_RANGE;
