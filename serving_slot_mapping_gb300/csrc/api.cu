@@ -1115,7 +1115,7 @@ pa_status paged_attention_decode_mass(const pa_kv_pool* pool, const pa_kv_scales
   m.num_q_heads = num_q_heads;
   m.max_keys = max_seq_len;
   m.max_len = std::min<int32_t>(max_seq_len, max_blocks_per_seq * pool->page_size);
-  return launched(pa::launch_key_mass(m, s));
+  return launched(pa::launch_key_mass(m, num_sms(), s));
 }
 
 namespace {

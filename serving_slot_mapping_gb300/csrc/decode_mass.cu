@@ -87,11 +87,16 @@ cudaError_t launch_mass(const KeyMassParams& p, cudaStream_t s) {
 
 }  // namespace
 
-cudaError_t launch_key_mass(const KeyMassParams& p, cudaStream_t s) {
+// Two tiles a block past 8 single ones an SM, the most whose threads it holds.  It sees the
+// bound of the lengths: blocks past a sequence's end return at once.
+int key_mass_tiles(int num_sms, int32_t batch, int32_t max_keys) {
+  const int64_t tiles = (int64_t)batch * (((int64_t)max_keys + kMassKeys - 1) / kMassKeys);
+  return tiles <= 8 * (int64_t)num_sms ? 1 : 2;
+}
+
+cudaError_t launch_key_mass(const KeyMassParams& p, int num_sms, cudaStream_t s) {
   if (p.max_keys <= 0) return cudaSuccess;
-  // two tiles a block once single ones are more than a GPU of 152 SMs holds at once (8 each)
-  const int64_t tiles = (int64_t)p.batch * ((p.max_keys + kMassKeys - 1) / kMassKeys);
-  return tiles <= 1216 ? launch_mass<1>(p, s) : launch_mass<2>(p, s);
+  return key_mass_tiles(num_sms, p.batch, p.max_keys) == 1 ? launch_mass<1>(p, s) : launch_mass<2>(p, s);
 }
 
 cudaError_t launch_decode_scores(const DecodeParams& p, cudaStream_t s) {

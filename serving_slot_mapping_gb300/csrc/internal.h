@@ -269,7 +269,8 @@ struct KeyMassParams {
   float decay;
   int32_t batch, num_q_heads, max_keys, max_len;
 };
-cudaError_t launch_key_mass(const KeyMassParams& p, cudaStream_t s);
+int key_mass_tiles(int num_sms, int32_t batch, int32_t max_keys);  // of 128 keys, to a block
+cudaError_t launch_key_mass(const KeyMassParams& p, int num_sms, cudaStream_t s);
 // Cascade: split kernel on s, then the combine after `prefix_done` (an event
 // recorded once the prefix partials are written) has completed.
 cudaError_t launch_decode_cascade_bf16(const DecodeParams& p, cudaStream_t s, cudaEvent_t prefix_done);
