@@ -13,9 +13,16 @@ from .capi import (  # noqa: F401
     paged_qk_norm_rope_append,
     paged_kv_copy_pages,
     paged_kv_compact,
+    paged_kv_append_int8,
+    paged_attention_decode_int8,
+    paged_attention_prefill_int8,
+    paged_attention_decode_mass,
+    paged_kv_evict_rows,
+    paged_kv_evict_pages,
     make_pools,
     decode_workspace,
     decode_workspace_size,
+    decode_mass_workspace,
     device_error,
     PagedAttnError,
     make_pool,
