@@ -572,7 +572,9 @@ typedef struct pa_kv_scales {
  *   becomes 0); where s is larger than the scale before, the codes c of the
  *   block's other rows become rint(c * (scale / s)).
  *
- * Arithmetic is fp32 (one division, rounding to nearest even).  A block's first
+ * Arithmetic is fp32 (one division, rounding to nearest even).  A row's code is off by
+ * half a step of the scale that it is written under, and by half a step more of each
+ * larger scale that it is re-encoded under later, once a call that raises it.  A block's first
  * slot is the first that a sequence writes, so a page taken into use again
  * starts anew; its slots not yet written may hold anything, and are left or
  * re-encoded.
@@ -582,8 +584,10 @@ typedef struct pa_kv_scales {
  *               (value_stride) elements, multiples of 8, at least a row.
  * slot_mapping  as for paged_kv_append.  The tokens of one block must follow one
  *               another in the call (as those of a sequence do; up to 31 padding
- *               tokens may stand between two): else which of their scales the
- *               block keeps is unspecified.
+ *               tokens may stand between two): else the block's codes and scale
+ *               are unspecified, its other rows' codes among them, and nothing is
+ *               recorded.  Two tokens of one slot: which of them lands is
+ *               unspecified, as for paged_kv_append.
  */
 pa_status paged_kv_append_int8(const pa_kv_pool* pool, const pa_kv_scales* scales, const void* key,
                                int64_t key_stride, const void* value, int64_t value_stride,

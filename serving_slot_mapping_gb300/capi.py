@@ -772,7 +772,8 @@ def paged_kv_append_int8(key_pool, value_pool, key_scales, value_scales, key, va
     keeping ``key_scales`` / ``value_scales`` (float32 ``[num_pages, page_size /
     block_tokens, Hkv]``) of the blocks that they lie in: a block's scale is its
     largest magnitude / 127; where it grows, the block's earlier codes are encoded
-    anew.  The tokens of one block must follow one another in the call (padding aside)."""
+    anew.  The tokens of one block must follow one another in the call (padding aside, at
+    most 31 in a row): else the block's codes and scale are unspecified."""
     pool = _pool_of(key_pool, value_pool, 1.0, 1.0)
     sc = _scales_of(pool, key_scales, value_scales)
     T = slot_mapping.numel()
