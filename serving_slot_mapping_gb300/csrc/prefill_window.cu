@@ -275,7 +275,7 @@ struct SortedWalker {
     }
     int rel = (int)(g - above);  // among the row tiles of this level
     it->hk = (int)(rank - g * Hkv);
-    for (int base = 0;; base += 32) {
+    for (int base = 0; base < p.batch; base += 32) {
       const int b = base + (threadIdx.x & 31), more = count(p, b, level + 1), mine = count(p, b, level) - more;
       int incl = mine;
 #pragma unroll
@@ -295,6 +295,7 @@ struct SortedWalker {
       }
       rel -= all;
     }
+    return false;  // (lengths that changed since they were counted)
   }
 };
 
