@@ -938,21 +938,11 @@ __global__ void __launch_bounds__(Cfg<D, HB, RT, KV8, WC, (EXT & kExtScales) != 
             lv[bb] = __log2f(clamp_scale(vs));
             iv[bb] = fast_exp2(-lv[bb]);  // of the very power that p' carries
           }
-          unsigned gone = 0u;  // bit i: keys 8 i .. + 7 have no page
-          if constexpr (MASS && !SC) {
-            gone = (*reinterpret_cast<const volatile uint32_t*>(smem + lay.scale_off + 4 * slot) >> (2 * jb)) & 3u;
-            if (gone != 0u) {  // as the rows past L_b below
-              constexpr int kCh = C::kRowBytes / 16;
-              for (int e = lane; e < 16 * C::kSlabs * kCh; e += 32) {
-                const int row = e / (C::kSlabs * kCh), rem = e % (C::kSlabs * kCh);
-                if ((gone >> (row >> 3)) & 1u)
-                  *reinterpret_cast<uint4*>(vt + (rem / kCh) * C::kBoxBytes + row * C::kRowBytes + (rem % kCh) * 16) =
-                      make_uint4(0, 0, 0, 0);
-              }
-              __syncwarp();
-              touched = true;
-            }
-          }
+          // bit i: keys 8 i .. + 7 have no page (read here, used behind the products)
+          const unsigned gone =
+              MASS && !SC
+                  ? (*reinterpret_cast<const volatile uint32_t*>(smem + lay.scale_off + 4 * slot) >> (2 * jb)) & 3u
+                  : 0u;
           if (valid[bb] < 16) {
             // rows past L_b may hold stale or poisoned data (NaN would survive
             // P = 0): zero them in V; K is masked below.  A row's chunks stay in
@@ -983,8 +973,6 @@ __global__ void __launch_bounds__(Cfg<D, HB, RT, KV8, WC, (EXT & kExtScales) != 
             __syncwarp();
             touched = true;
           }
-          // (beside each other: one register less where they are short)
-          if constexpr (MASS && !SC) valid[bb] = min(valid[bb], 16) | (int)(gone << 8);
           const uint32_t kbase = smem_u32(kt);
           if (KV8) {
             // e4m3 K as 16-bit pairs: matrix m = keys (m & 1) * 8 .. + 7 of
@@ -1014,6 +1002,20 @@ __global__ void __launch_bounds__(Cfg<D, HB, RT, KV8, WC, (EXT & kExtScales) != 
               mma_bf16_16816(s[2 * bb], qf[kk], b0, b1);
               mma_bf16_16816(s[2 * bb + 1], qf[kk], b2, b3);
             }
+          }
+          if constexpr (MASS && !SC) {
+            if (gone != 0u) {  // zeros in V, as in the rows past L_b
+              constexpr int kCh = C::kRowBytes / 16;
+              for (int e = lane; e < 16 * C::kSlabs * kCh; e += 32) {
+                const int row = e / (C::kSlabs * kCh), rem = e % (C::kSlabs * kCh);
+                if ((gone >> (row >> 3)) & 1u)
+                  *reinterpret_cast<uint4*>(vt + (rem / kCh) * C::kBoxBytes + row * C::kRowBytes + (rem % kCh) * 16) =
+                      make_uint4(0, 0, 0, 0);
+              }
+              __syncwarp();
+              touched = true;
+            }
+            valid[bb] = min(valid[bb], 16) | (int)(gone << 8);  // beside each other: one register
           }
         }
 #pragma unroll
