@@ -17,8 +17,9 @@
 // tokens, 8 heads of 128: 24.1 us, with one warp a run 36.4.)  A re-encoded block is rewritten
 // whole before the run's own rows, so the team need not know which rows are its own.
 // Six CTAs of an SM (80 registers a thread) hide each other's chains of slots, rows,
-// maximum and codes: 15.3 us for 10,304 tokens in blocks of 16 (9.3 of bytes); five 18.0,
-// eight, which spill, 15.4.
+// maximum and codes: 15.3-15.8 us for 10,304 tokens of sequences that begin a block of 16
+// (9.3 of bytes); five 18.0, eight, which spill, 15.4.  Where the sequences begin inside a
+// block (10,648 tokens after 0-8192, 9.6 of bytes) it is 17.2 us, and 18 with five as with six.
 #include <algorithm>
 
 #include "common.cuh"

@@ -42,9 +42,11 @@
 //   stays in f16's range whatever the scales of the visible blocks are, and l sums P / v.
 //   y is rounded before m is taken off it, so that the largest P is 1 however large the
 //   scores are: an addition for two elements of S, beside the fused multiply-add (8 chunks
-//   of 512-2048 after 0-8192 tokens, 32 / 8 heads of 128: 933 us, without it 919).
-//   (Scales multiplied into the codes, relative to their tile's largest, took 948 us there,
-//   and cost a row its keys' last bits for the sake of blocks that it does not see.)
+//   of 512-2048 after 0-8192 tokens, 32 / 8 heads of 128: 933 us, without it 919; behind a
+//   branch that only large scores take 997 where the plain addition took 957).
+//   (Scales multiplied into the codes, relative to their tile's largest, took 940 us where
+//   this takes 958, and cost a row its keys' last bits for the sake of blocks that it does
+//   not see.)
 // Sixteen warps for that: 2 x 144 + 2 x 112 registers a thread, and the softmax in loops
 // of 32 columns: written out, it and the conversion did not fit in the instruction cache.
 // A block_table entry out of range is noted by the TMA warp; a CTA that met one

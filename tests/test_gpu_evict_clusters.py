@@ -1,6 +1,7 @@
 """Evictions on clusters of each size, against the oracle."""
 import numpy as np
 import pytest
+import torch
 
 from serving_slot_mapping_gb300 import build as build_mod
 from serving_slot_mapping_gb300 import capi
@@ -29,3 +30,35 @@ def test_pages(cuda_device, B, pages):
     ps = 16
     lens = [pages * ps - 37 * b - 5 for b in range(B)]
     check_pages(cuda_device, masses(B, pages * ps, 3, ties=0.4), lens, ps, pages // 4, 4, 100)
+
+
+def test_captured_on_sixteen(cuda_device):
+    """Long sequences in a captured graph, replayed on other masses and lengths."""
+    width, ps = 140000, 16
+    m = torch.empty(1, width, device=cuda_device)
+    L = torch.empty(1, dtype=torch.int32, device=cuda_device)
+    bt = torch.arange(width // ps, dtype=torch.int32, device=cuda_device).view(1, -1)
+    m.fill_(1.0)
+    L.fill_(width)
+    rows = [t.clone() for t in capi.paged_kv_evict_rows(m, L, 9000, 4, 100)]
+    pages = [t.clone() for t in capi.paged_kv_evict_pages(m, bt, L, ps, 700, 4, 100)]
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        capi.paged_kv_evict_rows(m, L, 9000, 4, 100, keep_indptr=rows[0], keep=rows[1], base=rows[2], new_mass=rows[3])
+        capi.paged_kv_evict_pages(m, bt, L, ps, 700, 4, 100, new_block_table=pages[0], new_seq_lens=pages[1],
+                                  new_mass=pages[2])
+    for seed, n in enumerate((width, 100001, 8999)):
+        m.copy_(torch.from_numpy(masses(1, width, seed)))
+        L.fill_(n)
+        for t in rows + pages:
+            t.zero_()
+        g.replay()
+        torch.cuda.synchronize()
+        kept = int(rows[0][-1])
+        for got, want in zip(rows, capi.paged_kv_evict_rows(m, L, 9000, 4, 100)):
+            cut = kept if got is rows[1] else None
+            assert torch.equal(got[:cut], want[:cut])
+        for got, want in zip(pages, capi.paged_kv_evict_pages(m, bt, L, ps, 700, 4, 100)):
+            assert torch.equal(got, want)
+    assert capi.device_error() == (0, 0)
