@@ -91,9 +91,7 @@ struct WCfg : PCfg<D, KV8> {
   static_assert(SC ? 2 * kSoftmaxRegs + 2 * kOtherRegs <= 4 * 128 : 2 * kSoftmaxRegs + kOtherRegs <= 3 * 168,
                 "more registers than the launch has");
   // 8 tiles in flight: {KV head, valid, hid0, hid1} after the first slots of their boxes
-  // (int8: pages of 16 slots or more, so 8 boxes at most)
-  static constexpr int kBoxes = SC ? 8 : 32;
-  static constexpr int kMetaOff = Base::kPageOff + 8 * kBoxes * 4;
+  static constexpr int kMetaOff = Base::kPageOff + 8 * 32 * 4;
   static constexpr int kItemOff = kMetaOff + 8 * 16;
   static constexpr int kWBarOff = kItemOff + kItems * kItemBytes;
   static constexpr int kTmemOff = kWBarOff + kWBars * 8;  // the word that tcgen05.alloc writes, behind every barrier
@@ -109,9 +107,13 @@ struct WCfg : PCfg<D, KV8> {
   static constexpr int kCodeOff = Base::kKOff + (2 + kNSV) * Base::kKVTile;
   static constexpr int kCodeTile = kBN * D;
   static_assert(!SC || kCodeOff + 2 * kCodeTile <= Base::kPageOff, "the stages of codes");
-  static constexpr int kScaleOff = kTmemOff + 16;
-  static constexpr int kWSmem = kScaleOff + (SC ? kScaleTiles * kScaleBytes : 0) + 1024;
-  static_assert(kScaleOff % 16 == 0 && kWSmem <= 232448, "shared memory");
+  // int8: pages of 16 slots or more, so a tile has 8 boxes at most, and the scales take what
+  // the first slots of 32 have left
+  static constexpr int kBoxes = SC ? 8 : 32;
+  static constexpr int kScaleOff = Base::kPageOff + 8 * 8 * 4;
+  static_assert(!SC || (kScaleOff % 16 == 0 && kScaleOff + kScaleTiles * kScaleBytes <= kMetaOff), "the tiles' scales");
+  static constexpr int kWSmem = kTmemOff + 16 + 1024;
+  static_assert(kWSmem <= 232448, "shared memory");
   // SPLIT, once the item's products are done: its rows of O, fp32, padded against
   // bank conflicts, and their (reference max, sum) over the K and V rings
   static constexpr int kPartRow = D + 4;
